@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 DUAL, FAST = 0, 1
 ACT_F16, ACT_BF16 = 0, 1
@@ -25,7 +26,8 @@ STATUS = {0: "ROCMFP4_OK", 1: "ROCMFP4_ERR_INVALID_ARG", 2: "ROCMFP4_ERR_UNSUPPO
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "librocmfp4.so")
 EXPORTS = ("rocmfp4_block_bytes", "rocmfp4_row_bytes", "rocmfp4_gemv", "rocmfp4_gemv_ex", "rocmfp4_gemm",
-           "rocmfp4_gemm_ex", "rocmfp4_gemm_noalloc", "rocmfp4_gemv_gate_up", "rocmfp4_decode_attention", "rocmfp4_quantize", "rocmfp4_gemv_chain", "rocmfp4_gemv_chain_mixed", "rocmfp4_dequant", "rocmfp4_copy", "rocmfp4_validate", "rocmfp4_device_error_bits",
+           "rocmfp4_gemm_ex", "rocmfp4_gemm_noalloc", "rocmfp4_gemv_gate_up", "rocmfp4_decode_attention", "rocmfp4_add_rmsnorm", "rocmfp4_logprobs",
+           "rocmfp4_quantize", "rocmfp4_gemv_chain", "rocmfp4_gemv_chain_mixed", "rocmfp4_dequant", "rocmfp4_copy", "rocmfp4_validate", "rocmfp4_device_error_bits",
            "rocmfp4_status_string", "rocmfp4_last_error", "rocmfp4_launch_count", "rocmfp4_shutdown")
 
 _lib = None
@@ -63,6 +65,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "rocmfp4_gemv_gate_up": ([vp, vp, vp, i64, i64, i64, c_int, c_int, vp], c_int),
         "rocmfp4_decode_attention": ([vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, ctypes.c_float, c_int, c_int, vp],
                                      c_int),
+        "rocmfp4_add_rmsnorm": ([vp, c_int, i64, vp, vp, c_int, i64, i64, vp, c_int, ctypes.c_float, vp, c_int, vp, vp, i64,
+                                 i64, i64, vp], c_int),
+        "rocmfp4_logprobs": ([vp, c_int, i64, vp, ctypes.c_float, vp, vp, vp, vp, i64, i64, i64, vp], c_int),
         "rocmfp4_quantize": ([vp, c_int, vp, i64, i64, c_int, vp], c_int),
         "rocmfp4_gemv_chain": ([ctypes.POINTER(GemvOp), c_int, i64, c_int, c_int, vp], c_int),
         "rocmfp4_gemv_chain_mixed": ([ctypes.POINTER(GemvOp), ctypes.POINTER(c_int), c_int, i64, c_int, vp], c_int),
@@ -133,6 +138,15 @@ def _act_of(t) -> int:
     if dt == torch.bfloat16:
         return ACT_BF16
     raise TypeError(f"activations must be float16 or bfloat16, got {dt}")
+
+
+_DTYPES = {}  # torch dtype -> rocmfp4_out_dtype
+
+
+def _dtypes() -> dict:
+    torch = _torch()
+    _DTYPES.update({torch.float32: OUT_F32, torch.bfloat16: OUT_BF16, torch.float16: OUT_F16})
+    return _DTYPES
 
 
 def _ptr(t) -> int:
@@ -236,6 +250,118 @@ def decode_attention(q, K, V, lens, Hkv: int, Tmax: int, scale: float, variant: 
                                            float(scale), variant, _act_of(q), _stream(stream)),
            "rocmfp4_decode_attention")
     return out
+
+
+def _rows(t, name: str):
+    """(rows, width, row stride) of a [rows, width] or [width] CUDA tensor whose rows are contiguous."""
+    d = t.dim()
+    if d == 2:
+        M, D = t.shape
+        ld, step = t.stride()
+    elif d == 1:
+        M, D = 1, t.shape[0]
+        ld, step = D, t.stride(0)
+    else:
+        raise ValueError(f"{name} must be a [rows, width] or [width] tensor")
+    if not t.is_cuda or (step != 1 and D > 1):
+        raise ValueError(f"{name} must be a CUDA tensor with contiguous rows")
+    return M, D, (ld if M > 1 else max(ld, D))
+
+
+def _dense(t, name: str, dtype, shape):
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
+    return t
+
+
+class AddRmsNorm(NamedTuple):
+    """What add_rmsnorm gives; None for what was not asked for."""
+    y: object
+    residual: object
+    q: object
+    scales: object
+
+
+def add_rmsnorm(x, weight, residual=None, eps: float = 1e-6, dtype=None, y=None, residual_out=None, q=None, scales=None,
+                group: int = 0, stream=None) -> AddRmsNorm:
+    """h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight, per row.
+
+    x [M, D] (or [D]) float32 / bfloat16 / float16 with contiguous rows, residual
+    likewise (or None: h = x), weight [D].  Gives a tuple of
+    ``y``         [M, D] float16 or bfloat16, into ``y`` if given, else a new tensor of ``dtype`` (float16 by default);
+                  None if an 8-bit output is asked for and neither ``y`` nor ``dtype`` is given;
+    ``residual``  h in the residual's type, into ``residual_out`` if given, else in place of ``residual``;
+    ``q``, ``scales``  with group 32, 64 or 128 (or -1: the row), y in 8 bits: e4m3 values [M, D] and float32 scales
+                  [M, groups], y being about q * scale; into ``q`` and ``scales`` if given."""
+    torch = _torch()
+    codes = _DTYPES or _dtypes()
+    M, D, ldx = _rows(x, "x")
+    ldr = ldro = 0
+    rtype = OUT_F32
+    if residual is not None:
+        if residual_out is None:
+            residual_out = residual
+        Mr, Dr, ldr = _rows(residual, "residual")
+        Mo, Do, ldro = _rows(residual_out, "residual_out")
+        if (Mr, Dr, Mo, Do) != (M, D, M, D) or residual.dtype is not residual_out.dtype:
+            raise ValueError("residual and residual_out must have x's shape and one type")
+        rtype = codes.get(residual.dtype, -1)
+    elif residual_out is not None:
+        raise ValueError("residual_out without residual")
+    if not weight.is_cuda or not weight.is_contiguous() or weight.numel() != D:
+        raise ValueError("weight must be a contiguous CUDA tensor of D elements")
+    if y is None and (not group or dtype is not None):
+        y = torch.empty(x.shape, dtype=dtype or torch.float16, device=x.device)
+    act = ACT_F16
+    if y is not None:
+        if not y.is_cuda or not y.is_contiguous() or y.shape != x.shape:
+            raise ValueError("y must be a contiguous CUDA tensor of x's shape")
+        act = _act_of(y)
+    size = 0
+    if group:
+        size = 0 if group < 0 else group
+        groups = 1 if group < 0 else -(-D // group)
+        if q is None:
+            q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        if scales is None:
+            scales = torch.empty((M, groups), dtype=torch.float32, device=x.device)
+        _dense(q, "q", torch.float8_e4m3fn, x.shape)
+        _dense(scales, "scales", torch.float32, (M, groups))
+    elif q is not None or scales is not None:
+        raise ValueError("q and scales need a group")
+    if M:
+        _check(load().rocmfp4_add_rmsnorm(
+            x.data_ptr(), codes.get(x.dtype, -1), ldx, _ptr(residual), _ptr(residual_out), rtype, ldr, ldro, weight.data_ptr(),
+            codes.get(weight.dtype, -1), eps, _ptr(y), act, _ptr(q), _ptr(scales), size, M, D, _stream(stream)),
+            "rocmfp4_add_rmsnorm")
+    return AddRmsNorm(y, residual_out, q, scales)
+
+
+def logprobs(logits, targets=None, top_n: int = 0, scale: float = 1.0, logprob=None, entropy=None, top_ids=None,
+             top_logprobs=None, stream=None):
+    """(logprob [M], entropy [M], top_ids [M, top_n], top_logprobs [M, top_n]) of rows of logits [M, V] (or [V]; float32,
+    bfloat16 or float16, contiguous rows) at scale * logits: the log probability of targets [M] (int32 tokens; None gives
+    None; NaN for one outside the vocabulary), the entropy in nats, and the top_n (at most 32) tokens, ties to the lowest
+    index.  The outputs go into the tensors given, or into new ones."""
+    torch = _torch()
+    codes = _DTYPES or _dtypes()
+    M, V, ld = _rows(logits, "logits")
+    dev = logits.device
+    if targets is not None:
+        _dense(targets, "targets", torch.int32, (M,))
+        logprob = torch.empty(M, dtype=torch.float32, device=dev) if logprob is None else _dense(logprob, "logprob", torch.float32, (M,))
+    elif logprob is not None:
+        raise ValueError("logprob without targets")
+    entropy = torch.empty(M, dtype=torch.float32, device=dev) if entropy is None else _dense(entropy, "entropy", torch.float32, (M,))
+    shape = (M, top_n)
+    top_ids = torch.empty(shape, dtype=torch.int32, device=dev) if top_ids is None else _dense(top_ids, "top_ids", torch.int32, shape)
+    top_logprobs = (torch.empty(shape, dtype=torch.float32, device=dev) if top_logprobs is None
+                    else _dense(top_logprobs, "top_logprobs", torch.float32, shape))
+    if M:
+        _check(load().rocmfp4_logprobs(logits.data_ptr(), codes.get(logits.dtype, -1), ld, _ptr(targets), scale, _ptr(logprob),
+                                       _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs), top_n, M, V, _stream(stream)),
+               "rocmfp4_logprobs")
+    return logprob, entropy, top_ids, top_logprobs
 
 
 def gemv_chain(ops, variant=DUAL, stream=None):

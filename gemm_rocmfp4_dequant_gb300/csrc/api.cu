@@ -25,6 +25,8 @@ struct DeviceState {
   uint32_t* tccnt = nullptr;         // tensor-core kernel: split-tile counters
   float* attn_ws = nullptr;          // decode attention: split partials
   unsigned long long* vfirst = nullptr;
+  float* lp_ws = nullptr;            // log probabilities: records of split rows
+  uint32_t* lp_cnt = nullptr;        // log probabilities: arrivals per split row
 };
 
 constexpr int kMaxDevices = 64;
@@ -45,6 +47,10 @@ rocmfp4_status cuda_fail(cudaError_t e, const char* what) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool valid_variant(int v) { return v == ROCMFP4_DUAL || v == ROCMFP4_FAST; }
+bool valid_dtype(int t) { return t == ROCMFP4_OUT_F32 || t == ROCMFP4_OUT_BF16 || t == ROCMFP4_OUT_F16; }
+bool aligned_to(const void* p, int dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == ROCMFP4_OUT_F32 ? 3u : 1u)) == 0;
+}
 bool valid_act(int a) { return a == ROCMFP4_ACT_F16 || a == ROCMFP4_ACT_BF16; }
 
 int64_t block_bytes_of(int v) { return v == ROCMFP4_DUAL ? 18 : 17; }
@@ -87,6 +93,11 @@ rocmfp4_status device_state(DeviceState** out) {
       return cuda_fail(e, "cudaMemset");
     if ((e = cudaMalloc(&d.attn_ws, sizeof(float) * attn_ws_floats(d.sms))) != cudaSuccess)
       return cuda_fail(e, "cudaMalloc");
+    if ((e = cudaMalloc(&d.lp_ws, logprobs_ws_bytes(d.sms))) != cudaSuccess) return cuda_fail(e, "cudaMalloc");
+    if ((e = cudaMalloc(&d.lp_cnt, sizeof(uint32_t) * logprobs_cnt_words(d.sms))) != cudaSuccess)
+      return cuda_fail(e, "cudaMalloc");
+    if ((e = cudaMemset(d.lp_cnt, 0, sizeof(uint32_t) * logprobs_cnt_words(d.sms))) != cudaSuccess)
+      return cuda_fail(e, "cudaMemset");
     if ((e = cudaMemset(d.err, 0, sizeof(uint32_t))) != cudaSuccess) return cuda_fail(e, "cudaMemset");
     if ((e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
     d.ready = true;
@@ -328,6 +339,67 @@ rocmfp4_status decode_attention(const void* q, const void* K, const void* V, con
   return ROCMFP4_OK;
 }
 
+rocmfp4_status add_rmsnorm(const NormArgs& a, int64_t group, cudaStream_t s) {
+  if (!valid_dtype(a.x_type) || !valid_dtype(a.weight_type) || (a.residual && !valid_dtype(a.residual_type)))
+    return fail(ROCMFP4_ERR_INVALID_ARG, "unknown type");
+  if (!valid_act(a.y_act)) return fail(ROCMFP4_ERR_INVALID_ARG, "unknown activation type");
+  if (a.M < 0 || a.D < 0) return fail(ROCMFP4_ERR_INVALID_ARG, "negative size");
+  if (group != 0 && group != 32 && group != 64 && group != 128)
+    return fail(ROCMFP4_ERR_INVALID_ARG, "group must be 0 (the row), 32, 64 or 128");
+  if (!(a.eps >= 0.f) || a.eps > 3.4e38f) return fail(ROCMFP4_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (a.M == 0) return ROCMFP4_OK;
+  if (a.D == 0) return fail(ROCMFP4_ERR_INVALID_ARG, "D must be positive");
+  if (a.x == nullptr || a.weight == nullptr || (a.residual != nullptr && a.residual_out == nullptr) ||
+      (a.y == nullptr && a.q == nullptr) || (a.q == nullptr) != (a.scales == nullptr))
+    return fail(ROCMFP4_ERR_INVALID_ARG, "NULL pointer");
+  if (a.ldx < a.D || (a.residual && (a.ldr < a.D || a.ldro < a.D)))
+    return fail(ROCMFP4_ERR_INVALID_ARG, "row stride below D");
+  if (a.residual == a.residual_out && a.residual && a.ldr != a.ldro)
+    return fail(ROCMFP4_ERR_INVALID_ARG, "residual updated in place needs one stride");
+  if (!aligned_to(a.x, a.x_type) || !aligned_to(a.weight, a.weight_type) || !aligned_to(a.y, ROCMFP4_OUT_F16) ||
+      !aligned_to(a.scales, ROCMFP4_OUT_F32) ||
+      (a.residual && (!aligned_to(a.residual, a.residual_type) || !aligned_to(a.residual_out, a.residual_type))))
+    return fail(ROCMFP4_ERR_INVALID_ARG, "misaligned pointer");
+  if (a.D > norm_max_width()) return fail(ROCMFP4_ERR_UNSUPPORTED, "RMS norm: D at most 32768");
+  if (a.M >= (int64_t(1) << 31)) return fail(ROCMFP4_ERR_UNSUPPORTED, "RMS norm: M too large");
+  DeviceState* d = nullptr;
+  rocmfp4_status st = device_state(&d);
+  if (st != ROCMFP4_OK) return st;
+  cudaError_t e = launch_norm(a, d->sms, s);
+  if (e != cudaSuccess) return cuda_fail(e, "RMS norm launch");
+  g_launches.fetch_add(1);
+  return ROCMFP4_OK;
+}
+
+rocmfp4_status logprobs(LogprobsArgs a, int64_t top_n, cudaStream_t s) {
+  if (!valid_dtype(a.type)) return fail(ROCMFP4_ERR_INVALID_ARG, "unknown type");
+  if (a.M < 0 || a.V < 0 || top_n < 0) return fail(ROCMFP4_ERR_INVALID_ARG, "negative size");
+  if (!(a.scale > 0.f) || a.scale > 3.4e38f) return fail(ROCMFP4_ERR_INVALID_ARG, "scale must be finite and positive");
+  if (a.M == 0) return ROCMFP4_OK;
+  if (a.V == 0) return fail(ROCMFP4_ERR_INVALID_ARG, "V must be positive");
+  if (a.ld < a.V) return fail(ROCMFP4_ERR_INVALID_ARG, "row stride below V");
+  if (top_n > a.V) return fail(ROCMFP4_ERR_INVALID_ARG, "top_n above V");
+  if (a.logits == nullptr || (a.targets != nullptr && a.logprob == nullptr) ||
+      (top_n > 0 && (a.top_ids == nullptr || a.top_logprobs == nullptr)))
+    return fail(ROCMFP4_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned_to(a.logits, a.type) || !aligned_to(a.targets, 0) || !aligned_to(a.logprob, 0) ||
+      !aligned_to(a.entropy, 0) || !aligned_to(a.top_ids, 0) || !aligned_to(a.top_logprobs, 0))
+    return fail(ROCMFP4_ERR_INVALID_ARG, "misaligned pointer");
+  if (top_n > kMaxTop) return fail(ROCMFP4_ERR_UNSUPPORTED, "log probabilities: top_n at most 32");
+  if (a.V >= (int64_t(1) << 31) - 64 || a.M >= (int64_t(1) << 31))
+    return fail(ROCMFP4_ERR_UNSUPPORTED, "log probabilities: sizes too large");
+  DeviceState* d = nullptr;
+  rocmfp4_status st = device_state(&d);
+  if (st != ROCMFP4_OK) return st;
+  a.top_n = (int)top_n;
+  a.ws = d->lp_ws;
+  a.cnt = d->lp_cnt;
+  cudaError_t e = launch_logprobs(a, d->sms, s);
+  if (e != cudaSuccess) return cuda_fail(e, "log probabilities launch");
+  g_launches.fetch_add(1);
+  return ROCMFP4_OK;
+}
+
 }  // namespace
 
 namespace rocmfp4 {
@@ -376,6 +448,51 @@ rocmfp4_status rocmfp4_decode_attention(const void* q, const void* K, const void
                                         rocmfp4_variant variant, rocmfp4_act act, rocmfp4_stream_t stream) {
   return decode_attention(q, K, V, lens, out, B, H, Hkv, D, Tmax, scale, variant, act,
                           reinterpret_cast<cudaStream_t>(stream));
+}
+
+rocmfp4_status rocmfp4_add_rmsnorm(const void* x, rocmfp4_out_dtype x_type, int64_t ldx, const void* residual,
+                                   void* residual_out, rocmfp4_out_dtype residual_type, int64_t ldr, int64_t ldro,
+                                   const void* weight, rocmfp4_out_dtype weight_type, float eps, void* y,
+                                   rocmfp4_act y_type, void* q, float* scales, int64_t group, int64_t M, int64_t D,
+                                   rocmfp4_stream_t stream) {
+  NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.residual_out = residual_out;
+  a.weight = weight;
+  a.y = y;
+  a.q = static_cast<uint8_t*>(q);
+  a.scales = scales;
+  a.M = M;
+  a.D = D;
+  a.ldx = ldx;
+  a.ldr = ldr;
+  a.ldro = ldro;
+  a.x_type = x_type;
+  a.residual_type = residual_type;
+  a.weight_type = weight_type;
+  a.y_act = y_type;
+  a.group = (int)group;
+  a.eps = eps;
+  return add_rmsnorm(a, group, reinterpret_cast<cudaStream_t>(stream));
+}
+
+rocmfp4_status rocmfp4_logprobs(const void* logits, rocmfp4_out_dtype type, int64_t ld, const int32_t* targets,
+                                float scale, float* logprob, float* entropy, int32_t* top_ids, float* top_logprobs,
+                                int64_t top_n, int64_t M, int64_t V, rocmfp4_stream_t stream) {
+  LogprobsArgs a{};
+  a.logits = logits;
+  a.targets = targets;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  a.M = M;
+  a.V = V;
+  a.ld = ld;
+  a.scale = scale;
+  a.type = type;
+  return logprobs(a, top_n, reinterpret_cast<cudaStream_t>(stream));
 }
 
 rocmfp4_status rocmfp4_gemv_chain(const rocmfp4_gemv_op* ops, int count, int64_t M, rocmfp4_variant variant,
@@ -555,6 +672,8 @@ void rocmfp4_shutdown(void) {
     cudaFree(d.tccnt);
     cudaFree(d.attn_ws);
     cudaFree(d.vfirst);
+    cudaFree(d.lp_ws);
+    cudaFree(d.lp_cnt);
     d = DeviceState{};
   }
   cudaSetDevice(cur);

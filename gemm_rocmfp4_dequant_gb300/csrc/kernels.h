@@ -83,6 +83,43 @@ size_t attn_ws_floats(int sms);
 cudaError_t attn_prepare();
 cudaError_t launch_decode_attention(int variant, int act, const AttnArgs& a, int sms, cudaStream_t s, int* launches);
 
+// Residual addition and RMS norm (norm.cu).  Types are rocmfp4_out_dtype
+// values; row strides ld* in elements; y, q and scales are contiguous.
+struct NormArgs {
+  const void* x;
+  const void* residual;  // nullptr: none
+  void* residual_out;
+  const void* weight;
+  void* y;           // nullptr: not wanted
+  uint8_t* q;        // nullptr: not wanted
+  float* scales;     // M x ceil(D / group), or M when group is 0
+  int64_t M, D, ldx, ldr, ldro;
+  int x_type, residual_type, weight_type, y_act, group;
+  float eps;
+};
+int64_t norm_max_width();  // largest D
+cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t s);
+
+// Log probabilities, entropy and top alternatives of rows of logits (logprobs.cu).
+constexpr int kMaxTop = 32;
+struct LogprobsArgs {
+  const void* logits;
+  const int32_t* targets;  // nullptr: none
+  float* logprob;          // [M], with targets
+  float* entropy;          // [M], nullptr: not wanted
+  int32_t* top_ids;        // [M][top_n]
+  float* top_logprobs;     // [M][top_n]
+  int64_t M, V, ld;
+  float scale;
+  int type, top_n;
+  int splits;              // CTAs that share a row (set by the launch)
+  float* ws;               // logprobs_ws_bytes(sms) bytes, 8-byte aligned
+  uint32_t* cnt;           // logprobs_cnt_words(sms) words, zero between launches
+};
+size_t logprobs_ws_bytes(int sms);
+size_t logprobs_cnt_words(int sms);
+cudaError_t launch_logprobs(const LogprobsArgs& a, int sms, cudaStream_t s);
+
 // Any K % 32 == 0, any alignment: one warp per (row, column chunk).
 struct GenericArgs {
   const uint8_t* W;

@@ -1,0 +1,460 @@
+// Log probabilities of given tokens, entropy and top alternatives of rows of
+// logits, in one pass over the logits:
+//   z_v = scale * logit_v,  m = max z,  S = sum exp(z_v - m),
+//   logprob(t) = z_t - m - ln S,   entropy = ln S - (sum exp(z_v - m) (z_v - m)) / S,
+//   top n by (logit descending, index ascending) with their log probabilities.
+// Every thread keeps a running maximum, S and A = sum exp(z - m) (z - m) and
+// rescales them when its maximum grows; sums are fp32.
+//
+// Bound: memory for many rows (each logit is read once: about 10
+// instructions a value, one of them a MUFU), latency for few.  A row is cut
+// into contiguous ranges, one per CTA, when there are too few rows to fill
+// the GPU; the last CTA of a row to finish joins the ranges' records in
+// range order, so the result does not depend on which that was.
+//
+// Top n.  Values are compared as 64-bit keys (order-preserving bits of the
+// logit, complement of the index), so ties go to the lowest index and keys
+// are distinct.  From a first tile of the range a threshold T is taken that
+// at least n of its values reach: the n-th largest of 64 disjoint groups'
+// maxima.  Values that reach T go to a candidate list in shared memory; later
+// tiles contribute only values above T, so almost every value costs one
+// comparison.  The list is cut back to n when it fills, which raises T.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace rocmfp4 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVecs = 4;        // 16-byte vectors a thread takes of a tile
+constexpr int kGroups = 64;     // groups of 4 neighbouring threads
+constexpr int kCutAt = 256;     // candidates at which the list is cut back to n
+constexpr float kLog2e = 1.4426950408889634f;
+
+constexpr int list_cap(int per_thread) { return kMaxTop * per_thread + 2 * kMaxTop; }
+
+// Order-preserving bits: a < b as floats iff key(a) < key(b); -0 counts as +0
+// and every NaN as the largest.
+RF4_DEV uint32_t ordered(float f) {
+  if (f != f) return 0xFFFFFFFFu;
+  const uint32_t b = __float_as_uint(f + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+RF4_DEV float unordered(uint32_t k) {
+  if (k == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+RF4_DEV uint64_t key_of(float f, uint32_t index) { return ((uint64_t)ordered(f) << 32) | (uint32_t)~index; }
+
+RF4_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+RF4_DEV float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Running softmax of some of a row's logits: m is the largest logit, S and A
+// the sums of e and e * (logit - m) with e = exp(scale * (logit - m)).
+struct Stats {
+  float m = -INFINITY, S = 0.f, A = 0.f;
+};
+
+// Moves (S, A) from the maximum `from` to `to` >= from; no values yet (m = -inf) stay nothing.
+RF4_DEV void rescale(float& S, float& A, float from, float to, float c) {
+  if (from == to || (S == 0.f && A == 0.f)) return;
+  const float d = from - to, e = ex2(d * c);
+  // e = 0 (a maximum far above): both sums vanish, and d may be infinite
+  A = e > 0.f ? e * (A + d * S) : 0.f;
+  S = e * S;
+}
+RF4_DEV void merge(Stats& a, const Stats& b, float c) {
+  const float m = fmaxf(a.m, b.m);
+  float S = b.S, A = b.A;
+  rescale(a.S, a.A, a.m, m, c);
+  rescale(S, A, b.m, m, c);
+  a.m = m;
+  a.S += S;
+  a.A += A;
+}
+RF4_DEV Stats shfl_xor(const Stats& s, int o) {
+  Stats r;
+  r.m = __shfl_xor_sync(0xffffffffu, s.m, o);
+  r.S = __shfl_xor_sync(0xffffffffu, s.S, o);
+  r.A = __shfl_xor_sync(0xffffffffu, s.A, o);
+  return r;
+}
+
+template <int TYPE>
+struct Logit;
+template <>
+struct Logit<0> {
+  using type = float;
+  static constexpr int PER = 4;
+  static RF4_DEV float one(float v) { return v; }
+  static RF4_DEV void unpack(const uint4& w, float* v) {
+    v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y), v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
+  }
+};
+template <>
+struct Logit<1> {
+  using type = uint16_t;
+  static constexpr int PER = 8;
+  static RF4_DEV float one(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+  static RF4_DEV void unpack(const uint4& w, float* v) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+};
+template <>
+struct Logit<2> {
+  using type = uint16_t;
+  static constexpr int PER = 8;
+  static RF4_DEV float one(uint16_t v) { return __half2float(__ushort_as_half(v)); }
+  static RF4_DEV void unpack(const uint4& w, float* v) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+  }
+};
+
+struct TopState {  // in shared memory
+  int count;       // candidates pushed (may pass the capacity: then `over`)
+  int kept;        // candidates before the current tile
+  uint64_t floor;  // values must have a larger key to become candidates
+  uint64_t group[kGroups];
+  uint64_t best[kMaxTop];
+};
+
+// The n-th largest of the groups' largest keys (0 where fewer than n groups
+// have one): at least n keys reach it.  `mine` is the thread's largest key, 0
+// for none.  Every thread of the CTA calls it.
+RF4_DEV uint64_t group_threshold(TopState& st, uint64_t mine, int n) {
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    const uint64_t u = __shfl_xor_sync(0xffffffffu, mine, o);
+    mine = u > mine ? u : mine;
+  }
+  __shared__ uint64_t threshold;
+  if ((threadIdx.x & 3) == 0) st.group[threadIdx.x >> 2] = mine;
+  if (threadIdx.x == 0) threshold = 0;
+  __syncthreads();
+  if (threadIdx.x < kGroups) {
+    const uint64_t k = st.group[threadIdx.x];
+    int rank = 0;
+#pragma unroll 16
+    for (int i = 0; i < kGroups; ++i) rank += st.group[i] > k ? 1 : 0;
+    if (rank == n - 1 && k != 0) threshold = k;  // distinct keys: one thread
+  }
+  __syncthreads();
+  return threshold;
+}
+
+// As group_threshold, over single threads: at most n threads have keys that
+// reach it.  `keys` is room for kThreads keys.  Slower: for full lists only.
+RF4_DEV uint64_t thread_threshold(uint64_t* keys, uint64_t mine, int n) {
+  __shared__ uint64_t threshold;
+  keys[threadIdx.x] = mine;
+  if (threadIdx.x == 0) threshold = 0;
+  __syncthreads();
+  int rank = 0;
+#pragma unroll 16
+  for (int i = 0; i < kThreads; ++i) rank += keys[i] > mine ? 1 : 0;
+  if (rank == n - 1 && mine != 0) threshold = mine;
+  __syncthreads();
+  return threshold;
+}
+
+// The n largest of the candidate list's `count` keys to the list's front, in
+// order; floor becomes the n-th (if there are n).  Every thread calls it.
+RF4_DEV void cut(TopState& st, uint64_t* list, uint64_t* spare, int count, int n) {
+  int c = count;
+  uint64_t* from = list;
+  if (count > 2 * kGroups) {  // few enough to rank: those that reach the groups' threshold
+    uint64_t mine = 0;
+    for (int i = threadIdx.x; i < count; i += kThreads) mine = list[i] > mine ? list[i] : mine;
+    const uint64_t t = group_threshold(st, mine, n);
+    if (threadIdx.x == 0) st.kept = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < count; i += kThreads)
+      if (list[i] >= t) spare[atomicAdd(&st.kept, 1)] = list[i];
+    __syncthreads();
+    c = st.kept;
+    from = spare;
+  }
+  for (int i = threadIdx.x; i < c; i += kThreads) {
+    const uint64_t k = from[i];
+    int rank = 0;
+    for (int j = 0; j < c; ++j) rank += from[j] > k ? 1 : 0;
+    if (rank < n) st.best[rank] = k;
+  }
+  __syncthreads();
+  c = c < n ? c : n;
+  if (threadIdx.x < c) list[threadIdx.x] = st.best[threadIdx.x];
+  if (threadIdx.x == 0) {
+    st.count = c;
+    st.kept = c;
+    if (c == n) st.floor = st.best[n - 1];
+  }
+  __syncthreads();
+}
+
+// One record per range of a split row: m, S, A, the number of keys, then kMaxTop keys.
+constexpr int kRecordBytes = 16 + 8 * kMaxTop;
+
+template <int TYPE, bool TOP>
+__global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constant__ LogprobsArgs a) {
+  using L = Logit<TYPE>;
+  using E = typename L::type;
+  constexpr int PER = L::PER, N = kVecs * PER, CAP = list_cap(N);
+  __shared__ TopState st;
+  __shared__ uint64_t lists[TOP ? 2 * CAP : 1];
+  __shared__ Stats warp_stats[kThreads / 32];
+  __shared__ int last;
+  uint64_t* list = lists;
+  uint64_t* spare = lists + (TOP ? CAP : 0);
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int tid = threadIdx.x, n = a.top_n, P = a.splits;
+  const int64_t row = blockIdx.x / P;
+  const int part = blockIdx.x % P;
+  const E* z = static_cast<const E*>(a.logits) + row * a.ld;
+  const float c = a.scale * kLog2e;
+  if (TOP && tid == 0) {
+    st.count = st.kept = 0;
+    st.floor = 0;
+  }
+  __syncthreads();
+
+  // The row as vectors of PER values from the 16-byte boundary at or before
+  // its start: places before value 0 and past value V - 1 count as absent.
+  const int lead = (int)((reinterpret_cast<uintptr_t>(z) & 15u) / sizeof(E));
+  const uint4* vz = reinterpret_cast<const uint4*>(z - lead);
+  const int64_t vecs = (a.V + lead + PER - 1) / PER;
+  const int64_t v0 = vecs * part / P, v1 = vecs * (part + 1) / P;
+
+  Stats s;
+  bool first = true;
+  for (int64_t base = v0; base < v1; base += kThreads * kVecs) {
+    float v[N];
+    uint32_t idx[kVecs];  // index of the vector's first value
+    uint32_t have = 0;    // vectors that are wholly inside the row; others are read value by value
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int64_t p = base + k * kThreads + tid;
+      const int64_t e = p * PER - lead;
+      idx[k] = (uint32_t)e;
+      if (p < v1 && e >= 0 && e + PER <= a.V) {
+        L::unpack(__ldg(vz + p), v + k * PER);
+        have |= 1u << k;
+      } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) v[k * PER + j] = p < v1 && e + j >= 0 && e + j < a.V ? L::one(z[e + j]) : -INFINITY;
+      }
+    }
+    float tm = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) tm = fmaxf(tm, v[i]);
+    const float m = fmaxf(s.m, tm);
+    rescale(s.S, s.A, s.m, m, c);
+    s.m = m;
+    const float mm = m == -INFINITY ? 0.f : m;  // nothing but -inf yet: e = 0
+    float S[2] = {0.f, 0.f}, A[2] = {0.f, 0.f};  // the tile's sums on their own: short chains
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float d = v[i] - mm, e = ex2(d * c);
+      S[i & 1] += e;
+      A[i & 1] = fmaf(e, max_nan(d, -3.4028235e38f), A[i & 1]);  // a finite factor: 0 * d stays 0
+    }
+    s.S += S[0] + S[1];
+    s.A += A[0] + A[1];
+    if constexpr (TOP) {
+      // whether value i of this thread is one of the row's
+      auto present = [&](int i) {
+        const int k = i / PER, j = i % PER;
+        if (have >> k & 1u) return true;
+        const int64_t p = base + k * kThreads + tid, e = p * PER - lead + j;
+        return p < v1 && e >= 0 && e < a.V;
+      };
+      auto key = [&](int i) { return key_of(v[i], idx[i / PER] + i % PER); };
+      auto largest = [&](uint64_t above) {  // the thread's largest key above a bound, 0 for none
+        uint64_t best = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const uint64_t k = key(i);
+          if (k > best && k > above && present(i)) best = k;
+        }
+        return best;
+      };
+      // NaN compares as the largest value: fmaxf skips it, the sum does not
+      uint64_t floor = st.floor;
+      if (first) {
+        const uint64_t t = group_threshold(st, largest(0), n);
+        floor = t > 0 ? t - 1 : 0;
+        first = false;
+      }
+      const float fv = unordered((uint32_t)(floor >> 32));
+      if (!(tm < fv) || s.S != s.S || floor == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          if (v[i] < fv && floor != 0) continue;
+          const uint64_t k = key(i);
+          if (k > floor && present(i)) {
+            const int at = atomicAdd(&st.count, 1);
+            if (at < CAP) list[at] = k;
+          }
+        }
+      }
+      __syncthreads();
+      int count = st.count;
+      if (count > CAP) {
+        // More candidates than the list holds (a rising or constant row).
+        // Back to those before this tile; of the tile, the keys that reach
+        // the n-th largest of the threads' largest keys: at most n threads'.
+        const int kept = st.kept;
+        __syncthreads();
+        cut(st, list, spare, kept, n);
+        const uint64_t t = thread_threshold(spare, largest(st.floor), n);
+        const uint64_t above = t > st.floor ? t - 1 : st.floor;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const uint64_t k = key(i);
+          if (k > above && present(i)) {
+            const int at = atomicAdd(&st.count, 1);
+            if (at < CAP) list[at] = k;
+          }
+        }
+        __syncthreads();
+        count = st.count;
+      }
+      if (count > kCutAt) {
+        cut(st, list, spare, count, n);
+      } else {
+        if (tid == 0) st.kept = count;
+        __syncthreads();
+      }
+    }
+  }
+
+  // the CTA's statistics, joined in a fixed order
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) merge(s, shfl_xor(s, o), c);
+  if ((tid & 31) == 0) warp_stats[tid >> 5] = s;
+  if (TOP) cut(st, list, spare, st.count, n);
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kThreads / 32; ++w) merge(s, warp_stats[w], c);
+    warp_stats[0] = s;
+  }
+  __syncthreads();
+
+  if (P > 1) {
+    uint8_t* records = reinterpret_cast<uint8_t*>(a.ws) + (size_t)row * P * kRecordBytes;
+    uint8_t* mine = records + (size_t)part * kRecordBytes;
+    if (tid == 0) *reinterpret_cast<float4*>(mine) = make_float4(s.m, s.S, s.A, 0.f);
+    if (TOP && tid < n) reinterpret_cast<uint64_t*>(mine + 16)[tid] = tid < st.count ? list[tid] : 0;
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      const bool l = atomic_add_acq_rel_gpu(a.cnt + row, 1u) == (uint32_t)P - 1u;
+      if (l) store_relaxed_gpu(a.cnt + row, 0u);
+      last = l;
+    }
+    __syncthreads();
+    if (!last) return;
+    s = Stats{};
+    for (int p = tid; p < P; p += kThreads) {
+      const float4 r = __ldcg(reinterpret_cast<const float4*>(records + (size_t)p * kRecordBytes));
+      merge(s, Stats{r.x, r.y, r.z}, c);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) merge(s, shfl_xor(s, o), c);
+    if ((tid & 31) == 0) warp_stats[tid >> 5] = s;
+    if constexpr (TOP) {
+      // key j of record p at place j * P + p: the records' largest keys first
+      auto at = [&](int i) { return __ldcg(reinterpret_cast<const unsigned long long*>(records + (size_t)(i % P) * kRecordBytes + 16) + i / P); };
+      const int total = P * n;
+      uint64_t mx = 0;
+      for (int i = tid; i < P; i += kThreads) {  // a record's first key is its largest
+        const uint64_t k = at(i);
+        mx = k > mx ? k : mx;
+      }
+      if (tid == 0) st.count = 0;
+      const uint64_t t = group_threshold(st, mx, n);
+      if (tid == 0) st.floor = t > 0 ? t - 1 : 0;
+      __syncthreads();
+      for (int base = 0; base < total; base += kThreads) {
+        const uint64_t k = base + tid < total ? at(base + tid) : 0;
+        if (k > st.floor) list[atomicAdd(&st.count, 1)] = k;  // at most kCutAt + kThreads of them
+        __syncthreads();
+        const int count = st.count;
+        __syncthreads();
+        if (count > kCutAt) cut(st, list, spare, count, n);
+      }
+      cut(st, list, spare, st.count, n);
+    }
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 1; w < kThreads / 32; ++w) merge(s, warp_stats[w], c);
+      warp_stats[0] = s;
+    }
+    __syncthreads();
+  }
+
+  s = warp_stats[0];
+  const bool empty = s.m == -INFINITY && s.S == 0.f;  // every logit is -inf: no token is possible
+  const float ln = logf(s.S);
+  if (tid == 0) {
+    if (a.targets != nullptr) {
+      const int64_t t = a.targets[row];
+      const float x = t >= 0 && t < a.V ? L::one(z[t]) : __uint_as_float(0x7FC00000u);
+      a.logprob[row] = t >= 0 && t < a.V ? (empty ? -INFINITY : a.scale * (x - s.m) - ln) : x;
+    }
+    if (a.entropy != nullptr) a.entropy[row] = empty ? 0.f : ln - a.scale * s.A / s.S;
+  }
+  if (TOP && tid < n) {
+    const uint64_t k = list[tid];
+    a.top_ids[row * n + tid] = (int32_t)~(uint32_t)k;
+    a.top_logprobs[row * n + tid] = empty ? -INFINITY : a.scale * (unordered((uint32_t)(k >> 32)) - s.m) - ln;
+  }
+}
+
+using LogprobsFn = void (*)(LogprobsArgs);
+
+}  // namespace
+
+// A split row has at most 4 * sms + M records with M < 4 * sms.
+size_t logprobs_ws_bytes(int sms) { return (size_t)8 * sms * kRecordBytes; }
+size_t logprobs_cnt_words(int sms) { return (size_t)4 * sms; }
+
+cudaError_t launch_logprobs(const LogprobsArgs& args, int sms, cudaStream_t s) {
+  LogprobsArgs a = args;
+  const int per = a.type == 0 ? 4 : 8;
+  const int64_t tiles = (a.V / per + 1 + kThreads * kVecs - 1) / (kThreads * kVecs);
+  // About four CTAs per SM, each with at least one whole tile of its row.
+  int64_t P = a.M >= 4 * (int64_t)sms ? 1 : (4 * (int64_t)sms + a.M - 1) / a.M;
+  P = P < tiles ? P : tiles;
+  a.splits = (int)P;
+  LogprobsFn fn;
+  if (a.top_n > 0) fn = a.type == 0 ? logprobs_kernel<0, true> : a.type == 1 ? logprobs_kernel<1, true> : logprobs_kernel<2, true>;
+  else fn = a.type == 0 ? logprobs_kernel<0, false> : a.type == 1 ? logprobs_kernel<1, false> : logprobs_kernel<2, false>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.M * P));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, a);
+}
+
+}  // namespace rocmfp4

@@ -162,6 +162,68 @@ rocmfp4_status rocmfp4_decode_attention(const void *q, const void *K, const void
                                         rocmfp4_variant variant, rocmfp4_act act,
                                         rocmfp4_stream_t stream);
 
+/* Residual addition and RMS norm, the step between two products:
+ *
+ *   h = x + r,   y = h / sqrt(mean(h^2) + eps) * w        (per row of D values)
+ *
+ * in fp32; the norm is that of the unrounded sum h.  No counterpart in the
+ * format definition; it turns a product's fp32 output into the next product's
+ * fp16 / bf16 activations.
+ *   - x            [M] rows of D values of x_type, ldx values apart;
+ *   - residual     [M] rows of residual_type, ldr values apart, or NULL (h = x);
+ *   - residual_out [M] rows of residual_type, ldro values apart: receives h.
+ *                  It may be residual itself (same stride), updated in place;
+ *                  required with residual, ignored without;
+ *   - weight       D values of weight_type;
+ *   - y            [M][D] of type y_type, contiguous, or NULL;
+ *   - q, scales    8-bit output (both or neither; NULL: none): q [M][D] e4m3
+ *                  codes, contiguous, and one fp32 scale s = max|y| / 448 per
+ *                  group of `group` consecutive values of a row (32, 64 or
+ *                  128; the last may be short; scales is [M][ceil(D / group)]),
+ *                  or per row (group 0; scales is [M]): q = e4m3(y / s), round
+ *                  to nearest even; a group of zeros has s = 0 and codes 0.
+ *   - At least one of y and q.  Row strides are at least D.  x_type,
+ *     residual_type and weight_type are rocmfp4_out_dtype values.
+ *   - D at most 32768, else ROCMFP4_ERR_UNSUPPORTED; D < 1 with M > 0 is
+ *     invalid; M == 0 does nothing.
+ *   - A row with an infinity or a NaN follows the formula: y is 0 or NaN.
+ *   - One programmatic dependent launch on `stream`: it reads nothing before
+ *     the preceding kernel has completed and lets the next one begin early. */
+rocmfp4_status rocmfp4_add_rmsnorm(const void *x, rocmfp4_out_dtype x_type, int64_t ldx,
+                                   const void *residual, void *residual_out,
+                                   rocmfp4_out_dtype residual_type, int64_t ldr, int64_t ldro,
+                                   const void *weight, rocmfp4_out_dtype weight_type, float eps,
+                                   void *y, rocmfp4_act y_type, void *q, float *scales,
+                                   int64_t group, int64_t M, int64_t D, rocmfp4_stream_t stream);
+
+/* Log probabilities, entropy and top alternatives of rows of logits (the LM
+ * head's product), with z_v = scale * logit_v (scale: 1 / temperature):
+ *
+ *   lse = ln sum_v exp(z_v),   logprob = z_target - lse,
+ *   entropy = lse - sum_v p_v z_v  with p_v = exp(z_v - lse)     (in nats),
+ *   the top_n tokens by (logit descending, index ascending) and their z - lse.
+ *
+ * No counterpart in the format definition.
+ *   - logits       [M] rows of V values of `type`, ld values apart;
+ *   - targets      [M] int32 tokens, or NULL; logprob [M] fp32, required with
+ *                  targets.  A target outside 0 .. V-1 gives NaN;
+ *   - entropy      [M] fp32, or NULL;
+ *   - top_ids      [M][top_n] int32 and top_logprobs [M][top_n] fp32; both are
+ *                  required when top_n > 0.  top_n at most 32
+ *                  (ROCMFP4_ERR_UNSUPPORTED above) and at most V.
+ *   - Masked tokens have logit -inf: probability 0, log probability -inf, no
+ *     part in the entropy.  A row of nothing but -inf gives log probabilities
+ *     -inf and entropy 0.  A row that holds a NaN or +inf gives NaN for all of
+ *     its numbers; its top_ids order NaN first, then +inf.
+ *   - scale must be finite and above 0.  V below 2^31.
+ *   - One programmatic dependent launch on `stream`; sums are fp32, in a fixed
+ *     order.  A row may be shared by several CTAs, whose records use the
+ *     per-device workspace. */
+rocmfp4_status rocmfp4_logprobs(const void *logits, rocmfp4_out_dtype type, int64_t ld,
+                                const int32_t *targets, float scale, float *logprob,
+                                float *entropy, int32_t *top_ids, float *top_logprobs,
+                                int64_t top_n, int64_t M, int64_t V, rocmfp4_stream_t stream);
+
 /* One product of a chain: Y = X . W^T with the layouts of rocmfp4_gemm_ex
  * (X is M x K of the chain's activation type, Y is M x N fp32). */
 typedef struct rocmfp4_gemv_op {
