@@ -5,7 +5,9 @@ runs in the CUDA kernels of ``_build/librocmfp4.so``.  There is no CPU
 fallback: if the library is missing or no GPU is present, calls raise.
 
 Entry points (names as in the C ABI, without the ``rocmfp4_`` prefix):
-``gemv``, ``gemm``, ``dequant``, ``validate``, ``block_bytes``, ``row_bytes``.
+``gemv``, ``gemm``, ``gemv_gate_up``, ``gemv_chain``, ``decode_attention``,
+``add_rmsnorm``, ``moe``, ``logprobs``, ``quantize``, ``dequant``, ``validate``,
+``copy``, ``block_bytes``, ``row_bytes``.
 Tensors are torch CUDA tensors; packed weights are ``uint8`` tensors holding
 ``N * row_bytes(K, variant)`` bytes; activations are ``float16`` or
 ``bfloat16``; outputs are ``float32``.  Calls are asynchronous on torch's
@@ -20,13 +22,14 @@ from typing import NamedTuple
 DUAL, FAST = 0, 1
 ACT_F16, ACT_BF16 = 0, 1
 OUT_F32, OUT_BF16, OUT_F16 = 0, 1, 2
+ROUTE_SOFTMAX, ROUTE_SOFTMAX_TOPK, ROUTE_SIGMOID = 0, 1, 2
 STATUS = {0: "ROCMFP4_OK", 1: "ROCMFP4_ERR_INVALID_ARG", 2: "ROCMFP4_ERR_UNSUPPORTED",
           3: "ROCMFP4_ERR_INVALID_SCALE", 4: "ROCMFP4_ERR_CUDA"}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "librocmfp4.so")
 EXPORTS = ("rocmfp4_block_bytes", "rocmfp4_row_bytes", "rocmfp4_gemv", "rocmfp4_gemv_ex", "rocmfp4_gemm",
-           "rocmfp4_gemm_ex", "rocmfp4_gemm_noalloc", "rocmfp4_gemv_gate_up", "rocmfp4_decode_attention", "rocmfp4_add_rmsnorm", "rocmfp4_logprobs",
+           "rocmfp4_gemm_ex", "rocmfp4_gemm_noalloc", "rocmfp4_gemv_gate_up", "rocmfp4_decode_attention", "rocmfp4_add_rmsnorm", "rocmfp4_moe", "rocmfp4_logprobs",
            "rocmfp4_quantize", "rocmfp4_gemv_chain", "rocmfp4_gemv_chain_mixed", "rocmfp4_dequant", "rocmfp4_copy", "rocmfp4_validate", "rocmfp4_device_error_bits",
            "rocmfp4_status_string", "rocmfp4_last_error", "rocmfp4_launch_count", "rocmfp4_shutdown")
 
@@ -67,6 +70,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                      c_int),
         "rocmfp4_add_rmsnorm": ([vp, c_int, i64, vp, vp, c_int, i64, i64, vp, c_int, ctypes.c_float, vp, c_int, vp, vp, i64,
                                  i64, i64, vp], c_int),
+        "rocmfp4_moe": ([vp, vp, c_int, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, c_int, ctypes.c_float, c_int, c_int, vp],
+                        c_int),
         "rocmfp4_logprobs": ([vp, c_int, i64, vp, ctypes.c_float, vp, vp, vp, vp, i64, i64, i64, vp], c_int),
         "rocmfp4_quantize": ([vp, c_int, vp, i64, i64, c_int, vp], c_int),
         "rocmfp4_gemv_chain": ([ctypes.POINTER(GemvOp), c_int, i64, c_int, c_int, vp], c_int),
@@ -335,6 +340,35 @@ def add_rmsnorm(x, weight, residual=None, eps: float = 1e-6, dtype=None, y=None,
             codes.get(weight.dtype, -1), eps, _ptr(y), act, _ptr(q), _ptr(scales), size, M, D, _stream(stream)),
             "rocmfp4_add_rmsnorm")
     return AddRmsNorm(y, residual_out, q, scales)
+
+
+def moe(X, router, Wgu, Wd, I: int, top_k: int, variant: int = DUAL, route: int = ROUTE_SOFTMAX_TOPK, route_scale: float = 1.0,
+        Y=None, ids=None, probs=None, stream=None):
+    """(Y [M, K] float32, ids [M, top_k] int32, probs [M, top_k] float32) of a mixture-of-experts layer for up to 32 tokens.
+
+    X [M, K] float16 or bfloat16; router [E, K] float32, bfloat16 or float16; Wgu uint8 holding E packed matrices of 2I rows
+    (gate, then up) of K weights; Wd uint8 holding E packed matrices of K rows of I weights.  Each token takes the top_k
+    experts of its router logits; route (ROUTE_SOFTMAX, ROUTE_SOFTMAX_TOPK, ROUTE_SIGMOID) gives their weights.  The outputs
+    go into the tensors given, or into new ones."""
+    torch = _torch()
+    codes = _DTYPES or _dtypes()
+    if X.dim() == 1:
+        X = X.view(1, -1)
+    if X.dim() != 2 or not X.is_cuda or not X.is_contiguous():
+        raise ValueError("X must be a contiguous [M, K] CUDA tensor")
+    M, K = X.shape
+    if router.dim() != 2 or not router.is_cuda or not router.is_contiguous() or router.shape[1] != K:
+        raise ValueError("router must be a contiguous [E, K] CUDA tensor")
+    E = router.shape[0]
+    _check_w(Wgu, 2 * E * I, K, variant)
+    _check_w(Wd, E * K, I, variant)
+    dev, shape = X.device, (M, top_k)
+    Y = torch.empty((M, K), dtype=torch.float32, device=dev) if Y is None else _dense(Y, "Y", torch.float32, (M, K))
+    ids = torch.empty(shape, dtype=torch.int32, device=dev) if ids is None else _dense(ids, "ids", torch.int32, shape)
+    probs = torch.empty(shape, dtype=torch.float32, device=dev) if probs is None else _dense(probs, "probs", torch.float32, shape)
+    _check(load().rocmfp4_moe(_ptr(X), _ptr(router), codes.get(router.dtype, -1), _ptr(Wgu), _ptr(Wd), _ptr(Y), _ptr(ids), _ptr(probs), M,
+                              E, top_k, K, I, route, route_scale, variant, _act_of(X), _stream(stream)), "rocmfp4_moe")
+    return Y, ids, probs
 
 
 def logprobs(logits, targets=None, top_n: int = 0, scale: float = 1.0, logprob=None, entropy=None, top_ids=None,

@@ -27,6 +27,8 @@ struct DeviceState {
   unsigned long long* vfirst = nullptr;
   float* lp_ws = nullptr;            // log probabilities: records of split rows
   uint32_t* lp_cnt = nullptr;        // log probabilities: arrivals per split row
+  float* moe_ws = nullptr;           // mixture of experts: router logits and hidden values
+  uint32_t* moe_bars = nullptr;      // mixture of experts: barrier counters
 };
 
 constexpr int kMaxDevices = 64;
@@ -98,6 +100,10 @@ rocmfp4_status device_state(DeviceState** out) {
       return cuda_fail(e, "cudaMalloc");
     if ((e = cudaMemset(d.lp_cnt, 0, sizeof(uint32_t) * logprobs_cnt_words(d.sms))) != cudaSuccess)
       return cuda_fail(e, "cudaMemset");
+    if ((e = moe_prepare()) != cudaSuccess) return cuda_fail(e, "mixture-of-experts kernel set-up");
+    if ((e = cudaMalloc(&d.moe_ws, sizeof(float) * kMoeWsFloats)) != cudaSuccess) return cuda_fail(e, "cudaMalloc");
+    if ((e = cudaMalloc(&d.moe_bars, sizeof(uint32_t) * kMoeBarWords)) != cudaSuccess) return cuda_fail(e, "cudaMalloc");
+    if ((e = cudaMemset(d.moe_bars, 0, sizeof(uint32_t) * kMoeBarWords)) != cudaSuccess) return cuda_fail(e, "cudaMemset");
     if ((e = cudaMemset(d.err, 0, sizeof(uint32_t))) != cudaSuccess) return cuda_fail(e, "cudaMemset");
     if ((e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
     d.ready = true;
@@ -371,6 +377,39 @@ rocmfp4_status add_rmsnorm(const NormArgs& a, int64_t group, cudaStream_t s) {
   return ROCMFP4_OK;
 }
 
+rocmfp4_status moe(MoeArgs a, int variant, int act, cudaStream_t s) {
+  if (!valid_variant(variant)) return fail(ROCMFP4_ERR_INVALID_ARG, "unknown variant");
+  if (!valid_act(act)) return fail(ROCMFP4_ERR_INVALID_ARG, "unknown activation type");
+  if (!valid_dtype(a.router_type)) return fail(ROCMFP4_ERR_INVALID_ARG, "unknown type");
+  if (a.route != ROCMFP4_ROUTE_SOFTMAX && a.route != ROCMFP4_ROUTE_SOFTMAX_TOPK && a.route != ROCMFP4_ROUTE_SIGMOID)
+    return fail(ROCMFP4_ERR_INVALID_ARG, "unknown route");
+  if (a.M < 0) return fail(ROCMFP4_ERR_INVALID_ARG, "negative size");
+  if (a.E < 1 || a.top_k < 1 || a.top_k > a.E) return fail(ROCMFP4_ERR_INVALID_ARG, "1 <= top_k <= E is needed");
+  if (a.K < 32 || a.I < 32 || a.K % 32 != 0 || a.I % 32 != 0)
+    return fail(ROCMFP4_ERR_INVALID_ARG, "K and I must be positive multiples of 32");
+  if (!(a.route_scale >= -3.4e38f && a.route_scale <= 3.4e38f)) return fail(ROCMFP4_ERR_INVALID_ARG, "route_scale must be finite");
+  if (a.M == 0) return ROCMFP4_OK;
+  if (!a.X || !a.router || !a.Wgu || !a.Wd || !a.Y) return fail(ROCMFP4_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned_to(a.Y, 0) || !aligned_to(a.ids, 0) || !aligned_to(a.probs, 0))
+    return fail(ROCMFP4_ERR_INVALID_ARG, "misaligned pointer");
+  if (a.M > kMoeMaxTokens || a.E > kMoeMaxExperts || a.top_k > kMoeMaxTop || a.K > kMoeMaxWidth || a.I > kMoeMaxWidth ||
+      a.M * a.top_k * a.I > kMoeMaxHidden)
+    return fail(ROCMFP4_ERR_UNSUPPORTED,
+                "mixture of experts: at most 32 tokens, 512 experts, 16 choices, widths of 32768 and 2^22 hidden values");
+  if (!aligned16(a.X) || !aligned16(a.router) || !aligned16(a.Wgu) || !aligned16(a.Wd))
+    return fail(ROCMFP4_ERR_UNSUPPORTED, "mixture of experts: X, router, Wgu and Wd must be 16-byte aligned");
+  DeviceState* d = nullptr;
+  rocmfp4_status st = device_state(&d);
+  if (st != ROCMFP4_OK) return st;
+  a.ws = d->moe_ws;
+  a.bars = d->moe_bars;
+  a.err = d->err;
+  cudaError_t e = launch_moe(variant, act, a, d->sms, s);
+  if (e != cudaSuccess) return cuda_fail(e, "mixture-of-experts launch");
+  g_launches.fetch_add(1);
+  return ROCMFP4_OK;
+}
+
 rocmfp4_status logprobs(LogprobsArgs a, int64_t top_n, cudaStream_t s) {
   if (!valid_dtype(a.type)) return fail(ROCMFP4_ERR_INVALID_ARG, "unknown type");
   if (a.M < 0 || a.V < 0 || top_n < 0) return fail(ROCMFP4_ERR_INVALID_ARG, "negative size");
@@ -475,6 +514,29 @@ rocmfp4_status rocmfp4_add_rmsnorm(const void* x, rocmfp4_out_dtype x_type, int6
   a.group = (int)group;
   a.eps = eps;
   return add_rmsnorm(a, group, reinterpret_cast<cudaStream_t>(stream));
+}
+
+rocmfp4_status rocmfp4_moe(const void* X, const void* router, rocmfp4_out_dtype router_type, const void* Wgu,
+                           const void* Wd, float* Y, int32_t* ids, float* probs, int64_t M, int64_t E, int64_t top_k,
+                           int64_t K, int64_t I, rocmfp4_route route, float route_scale, rocmfp4_variant variant,
+                           rocmfp4_act act, rocmfp4_stream_t stream) {
+  MoeArgs a{};
+  a.X = static_cast<const uint16_t*>(X);
+  a.router = router;
+  a.Wgu = static_cast<const uint8_t*>(Wgu);
+  a.Wd = static_cast<const uint8_t*>(Wd);
+  a.Y = Y;
+  a.ids = ids;
+  a.probs = probs;
+  a.M = M;
+  a.E = E;
+  a.top_k = top_k;
+  a.K = K;
+  a.I = I;
+  a.router_type = router_type;
+  a.route = route;
+  a.route_scale = route_scale;
+  return moe(a, variant, act, reinterpret_cast<cudaStream_t>(stream));
 }
 
 rocmfp4_status rocmfp4_logprobs(const void* logits, rocmfp4_out_dtype type, int64_t ld, const int32_t* targets,
@@ -632,6 +694,7 @@ uint32_t rocmfp4_device_error_bits(rocmfp4_stream_t stream) {
       cudaMemsetAsync(d->err, 0, sizeof(uint32_t), s);
       cudaMemsetAsync(d->cnt, 0, sizeof(uint32_t) * d->wmax, s);
       cudaMemsetAsync(d->tccnt, 0, sizeof(uint32_t) * tc_cnt_words(d->sms), s);
+      cudaMemsetAsync(d->moe_bars, 0, sizeof(uint32_t) * kMoeBarWords, s);
       if (cudaStreamSynchronize(s) != cudaSuccess) return 0xFFFFFFFFu;
     }
   }
@@ -674,6 +737,8 @@ void rocmfp4_shutdown(void) {
     cudaFree(d.vfirst);
     cudaFree(d.lp_ws);
     cudaFree(d.lp_cnt);
+    cudaFree(d.moe_ws);
+    cudaFree(d.moe_bars);
     d = DeviceState{};
   }
   cudaSetDevice(cur);

@@ -120,6 +120,32 @@ size_t logprobs_ws_bytes(int sms);
 size_t logprobs_cnt_words(int sms);
 cudaError_t launch_logprobs(const LogprobsArgs& a, int sms, cudaStream_t s);
 
+// Mixture-of-experts layer for M <= kMoeMaxTokens tokens (moe.cu).  X, router,
+// Wgu and Wd 16-byte aligned; K and I multiples of 32, at most kMoeMaxWidth;
+// E <= kMoeMaxExperts; top_k <= min(E, kMoeMaxTop); M * top_k * I at most
+// kMoeMaxHidden.  One cooperative launch of one CTA per SM.
+constexpr int kMoeMaxTokens = 32, kMoeMaxExperts = 512, kMoeMaxTop = 16, kMoeMaxWidth = 32768;
+constexpr int64_t kMoeMaxHidden = int64_t(1) << 22;
+constexpr size_t kMoeWsFloats = (size_t)kMoeMaxTokens * kMoeMaxExperts + kMoeMaxHidden;
+constexpr int kMoeBarWords = 3;
+struct MoeArgs {
+  const uint16_t* X;   // M x K
+  const void* router;  // E x K
+  const uint8_t* Wgu;  // E x (I gate rows, I up rows) of K weights
+  const uint8_t* Wd;   // E x K rows of I weights
+  float* Y;            // M x K
+  int32_t* ids;        // M x top_k, nullptr: not wanted
+  float* probs;        // M x top_k, nullptr: not wanted
+  float* ws;           // kMoeWsFloats floats
+  uint32_t* bars;      // kMoeBarWords words, zero between launches
+  uint32_t* err;
+  int64_t M, E, top_k, K, I;
+  int router_type, route;
+  float route_scale;
+};
+cudaError_t moe_prepare();
+cudaError_t launch_moe(int variant, int act, const MoeArgs& a, int sms, cudaStream_t s);
+
 // Any K % 32 == 0, any alignment: one warp per (row, column chunk).
 struct GenericArgs {
   const uint8_t* W;

@@ -26,8 +26,8 @@
  * Conventions shared by every entry point
  *   - Every pointer to matrix, activation or output data is DEVICE memory
  *     owned by the caller.  Calls do not allocate per call; a per-device
- *     workspace (split-reduction partials and counters: about 0.18 MiB per
- *     SM, 27 MiB on a 152-SM GPU) is allocated once, on first use, and
+ *     workspace (split-reduction partials and counters, and hidden values
+ *     of rocmfp4_moe: 43 MiB on a 152-SM GPU) is allocated once, on first use, and
  *     released by rocmfp4_shutdown().
  *   - Calls on one device share that workspace: calls that overlap on the GPU
  *     (unordered streams, or graphs replayed concurrently) race and give wrong
@@ -195,6 +195,45 @@ rocmfp4_status rocmfp4_add_rmsnorm(const void *x, rocmfp4_out_dtype x_type, int6
                                    const void *weight, rocmfp4_out_dtype weight_type, float eps,
                                    void *y, rocmfp4_act y_type, void *q, float *scales,
                                    int64_t group, int64_t M, int64_t D, rocmfp4_stream_t stream);
+
+typedef enum {
+  ROCMFP4_ROUTE_SOFTMAX = 0,      /* p = softmax over all experts            */
+  ROCMFP4_ROUTE_SOFTMAX_TOPK = 1, /* p = softmax over the chosen experts     */
+  ROCMFP4_ROUTE_SIGMOID = 2       /* p = sigmoid(l) / sum over the chosen    */
+} rocmfp4_route;
+
+/* A whole mixture-of-experts layer for a few tokens (decode):
+ *
+ *   l[m][e] = sum_k X[m][k] router[e][k]
+ *   the top_k experts of a token by (l descending, index ascending), with
+ *   weights p by `route`, times route_scale
+ *   h = SiLU(Wg x) * (Wu x),   Y[m] = sum over the token's choices p * (Wd h)
+ *
+ * No counterpart in the format definition; the experts' matrices are packed
+ * ROCmFP4 blocks, and each chosen expert's blocks are read once for all the
+ * tokens that chose it.
+ *   - X        [M][K] of type act; router [E][K] of router_type
+ *              (rocmfp4_out_dtype);
+ *   - Wgu      [E] packed matrices of 2I rows (the I gate rows, then the I up
+ *              rows) of K weights; Wd [E] packed matrices of K rows of I
+ *              weights; both of `variant`;
+ *   - Y        [M][K] fp32, overwritten;
+ *   - ids      [M][top_k] int32, the chosen experts in order, or NULL; probs
+ *              [M][top_k] fp32, their weights (route_scale included), or NULL.
+ *   - Logits, h and every sum are fp32; results are bitwise repeatable.  A NaN
+ *     logit orders below every number; a token with a NaN or +inf logit, or
+ *     with none above -inf, may get NaN weights, and then a NaN output.
+ *   - K and I positive multiples of 32; 1 <= top_k <= E.  M at most 32, E at
+ *     most 512, top_k at most 16, K and I at most 32768, M * top_k * I at most
+ *     2^22, and X, router, Wgu and Wd 16-byte aligned, else
+ *     ROCMFP4_ERR_UNSUPPORTED.  M == 0 does nothing.
+ *   - One cooperative launch (a CTA on every SM) on `stream`; h uses the
+ *     per-device workspace. */
+rocmfp4_status rocmfp4_moe(const void *X, const void *router, rocmfp4_out_dtype router_type,
+                           const void *Wgu, const void *Wd, float *Y, int32_t *ids, float *probs,
+                           int64_t M, int64_t E, int64_t top_k, int64_t K, int64_t I,
+                           rocmfp4_route route, float route_scale, rocmfp4_variant variant,
+                           rocmfp4_act act, rocmfp4_stream_t stream);
 
 /* Log probabilities, entropy and top alternatives of rows of logits (the LM
  * head's product), with z_v = scale * logit_v (scale: 1 / temperature):

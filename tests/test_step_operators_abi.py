@@ -1,4 +1,4 @@
-"""CPU tests of the argument checks of rocmfp4_add_rmsnorm and rocmfp4_logprobs: every call below is refused on the host
+"""CPU tests of the argument checks of rocmfp4_add_rmsnorm, rocmfp4_moe and rocmfp4_logprobs: every call below is refused on the host
 (or has nothing to do) before any pointer is used."""
 import ctypes
 
@@ -63,3 +63,31 @@ def test_logprobs_unsupported_and_empty(L):
     assert logprobs(L, top_n=33) == UNSUPPORTED
     assert logprobs(L, V=1 << 31, ld=1 << 31) == UNSUPPORTED
     assert logprobs(L, M=0, logits=None, targets=None) == 0
+
+
+def moe(L, **kw):
+    a = dict(X=PTR, router=PTR, router_type=1, Wgu=PTR, Wd=PTR, Y=PTR, ids=PTR, probs=PTR, M=2, E=8, top_k=2, K=64, I=96, route=1,
+             route_scale=1.0, variant=0, act=0, stream=None)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return L.rocmfp4_moe(*a.values())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(variant=2), dict(act=2), dict(router_type=3), dict(route=3), dict(route=-1), dict(M=-1), dict(E=0), dict(top_k=0), dict(top_k=9),
+    dict(K=0), dict(K=63), dict(I=0), dict(I=-32), dict(I=48), dict(route_scale=NAN), dict(route_scale=INF), dict(X=None), dict(router=None),
+    dict(Wgu=None), dict(Wd=None), dict(Y=None), dict(Y=PTR + 2), dict(ids=PTR + 1), dict(probs=PTR + 2)])
+def test_moe_invalid(L, kw):
+    assert moe(L, **kw) == INVALID
+    assert L.rocmfp4_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(M=33), dict(E=513), dict(E=64, top_k=17), dict(K=32800), dict(I=32800), dict(M=32, E=16, top_k=16, I=32768), dict(X=PTR + 8),
+    dict(router=PTR + 4), dict(Wgu=PTR + 2), dict(Wd=PTR + 8)])
+def test_moe_unsupported(L, kw):
+    assert moe(L, **kw) == UNSUPPORTED
+
+
+def test_moe_empty(L):
+    assert moe(L, M=0, X=None, router=None, Wgu=None, Wd=None, Y=None) == 0
