@@ -6,32 +6,44 @@
 // with every expert's Wg, Wu (stacked) and Wd in packed ROCmFP4 blocks.  Only
 // the blocks of chosen experts are read, each once.
 //
-// Bound: memory (3 I K / 32 blocks per chosen expert) at a token or two per
-// expert; the decode's ALU work (about 5 instructions a byte) is close behind.
-//
 // One persistent CTA per SM, launched cooperatively, in three phases with two
-// grid barriers: router logits; gate and up products (h goes to the
-// workspace); down products.  Every CTA repeats the small top-k selection for
-// itself, which costs less than handing its result on.  The products are
-// cut into tasks of a few whole rows that warps take on their own: a warp
-// streams its tasks' rows by bulk copies into a private ring of shared-memory
-// stages, and because the down tasks are known as soon as the routing is, the
+// grid barriers: router logits (and the activations in fragment order); gate
+// and up products (h goes to the workspace); down products.  Every CTA repeats
+// the small top-k selection for itself, which costs less than handing its
+// result on.
+//
+// Products.  A tile is 16 rows: 8 gate and the 8 up rows of the same hidden
+// values, or 16 output rows.  A span is 144 bytes (8 dual blocks) or 272 bytes
+// (16 single-scale blocks) of each row.  A warp takes tiles on its own (or
+// KP neighbouring warps share a tile's spans where tiles are few) and streams
+// their spans through a private ring of shared-memory stages, by tensor copies
+// of 16-row boxes.  The down tasks are known as soon as the routing is, so the
 // ring runs on into them before the second barrier.
+// The arithmetic is mma.sync m16n8k16 on fp16 with fp32 accumulators: A is
+// the decoded weights, exact in fp16, decoded once for all the tokens of the
+// expert; B's columns are tokens.  Lane (q, c) decodes blocks of rows q and
+// q + 8; byte j of a block is the pair (j, j + 16), so activations are kept in
+// that pair order, 16 bytes a lane and load.  Eight MMAs run in the tensor
+// core's accumulator, then add to fp32 registers, round to nearest.
 //
-// Products.  A unit is a 4-byte multiple of whole blocks of a row: two dual
-// blocks (36 bytes) or four single-scale blocks (68 bytes).  L lanes share a
-// row, taking units c, c + L, ...; a warp holds 32 / L groups of R rows, and
-// the activations of a block, loaded once, serve the R rows.  Unit strides
-// of 9 or 17 words keep the shared-memory reads free of bank conflicts.  A
-// block's codes become fp16 pairs (weights j, j + 16), widen to fp32 exactly,
-// and accumulate by packed fp32 FMAs, one chain per half, so a half-scale is
-// applied once per half.  Everything from the codes to the sums is fp32 round
-// to nearest: h needs no second rounding to a 16-bit type.
+// Precision.  bf16 activations become fp16 after scaling a token by the power
+// of two that brings its largest magnitude to [2^14, 2^15): values down to
+// 2^-28 of the largest stay exact, smaller ones are off by at most 2^-39 of
+// it.  h is fp32; the down product takes it as two fp16 columns, high and
+// remainder, 22 bits together.  The pair is made where h is, times 16, if the
+// choice's largest |h| proves to be in [2^-5, 2^11); outside that range the
+// reader makes it from the fp32 h, scaled like a bf16 token.
 //
-// Rows whose length is no multiple of 4 bytes (K / 32 odd, dual; K / 32 not a
-// multiple of 4, single-scale) are shifted into place word by word; copies
-// start at the 16-byte boundary before a row and end at the one after it,
-// which stays inside the matrices as their sizes are multiples of 16.
+// Bound: memory (3 I K / 32 blocks per chosen expert), with the decode's issue
+// slots (about 3.7 instructions per pair of weights) close behind.
+//
+// Rows whose length is no multiple of 16 bytes (K / 32 not a multiple of 8,
+// dual, or 16, single-scale) cannot be boxes of a tensor copy.  They come by a
+// bulk copy per row from the 16-byte boundary before the span to the one
+// after it (which stays inside the matrices, as their sizes are multiples of
+// 16), and are shifted into place word by word.
+#include <cudaTypedefs.h>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -40,24 +52,29 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTileRows = 16;    // output rows of a down tile
-constexpr int kMaxStages = 4;
-constexpr int kRouterTokens = 8;  // tokens a router pass holds
+constexpr int kTileRows = 16;
+constexpr int kMaxStages = 8;
+constexpr int kRouterTokens = 8;   // tokens a router pass holds
+constexpr int kGuGroups = 4;       // groups of 8 tokens of an expert
+constexpr int kDnGroups = 8;       // groups of 4 tokens: high and low columns
+constexpr int kFastExp = 4;        // h times 2^4 in its fp16 pair
 
-// Shape of one product: rows of nb blocks, cut among lanes and stages.
-struct RowGeom {
-  int nb;          // blocks per row
-  int rb;          // bytes per row
-  int lanes;       // L: lanes that share a row (4, 8, 16 or 32)
-  int iters;       // units per lane
-  int seg_iters;   // iterations held by one stage
-  int segs;        // stages per task
-  int rows;        // rows of a task: 32 / L * R
-  int pitch;       // bytes between row slots of a stage (rb when a stage holds whole rows)
-  int half;        // offset of the up rows' region (gate/up tasks)
+template <int V>
+struct Unit {
+  static constexpr int BLOCKS = Fmt<V>::BPL;       // blocks a lane has of a span: 2 / 4
+  static constexpr int BYTES = Fmt<V>::LANE_BYTES; // 36 / 68
+  static constexpr int SPAN = Fmt<V>::SPAN;        // 144 / 272
+  static constexpr int SPAN_BLOCKS = 4 * BLOCKS;   // 8 / 16
+  static constexpr int NS = V == 0 ? 2 : 1;        // spans a stage holds
+  static constexpr int X_SPAN = SPAN_BLOCKS * 64;  // bytes of a span's fp16 activations
+  static constexpr int PITCH = 304;                // row slots of unaligned rows: NS spans, 16-byte slack, no bank conflicts
+  static constexpr int STAGE = (kTileRows * PITCH + 127) / 128 * 128;
+  static_assert(NS * SPAN + 15 <= PITCH && NS * SPAN * kTileRows <= STAGE, "stage holds either form");
 };
 
 struct MoeParams {
+  CUtensorMap map_gu;  // aligned rows: {words, I rows, 2 E halves}, box {span, 8, 2}
+  CUtensorMap map_dn;  // {words, E K rows}, box {span, 16}
   const uint16_t* X;
   const void* router;
   const uint8_t* Wgu;
@@ -65,47 +82,24 @@ struct MoeParams {
   float* Y;
   int32_t* ids;
   float* probs;
-  float* logits;   // workspace [M][E]
-  float* h;        // workspace [M * top_k][I]
-  uint32_t* bars;  // workspace: two barrier counters and one of finished CTAs, zero between launches
+  float* logits;       // workspace [M][E]
+  float* x_unscale;    // workspace [M]
+  uint32_t* amax;      // workspace [M * top_k]: bits of the largest |h|
+  uint8_t* xf;         // workspace: activations in fragment order, fp16
+  float* h;            // workspace [M * top_k][I]
+  uint8_t* h_hi;       // workspace: h * 16 in fragment order, fp16 and its remainder
+  uint8_t* h_lo;
+  uint32_t* bars;      // workspace: two barrier counters and one of finished CTAs, zero between launches
   uint32_t* err;
   int M, E, top_k, K, I;
   int router_type, route;
   float route_scale;
-  RowGeom gu, dn;
-  int stage_bytes, stages;
+  int parts;           // KP: warps that share a gate/up tile
+  int stages;          // ring stages of a warp
   // offsets in shared memory
-  int off_mask, off_list, off_slot, off_acc, off_ring;
-  int acc_floats;  // per warp
+  int off_mask, off_list, off_slot, off_unscale, off_acc, off_ring;
+  int acc_floats;      // per warp
 };
-
-template <int V>
-struct Unit {
-  static constexpr int BLOCKS = V == 0 ? 2 : 4;
-  static constexpr int BYTES = BLOCKS * Fmt<V>::BB;  // 36 / 68
-  static constexpr int R_GU = V == 0 ? 4 : 2;        // rows a lane holds: gate and up rows in equal parts
-  static constexpr int R_DN = V == 0 ? 2 : 1;
-};
-
-RF4_DEV uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-RF4_DEV float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-RF4_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-RF4_DEV uint64_t half2_to_f32x2(uint32_t h) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  return pack2(f.x, f.y);
-}
 
 template <int ACT>
 RF4_DEV float act_f32(uint32_t bits16) {
@@ -113,45 +107,29 @@ RF4_DEV float act_f32(uint32_t bits16) {
   else return __half2float(__ushort_as_half((uint16_t)bits16));
 }
 
-// A block's 32 activations as pairs (x_j, x_{j+16}).  SRC 0 / 1: fp16 / bf16 input; 2: fp32 workspace.
-template <int SRC>
-RF4_DEV void load_x(const void* base, int64_t off, uint64_t (&xp)[16]) {
-  if constexpr (SRC == 2) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + off);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 a = p[i], b = p[4 + i];
-      xp[4 * i] = pack2(a.x, b.x);
-      xp[4 * i + 1] = pack2(a.y, b.y);
-      xp[4 * i + 2] = pack2(a.z, b.z);
-      xp[4 * i + 3] = pack2(a.w, b.w);
-    }
-  } else {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 a = __ldg(p + i), b = __ldg(p + 2 + i);
-      const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (SRC == 1) {
-          xp[8 * i + 2 * j] = pack2(__uint_as_float(u[j] << 16), __uint_as_float(v[j] << 16));
-          xp[8 * i + 2 * j + 1] = pack2(__uint_as_float(u[j] & 0xFFFF0000u), __uint_as_float(v[j] & 0xFFFF0000u));
-        } else {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
-          const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&v[j]));
-          xp[8 * i + 2 * j] = pack2(f.x, g.x);
-          xp[8 * i + 2 * j + 1] = pack2(f.y, g.y);
-        }
-      }
-    }
-  }
+// 2^k, k clamped to a range that its inverse shares.
+RF4_DEV float exp2i(int k) { return __uint_as_float((uint32_t)(127 + max(-120, min(120, k))) << 23); }
+// The power of two that brings a magnitude (its bits) to [2^14, 2^15); 0 for zero and non-finite ones.
+RF4_DEV int scale_exp(uint32_t amax_bits) {
+  const int e = (int)(amax_bits >> 23);
+  if (e == 255 || amax_bits == 0) return 0;
+  return max(-120, min(120, 141 - e));
+}
+// Whether the fp16 pair of h made with the fixed scale is good: 0, [2^-5, 2^11) or not finite (then so is the output).
+RF4_DEV bool fast_range(uint32_t amax_bits) {
+  const int e = (int)(amax_bits >> 23);
+  return amax_bits == 0 || e == 255 || (e >= 127 - 5 && e < 127 + 11);
 }
 
-// The five words that hold block PHI of a unit at `unit` (any byte address
+RF4_DEV uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The five words that hold block PHI of a lane's unit (any byte address
 // unless ALIGNED): code byte j at byte (PHI * block bytes) % 4 + j.
 template <int V, bool ALIGNED, int PHI>
-RF4_DEV void block_words(const uint8_t* unit, uint32_t (&w)[5]) {
+RF4_DEV void block_words(const uint8_t* unit, bool have, uint32_t (&w)[5]) {
   constexpr int FIRST = PHI * Fmt<V>::BB / 4;
   if constexpr (ALIGNED) {
     const uint32_t* p = reinterpret_cast<const uint32_t*>(unit) + FIRST;
@@ -162,7 +140,7 @@ RF4_DEV void block_words(const uint8_t* unit, uint32_t (&w)[5]) {
     const uint32_t* p = reinterpret_cast<const uint32_t*>(unit - mis) + FIRST;
     uint32_t a[6];
 #pragma unroll
-    for (int i = 0; i < 6; ++i) a[i] = p[i];
+    for (int i = 0; i < 6; ++i) a[i] = have ? p[i] : 0u;  // past the row: zero codes under zero scales
 #pragma unroll
     for (int i = 0; i < 5; ++i) w[i] = __funnelshift_r(a[i], a[i + 1], 8 * mis);
   }
@@ -178,91 +156,72 @@ RF4_DEV uint32_t codes_at(const uint32_t (&w)[5], int pos) {
   }
 }
 
-// Adds block PHI of R rows (row r at unit + r * stride) times T tokens' activations.
-template <int V, bool ALIGNED, int R, int T, int PHI>
-RF4_DEV void block_rows(const uint8_t* const (&unit)[R], const uint64_t (&xp)[T][16], float (&tot)[R][T]) {
+// The 16 pairs (w_j, w_{j+16}) of block PHI of a unit, exact in fp16.
+template <int V, bool ALIGNED, int PHI>
+RF4_DEV void decode_block(const uint8_t* unit, bool have, uint32_t (&a)[16]) {
   constexpr int O = PHI * Fmt<V>::BB % 4;
+  uint32_t w[5];
+  block_words<V, ALIGNED, PHI>(unit, have, w);
+  uint32_t s2;
+  if constexpr (V == 0) s2 = O == 0 ? e4m3x2<0>(w[4]) : e4m3x2<1>(w[4]);
+  else s2 = e4m3x2<0>(__byte_perm(w[4], 0u, O * 0x11));
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    uint32_t w[5];
-    block_words<V, ALIGNED, PHI>(unit[r], w);
-    uint64_t acc[T][2];
-#pragma unroll
-    for (int t = 0; t < T; ++t) acc[t][0] = acc[t][1] = 0;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const uint64_t wp = half2_to_f32x2(clamp5(codes_at(w, O + j)));
-#pragma unroll
-      for (int t = 0; t < T; ++t) acc[t][j & 1] = fma2(wp, xp[t][j], acc[t][j & 1]);
-    }
-    float2 s;
-    if constexpr (V == 0) {
-      const uint32_t h = O == 0 ? e4m3x2<0>(w[4]) : e4m3x2<1>(w[4]);
-      s = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    } else {
-      const uint32_t h = e4m3x2<0>(__byte_perm(w[4], 0u, O * 0x11));
-      s = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    }
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const float2 a = unpack2(acc[t][0]), b = unpack2(acc[t][1]);
-      tot[r][t] = fmaf(s.x, a.x + b.x, tot[r][t]);
-      tot[r][t] = fmaf(s.y, a.y + b.y, tot[r][t]);
-    }
-  }
+  for (int j = 0; j < 16; ++j) a[j] = hmul2(clamp5(codes_at(w, O + j)), s2);
 }
 
-template <int V, bool ALIGNED, int R, int T, int SRC, int PHI>
-RF4_DEV void unit_blocks(const uint8_t* const (&unit)[R], const void* xbase, const int64_t (&xoff)[T], int blk, int nb,
-                         float (&tot)[R][T]) {
-  if (blk + PHI < nb) {
-    uint64_t xp[T][16];
-#pragma unroll
-    for (int t = 0; t < T; ++t) load_x<SRC>(xbase, xoff[t] + (int64_t)(blk + PHI) * 32, xp[t]);
-    block_rows<V, ALIGNED, R, T, PHI>(unit, xp, tot);
-  }
-  if constexpr (PHI + 1 < Unit<V>::BLOCKS) unit_blocks<V, ALIGNED, R, T, SRC, PHI + 1>(unit, xbase, xoff, blk, nb, tot);
+RF4_DEV void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One stage's products for T tokens: tot[r][t], summed over the lanes of a row
-// (each of them gets the sum).  `row`: the row slots in shared memory; u0: the
-// first unit held.
-template <int V, bool ALIGNED, int R, int T, int SRC>
-RF4_DEV void stage_products(const RowGeom& g, const uint8_t* const (&row)[R], int u0, int c, const void* xbase,
-                            const int64_t (&xoff)[T], float (&tot)[R][T]) {
+// Byte offset of chunk kk (pairs 4 kk .. 4 kk + 3) of block PHI of lane group c
+// in a span's activations: the four c lie side by side.
+RF4_DEV int x_chunk(int phi, int kk, int c) { return ((phi * 4 + kk) * 4 + c) * 16; }
+
+// acc += the products of a decoded block of 16 rows with the columns' activations b.
+RF4_DEV void block_mma(const uint32_t (&a0)[16], const uint32_t (&a1)[16], const uint4 (&b)[4], float (&acc)[4]) {
+  float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int t = 0; t < T; ++t) tot[r][t] = 0.f;
-  for (int i = 0; i < g.seg_iters; ++i) {
-    const int ul = i * g.lanes + c;  // unit within the stage
-    const int blk = (u0 + ul) * Unit<V>::BLOCKS;
-    if (blk >= g.nb) break;
-    const uint8_t* unit[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) unit[r] = row[r] + ul * Unit<V>::BYTES;
-    unit_blocks<V, ALIGNED, R, T, SRC, 0>(unit, xbase, xoff, blk, g.nb, tot);
+  for (int kk = 0; kk < 4; ++kk) {
+    mma(d, a0[4 * kk], a1[4 * kk], a0[4 * kk + 1], a1[4 * kk + 1], b[kk].x, b[kk].y);
+    mma(d, a0[4 * kk + 2], a1[4 * kk + 2], a0[4 * kk + 3], a1[4 * kk + 3], b[kk].z, b[kk].w);
   }
-  __syncwarp();
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    if (o >= g.lanes) continue;
+  for (int i = 0; i < 4; ++i) acc[i] += d[i];
+}
+
+// One span of a tile: `ra`, `rb` are rows q and q + 8 at the lane's unit,
+// `load` gives the activations of a group's column.  have(PHI): the block is
+// inside the row.
+template <int V, bool ALIGNED, int PHI, int GROUPS, class Load>
+RF4_DEV void span_products(const uint8_t* ra, const uint8_t* rb, int blk, int nb, int ng, Load&& load, float (&acc)[GROUPS][4]) {
+  const bool have = ALIGNED || blk + PHI < nb;
+  uint32_t a0[16], a1[16];
+  decode_block<V, ALIGNED, PHI>(ra, have, a0);
+  decode_block<V, ALIGNED, PHI>(rb, have, a1);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int t = 0; t < T; ++t) tot[r][t] += __shfl_xor_sync(0xffffffffu, tot[r][t], o);
+  for (int g = 0; g < GROUPS; ++g) {
+    if (g >= ng) break;
+    uint4 b[4];
+    load(g, PHI, have, b);
+    block_mma(a0, a1, b, acc[g]);
   }
+  if constexpr (PHI + 1 < Unit<V>::BLOCKS) span_products<V, ALIGNED, PHI + 1, GROUPS>(ra, rb, blk, nb, ng, load, acc);
 }
 
 // The bytes [a, a + n) as a copy from 16-byte boundary to 16-byte boundary.
-RF4_DEV uint32_t span_bytes(const uint8_t* a, int64_t n) {
+RF4_DEV uint32_t span_bytes(const uint8_t* a, int n) {
   const uintptr_t b = reinterpret_cast<uintptr_t>(a) & ~uintptr_t(15), e = (reinterpret_cast<uintptr_t>(a) + n + 15) & ~uintptr_t(15);
   return (uint32_t)(e - b);
 }
-RF4_DEV void copy_span(uint8_t* dst, const uint8_t* a, int64_t n, uint32_t bar) {
+RF4_DEV void copy_span(uint8_t* dst, const uint8_t* a, int n, uint32_t bar) {
   bulk_g2s(smem_addr(dst), reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(a) & ~uintptr_t(15)), span_bytes(a, n), bar);
 }
 RF4_DEV int mis16(const uint8_t* a) { return (int)(reinterpret_cast<uintptr_t>(a) & 15u); }
+
+// Barrier of some whole warps of the CTA (id 1 .. 15).
+RF4_DEV void team_barrier(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
 RF4_DEV uint32_t load_acquire(const uint32_t* p) {
   uint32_t v;
@@ -296,12 +255,12 @@ RF4_DEV void load8_router(int type, const void* base, int64_t off, float (&v)[8]
 template <int V, int ACT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant__ MoeParams p) {
   using U = Unit<V>;
-  constexpr int RG = U::R_GU, RD = U::R_DN;
   extern __shared__ __align__(128) uint8_t smem[];
   float* s_probs = reinterpret_cast<float*>(smem);                           // [M][top_k]
   uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + p.off_mask);         // [E]: tokens of an expert
   uint16_t* s_list = reinterpret_cast<uint16_t*>(smem + p.off_list);         // chosen experts, ascending
   uint8_t* s_slot = smem + p.off_slot;                                       // [M][E]: which choice of the token
+  float* s_unscale = reinterpret_cast<float*>(smem + p.off_unscale);         // [M]: 1 / the activations' scale
   float* s_acc = reinterpret_cast<float*>(smem + p.off_acc);                 // [kWarps][acc_floats]
   __shared__ uint64_t s_bars[kWarps * kMaxStages];
   __shared__ float s_red[kWarps][kRouterTokens];
@@ -373,6 +332,48 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       __syncthreads();
     }
   }
+  // ---- activations in fragment order, by the CTAs that have the fewest experts ----
+  const int nb_k = p.K / 32, spans_k = (nb_k + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS;
+  for (int m = G - 1 - (int)blockIdx.x; m < p.M; m += G) {
+    const uint16_t* x = p.X + (int64_t)m * p.K;
+    float scale = 1.f;
+    if constexpr (ACT == 1) {
+      uint32_t mx = 0;  // bf16 magnitudes order as their bits
+      for (int k = tid * 2; k < p.K; k += kThreads * 2) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(x + k) & 0x7FFF7FFFu;
+        mx = max(mx, max(w & 0xFFFFu, w >> 16));
+      }
+      mx = __reduce_max_sync(0xffffffffu, mx);
+      if (lane == 0) s_red[warp][0] = __uint_as_float(mx << 16);
+      __syncthreads();
+      mx = 0;
+      for (int w = 0; w < kWarps; ++w) mx = max(mx, __float_as_uint(s_red[w][0]));
+      const int k = scale_exp(mx);
+      scale = exp2i(k);
+      if (tid == 0) p.x_unscale[m] = exp2i(-k);
+      __syncthreads();
+    } else if (tid == 0) {
+      p.x_unscale[m] = 1.f;
+    }
+    for (int i = tid; i < nb_k * 4; i += kThreads) {
+      const int blk = i >> 2, kk = i & 3, in = blk % U::SPAN_BLOCKS;
+      const uint2 a = *reinterpret_cast<const uint2*>(x + blk * 32 + 4 * kk);
+      const uint2 b = *reinterpret_cast<const uint2*>(x + blk * 32 + 16 + 4 * kk);
+      uint4 v;
+      if constexpr (ACT == 0) {
+        v = make_uint4(__byte_perm(a.x, b.x, 0x5410), __byte_perm(a.x, b.x, 0x7632), __byte_perm(a.y, b.y, 0x5410), __byte_perm(a.y, b.y, 0x7632));
+      } else {
+        v.x = pack_half2(act_f32<1>(a.x & 0xFFFFu) * scale, act_f32<1>(b.x & 0xFFFFu) * scale);
+        v.y = pack_half2(act_f32<1>(a.x >> 16) * scale, act_f32<1>(b.x >> 16) * scale);
+        v.z = pack_half2(act_f32<1>(a.y & 0xFFFFu) * scale, act_f32<1>(b.y & 0xFFFFu) * scale);
+        v.w = pack_half2(act_f32<1>(a.y >> 16) * scale, act_f32<1>(b.y >> 16) * scale);
+      }
+      uint8_t* dst = p.xf + ((int64_t)m * spans_k + blk / U::SPAN_BLOCKS) * U::X_SPAN + x_chunk(in % U::BLOCKS, kk, in / U::BLOCKS);
+      *reinterpret_cast<uint4*>(dst) = v;
+    }
+  }
+  if (blockIdx.x == 0)
+    for (int i = tid; i < p.M * p.top_k; i += kThreads) p.amax[i] = 0u;
   bool ok = grid_barrier(p.bars);
 
   // ---- top k of every token (one warp per token), repeated by every CTA ----
@@ -435,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       }
     }
   }
+  if (ok && tid < p.M) s_unscale[tid] = __ldcg(p.x_unscale + tid);
   __syncthreads();
   if (warp == 0) {
     int n = 0;
@@ -449,234 +451,305 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   __syncthreads();
   const int A = ok ? s_active : 0;
 
-  // ---- this warp's stages: gate/up tasks, then down tasks -------------------------------
-  const RowGeom gu = p.gu, dn = p.dn;
-  const int pairs = gu.rows / 2;                          // gate/up row pairs of a task
-  const int per_expert = (p.I + pairs - 1) / pairs;       // gate/up tasks of an expert
-  const int gu_tasks = A * per_expert;                    // dealt round robin over all CTAs, then warps
-  const int first_gu = blockIdx.x + G * warp;
-  const int n_gu = first_gu < gu_tasks ? (gu_tasks - first_gu + G * kWarps - 1) / (G * kWarps) : 0;
+  // ---- this warp's stages: gate/up tiles, then down tiles --------------------------------
+  const int nb_i = p.I / 32, spans_i = (nb_i + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS;
+  const int rb_k = nb_k * Fmt<V>::BB, rb_i = nb_i * Fmt<V>::BB;
+  const int KP = p.parts, team = warp / KP, part = warp % KP, teams = kWarps / KP;
+  const int span0 = spans_k * part / KP, span1 = spans_k * (part + 1) / KP;  // this warp's spans of a gate/up tile
+  const int per_expert = p.I / 8;                                          // gate/up tiles of an expert
+  const int gu_tiles = A * per_expert;                                     // dealt round robin over CTAs, then teams
+  const int first_gu = blockIdx.x + G * team;
   const int tiles = p.K / kTileRows;
   const int my_tiles = (int)blockIdx.x < tiles ? (tiles - (int)blockIdx.x + G - 1) / G : 0;
-  const int subs = kTileRows / dn.rows;                   // down tasks of a tile and expert
-  const int tile_tasks = A * subs;
-  const int per_tile = warp < tile_tasks ? (tile_tasks - warp + kWarps - 1) / kWarps : 0;
-  const int n_stages_gu = n_gu * gu.segs;
-  const int n_stages = n_stages_gu + my_tiles * per_tile * dn.segs;
-  uint8_t* ring = smem + p.off_ring + (size_t)warp * p.stages * p.stage_bytes;
+  const int sd = (spans_i + U::NS - 1) / U::NS;                            // stages of an expert's rows in a down tile
+  const int u0 = warp * (A * sd) / kWarps, u1 = (warp + 1) * (A * sd) / kWarps;  // this warp's share of a down tile's stages
+  uint8_t* ring = smem + p.off_ring + (size_t)warp * p.stages * U::STAGE;
 
-  // na rows from `a` to slots from dst, nbr rows from `b` to slots from dst + half: part `seg` of each row
-  auto arm_and_copy = [&](uint8_t* dst, const uint8_t* a, int na, const uint8_t* b, int nbr, int half, const RowGeom& g, int seg, int slot) {
+  // Lane's rows q and q + 8 of a stage, at its unit of span `sp` of the stage.
+  // Unaligned rows start at their own place within 16 bytes.
+  const int q = lane >> 2, c = lane & 3;
+  auto unit_at = [&](const uint8_t* stage, int r, int sp, const uint8_t* src) {
+    if constexpr (ALIGNED) return stage + sp * (kTileRows * U::SPAN) + r * U::SPAN + c * U::BYTES;
+    else return stage + r * U::PITCH + mis16(src) + sp * U::SPAN + c * U::BYTES;
+  };
+  auto gu_row = [&](int e, int i0, int r) { return p.Wgu + ((int64_t)e * 2 * p.I + (r < 8 ? 0 : p.I) + i0 + (r & 7)) * rb_k; };
+  auto dn_row = [&](int e, int n0, int r) { return p.Wd + ((int64_t)e * p.K + n0 + r) * rb_i; };
+
+  // Copies of spans [span, span + n) of a tile's 16 rows into a stage.
+  auto fill = [&](bool down, int e, int row0, int span, int n, int slot) {
+    uint8_t* dst = ring + (size_t)slot * U::STAGE;
     const uint32_t bar = smem_addr(&bars[slot]);
-    if (g.segs == 1) {  // whole rows: one copy for each run of rows
+    if constexpr (ALIGNED) {
       if (lane == 0) {
-        mbar_arrive_expect_tx(bar, span_bytes(a, (int64_t)na * g.rb) + (nbr ? span_bytes(b, (int64_t)nbr * g.rb) : 0u));
-        copy_span(dst, a, (int64_t)na * g.rb, bar);
-        if (nbr) copy_span(dst + half, b, (int64_t)nbr * g.rb, bar);
+        mbar_arrive_expect_tx(bar, (uint32_t)(n * kTileRows * U::SPAN));
+        for (int k = 0; k < n; ++k) {
+          const uint32_t to = smem_addr(dst + k * kTileRows * U::SPAN);
+          if (down) tma_load_2d(to, &p.map_dn, (span + k) * (U::SPAN / 4), e * p.K + row0, bar);
+          else tma_load_3d(to, &p.map_gu, (span + k) * (U::SPAN / 4), row0, 2 * e, bar);
+        }
       }
-    } else {  // part of every row: one copy per row, by lanes
-      const int lo = seg * g.seg_iters * g.lanes * U::BYTES;
-      const int len = min(g.rb - lo, g.seg_iters * g.lanes * U::BYTES);
-      uint32_t bytes = 0;
-      for (int r = lane; r < na + nbr; r += 32) bytes += span_bytes((r < na ? a + (int64_t)r * g.rb : b + (int64_t)(r - na) * g.rb) + lo, len);
-      bytes = __reduce_add_sync(0xffffffffu, bytes);
+    } else {
+      const int rb = down ? rb_i : rb_k, lo = span * U::SPAN, len = min(rb - lo, n * U::SPAN);
+      const uint8_t* src = (down ? dn_row(e, row0, lane & 15) : gu_row(e, row0, lane & 15)) + lo;
+      const uint32_t bytes = __reduce_add_sync(0xffffffffu, lane < kTileRows ? span_bytes(src, len) : 0u);
       if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
       __syncwarp();
-      for (int r = lane; r < na + nbr; r += 32) {
-        const uint8_t* src = (r < na ? a + (int64_t)r * g.rb : b + (int64_t)(r - na) * g.rb) + lo;
-        copy_span(dst + (r < na ? r * g.pitch : half + (r - na) * g.pitch), src, len, bar);
+      if (lane < kTileRows) copy_span(dst + lane * U::PITCH, src, len, bar);
+    }
+  };
+  // The next stage to fill.
+  struct {
+    bool gu, any;
+    int id, e, row0, span;  // gate/up: tile number, expert, first row, next span
+    int tile, u, a, s;      // down: tile of this CTA, unit, place in the list, stage of the row
+  } nx;
+  auto start_gu = [&](int id) {
+    nx.id = id;
+    nx.e = s_list[id / per_expert];
+    nx.row0 = id % per_expert * 8;
+    nx.span = span0;
+  };
+  auto start_dn = [&]() {
+    nx.u = u0;
+    nx.a = u0 / sd;
+    nx.s = u0 - nx.a * sd;
+  };
+  nx.tile = 0;
+  nx.gu = first_gu < gu_tiles;
+  nx.any = nx.gu || (u0 < u1 && my_tiles > 0);
+  if (nx.gu) start_gu(first_gu);
+  if (u0 < u1) start_dn();
+  int fill_slot = 0, filled = 0;
+  auto fill_next = [&]() {
+    if (!nx.any) return;
+    if (nx.gu) {
+      fill(false, nx.e, nx.row0, nx.span, min(U::NS, span1 - nx.span), fill_slot);
+      nx.span += U::NS;
+      if (nx.span >= span1) {
+        if (nx.id + G * teams < gu_tiles) {
+          start_gu(nx.id + G * teams);
+        } else {
+          nx.gu = false;
+          nx.any = u0 < u1 && my_tiles > 0;
+        }
+      }
+    } else {
+      fill(true, s_list[nx.a], (blockIdx.x + nx.tile * G) * kTileRows, nx.s * U::NS, min(U::NS, spans_i - nx.s * U::NS), fill_slot);
+      if (++nx.s == sd) nx.s = 0, ++nx.a;
+      if (++nx.u == u1) {
+        if (++nx.tile < my_tiles) start_dn();
+        else nx.any = false;
       }
     }
+    if (++fill_slot == p.stages) fill_slot = 0;
+    ++filled;
   };
-  struct Task {
-    int expert, row0, rows, seg, tile;
+  int slot = 0, used = 0;
+  uint32_t parity = 0;
+  bool live = ok;
+  if (ok)
+    for (int i = 0; i < p.stages; ++i) fill_next();
+  auto wait_stage = [&]() {  // warp-uniform: every lane waits on the same barrier
+    const bool landed = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&bars[slot]), parity));
+    if (!landed && lane == 0) atomicOr(p.err, kErrWaitTimeout);
+    return landed;
   };
-  auto task_of = [&](int s) {
-    Task t;
-    if (s < n_stages_gu) {
-      const int id = first_gu + s / gu.segs * (G * kWarps);
-      t.seg = s % gu.segs;
-      t.expert = s_list[id / per_expert];
-      t.row0 = id % per_expert * pairs;
-      t.rows = min(pairs, p.I - t.row0);
-      t.tile = -1;
-    } else {
-      const int q = s - n_stages_gu, task = q / dn.segs;
-      t.seg = q % dn.segs;
-      t.tile = task / per_tile;
-      const int idx = warp + kWarps * (task % per_tile);
-      t.expert = s_list[idx / subs];
-      t.row0 = (blockIdx.x + t.tile * G) * kTileRows + idx % subs * dn.rows;
-      t.rows = dn.rows;  // rows divide a tile, and tiles divide K
-    }
-    return t;
-  };
-  auto issue = [&](int s) {
-    const Task t = task_of(s);
-    const int slot = s % p.stages;
-    uint8_t* dst = ring + (size_t)slot * p.stage_bytes;
-    if (t.tile < 0) {
-      const uint8_t* a = p.Wgu + ((int64_t)t.expert * 2 * p.I + t.row0) * gu.rb;
-      arm_and_copy(dst, a, t.rows, a + (int64_t)p.I * gu.rb, t.rows, gu.half, gu, t.seg, slot);
-    } else {
-      const uint8_t* a = p.Wd + ((int64_t)t.expert * p.K + t.row0) * dn.rb;
-      arm_and_copy(dst, a, t.rows, nullptr, 0, 0, dn, t.seg, slot);
-    }
-  };
-  int issued = 0, s = 0;
-  for (; issued < p.stages && issued < n_stages; ++issued) issue(issued);
-  auto wait_stage = [&](int i) {  // warp-uniform: every lane waits on the same barrier
-    const bool landed = mbar_wait_bounded(smem_addr(&bars[i % p.stages]), (uint32_t)((i / p.stages) & 1));
-    if (__all_sync(0xffffffffu, landed)) return true;
-    if (lane == 0) atomicOr(p.err, kErrWaitTimeout);
-    return false;
+  auto next_slot = [&]() {
+    ++used;
+    if (++slot == p.stages) slot = 0, parity ^= 1u;
   };
   auto release_stage = [&]() {
     __syncwarp();
     fence_proxy_async();  // the stage's reads precede the next copy into it
-    if (issued < n_stages) issue(issued), ++issued;
+    fill_next();
+    next_slot();
   };
-
-  float* acc = s_acc + (size_t)warp * p.acc_floats;
-  bool live = ok;
+  // Token of column n (0 .. 7) of group g of `per` tokens, -1 for none.
+  auto token_of = [&](uint32_t tokens, int skip) {
+    for (int i = 0; i < skip; ++i) tokens &= tokens - 1;
+    return tokens ? __ffs(tokens) - 1 : -1;
+  };
+  float* acc_w = s_acc + (size_t)warp * p.acc_floats;
 
   // ---- gate and up ----
-  {
-    const int c = lane % gu.lanes, g = lane / gu.lanes, groups = 32 / gu.lanes;
-    for (; s < n_stages_gu && live; ++s) {
-      if (!wait_stage(s)) {
+  for (int id = first_gu; id < gu_tiles; id += G * teams) {
+    const int e = s_list[id / per_expert], i0 = id % per_expert * 8;
+    const uint32_t tokens = s_mask[e];
+    const int ng = (__popc(tokens) + 7) / 8;
+    int tok[kGuGroups];
+#pragma unroll
+    for (int g = 0; g < kGuGroups; ++g) tok[g] = g < ng ? token_of(tokens, 8 * g + q) : -1;
+    float acc[kGuGroups][4];
+#pragma unroll
+    for (int g = 0; g < kGuGroups; ++g) acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
+    for (int span = span0; span < span1 && live; span += U::NS) {
+      if (!wait_stage()) {
         live = false;
         break;
       }
-      const Task t = task_of(s);
-      const uint8_t* st = ring + (size_t)(s % p.stages) * p.stage_bytes;
-      const uint8_t* ga = p.Wgu + ((int64_t)t.expert * 2 * p.I + t.row0) * gu.rb;
-      const uint8_t* ua = ga + (int64_t)p.I * gu.rb;
-      const bool whole = gu.segs == 1;
-      const uint8_t* row[RG];
+      const uint8_t* st = ring + (size_t)slot * U::STAGE;
+      const int n = min(U::NS, span1 - span);
+      for (int k = 0; k < n; ++k) {
+        const uint8_t* xs = p.xf + (int64_t)(span + k) * U::X_SPAN + c * 16;
+        auto load = [&](int g, int phi, bool have, uint4 (&b)[4]) {
+          const uint4* src = reinterpret_cast<const uint4*>(xs + (int64_t)tok[g] * spans_k * U::X_SPAN + phi * 256);
 #pragma unroll
-      for (int r = 0; r < RG; ++r) {
-        const int i = r % (RG / 2) * groups + g;  // pair of the task
-        const uint8_t* a = r < RG / 2 ? ga : ua;
-        row[r] = st + (r < RG / 2 ? 0 : gu.half) + i * gu.pitch + mis16(whole ? a : a + (int64_t)i * gu.rb);
-      }
-      const int u0 = t.seg * gu.seg_iters * gu.lanes;
-      // products of one or two tokens at a time
-      auto finish = [&](float gate, float up, int i, int pos, int m) {
-        if (gu.segs > 1) {
-          float* q = acc + 2 * (pos * pairs + i);
-          if (t.seg > 0) gate += q[0], up += q[1];
-          if (t.seg < gu.segs - 1) {
-            q[0] = gate, q[1] = up;
-            return;
-          }
-        }
-        const int j = s_slot[m * p.E + t.expert];
-        p.h[(int64_t)(m * p.top_k + j) * p.I + t.row0 + i] = gate / (1.f + expf(-gate)) * up;
-      };
-      uint32_t tokens = s_mask[t.expert];
-      for (int pos = 0; tokens != 0; pos += 2) {
-        const int m0 = __ffs(tokens) - 1;
-        tokens &= tokens - 1;
-        if (tokens == 0) {
-          const int64_t off[1] = {(int64_t)m0 * p.K};
-          float tot[RG][1];
-          stage_products<V, ALIGNED, RG, 1, ACT>(gu, row, u0, c, p.X, off, tot);
-#pragma unroll
-          for (int r = 0; r < RG / 2; ++r) {
-            const int i = r * groups + g;
-            if (c == 0 && i < t.rows) finish(tot[r][0], tot[r + RG / 2][0], i, pos, m0);
-          }
-        } else {
-          const int m1 = __ffs(tokens) - 1;
-          tokens &= tokens - 1;
-          const int64_t off[2] = {(int64_t)m0 * p.K, (int64_t)m1 * p.K};
-          float tot[RG][2];
-          stage_products<V, ALIGNED, RG, 2, ACT>(gu, row, u0, c, p.X, off, tot);
-#pragma unroll
-          for (int r = 0; r < RG / 2; ++r) {
-            const int i = r * groups + g;
-            if (c == 0 && i < t.rows) {
-              finish(tot[r][0], tot[r + RG / 2][0], i, pos, m0);
-              finish(tot[r][1], tot[r + RG / 2][1], i, pos + 1, m1);
-            }
-          }
-        }
+          for (int kk = 0; kk < 4; ++kk) b[kk] = have && tok[g] >= 0 ? src[kk * 4] : make_uint4(0, 0, 0, 0);
+        };
+        const uint8_t* ra = unit_at(st, q, k, gu_row(e, i0, q) + span * U::SPAN);
+        const uint8_t* rb = unit_at(st, q + 8, k, gu_row(e, i0, q + 8) + span * U::SPAN);
+        span_products<V, ALIGNED, 0, kGuGroups>(ra, rb, (span + k) * U::SPAN_BLOCKS + c * U::BLOCKS, nb_k, ng, load, acc);
       }
       release_stage();
+    }
+    if (KP > 1) {  // the parts' sums, in order
+      if (part > 0) {
+#pragma unroll
+        for (int g = 0; g < kGuGroups; ++g)
+          if (g < ng) *reinterpret_cast<float4*>(acc_w + (g * 32 + lane) * 4) = make_float4(acc[g][0], acc[g][1], acc[g][2], acc[g][3]);
+      }
+      team_barrier(1 + team, KP * 32);
+      if (part == 0) {
+        for (int w = 1; w < KP; ++w) {
+          const float* other = acc_w + (size_t)w * p.acc_floats;
+#pragma unroll
+          for (int g = 0; g < kGuGroups; ++g) {
+            if (g >= ng) break;
+            const float4 v = *reinterpret_cast<const float4*>(other + (g * 32 + lane) * 4);
+            acc[g][0] += v.x, acc[g][1] += v.y, acc[g][2] += v.z, acc[g][3] += v.w;
+          }
+        }
+      }
+      team_barrier(1 + team, KP * 32);
+      if (part > 0) continue;
+    }
+    // Lane (q, c): gate and up of hidden value i0 + q for columns 2 c and 2 c + 1.
+    const int i = i0 + q, in = i / 32 % U::SPAN_BLOCKS, pj = i & 15;
+    const int64_t place = (int64_t)(i / 32 / U::SPAN_BLOCKS) * U::X_SPAN + x_chunk(in % U::BLOCKS, pj >> 2, in / U::BLOCKS) + (pj & 3) * 4 + (i >> 4 & 1) * 2;
+#pragma unroll
+    for (int g = 0; g < kGuGroups; ++g) {
+      if (g >= ng) break;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int m = __shfl_sync(0xffffffffu, tok[g], (2 * c + j) * 4);
+        float h = 0.f;
+        int a = 0;
+        if (m >= 0) {
+          const float un = s_unscale[m], gate = acc[g][j] * un, up = acc[g][2 + j] * un;
+          h = gate / (1.f + expf(-gate)) * up;
+          a = m * p.top_k + s_slot[m * p.E + e];
+          p.h[(int64_t)a * p.I + i] = h;
+          const float hs = h * (float)(1 << kFastExp);
+          const __half hi = __float2half_rn(hs);
+          *reinterpret_cast<__half*>(p.h_hi + (int64_t)a * spans_i * U::X_SPAN + place) = hi;
+          *reinterpret_cast<__half*>(p.h_lo + (int64_t)a * spans_i * U::X_SPAN + place) = __float2half_rn(hs - __half2float(hi));
+        }
+        uint32_t mx = __float_as_uint(h) & 0x7FFFFFFFu;
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        if (q == 0 && m >= 0) atomicMax(p.amax + a, mx);
+      }
     }
   }
   ok = grid_barrier(p.bars + 1) && ok;  // every h is written
   live = live && ok;
 
-  // ---- down: a tile of output rows at a time, the warps over its experts ----
-  if (ok) {
-    const int c = lane % dn.lanes, g = lane / dn.lanes, groups = 32 / dn.lanes;
-    for (int tile = 0; tile < my_tiles; ++tile) {
-      for (int i = lane; i < kTileRows * p.M; i += 32) acc[i] = 0.f;
-      __syncwarp();
-      for (int q = 0; q < per_tile * dn.segs && live; ++q, ++s) {
-        if (!wait_stage(s)) {
+  // ---- down: a tile of output rows at a time, its experts' stages shared by the warps ----
+  for (int tile = 0; tile < my_tiles && ok; ++tile) {
+    const int n0 = (blockIdx.x + tile * G) * kTileRows;
+    for (int i = lane; i < kTileRows * p.M; i += 32) acc_w[i] = 0.f;
+    __syncwarp();
+    for (int u = u0; u < u1 && live;) {
+      const int at = u / sd, end = min(u1, (at + 1) * sd);  // stages [u, end) of one expert
+      const int e = s_list[at];
+      const uint32_t tokens = s_mask[e];
+      const int ng = (__popc(tokens) + 3) / 4;
+      // column n < 4: the high part of token n of the group; n >= 4: the remainder of token n - 4
+      int tok[kDnGroups];
+      bool fast = true;
+#pragma unroll
+      for (int g = 0; g < kDnGroups; ++g) {
+        tok[g] = g < ng ? token_of(tokens, 4 * g + (q & 3)) : -1;
+        if (tok[g] >= 0) fast = fast && fast_range(__ldcg(p.amax + tok[g] * p.top_k + s_slot[tok[g] * p.E + e]));
+      }
+      fast = __all_sync(0xffffffffu, fast);
+      float acc[kDnGroups][4];
+#pragma unroll
+      for (int g = 0; g < kDnGroups; ++g) acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
+      for (; u < end; ++u) {
+        if (!wait_stage()) {
           live = false;
           break;
         }
-        const Task t = task_of(s);
-        const uint8_t* st = ring + (size_t)(s % p.stages) * p.stage_bytes;
-        const uint8_t* da = p.Wd + ((int64_t)t.expert * p.K + t.row0) * dn.rb;
-        const int in_tile = t.row0 - (blockIdx.x + tile * G) * kTileRows;
-        const uint8_t* row[RD];
+        const uint8_t* st = ring + (size_t)slot * U::STAGE;
+        const int span = (u - at * sd) * U::NS, n = min(U::NS, spans_i - span);
+        for (int k = 0; k < n; ++k) {
+          const int blk = (span + k) * U::SPAN_BLOCKS + c * U::BLOCKS;
+          const uint8_t* hs = (q < 4 ? p.h_hi : p.h_lo) + (int64_t)(span + k) * U::X_SPAN + c * 16;
+          auto load = [&](int g, int phi, bool have, uint4 (&b)[4]) {
+            const int m = tok[g];
+            if (!have || m < 0) {
 #pragma unroll
-        for (int r = 0; r < RD; ++r) {
-          const int i = r * groups + g;
-          row[r] = st + i * dn.pitch + mis16(dn.segs == 1 ? da : da + (int64_t)i * dn.rb);
-        }
-        const int u0 = t.seg * dn.seg_iters * dn.lanes;
-        uint32_t tokens = s_mask[t.expert];
-        while (tokens != 0) {
-          const int m0 = __ffs(tokens) - 1;
-          tokens &= tokens - 1;
-          const int a0 = m0 * p.top_k + s_slot[m0 * p.E + t.expert];
-          if (tokens == 0) {
-            const int64_t off[1] = {(int64_t)a0 * p.I};
-            float tot[RD][1];
-            stage_products<V, ALIGNED, RD, 1, 2>(dn, row, u0, c, p.h, off, tot);
-#pragma unroll
-            for (int r = 0; r < RD; ++r) {
-              const int i = r * groups + g;
-              if (c == 0 && i < t.rows) acc[(in_tile + i) * p.M + m0] += s_probs[a0] * tot[r][0];
+              for (int kk = 0; kk < 4; ++kk) b[kk] = make_uint4(0, 0, 0, 0);
+              return;
             }
-          } else {
-            const int m1 = __ffs(tokens) - 1;
-            tokens &= tokens - 1;
-            const int a1 = m1 * p.top_k + s_slot[m1 * p.E + t.expert];
-            const int64_t off[2] = {(int64_t)a0 * p.I, (int64_t)a1 * p.I};
-            float tot[RD][2];
-            stage_products<V, ALIGNED, RD, 2, 2>(dn, row, u0, c, p.h, off, tot);
+            const int a = m * p.top_k + s_slot[m * p.E + e];
+            if (fast) {
+              const uint4* src = reinterpret_cast<const uint4*>(hs + (int64_t)a * spans_i * U::X_SPAN + phi * 256);
 #pragma unroll
-            for (int r = 0; r < RD; ++r) {
-              const int i = r * groups + g;
-              if (c == 0 && i < t.rows) {
-                acc[(in_tile + i) * p.M + m0] += s_probs[a0] * tot[r][0];
-                acc[(in_tile + i) * p.M + m1] += s_probs[a1] * tot[r][1];
+              for (int kk = 0; kk < 4; ++kk) b[kk] = src[kk * 4];
+            } else {
+              const float scale = exp2i(scale_exp(__ldcg(p.amax + a)));
+              const float4* src = reinterpret_cast<const float4*>(p.h + (int64_t)a * p.I + (blk + phi) * 32);
+              auto pair = [&](float x, float y) {
+                x *= scale, y *= scale;
+                const uint32_t hi = pack_half2(x, y);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                return q < 4 ? hi : pack_half2(x - f.x, y - f.y);
+              };
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                const float4 x = src[kk], y = src[4 + kk];
+                b[kk] = make_uint4(pair(x.x, y.x), pair(x.y, y.y), pair(x.z, y.z), pair(x.w, y.w));
               }
             }
-          }
+          };
+          const uint8_t* ra = unit_at(st, q, k, dn_row(e, n0, q) + span * U::SPAN);
+          const uint8_t* rb = unit_at(st, q + 8, k, dn_row(e, n0, q + 8) + span * U::SPAN);
+          span_products<V, ALIGNED, 0, kDnGroups>(ra, rb, blk, nb_i, ng, load, acc);
         }
         release_stage();
       }
-      __syncthreads();
-      const int n0 = (blockIdx.x + tile * G) * kTileRows;
-      for (int i = tid; i < kTileRows * p.M; i += kThreads) {
-        const int m = i / kTileRows, r = i % kTileRows;
-        float y = 0.f;
-        for (int w = 0; w < kWarps; ++w) y += s_acc[(size_t)w * p.acc_floats + r * p.M + m];
-        p.Y[(int64_t)m * p.K + n0 + r] = y;
+      // columns 2 c, 2 c + 1 (c < 2) with their remainders, of rows q and q + 8
+#pragma unroll
+      for (int g = 0; g < kDnGroups; ++g) {
+        if (g >= ng) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[g][i] += __shfl_xor_sync(0xffffffffu, acc[g][i], 2);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int m = __shfl_sync(0xffffffffu, tok[g], ((2 * c + j) & 3) * 4);
+          if (c < 2 && m >= 0) {
+            const int a = m * p.top_k + s_slot[m * p.E + e];
+            const float w = s_probs[a] * exp2i(fast ? -kFastExp : -scale_exp(__ldcg(p.amax + a)));
+            acc_w[q * p.M + m] += w * acc[g][j];
+            acc_w[(q + 8) * p.M + m] += w * acc[g][2 + j];
+          }
+        }
       }
-      __syncthreads();
     }
+    __syncthreads();
+    for (int i = tid; i < kTileRows * p.M; i += kThreads) {
+      const int m = i / kTileRows, r = i % kTileRows;
+      float y = 0.f;
+      for (int w = 0; w < kWarps; ++w) y += s_acc[(size_t)w * p.acc_floats + r * p.M + m];
+      p.Y[(int64_t)m * p.K + n0 + r] = y;
+    }
+    __syncthreads();
   }
   // copies that no one waited for (after a wait gave up) land before the CTA leaves
-  for (; s < issued; ++s) (void)mbar_wait_bounded(smem_addr(&bars[s % p.stages]), (uint32_t)((s / p.stages) & 1));
+  for (; used < filled; next_slot()) (void)mbar_wait_bounded(smem_addr(&bars[slot]), parity);
   __syncthreads();
   if (tid == 0 && atomic_add_acq_rel_gpu(p.bars + 2, 1u) == (uint32_t)G - 1u) {
     store_relaxed_gpu(p.bars, 0u);
@@ -693,49 +766,88 @@ MoeFn pick(int act, bool aligned) {
   return aligned ? moe_kernel<V, 1, true> : moe_kernel<V, 1, false>;
 }
 
-constexpr int kSmemMax = 227 * 1024 - 2048;  // dynamic; the rest is the kernel's static shared memory
-constexpr int kStageTarget = 6144;           // a stage holds whole rows where they fit into this
-constexpr int kStageSlack = 32;              // word reads past a row's end
+constexpr int kSmemMax = 227 * 1024 - 2560;  // dynamic; the rest is the kernel's static shared memory
+constexpr int kSlack = 32;                   // word reads past the last row slot
 
 int up16(int v) { return (v + 15) / 16 * 16; }
 
-// Rows of K weights over R rows a lane; `both`: gate and up rows in two regions.
-RowGeom geometry(int variant, int64_t K, int R, bool both, int* stage_bytes) {
-  RowGeom g{};
-  const int ub = variant == 0 ? Unit<0>::BYTES : Unit<1>::BYTES, per = variant == 0 ? Unit<0>::BLOCKS : Unit<1>::BLOCKS;
-  g.nb = (int)(K / 32);
-  g.rb = g.nb * (variant == 0 ? 18 : 17);
-  const int units = (g.nb + per - 1) / per;
-  // Lanes to a row: as few idle as possible, the most lanes among equals
-  // (rows then lie in fewer places of the shared-memory banks).
-  int best = 1 << 30;
-  for (int L = 32; L >= 4; L /= 2) {
-    const int padded = (units + L - 1) / L * L;
-    if (padded < best) best = padded, g.lanes = L;
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+template <int V>
+cudaError_t set_up(const MoeArgs& a, int sms, MoeParams* p, int* smem) {
+  using U = Unit<V>;
+  int at = up16(p->M * p->top_k * 4);
+  p->off_mask = at;
+  at += up16(p->E * 4);
+  p->off_list = at;
+  at += up16(p->E * 2);
+  p->off_slot = at;
+  at += up16(p->M * p->E);
+  p->off_unscale = at;
+  at += up16(p->M * 4);
+  p->off_acc = at;
+  const int groups = (p->M + 7) / 8;
+  p->acc_floats = kTileRows * p->M > groups * 128 ? kTileRows * p->M : groups * 128;
+  at += kWarps * p->acc_floats * 4;
+  p->off_ring = (at + 127) / 128 * 128;
+  const int room = (kSmemMax - p->off_ring - kSlack) / (kWarps * U::STAGE);
+  p->stages = room < kMaxStages ? room : kMaxStages;
+  if (p->stages < 1) return cudaErrorInvalidConfiguration;
+  *smem = p->off_ring + kWarps * p->stages * U::STAGE + kSlack;
+  // Warps to a gate/up tile: one where every SM has tiles for its warps, more
+  // where the (at most min(E, M top_k)) chosen experts give it fewer.
+  const int64_t spans_k = (a.K / 32 + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS, spans_i = (a.I / 32 + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS;
+  const int64_t experts = a.M * a.top_k < a.E ? a.M * a.top_k : a.E;
+  p->parts = 1;
+  while (p->parts < 8 && 2 * p->parts <= spans_k && experts * (a.I / 8) * p->parts < 8 * (int64_t)sms) p->parts *= 2;
+  // Workspace: logits, activation scales, largest |h|, then 16-byte aligned arrays.
+  const int64_t choices = a.M * a.top_k;
+  float* w = a.ws;
+  p->logits = w;
+  w += kMoeMaxTokens * kMoeMaxExperts;
+  p->x_unscale = w;
+  w += kMoeMaxTokens;
+  p->amax = reinterpret_cast<uint32_t*>(w);
+  w += kMoeMaxTokens * kMoeMaxTop;
+  p->h = w;
+  w += choices * a.I;
+  p->xf = reinterpret_cast<uint8_t*>(w);
+  p->h_hi = p->xf + a.M * spans_k * U::X_SPAN;
+  p->h_lo = p->h_hi + choices * spans_i * U::X_SPAN;
+  return cudaSuccess;
+}
+
+template <int V>
+cudaError_t encode_maps(const MoeArgs& a, MoeParams* p) {
+  using U = Unit<V>;
+  const cuuint64_t rb_k = a.K / 32 * Fmt<V>::BB, rb_i = a.I / 32 * Fmt<V>::BB;
+  const cuuint32_t one[3] = {1, 1, 1};
+  {
+    const cuuint64_t dims[3] = {rb_k / 4, (cuuint64_t)a.I, 2 * (cuuint64_t)a.E}, strides[2] = {rb_k, rb_k * a.I};
+    const cuuint32_t box[3] = {U::SPAN / 4, 8, 2};
+    if (g_encode(&p->map_gu, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(a.Wgu), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                 CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
   }
-  g.iters = (units + g.lanes - 1) / g.lanes;
-  g.rows = 32 / g.lanes * R;
-  const int parts = both ? 2 : 1, n = g.rows / parts;
-  g.pitch = g.rb;
-  g.half = up16(n * g.rb) + 16 + kStageSlack;
-  g.seg_iters = g.iters;
-  g.segs = 1;
-  if (parts * g.half > kStageTarget && g.iters > 1) {  // not whole rows: slots of up to seg_iters units a lane
-    const int fit = (kStageTarget / g.rows - 16 - kStageSlack) / (g.lanes * ub);
-    g.segs = (g.iters + (fit > 1 ? fit : 1) - 1) / (fit > 1 ? fit : 1);
-    g.seg_iters = (g.iters + g.segs - 1) / g.segs;
-    g.segs = (g.iters + g.seg_iters - 1) / g.seg_iters;
-    g.pitch = up16(g.seg_iters * g.lanes * ub) + 16 + kStageSlack;
-    g.half = n * g.pitch;
-  }
-  if (g.segs == 1) g.pitch = g.rb, g.half = up16(n * g.rb) + 16 + kStageSlack;
-  *stage_bytes = parts * g.half;
-  return g;
+  const cuuint64_t dims[2] = {rb_i / 4, (cuuint64_t)(a.E * a.K)}, strides[1] = {rb_i};
+  const cuuint32_t box[2] = {U::SPAN / 4, kTileRows};
+  if (g_encode(&p->map_dn, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(a.Wd), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  return cudaSuccess;
 }
 
 }  // namespace
 
 cudaError_t moe_prepare() {
+  if (!g_encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+    if (e != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorSymbolNotFound;
+    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
   for (int v = 0; v < 2; ++v)
     for (int act = 0; act < 2; ++act)
       for (int al = 0; al < 2; ++al) {
@@ -755,8 +867,6 @@ cudaError_t launch_moe(int variant, int act, const MoeArgs& a, int sms, cudaStre
   p.Y = a.Y;
   p.ids = a.ids;
   p.probs = a.probs;
-  p.logits = a.ws;
-  p.h = a.ws + kMoeMaxTokens * kMoeMaxExperts;
   p.bars = a.bars;
   p.err = a.err;
   p.M = (int)a.M;
@@ -767,27 +877,12 @@ cudaError_t launch_moe(int variant, int act, const MoeArgs& a, int sms, cudaStre
   p.router_type = a.router_type;
   p.route = a.route;
   p.route_scale = a.route_scale;
-  int gu_bytes = 0, dn_bytes = 0;
-  p.gu = geometry(variant, a.K, variant == 0 ? Unit<0>::R_GU : Unit<1>::R_GU, true, &gu_bytes);
-  p.dn = geometry(variant, a.I, variant == 0 ? Unit<0>::R_DN : Unit<1>::R_DN, false, &dn_bytes);
-  p.stage_bytes = (gu_bytes > dn_bytes ? gu_bytes : dn_bytes) / 128 * 128 + 128;
-  int at = up16(p.M * p.top_k * 4);
-  p.off_mask = at;
-  at += up16(p.E * 4);
-  p.off_list = at;
-  at += up16(p.E * 2);
-  p.off_slot = at;
-  at += up16(p.M * p.E);
-  p.off_acc = at;
-  p.acc_floats = kTileRows * p.M;
-  if (p.gu.segs > 1 && p.gu.rows * p.M > p.acc_floats) p.acc_floats = p.gu.rows * p.M;
-  at += kWarps * p.acc_floats * 4;
-  p.off_ring = (at + 127) / 128 * 128;
-  const int room = (kSmemMax - p.off_ring - kStageSlack) / (kWarps * p.stage_bytes);
-  p.stages = room < kMaxStages ? room : kMaxStages;
-  if (p.stages < 1) return cudaErrorInvalidConfiguration;
-  const int smem = p.off_ring + kWarps * p.stages * p.stage_bytes + kStageSlack;
-  const bool aligned = p.gu.rb % 4 == 0 && p.dn.rb % 4 == 0;
+  int smem = 0;
+  cudaError_t e = variant == 0 ? set_up<0>(a, sms, &p, &smem) : set_up<1>(a, sms, &p, &smem);
+  if (e != cudaSuccess) return e;
+  const int ku = variant == 0 ? Fmt<0>::KU : Fmt<1>::KU;
+  const bool aligned = a.K % ku == 0 && a.I % ku == 0 && a.E * a.K < (int64_t(1) << 31);
+  if (aligned && (e = variant == 0 ? encode_maps<0>(a, &p) : encode_maps<1>(a, &p)) != cudaSuccess) return e;
   const MoeFn fn = variant == 0 ? pick<0>(act, aligned) : pick<1>(act, aligned);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)sms);
