@@ -127,10 +127,11 @@ cudaError_t launch_logprobs(const LogprobsArgs& a, int sms, cudaStream_t s);
 constexpr int kMoeMaxTokens = 32, kMoeMaxExperts = 512, kMoeMaxTop = 16, kMoeMaxWidth = 32768;
 constexpr int64_t kMoeMaxHidden = int64_t(1) << 22;
 // router logits, activation scales, largest hidden values, hidden values in
-// fp32 and as two fp16 parts (rows padded to 512), activations (likewise)
+// fp32 and as two fp16 parts (rows padded to 512), activations (likewise),
+// room for a read past the last
 constexpr size_t kMoeWsFloats = (size_t)kMoeMaxTokens * (kMoeMaxExperts + 1 + kMoeMaxTop) + 2 * kMoeMaxHidden +
-                                (size_t)kMoeMaxTokens * kMoeMaxTop * 512 + (size_t)kMoeMaxTokens * (kMoeMaxWidth + 512) / 2;
-constexpr int kMoeBarWords = 3;
+                                (size_t)kMoeMaxTokens * kMoeMaxTop * 512 + (size_t)kMoeMaxTokens * (kMoeMaxWidth + 512) / 2 + 256;
+constexpr int kMoeBarWords = 4;
 struct MoeArgs {
   const uint16_t* X;   // M x K
   const void* router;  // E x K

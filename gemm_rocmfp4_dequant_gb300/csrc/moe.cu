@@ -31,8 +31,9 @@
 // 2^-28 of the largest stay exact, smaller ones are off by at most 2^-39 of
 // it.  h is fp32; the down product takes it as two fp16 columns, high and
 // remainder, 22 bits together.  The pair is made where h is, times 16, if the
-// choice's largest |h| proves to be in [2^-5, 2^11); outside that range the
-// reader makes it from the fp32 h, scaled like a bf16 token.
+// choice's largest |h| proves to be in [2^-5, 2^11); a choice outside that
+// range has its pairs made again from the fp32 h, scaled like a bf16 token,
+// behind a third barrier that other calls do not meet.
 //
 // Bound: memory (3 I K / 32 blocks per chosen expert), with the decode's issue
 // slots (about 3.7 instructions per pair of weights) close behind.
@@ -43,6 +44,8 @@
 // after it (which stays inside the matrices, as their sizes are multiples of
 // 16), and are shifted into place word by word.
 #include <cudaTypedefs.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -89,7 +92,7 @@ struct MoeParams {
   float* h;            // workspace [M * top_k][I]
   uint8_t* h_hi;       // workspace: h * 16 in fragment order, fp16 and its remainder
   uint8_t* h_lo;
-  uint32_t* bars;      // workspace: two barrier counters and one of finished CTAs, zero between launches
+  uint32_t* bars;      // workspace: three barrier counters and one of finished CTAs, zero between launches
   uint32_t* err;
   int M, E, top_k, K, I;
   int router_type, route;
@@ -97,7 +100,8 @@ struct MoeParams {
   int parts;           // KP: warps that share a gate/up tile
   int stages;          // ring stages of a warp
   // offsets in shared memory
-  int off_mask, off_list, off_slot, off_unscale, off_acc, off_ring;
+  int off_mask, off_list, off_slot, off_unscale, off_keys, off_x, off_acc, off_ring;
+  int x_pitch;         // bytes between tokens of the activations in shared memory, 0: they stay in the workspace
   int acc_floats;      // per warp
 };
 
@@ -191,23 +195,50 @@ RF4_DEV void block_mma(const uint32_t (&a0)[16], const uint32_t (&a1)[16], const
   for (int i = 0; i < 4; ++i) acc[i] += d[i];
 }
 
-// One span of a tile: `ra`, `rb` are rows q and q + 8 at the lane's unit,
-// `load` gives the activations of a group's column.  have(PHI): the block is
-// inside the row.
-template <int V, bool ALIGNED, int PHI, int GROUPS, class Load>
-RF4_DEV void span_products(const uint8_t* ra, const uint8_t* rb, int blk, int nb, int ng, Load&& load, float (&acc)[GROUPS][4]) {
+RF4_DEV void load_b(const uint8_t* p, uint4 (&b)[4]) {
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) b[kk] = *reinterpret_cast<const uint4*>(p + kk * 64);
+}
+
+// Activations of the lane's column, one pointer per group of tokens, moving on
+// through the row 256 bytes a block.  One group (most experts of a few tokens):
+// the next block's are loaded while this one's weights are decoded.  Columns
+// beyond the expert's tokens repeat its first; their sums are not used.
+template <int GROUPS>
+struct Columns {
+  const uint8_t* p[GROUPS];
+  uint4 b[4];
+  RF4_DEV void start() {
+    if constexpr (GROUPS == 1) load_b(p[0], b);
+  }
+};
+
+// One span of a tile: `ra`, `rb` are rows q and q + 8 at the lane's unit, blk
+// the unit's first block.
+template <int V, bool ALIGNED, int PHI, int GROUPS>
+RF4_DEV void span_products(const uint8_t* ra, const uint8_t* rb, int blk, int nb, int ng, Columns<GROUPS>& col, float (&acc)[GROUPS][4]) {
   const bool have = ALIGNED || blk + PHI < nb;
+  uint4 next[4];
+  if constexpr (GROUPS == 1) load_b(col.p[0] + 256, next);  // reads past the row's last block stay in the workspace
   uint32_t a0[16], a1[16];
   decode_block<V, ALIGNED, PHI>(ra, have, a0);
   decode_block<V, ALIGNED, PHI>(rb, have, a1);
+  if constexpr (GROUPS == 1) {
+    block_mma(a0, a1, col.b, acc[0]);
 #pragma unroll
-  for (int g = 0; g < GROUPS; ++g) {
-    if (g >= ng) break;
-    uint4 b[4];
-    load(g, PHI, have, b);
-    block_mma(a0, a1, b, acc[g]);
+    for (int kk = 0; kk < 4; ++kk) col.b[kk] = next[kk];
+    col.p[0] += 256;
+  } else {
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      if (g < ng) {
+        load_b(col.p[g], next);
+        block_mma(a0, a1, next, acc[g]);
+        col.p[g] += 256;
+      }
+    }
   }
-  if constexpr (PHI + 1 < Unit<V>::BLOCKS) span_products<V, ALIGNED, PHI + 1, GROUPS>(ra, rb, blk, nb, ng, load, acc);
+  if constexpr (PHI + 1 < Unit<V>::BLOCKS) span_products<V, ALIGNED, PHI + 1, GROUPS>(ra, rb, blk, nb, ng, col, acc);
 }
 
 // The bytes [a, a + n) as a copy from 16-byte boundary to 16-byte boundary.
@@ -261,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   uint16_t* s_list = reinterpret_cast<uint16_t*>(smem + p.off_list);         // chosen experts, ascending
   uint8_t* s_slot = smem + p.off_slot;                                       // [M][E]: which choice of the token
   float* s_unscale = reinterpret_cast<float*>(smem + p.off_unscale);         // [M]: 1 / the activations' scale
+  uint32_t* s_keys = reinterpret_cast<uint32_t*>(smem + p.off_keys);         // [kWarps][E]: order of a token's logits
   float* s_acc = reinterpret_cast<float*>(smem + p.off_acc);                 // [kWarps][acc_floats]
   __shared__ uint64_t s_bars[kWarps * kMaxStages];
   __shared__ float s_red[kWarps][kRouterTokens];
@@ -269,8 +301,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 
   uint64_t* bars = s_bars + warp * kMaxStages;
   if (lane == 0) {
-    for (int i = 0; i < kMaxStages; ++i) mbar_init(smem_addr(&bars[i]), 1);
+    for (int i = 0; i < p.stages; ++i) mbar_init(smem_addr(&bars[i]), 1);
     fence_mbar_init();
+  }
+  if (ALIGNED && tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.map_gu)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.map_dn)) : "memory");
   }
   if (tid == 0) s_ok = 1;
   for (int e = tid; e < p.E; e += kThreads) s_mask[e] = 0;
@@ -278,7 +314,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 
   // Every CTA arrives and waits (bounded) for the others; false if one gave up.
   auto grid_barrier = [&](uint32_t* counter) {
-    __threadfence();
     __syncthreads();
     if (tid == 0) {
       atomic_add_acq_rel_gpu(counter, 1u);
@@ -355,10 +390,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     } else if (tid == 0) {
       p.x_unscale[m] = 1.f;
     }
-    for (int i = tid; i < nb_k * 4; i += kThreads) {
+    for (int i = tid; i < spans_k * U::SPAN_BLOCKS * 4; i += kThreads) {
       const int blk = i >> 2, kk = i & 3, in = blk % U::SPAN_BLOCKS;
-      const uint2 a = *reinterpret_cast<const uint2*>(x + blk * 32 + 4 * kk);
-      const uint2 b = *reinterpret_cast<const uint2*>(x + blk * 32 + 16 + 4 * kk);
+      uint2 a = make_uint2(0, 0), b = a;  // zeros past the row
+      if (blk < nb_k) {
+        a = *reinterpret_cast<const uint2*>(x + blk * 32 + 4 * kk);
+        b = *reinterpret_cast<const uint2*>(x + blk * 32 + 16 + 4 * kk);
+      }
       uint4 v;
       if constexpr (ACT == 0) {
         v = make_uint4(__byte_perm(a.x, b.x, 0x5410), __byte_perm(a.x, b.x, 0x7632), __byte_perm(a.y, b.y, 0x5410), __byte_perm(a.y, b.y, 0x7632));
@@ -372,42 +410,52 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       *reinterpret_cast<uint4*>(dst) = v;
     }
   }
-  if (blockIdx.x == 0)
-    for (int i = tid; i < p.M * p.top_k; i += kThreads) p.amax[i] = 0u;
+  const int choices = p.M * p.top_k;
+  if (blockIdx.x == 0 && tid < choices) p.amax[tid] = 0u;
+  const int nb_i = p.I / 32, spans_i = (nb_i + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS;
+  const int64_t h_row = (int64_t)spans_i * U::X_SPAN;  // bytes of a choice's h parts
+  // Place of hidden value i in its row of h parts.
+  auto h_place = [&](int i) {
+    const int in = i / 32 % U::SPAN_BLOCKS, pj = i & 15;
+    return (int64_t)(i / 32 / U::SPAN_BLOCKS) * U::X_SPAN + x_chunk(in % U::BLOCKS, pj >> 2, in / U::BLOCKS) + (pj & 3) * 4 + (i >> 4 & 1) * 2;
+  };
+  if constexpr (!ALIGNED) {  // zeros past the rows of h
+    for (int a = blockIdx.x; a < choices; a += G)
+      for (int i = p.I + tid; i < spans_i * U::SPAN_BLOCKS * 32; i += kThreads) {
+        *reinterpret_cast<uint16_t*>(p.h_hi + a * h_row + h_place(i)) = 0;
+        *reinterpret_cast<uint16_t*>(p.h_lo + a * h_row + h_place(i)) = 0;
+      }
+  }
   bool ok = grid_barrier(p.bars);
 
   // ---- top k of every token (one warp per token), repeated by every CTA ----
   if (ok) {
+    uint32_t* keys = s_keys + warp * p.E;  // a lane reads only what it wrote: entries lane, lane + 32, ...
     for (int m = warp; m < p.M; m += kWarps) {
-      constexpr int PL = 16;  // experts per lane: E <= 512
-      uint32_t key[PL];
-      float val[PL];
-#pragma unroll
-      for (int i = 0; i < PL; ++i) {
-        const int e = i * 32 + lane;
-        val[i] = e < p.E ? __ldcg(p.logits + (int64_t)m * p.E + e) : 0.f;
-        key[i] = e < p.E ? logit_key(val[i]) : 0u;
+      const float* logits = p.logits + (int64_t)m * p.E;
+      uint32_t best = 0, next = 0;  // the lane's largest remaining key and its expert
+      for (int e = lane; e < p.E; e += 32) {
+        const uint32_t k = logit_key(__ldcg(logits + e));
+        keys[e] = k;
+        if (k > best) best = k, next = e;
       }
-      float top = 0.f, mine = 0.f, denom = 0.f;
       int my_id = 0;
       for (int j = 0; j < p.top_k; ++j) {
-        uint32_t best = 0;
-        int at = 0;
-        float bv = 0.f;
-#pragma unroll
-        for (int i = 0; i < PL; ++i)
-          if (key[i] > best) best = key[i], at = i, bv = val[i];
         const uint32_t mx = __reduce_max_sync(0xffffffffu, best);
-        const uint32_t e = __reduce_min_sync(0xffffffffu, best == mx ? (uint32_t)(at * 32 + lane) : 0xFFFFu);
-        const float l = __shfl_sync(0xffffffffu, bv, e & 31);
+        const uint32_t e = __reduce_min_sync(0xffffffffu, best == mx ? next : 0xFFFFu);
+        if (lane == j) my_id = (int)e;
         if ((int)(e & 31) == lane) {
-#pragma unroll
-          for (int i = 0; i < PL; ++i)
-            if (i == (int)(e >> 5)) key[i] = 0u;
+          keys[e] = 0;
+          best = 0;
+          for (int i = lane; i < p.E; i += 32) {
+            const uint32_t k = keys[i];
+            if (k > best) best = k, next = i;
+          }
         }
-        if (j == 0) top = l;
-        if (lane == j) my_id = (int)e, mine = l;
       }
+      const float mine = __ldcg(logits + my_id);
+      const float top = __shfl_sync(0xffffffffu, mine, 0);
+      float denom = 0.f;
       float num = 0.f;
       if (p.route == 2) {
         num = lane < p.top_k ? 1.f / (1.f + expf(-mine)) : 0.f;
@@ -417,9 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         if (p.route == 1) {
           denom = num;
         } else {
-#pragma unroll
-          for (int i = 0; i < PL; ++i)
-            if (i * 32 + lane < p.E) denom += expf(val[i] - top);
+          for (int e = lane; e < p.E; e += 32) denom += expf(__ldcg(logits + e) - top);
         }
       }
 #pragma unroll
@@ -437,6 +483,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     }
   }
   if (ok && tid < p.M) s_unscale[tid] = __ldcg(p.x_unscale + tid);
+  if (ok && p.x_pitch != 0) {
+    const int per = spans_k * U::X_SPAN / 16;  // 16-byte chunks of a token
+    for (int i = tid; i < p.M * per; i += kThreads)
+      *reinterpret_cast<uint4*>(smem + p.off_x + i / per * p.x_pitch + i % per * 16) = __ldcg(reinterpret_cast<const uint4*>(p.xf) + i);
+  }
   __syncthreads();
   if (warp == 0) {
     int n = 0;
@@ -452,7 +503,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   const int A = ok ? s_active : 0;
 
   // ---- this warp's stages: gate/up tiles, then down tiles --------------------------------
-  const int nb_i = p.I / 32, spans_i = (nb_i + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS;
   const int rb_k = nb_k * Fmt<V>::BB, rb_i = nb_i * Fmt<V>::BB;
   const int KP = p.parts, team = warp / KP, part = warp % KP, teams = kWarps / KP;
   const int span0 = spans_k * part / KP, span1 = spans_k * (part + 1) / KP;  // this warp's spans of a gate/up tile
@@ -465,12 +515,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   const int u0 = warp * (A * sd) / kWarps, u1 = (warp + 1) * (A * sd) / kWarps;  // this warp's share of a down tile's stages
   uint8_t* ring = smem + p.off_ring + (size_t)warp * p.stages * U::STAGE;
 
-  // Lane's rows q and q + 8 of a stage, at its unit of span `sp` of the stage.
-  // Unaligned rows start at their own place within 16 bytes.
+  // Row r of a stage at the lane's unit of the stage's first span; further
+  // spans lie SPAN_STEP on.  Unaligned rows start at their own place within 16 bytes.
   const int q = lane >> 2, c = lane & 3;
-  auto unit_at = [&](const uint8_t* stage, int r, int sp, const uint8_t* src) {
-    if constexpr (ALIGNED) return stage + sp * (kTileRows * U::SPAN) + r * U::SPAN + c * U::BYTES;
-    else return stage + r * U::PITCH + mis16(src) + sp * U::SPAN + c * U::BYTES;
+  constexpr int SPAN_STEP = ALIGNED ? kTileRows * U::SPAN : U::SPAN;
+  auto unit_at = [&](const uint8_t* stage, int r, const uint8_t* src) {
+    if constexpr (ALIGNED) return stage + r * U::SPAN + c * U::BYTES;
+    else return stage + r * U::PITCH + mis16(src) + c * U::BYTES;
   };
   auto gu_row = [&](int e, int i0, int r) { return p.Wgu + ((int64_t)e * 2 * p.I + (r < 8 ? 0 : p.I) + i0 + (r & 7)) * rb_k; };
   auto dn_row = [&](int e, int n0, int r) { return p.Wd + ((int64_t)e * p.K + n0 + r) * rb_i; };
@@ -564,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     fill_next();
     next_slot();
   };
-  // Token of column n (0 .. 7) of group g of `per` tokens, -1 for none.
+  // The token after `skip` others of a set, -1 for none.
   auto token_of = [&](uint32_t tokens, int skip) {
     for (int i = 0; i < skip; ++i) tokens &= tokens - 1;
     return tokens ? __ffs(tokens) - 1 : -1;
@@ -572,40 +623,38 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   float* acc_w = s_acc + (size_t)warp * p.acc_floats;
 
   // ---- gate and up ----
-  for (int id = first_gu; id < gu_tiles; id += G * teams) {
-    const int e = s_list[id / per_expert], i0 = id % per_expert * 8;
-    const uint32_t tokens = s_mask[e];
-    const int ng = (__popc(tokens) + 7) / 8;
-    int tok[kGuGroups];
+  const uint8_t* x_base = p.x_pitch != 0 ? smem + p.off_x : p.xf;
+  const int64_t x_row = p.x_pitch != 0 ? p.x_pitch : spans_k * U::X_SPAN;
+  auto gu_tile = [&](auto groups, int e, int i0, uint32_t tokens) {
+    constexpr int GROUPS = decltype(groups)::value;
+    const int ng = GROUPS == 1 ? 1 : (__popc(tokens) + 7) / 8;
+    int tok[GROUPS];
+    float acc[GROUPS][4];
+    Columns<GROUPS> col;
 #pragma unroll
-    for (int g = 0; g < kGuGroups; ++g) tok[g] = g < ng ? token_of(tokens, 8 * g + q) : -1;
-    float acc[kGuGroups][4];
-#pragma unroll
-    for (int g = 0; g < kGuGroups; ++g) acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
+    for (int g = 0; g < GROUPS; ++g) {
+      tok[g] = g < ng ? token_of(tokens, 8 * g + q) : -1;
+      col.p[g] = x_base + (tok[g] >= 0 ? tok[g] : __ffs(tokens) - 1) * x_row + span0 * U::X_SPAN + c * 16;
+      acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
+    }
+    col.start();
     for (int span = span0; span < span1 && live; span += U::NS) {
       if (!wait_stage()) {
         live = false;
         break;
       }
       const uint8_t* st = ring + (size_t)slot * U::STAGE;
+      const uint8_t* ra = unit_at(st, q, gu_row(e, i0, q) + span * U::SPAN);
+      const uint8_t* rb = unit_at(st, q + 8, gu_row(e, i0, q + 8) + span * U::SPAN);
       const int n = min(U::NS, span1 - span);
-      for (int k = 0; k < n; ++k) {
-        const uint8_t* xs = p.xf + (int64_t)(span + k) * U::X_SPAN + c * 16;
-        auto load = [&](int g, int phi, bool have, uint4 (&b)[4]) {
-          const uint4* src = reinterpret_cast<const uint4*>(xs + (int64_t)tok[g] * spans_k * U::X_SPAN + phi * 256);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) b[kk] = have && tok[g] >= 0 ? src[kk * 4] : make_uint4(0, 0, 0, 0);
-        };
-        const uint8_t* ra = unit_at(st, q, k, gu_row(e, i0, q) + span * U::SPAN);
-        const uint8_t* rb = unit_at(st, q + 8, k, gu_row(e, i0, q + 8) + span * U::SPAN);
-        span_products<V, ALIGNED, 0, kGuGroups>(ra, rb, (span + k) * U::SPAN_BLOCKS + c * U::BLOCKS, nb_k, ng, load, acc);
-      }
+      for (int k = 0; k < n; ++k)
+        span_products<V, ALIGNED, 0, GROUPS>(ra + k * SPAN_STEP, rb + k * SPAN_STEP, (span + k) * U::SPAN_BLOCKS + c * U::BLOCKS, nb_k, ng, col, acc);
       release_stage();
     }
     if (KP > 1) {  // the parts' sums, in order
       if (part > 0) {
 #pragma unroll
-        for (int g = 0; g < kGuGroups; ++g)
+        for (int g = 0; g < GROUPS; ++g)
           if (g < ng) *reinterpret_cast<float4*>(acc_w + (g * 32 + lane) * 4) = make_float4(acc[g][0], acc[g][1], acc[g][2], acc[g][3]);
       }
       team_barrier(1 + team, KP * 32);
@@ -613,21 +662,21 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         for (int w = 1; w < KP; ++w) {
           const float* other = acc_w + (size_t)w * p.acc_floats;
 #pragma unroll
-          for (int g = 0; g < kGuGroups; ++g) {
-            if (g >= ng) break;
-            const float4 v = *reinterpret_cast<const float4*>(other + (g * 32 + lane) * 4);
-            acc[g][0] += v.x, acc[g][1] += v.y, acc[g][2] += v.z, acc[g][3] += v.w;
-          }
+          for (int g = 0; g < GROUPS; ++g)
+            if (g < ng) {
+              const float4 v = *reinterpret_cast<const float4*>(other + (g * 32 + lane) * 4);
+              acc[g][0] += v.x, acc[g][1] += v.y, acc[g][2] += v.z, acc[g][3] += v.w;
+            }
         }
       }
       team_barrier(1 + team, KP * 32);
-      if (part > 0) continue;
+      if (part > 0) return;
     }
     // Lane (q, c): gate and up of hidden value i0 + q for columns 2 c and 2 c + 1.
-    const int i = i0 + q, in = i / 32 % U::SPAN_BLOCKS, pj = i & 15;
-    const int64_t place = (int64_t)(i / 32 / U::SPAN_BLOCKS) * U::X_SPAN + x_chunk(in % U::BLOCKS, pj >> 2, in / U::BLOCKS) + (pj & 3) * 4 + (i >> 4 & 1) * 2;
+    const int i = i0 + q;
+    const int64_t place = h_place(i);
 #pragma unroll
-    for (int g = 0; g < kGuGroups; ++g) {
+    for (int g = 0; g < GROUPS; ++g) {
       if (g >= ng) break;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -641,8 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
           p.h[(int64_t)a * p.I + i] = h;
           const float hs = h * (float)(1 << kFastExp);
           const __half hi = __float2half_rn(hs);
-          *reinterpret_cast<__half*>(p.h_hi + (int64_t)a * spans_i * U::X_SPAN + place) = hi;
-          *reinterpret_cast<__half*>(p.h_lo + (int64_t)a * spans_i * U::X_SPAN + place) = __float2half_rn(hs - __half2float(hi));
+          *reinterpret_cast<__half*>(p.h_hi + a * h_row + place) = hi;
+          *reinterpret_cast<__half*>(p.h_lo + a * h_row + place) = __float2half_rn(hs - __half2float(hi));
         }
         uint32_t mx = __float_as_uint(h) & 0x7FFFFFFFu;
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
@@ -651,93 +700,97 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         if (q == 0 && m >= 0) atomicMax(p.amax + a, mx);
       }
     }
+  };
+  for (int id = first_gu; id < gu_tiles; id += G * teams) {
+    const int e = s_list[id / per_expert], i0 = id % per_expert * 8;
+    const uint32_t tokens = s_mask[e];
+    if (__popc(tokens) <= 8) gu_tile(std::integral_constant<int, 1>{}, e, i0, tokens);
+    else gu_tile(std::integral_constant<int, kGuGroups>{}, e, i0, tokens);
   }
   ok = grid_barrier(p.bars + 1) && ok;  // every h is written
+
+  // ---- h parts outside the fixed scale's range, made again; a choice's weight takes its scale ----
+  {
+    bool again = false;
+    if (ok && tid < choices) {
+      const uint32_t mx = __ldcg(p.amax + tid);
+      again = !fast_range(mx);
+      s_probs[tid] *= exp2i(again ? -scale_exp(mx) : -kFastExp);
+    }
+    if (__syncthreads_or(again)) {  // the same answer in every CTA
+      for (int a = blockIdx.x; a < choices; a += G) {
+        const uint32_t mx = __ldcg(p.amax + a);
+        if (fast_range(mx)) continue;
+        const float scale = exp2i(scale_exp(mx));
+        for (int i = tid; i < p.I; i += kThreads) {
+          const float hs = __ldcg(p.h + (int64_t)a * p.I + i) * scale;
+          const __half hi = __float2half_rn(hs);
+          *reinterpret_cast<__half*>(p.h_hi + a * h_row + h_place(i)) = hi;
+          *reinterpret_cast<__half*>(p.h_lo + a * h_row + h_place(i)) = __float2half_rn(hs - __half2float(hi));
+        }
+      }
+      ok = grid_barrier(p.bars + 2) && ok;
+    }
+  }
   live = live && ok;
 
   // ---- down: a tile of output rows at a time, its experts' stages shared by the warps ----
+  // column n < 4: the high part of the group's token n; n >= 4: the remainder of token n - 4
+  const uint8_t* h_base = (q < 4 ? p.h_hi : p.h_lo) + c * 16;
+  int u = 0;
+  auto dn_run = [&](auto groups, int e, int n0, int at, int end, uint32_t tokens) {  // stages [u, end) of one expert
+    constexpr int GROUPS = decltype(groups)::value;
+    const int ng = GROUPS == 1 ? 1 : (__popc(tokens) + 3) / 4;
+    int tok[GROUPS];
+    float acc[GROUPS][4];
+    Columns<GROUPS> col;
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      tok[g] = g < ng ? token_of(tokens, 4 * g + (q & 3)) : -1;
+      const int m = tok[g] >= 0 ? tok[g] : __ffs(tokens) - 1;
+      col.p[g] = h_base + (m * p.top_k + s_slot[m * p.E + e]) * h_row + (u - at * sd) * (U::NS * U::X_SPAN);
+      acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
+    }
+    col.start();
+    for (; u < end; ++u) {
+      if (!wait_stage()) {
+        live = false;
+        break;
+      }
+      const uint8_t* st = ring + (size_t)slot * U::STAGE;
+      const int span = (u - at * sd) * U::NS, n = min(U::NS, spans_i - span);
+      const uint8_t* ra = unit_at(st, q, dn_row(e, n0, q) + span * U::SPAN);
+      const uint8_t* rb = unit_at(st, q + 8, dn_row(e, n0, q + 8) + span * U::SPAN);
+      for (int k = 0; k < n; ++k)
+        span_products<V, ALIGNED, 0, GROUPS>(ra + k * SPAN_STEP, rb + k * SPAN_STEP, (span + k) * U::SPAN_BLOCKS + c * U::BLOCKS, nb_i, ng, col, acc);
+      release_stage();
+    }
+    // columns 2 c, 2 c + 1 (c < 2) with their remainders, of rows q and q + 8
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      if (g >= ng) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[g][i] += __shfl_xor_sync(0xffffffffu, acc[g][i], 2);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int m = __shfl_sync(0xffffffffu, tok[g], ((2 * c + j) & 3) * 4);
+        if (c < 2 && m >= 0) {
+          const float w = s_probs[m * p.top_k + s_slot[m * p.E + e]];
+          acc_w[q * p.M + m] += w * acc[g][j];
+          acc_w[(q + 8) * p.M + m] += w * acc[g][2 + j];
+        }
+      }
+    }
+  };
   for (int tile = 0; tile < my_tiles && ok; ++tile) {
     const int n0 = (blockIdx.x + tile * G) * kTileRows;
     for (int i = lane; i < kTileRows * p.M; i += 32) acc_w[i] = 0.f;
     __syncwarp();
-    for (int u = u0; u < u1 && live;) {
-      const int at = u / sd, end = min(u1, (at + 1) * sd);  // stages [u, end) of one expert
-      const int e = s_list[at];
+    for (u = u0; u < u1 && live;) {
+      const int at = u / sd, end = min(u1, (at + 1) * sd), e = s_list[at];
       const uint32_t tokens = s_mask[e];
-      const int ng = (__popc(tokens) + 3) / 4;
-      // column n < 4: the high part of token n of the group; n >= 4: the remainder of token n - 4
-      int tok[kDnGroups];
-      bool fast = true;
-#pragma unroll
-      for (int g = 0; g < kDnGroups; ++g) {
-        tok[g] = g < ng ? token_of(tokens, 4 * g + (q & 3)) : -1;
-        if (tok[g] >= 0) fast = fast && fast_range(__ldcg(p.amax + tok[g] * p.top_k + s_slot[tok[g] * p.E + e]));
-      }
-      fast = __all_sync(0xffffffffu, fast);
-      float acc[kDnGroups][4];
-#pragma unroll
-      for (int g = 0; g < kDnGroups; ++g) acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
-      for (; u < end; ++u) {
-        if (!wait_stage()) {
-          live = false;
-          break;
-        }
-        const uint8_t* st = ring + (size_t)slot * U::STAGE;
-        const int span = (u - at * sd) * U::NS, n = min(U::NS, spans_i - span);
-        for (int k = 0; k < n; ++k) {
-          const int blk = (span + k) * U::SPAN_BLOCKS + c * U::BLOCKS;
-          const uint8_t* hs = (q < 4 ? p.h_hi : p.h_lo) + (int64_t)(span + k) * U::X_SPAN + c * 16;
-          auto load = [&](int g, int phi, bool have, uint4 (&b)[4]) {
-            const int m = tok[g];
-            if (!have || m < 0) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) b[kk] = make_uint4(0, 0, 0, 0);
-              return;
-            }
-            const int a = m * p.top_k + s_slot[m * p.E + e];
-            if (fast) {
-              const uint4* src = reinterpret_cast<const uint4*>(hs + (int64_t)a * spans_i * U::X_SPAN + phi * 256);
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) b[kk] = src[kk * 4];
-            } else {
-              const float scale = exp2i(scale_exp(__ldcg(p.amax + a)));
-              const float4* src = reinterpret_cast<const float4*>(p.h + (int64_t)a * p.I + (blk + phi) * 32);
-              auto pair = [&](float x, float y) {
-                x *= scale, y *= scale;
-                const uint32_t hi = pack_half2(x, y);
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-                return q < 4 ? hi : pack_half2(x - f.x, y - f.y);
-              };
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                const float4 x = src[kk], y = src[4 + kk];
-                b[kk] = make_uint4(pair(x.x, y.x), pair(x.y, y.y), pair(x.z, y.z), pair(x.w, y.w));
-              }
-            }
-          };
-          const uint8_t* ra = unit_at(st, q, k, dn_row(e, n0, q) + span * U::SPAN);
-          const uint8_t* rb = unit_at(st, q + 8, k, dn_row(e, n0, q + 8) + span * U::SPAN);
-          span_products<V, ALIGNED, 0, kDnGroups>(ra, rb, blk, nb_i, ng, load, acc);
-        }
-        release_stage();
-      }
-      // columns 2 c, 2 c + 1 (c < 2) with their remainders, of rows q and q + 8
-#pragma unroll
-      for (int g = 0; g < kDnGroups; ++g) {
-        if (g >= ng) break;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[g][i] += __shfl_xor_sync(0xffffffffu, acc[g][i], 2);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int m = __shfl_sync(0xffffffffu, tok[g], ((2 * c + j) & 3) * 4);
-          if (c < 2 && m >= 0) {
-            const int a = m * p.top_k + s_slot[m * p.E + e];
-            const float w = s_probs[a] * exp2i(fast ? -kFastExp : -scale_exp(__ldcg(p.amax + a)));
-            acc_w[q * p.M + m] += w * acc[g][j];
-            acc_w[(q + 8) * p.M + m] += w * acc[g][2 + j];
-          }
-        }
-      }
+      if (__popc(tokens) <= 4) dn_run(std::integral_constant<int, 1>{}, e, n0, at, end, tokens);
+      else dn_run(std::integral_constant<int, kDnGroups>{}, e, n0, at, end, tokens);
     }
     __syncthreads();
     for (int i = tid; i < kTileRows * p.M; i += kThreads) {
@@ -751,11 +804,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   // copies that no one waited for (after a wait gave up) land before the CTA leaves
   for (; used < filled; next_slot()) (void)mbar_wait_bounded(smem_addr(&bars[slot]), parity);
   __syncthreads();
-  if (tid == 0 && atomic_add_acq_rel_gpu(p.bars + 2, 1u) == (uint32_t)G - 1u) {
-    store_relaxed_gpu(p.bars, 0u);
-    store_relaxed_gpu(p.bars + 1, 0u);
-    store_relaxed_gpu(p.bars + 2, 0u);
-  }
+  if (tid == 0 && atomic_add_acq_rel_gpu(p.bars + 3, 1u) == (uint32_t)G - 1u)
+    for (int i = 0; i < kMoeBarWords; ++i) store_relaxed_gpu(p.bars + i, 0u);
 }
 
 using MoeFn = void (*)(MoeParams);
@@ -785,10 +835,22 @@ cudaError_t set_up(const MoeArgs& a, int sms, MoeParams* p, int* smem) {
   at += up16(p->M * p->E);
   p->off_unscale = at;
   at += up16(p->M * 4);
+  p->off_keys = at;
+  at += kWarps * up16(p->E * 4);
   p->off_acc = at;
   const int groups = (p->M + 7) / 8;
   p->acc_floats = kTileRows * p->M > groups * 128 ? kTileRows * p->M : groups * 128;
   at += kWarps * p->acc_floats * 4;
+  const int64_t spans_k = (a.K / 32 + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS, spans_i = (a.I / 32 + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS;
+  // The activations go to shared memory where the ring keeps two stages next
+  // to them; rows 64 bytes off a multiple of 128, so that two tokens' loads
+  // meet no bank twice.  Else they are read through L1.
+  const int64_t x_bytes = a.M * (spans_k * U::X_SPAN + 64) + 256;
+  p->off_x = at;
+  if (x_bytes <= kSmemMax - kSlack - 128 - at - 2 * kWarps * U::STAGE) {
+    p->x_pitch = (int)(spans_k * U::X_SPAN + 64);
+    at += (int)x_bytes;
+  }
   p->off_ring = (at + 127) / 128 * 128;
   const int room = (kSmemMax - p->off_ring - kSlack) / (kWarps * U::STAGE);
   p->stages = room < kMaxStages ? room : kMaxStages;
@@ -796,7 +858,6 @@ cudaError_t set_up(const MoeArgs& a, int sms, MoeParams* p, int* smem) {
   *smem = p->off_ring + kWarps * p->stages * U::STAGE + kSlack;
   // Warps to a gate/up tile: one where every SM has tiles for its warps, more
   // where the (at most min(E, M top_k)) chosen experts give it fewer.
-  const int64_t spans_k = (a.K / 32 + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS, spans_i = (a.I / 32 + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS;
   const int64_t experts = a.M * a.top_k < a.E ? a.M * a.top_k : a.E;
   p->parts = 1;
   while (p->parts < 8 && 2 * p->parts <= spans_k && experts * (a.I / 8) * p->parts < 8 * (int64_t)sms) p->parts *= 2;
