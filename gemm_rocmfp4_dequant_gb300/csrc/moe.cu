@@ -160,40 +160,34 @@ RF4_DEV uint32_t codes_at(const uint32_t (&w)[5], int pos) {
   }
 }
 
-// The 16 pairs (w_j, w_{j+16}) of block PHI of a unit, exact in fp16.
+// A block's words and its scale pair (fp16).
 template <int V, bool ALIGNED, int PHI>
-RF4_DEV void decode_block(const uint8_t* unit, bool have, uint32_t (&a)[16]) {
-  constexpr int O = PHI * Fmt<V>::BB % 4;
-  uint32_t w[5];
-  block_words<V, ALIGNED, PHI>(unit, have, w);
-  uint32_t s2;
-  if constexpr (V == 0) s2 = O == 0 ? e4m3x2<0>(w[4]) : e4m3x2<1>(w[4]);
-  else s2 = e4m3x2<0>(__byte_perm(w[4], 0u, O * 0x11));
-#pragma unroll
-  for (int j = 0; j < 16; ++j) a[j] = hmul2(clamp5(codes_at(w, O + j)), s2);
-}
+struct Block {
+  static constexpr int O = PHI * Fmt<V>::BB % 4;
+  uint32_t w[5], s2;
+  RF4_DEV Block(const uint8_t* unit, bool have) {
+    block_words<V, ALIGNED, PHI>(unit, have, w);
+    if constexpr (V == 0) s2 = O == 0 ? e4m3x2<0>(w[4]) : e4m3x2<1>(w[4]);
+    else s2 = e4m3x2<0>(__byte_perm(w[4], 0u, O * 0x11));
+  }
+  // the pair (w_j, w_{j+16}), exact in fp16
+  RF4_DEV uint32_t pair(int j) const { return hmul2(clamp5(codes_at(w, O + j)), s2); }
+};
 
 RF4_DEV void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+RF4_DEV void mma_z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 
 // Byte offset of chunk kk (pairs 4 kk .. 4 kk + 3) of block PHI of lane group c
 // in a span's activations: the four c lie side by side.
 RF4_DEV int x_chunk(int phi, int kk, int c) { return ((phi * 4 + kk) * 4 + c) * 16; }
-
-// acc += the products of a decoded block of 16 rows with the columns' activations b.
-RF4_DEV void block_mma(const uint32_t (&a0)[16], const uint32_t (&a1)[16], const uint4 (&b)[4], float (&acc)[4]) {
-  float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int kk = 0; kk < 4; ++kk) {
-    mma(d, a0[4 * kk], a1[4 * kk], a0[4 * kk + 1], a1[4 * kk + 1], b[kk].x, b[kk].y);
-    mma(d, a0[4 * kk + 2], a1[4 * kk + 2], a0[4 * kk + 3], a1[4 * kk + 3], b[kk].z, b[kk].w);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] += d[i];
-}
 
 RF4_DEV void load_b(const uint8_t* p, uint4 (&b)[4]) {
 #pragma unroll
@@ -214,26 +208,44 @@ struct Columns {
 };
 
 // One span of a tile: `ra`, `rb` are rows q and q + 8 at the lane's unit, blk
-// the unit's first block.
+// the unit's first block.  A block is eight MMAs in two chains of four.
 template <int V, bool ALIGNED, int PHI, int GROUPS>
 RF4_DEV void span_products(const uint8_t* ra, const uint8_t* rb, int blk, int nb, int ng, Columns<GROUPS>& col, float (&acc)[GROUPS][4]) {
   const bool have = ALIGNED || blk + PHI < nb;
-  uint4 next[4];
-  if constexpr (GROUPS == 1) load_b(col.p[0] + 256, next);  // reads past the row's last block stay in the workspace
-  uint32_t a0[16], a1[16];
-  decode_block<V, ALIGNED, PHI>(ra, have, a0);
-  decode_block<V, ALIGNED, PHI>(rb, have, a1);
+  const Block<V, ALIGNED, PHI> x(ra, have), y(rb, have);
   if constexpr (GROUPS == 1) {
-    block_mma(a0, a1, col.b, acc[0]);
+    uint4 next[4];
+    load_b(col.p[0] + 256, next);  // reads past the row's last block stay in the workspace
+    float d[2][4];
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) col.b[kk] = next[kk];
+    for (int kk = 0; kk < 4; ++kk) {
+      const uint4 b = col.b[kk];
+      if (kk < 2) mma_z(d[kk & 1], x.pair(4 * kk), y.pair(4 * kk), x.pair(4 * kk + 1), y.pair(4 * kk + 1), b.x, b.y);
+      else mma(d[kk & 1], x.pair(4 * kk), y.pair(4 * kk), x.pair(4 * kk + 1), y.pair(4 * kk + 1), b.x, b.y);
+      mma(d[kk & 1], x.pair(4 * kk + 2), y.pair(4 * kk + 2), x.pair(4 * kk + 3), y.pair(4 * kk + 3), b.z, b.w);
+      col.b[kk] = next[kk];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[0][i] += d[0][i] + d[1][i];
     col.p[0] += 256;
   } else {
+    uint32_t a0[16], a1[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) a0[j] = x.pair(j), a1[j] = y.pair(j);
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
       if (g < ng) {
-        load_b(col.p[g], next);
-        block_mma(a0, a1, next, acc[g]);
+        uint4 b[4];
+        load_b(col.p[g], b);
+        float d[4];
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          if (kk == 0) mma_z(d, a0[0], a1[0], a0[1], a1[1], b[0].x, b[0].y);
+          else mma(d, a0[4 * kk], a1[4 * kk], a0[4 * kk + 1], a1[4 * kk + 1], b[kk].x, b[kk].y);
+          mma(d, a0[4 * kk + 2], a1[4 * kk + 2], a0[4 * kk + 3], a1[4 * kk + 3], b[kk].z, b[kk].w);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[g][i] += d[i];
         col.p[g] += 256;
       }
     }
@@ -261,6 +273,9 @@ RF4_DEV uint32_t load_acquire(const uint32_t* p) {
 }
 
 // Order-preserving bits of a router logit, above 0; NaN orders below every number.
+RF4_DEV float logit_of(uint32_t key) {
+  return key == 1u ? __uint_as_float(0x7FC00000u) : __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
 RF4_DEV uint32_t logit_key(float f) {
   if (f != f) return 1u;
   const uint32_t b = __float_as_uint(f + 0.f);
@@ -333,27 +348,32 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   // ---- router logits: one expert per CTA and pass, eight tokens at a time ----
   for (int e = blockIdx.x; e < p.E; e += G) {
     for (int m0 = 0; m0 < p.M; m0 += kRouterTokens) {
+      const int mc = min(kRouterTokens, p.M - m0);
       float acc[kRouterTokens];
 #pragma unroll
       for (int m = 0; m < kRouterTokens; ++m) acc[m] = 0.f;
       for (int k = tid * 8; k < p.K; k += kThreads * 8) {
         float r[8];
         load8_router(p.router_type, p.router, (int64_t)e * p.K + k, r);
+        uint4 a[kRouterTokens];
+#pragma unroll
+        for (int m = 0; m < kRouterTokens; ++m)
+          if (m < mc) a[m] = __ldg(reinterpret_cast<const uint4*>(p.X + (int64_t)(m0 + m) * p.K + k));
 #pragma unroll
         for (int m = 0; m < kRouterTokens; ++m) {
-          if (m0 + m >= p.M) break;
-          const uint4 a = __ldg(reinterpret_cast<const uint4*>(p.X + (int64_t)(m0 + m) * p.K + k));
-          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+          if (m < mc) {
+            const uint32_t w[4] = {a[m].x, a[m].y, a[m].z, a[m].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            acc[m] = fmaf(r[2 * i], act_f32<ACT>(w[i] & 0xFFFFu), acc[m]);
-            acc[m] = fmaf(r[2 * i + 1], act_f32<ACT>(w[i] >> 16), acc[m]);
+            for (int i = 0; i < 4; ++i) {
+              acc[m] = fmaf(r[2 * i], act_f32<ACT>(w[i] & 0xFFFFu), acc[m]);
+              acc[m] = fmaf(r[2 * i + 1], act_f32<ACT>(w[i] >> 16), acc[m]);
+            }
           }
         }
       }
 #pragma unroll
       for (int m = 0; m < kRouterTokens; ++m) {
-        if (m0 + m >= p.M) break;
+        if (m >= mc) break;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], o);
         if (lane == 0) s_red[warp][m] = acc[m];
@@ -411,7 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     }
   }
   const int choices = p.M * p.top_k;
-  if (blockIdx.x == 0 && tid < choices) p.amax[tid] = 0u;
+  if (blockIdx.x == 0)
+    for (int a = tid; a < choices; a += kThreads) p.amax[a] = 0u;
   const int nb_i = p.I / 32, spans_i = (nb_i + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS;
   const int64_t h_row = (int64_t)spans_i * U::X_SPAN;  // bytes of a choice's h parts
   // Place of hidden value i in its row of h parts.
@@ -439,11 +460,17 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         keys[e] = k;
         if (k > best) best = k, next = e;
       }
+      // the softmax over all experts needs its sum before choices leave the keys
+      float denom = 0.f;
+      const float top = logit_of(__reduce_max_sync(0xffffffffu, best));
+      if (p.route == 0)
+        for (int e = lane; e < p.E; e += 32) denom += expf(logit_of(keys[e]) - top);
+      uint32_t my_key = 1;
       int my_id = 0;
       for (int j = 0; j < p.top_k; ++j) {
         const uint32_t mx = __reduce_max_sync(0xffffffffu, best);
         const uint32_t e = __reduce_min_sync(0xffffffffu, best == mx ? next : 0xFFFFu);
-        if (lane == j) my_id = (int)e;
+        if (lane == j) my_id = (int)e, my_key = mx;
         if ((int)(e & 31) == lane) {
           keys[e] = 0;
           best = 0;
@@ -453,20 +480,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
           }
         }
       }
-      const float mine = __ldcg(logits + my_id);
-      const float top = __shfl_sync(0xffffffffu, mine, 0);
-      float denom = 0.f;
+      const float mine = logit_of(my_key);
       float num = 0.f;
       if (p.route == 2) {
         num = lane < p.top_k ? 1.f / (1.f + expf(-mine)) : 0.f;
         denom = num;
       } else {
         num = lane < p.top_k ? expf(mine - top) : 0.f;
-        if (p.route == 1) {
-          denom = num;
-        } else {
-          for (int e = lane; e < p.E; e += 32) denom += expf(__ldcg(logits + e) - top);
-        }
+        if (p.route == 1) denom = num;
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) denom += __shfl_xor_sync(0xffffffffu, denom, o);
@@ -712,10 +733,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   // ---- h parts outside the fixed scale's range, made again; a choice's weight takes its scale ----
   {
     bool again = false;
-    if (ok && tid < choices) {
-      const uint32_t mx = __ldcg(p.amax + tid);
-      again = !fast_range(mx);
-      s_probs[tid] *= exp2i(again ? -scale_exp(mx) : -kFastExp);
+    for (int a = tid; a < choices && ok; a += kThreads) {
+      const uint32_t mx = __ldcg(p.amax + a);
+      const bool out = !fast_range(mx);
+      s_probs[a] *= exp2i(out ? -scale_exp(mx) : -kFastExp);
+      again = again || out;
     }
     if (__syncthreads_or(again)) {  // the same answer in every CTA
       for (int a = blockIdx.x; a < choices; a += G) {
@@ -860,7 +882,7 @@ cudaError_t set_up(const MoeArgs& a, int sms, MoeParams* p, int* smem) {
   // where the (at most min(E, M top_k)) chosen experts give it fewer.
   const int64_t experts = a.M * a.top_k < a.E ? a.M * a.top_k : a.E;
   p->parts = 1;
-  while (p->parts < 8 && 2 * p->parts <= spans_k && experts * (a.I / 8) * p->parts < 8 * (int64_t)sms) p->parts *= 2;
+  while (kWarps % (2 * p->parts) == 0 && p->parts < 8 && 2 * p->parts <= spans_k && experts * (a.I / 8) * p->parts < 8 * (int64_t)sms) p->parts *= 2;
   // Workspace: logits, activation scales, largest |h|, then 16-byte aligned arrays.
   const int64_t choices = a.M * a.top_k;
   float* w = a.ws;
