@@ -16,9 +16,9 @@
 // values, or 16 output rows.  A span is 144 bytes (8 dual blocks) or 272 bytes
 // (16 single-scale blocks) of each row.  A warp takes tiles on its own (or
 // KP neighbouring warps share a tile's spans where tiles are few) and streams
-// their spans through a private ring of shared-memory stages, by tensor copies
-// of 16-row boxes.  The down tasks are known as soon as the routing is, so the
-// ring runs on into them before the second barrier.
+// their spans through a private ring of shared-memory stages, one tensor copy
+// of a 16-row box a stage.  The down tasks are known as soon as the routing is,
+// so the ring runs on into them before the second barrier.
 // The arithmetic is mma.sync m16n8k16 on fp16 with fp32 accumulators: A is
 // the decoded weights, exact in fp16, decoded once for all the tokens of the
 // expert; B's columns are tokens.  Lane (q, c) decodes blocks of rows q and
@@ -56,10 +56,9 @@ namespace {
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTileRows = 16;
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 6;
 constexpr int kRouterTokens = 8;   // tokens a router pass holds
-constexpr int kGuGroups = 4;       // groups of 8 tokens of an expert
-constexpr int kDnGroups = 8;       // groups of 4 tokens: high and low columns
+constexpr int kTouchBytes = 32768;  // activations asked for ahead of use
 constexpr int kFastExp = 4;        // h times 2^4 in its fp16 pair
 
 template <int V>
@@ -68,12 +67,17 @@ struct Unit {
   static constexpr int BYTES = Fmt<V>::LANE_BYTES; // 36 / 68
   static constexpr int SPAN = Fmt<V>::SPAN;        // 144 / 272
   static constexpr int SPAN_BLOCKS = 4 * BLOCKS;   // 8 / 16
-  static constexpr int NS = V == 0 ? 2 : 1;        // spans a stage holds
   static constexpr int X_SPAN = SPAN_BLOCKS * 64;  // bytes of a span's fp16 activations
-  static constexpr int PITCH = 304;                // row slots of unaligned rows: NS spans, 16-byte slack, no bank conflicts
-  static constexpr int STAGE = (kTileRows * PITCH + 127) / 128 * 128;
-  static_assert(NS * SPAN + 15 <= PITCH && NS * SPAN * kTileRows <= STAGE, "stage holds either form");
 };
+
+// A stage of ns spans: aligned rows as ns boxes of 16 rows x one span (36 or 68
+// words: rows an odd multiple of 16 bytes apart, whose reads meet no bank
+// twice), unaligned ones as 16 slots of ns spans, with room for their place
+// within 16 bytes and to end in.
+template <int V, bool ALIGNED>
+RF4_HOSTDEV constexpr int row_pitch(int ns) { return ALIGNED ? Unit<V>::SPAN : ns * Unit<V>::SPAN + 32; }
+template <int V, bool ALIGNED>
+RF4_HOSTDEV constexpr int span_step() { return ALIGNED ? kTileRows * Unit<V>::SPAN : Unit<V>::SPAN; }
 
 struct MoeParams {
   CUtensorMap map_gu;  // aligned rows: {words, I rows, 2 E halves}, box {span, 8, 2}
@@ -98,10 +102,10 @@ struct MoeParams {
   int router_type, route;
   float route_scale;
   int parts;           // KP: warps that share a gate/up tile
-  int stages;          // ring stages of a warp
+  int ns;              // spans of a stage
+  int stages, stage_bytes;  // ring of a warp
   // offsets in shared memory
-  int off_mask, off_list, off_slot, off_unscale, off_keys, off_x, off_acc, off_ring;
-  int x_pitch;         // bytes between tokens of the activations in shared memory, 0: they stay in the workspace
+  int off_mask, off_list, off_slot, off_unscale, off_y, off_acc, off_ring;
   int acc_floats;      // per warp
 };
 
@@ -194,64 +198,76 @@ RF4_DEV void load_b(const uint8_t* p, uint4 (&b)[4]) {
   for (int kk = 0; kk < 4; ++kk) b[kk] = *reinterpret_cast<const uint4*>(p + kk * 64);
 }
 
-// Activations of the lane's column, one pointer per group of tokens, moving on
-// through the row 256 bytes a block.  One group (most experts of a few tokens):
-// the next block's are loaded while this one's weights are decoded.  Columns
+// One group of at most eight columns (most experts of a few tokens).  `p` moves
+// through the lane's activations, 256 bytes a block; the next block's are
+// loaded while this one's weights are decoded, in turn into a and b.  Columns
 // beyond the expert's tokens repeat its first; their sums are not used.
-template <int GROUPS>
-struct Columns {
-  const uint8_t* p[GROUPS];
-  uint4 b[4];
-  RF4_DEV void start() {
-    if constexpr (GROUPS == 1) load_b(p[0], b);
+struct Column {
+  const uint8_t* p;
+  uint4 a[4], b[4];
+  float acc[4];
+  RF4_DEV void start(const uint8_t* first) {
+    p = first;
+    load_b(p, a);
+    acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+  }
+  // Block PHI and those after it of a unit; ra, rb: rows q and q + 8 at the lane's unit; blk: its first block.
+  template <int V, bool ALIGNED, int PHI>
+  RF4_DEV void unit(const uint8_t* ra, const uint8_t* rb, int blk, int nb) {
+    const bool have = ALIGNED || blk + PHI < nb;
+    const Block<V, ALIGNED, PHI> x(ra, have), y(rb, have);
+    uint4(&now)[4] = PHI % 2 ? b : a;
+    load_b(p + 256 * (PHI + 1), PHI % 2 ? a : b);  // reads past the row's last block stay in the workspace
+    float d[2][4];  // eight MMAs in two chains
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      if (kk < 2) mma_z(d[kk & 1], x.pair(4 * kk), y.pair(4 * kk), x.pair(4 * kk + 1), y.pair(4 * kk + 1), now[kk].x, now[kk].y);
+      else mma(d[kk & 1], x.pair(4 * kk), y.pair(4 * kk), x.pair(4 * kk + 1), y.pair(4 * kk + 1), now[kk].x, now[kk].y);
+      mma(d[kk & 1], x.pair(4 * kk + 2), y.pair(4 * kk + 2), x.pair(4 * kk + 3), y.pair(4 * kk + 3), now[kk].z, now[kk].w);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] += d[0][i] + d[1][i];
+    if constexpr (PHI + 1 < Unit<V>::BLOCKS) unit<V, ALIGNED, PHI + 1>(ra, rb, blk, nb);
+    else p += 256 * Unit<V>::BLOCKS;
   }
 };
 
-// One span of a tile: `ra`, `rb` are rows q and q + 8 at the lane's unit, blk
-// the unit's first block.  A block is eight MMAs in two chains of four.
-template <int V, bool ALIGNED, int PHI, int GROUPS>
-RF4_DEV void span_products(const uint8_t* ra, const uint8_t* rb, int blk, int nb, int ng, Columns<GROUPS>& col, float (&acc)[GROUPS][4]) {
-  const bool have = ALIGNED || blk + PHI < nb;
-  const Block<V, ALIGNED, PHI> x(ra, have), y(rb, have);
-  if constexpr (GROUPS == 1) {
-    uint4 next[4];
-    load_b(col.p[0] + 256, next);  // reads past the row's last block stay in the workspace
-    float d[2][4];
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      const uint4 b = col.b[kk];
-      if (kk < 2) mma_z(d[kk & 1], x.pair(4 * kk), y.pair(4 * kk), x.pair(4 * kk + 1), y.pair(4 * kk + 1), b.x, b.y);
-      else mma(d[kk & 1], x.pair(4 * kk), y.pair(4 * kk), x.pair(4 * kk + 1), y.pair(4 * kk + 1), b.x, b.y);
-      mma(d[kk & 1], x.pair(4 * kk + 2), y.pair(4 * kk + 2), x.pair(4 * kk + 3), y.pair(4 * kk + 3), b.z, b.w);
-      col.b[kk] = next[kk];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[0][i] += d[0][i] + d[1][i];
-    col.p[0] += 256;
-  } else {
+// Several groups: the weights are decoded once, then meet each group's columns.
+// The sums lie in shared memory (one float4 a lane and group): registers and
+// code stay small, and the eight MMAs of a group cover the way there and back.
+struct Columns {
+  const uint8_t* p;
+  const uint32_t* off;  // bytes from p to the activations of the lane's column, one in eight words a group
+  float4* sums;
+  int ng;
+  template <int V, bool ALIGNED, int PHI>
+  RF4_DEV void unit(const uint8_t* ra, const uint8_t* rb, int blk, int nb) {
+    const bool have = ALIGNED || blk + PHI < nb;
     uint32_t a0[16], a1[16];
+    {
+      const Block<V, ALIGNED, PHI> x(ra, have), y(rb, have);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) a0[j] = x.pair(j), a1[j] = y.pair(j);
-#pragma unroll
-    for (int g = 0; g < GROUPS; ++g) {
-      if (g < ng) {
-        uint4 b[4];
-        load_b(col.p[g], b);
-        float d[4];
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          if (kk == 0) mma_z(d, a0[0], a1[0], a0[1], a1[1], b[0].x, b[0].y);
-          else mma(d, a0[4 * kk], a1[4 * kk], a0[4 * kk + 1], a1[4 * kk + 1], b[kk].x, b[kk].y);
-          mma(d, a0[4 * kk + 2], a1[4 * kk + 2], a0[4 * kk + 3], a1[4 * kk + 3], b[kk].z, b[kk].w);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[g][i] += d[i];
-        col.p[g] += 256;
-      }
+      for (int j = 0; j < 16; ++j) a0[j] = x.pair(j), a1[j] = y.pair(j);
     }
+#pragma unroll 1
+    for (int g = 0; g < ng; ++g) {
+      uint4 b[4];
+      load_b(p + off[8 * g] + 256 * PHI, b);
+      float d[2][4];
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        if (kk < 2) mma_z(d[kk & 1], a0[4 * kk], a1[4 * kk], a0[4 * kk + 1], a1[4 * kk + 1], b[kk].x, b[kk].y);
+        else mma(d[kk & 1], a0[4 * kk], a1[4 * kk], a0[4 * kk + 1], a1[4 * kk + 1], b[kk].x, b[kk].y);
+        mma(d[kk & 1], a0[4 * kk + 2], a1[4 * kk + 2], a0[4 * kk + 3], a1[4 * kk + 3], b[kk].z, b[kk].w);
+      }
+      float4 s = sums[32 * g];
+      s.x += d[0][0] + d[1][0], s.y += d[0][1] + d[1][1], s.z += d[0][2] + d[1][2], s.w += d[0][3] + d[1][3];
+      sums[32 * g] = s;
+    }
+    if constexpr (PHI + 1 < Unit<V>::BLOCKS) unit<V, ALIGNED, PHI + 1>(ra, rb, blk, nb);
+    else p += 256 * Unit<V>::BLOCKS;
   }
-  if constexpr (PHI + 1 < Unit<V>::BLOCKS) span_products<V, ALIGNED, PHI + 1, GROUPS>(ra, rb, blk, nb, ng, col, acc);
-}
+};
 
 // The bytes [a, a + n) as a copy from 16-byte boundary to 16-byte boundary.
 RF4_DEV uint32_t span_bytes(const uint8_t* a, int n) {
@@ -262,6 +278,13 @@ RF4_DEV void copy_span(uint8_t* dst, const uint8_t* a, int n, uint32_t bar) {
   bulk_g2s(smem_addr(dst), reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(a) & ~uintptr_t(15)), span_bytes(a, n), bar);
 }
 RF4_DEV int mis16(const uint8_t* a) { return (int)(reinterpret_cast<uintptr_t>(a) & 15u); }
+
+// Asks for a line of global memory to be brought to L1; nothing waits for it.
+RF4_DEV void touch(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.ca.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  (void)v;
+}
 
 // Barrier of some whole warps of the CTA (id 1 .. 15).
 RF4_DEV void team_barrier(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
@@ -307,10 +330,17 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   uint16_t* s_list = reinterpret_cast<uint16_t*>(smem + p.off_list);         // chosen experts, ascending
   uint8_t* s_slot = smem + p.off_slot;                                       // [M][E]: which choice of the token
   float* s_unscale = reinterpret_cast<float*>(smem + p.off_unscale);         // [M]: 1 / the activations' scale
-  uint32_t* s_keys = reinterpret_cast<uint32_t*>(smem + p.off_keys);         // [kWarps][E]: order of a token's logits
+  float* s_y = reinterpret_cast<float*>(smem + p.off_y);                     // [kWarps][M][16]: outputs of a down tile
   float* s_acc = reinterpret_cast<float*>(smem + p.off_acc);                 // [kWarps][acc_floats]
   __shared__ uint64_t s_bars[kWarps * kMaxStages];
+  __shared__ uint64_t s_pick[kWarps][kMoeMaxTop];
   __shared__ float s_red[kWarps][kRouterTokens];
+  // Columns of the expert a warp is at: bytes to their activations, their
+  // choice (gate/up) or token (down), -1 for none, and, of its activations, 1 / the scale (gate/up) or the choice's weight (down).
+  __shared__ uint32_t s_off[kWarps * 64];
+  __shared__ int16_t s_choice[kWarps * 64];
+  __shared__ float s_un[kWarps * 64];
+  __shared__ uint32_t s_amax[kMoeMaxTokens * kMoeMaxTop];  // bits of the choices' largest |h| in this CTA
   __shared__ int s_active, s_ok;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = gridDim.x;
 
@@ -325,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   }
   if (tid == 0) s_ok = 1;
   for (int e = tid; e < p.E; e += kThreads) s_mask[e] = 0;
+  for (int a = tid; a < p.M * p.top_k; a += kThreads) s_amax[a] = 0;
   __syncthreads();
 
   // Every CTA arrives and waits (bounded) for the others; false if one gave up.
@@ -352,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       float acc[kRouterTokens];
 #pragma unroll
       for (int m = 0; m < kRouterTokens; ++m) acc[m] = 0.f;
+#pragma unroll 1
       for (int k = tid * 8; k < p.K; k += kThreads * 8) {
         float r[8];
         load8_router(p.router_type, p.router, (int64_t)e * p.K + k, r);
@@ -394,6 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     float scale = 1.f;
     if constexpr (ACT == 1) {
       uint32_t mx = 0;  // bf16 magnitudes order as their bits
+#pragma unroll 2
       for (int k = tid * 2; k < p.K; k += kThreads * 2) {
         const uint32_t w = *reinterpret_cast<const uint32_t*>(x + k) & 0x7FFF7FFFu;
         mx = max(mx, max(w & 0xFFFFu, w >> 16));
@@ -410,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     } else if (tid == 0) {
       p.x_unscale[m] = 1.f;
     }
+#pragma unroll 1
     for (int i = tid; i < spans_k * U::SPAN_BLOCKS * 4; i += kThreads) {
       const int blk = i >> 2, kk = i & 3, in = blk % U::SPAN_BLOCKS;
       uint2 a = make_uint2(0, 0), b = a;  // zeros past the row
@@ -449,37 +483,60 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   }
   bool ok = grid_barrier(p.bars);
 
+  if (ok && tid < p.M) s_unscale[tid] = __ldcg(p.x_unscale + tid);
+  // The activations on their way to L1 while the choices are made (the
+  // products would meet each line's latency in turn); not more than it holds.
+  for (int64_t i = (int64_t)tid * 128; ok && i < p.M * spans_k * U::X_SPAN && i < kTouchBytes; i += kThreads * 128) touch(p.xf + i);
   // ---- top k of every token (one warp per token), repeated by every CTA ----
   if (ok) {
-    uint32_t* keys = s_keys + warp * p.E;  // a lane reads only what it wrote: entries lane, lane + 32, ...
+    // Room in the idle ring: the order of every expert's logit, then the
+    // candidates: those that reach the top_k-th largest of the lanes' maxima.
+    uint32_t* keys = reinterpret_cast<uint32_t*>(smem + p.off_ring) + warp * 4 * p.E;
+    uint64_t* cand = reinterpret_cast<uint64_t*>(keys + 2 * p.E);
     for (int m = warp; m < p.M; m += kWarps) {
-      const float* logits = p.logits + (int64_t)m * p.E;
-      uint32_t best = 0, next = 0;  // the lane's largest remaining key and its expert
+      uint32_t best = 0;
       for (int e = lane; e < p.E; e += 32) {
-        const uint32_t k = logit_key(__ldcg(logits + e));
+        const uint32_t k = logit_key(__ldcg(p.logits + (int64_t)m * p.E + e));
         keys[e] = k;
-        if (k > best) best = k, next = e;
+        best = max(best, k);
       }
-      // the softmax over all experts needs its sum before choices leave the keys
-      float denom = 0.f;
+      __syncwarp();
       const float top = logit_of(__reduce_max_sync(0xffffffffu, best));
-      if (p.route == 0)
-        for (int e = lane; e < p.E; e += 32) denom += expf(logit_of(keys[e]) - top);
-      uint32_t my_key = 1;
-      int my_id = 0;
-      for (int j = 0; j < p.top_k; ++j) {
-        const uint32_t mx = __reduce_max_sync(0xffffffffu, best);
-        const uint32_t e = __reduce_min_sync(0xffffffffu, best == mx ? next : 0xFFFFu);
-        if (lane == j) my_id = (int)e, my_key = mx;
-        if ((int)(e & 31) == lane) {
-          keys[e] = 0;
-          best = 0;
-          for (int i = lane; i < p.E; i += 32) {
-            const uint32_t k = keys[i];
-            if (k > best) best = k, next = i;
-          }
-        }
+      int rank = 0;  // of the lane's maximum, equal ones in lane order
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) {
+        const uint32_t o = __shfl_sync(0xffffffffu, best, i);
+        rank += o > best || (o == best && i < lane) ? 1 : 0;
       }
+      const uint32_t least = __shfl_sync(0xffffffffu, best, __ffs(__ballot_sync(0xffffffffu, rank == p.top_k - 1)) - 1);
+      int n = 0;
+#pragma unroll 1
+      for (int e0 = 0; e0 < p.E; e0 += 32) {
+        const int e = e0 + lane;
+        const uint32_t k = e < p.E ? keys[e] : 0u;
+        const bool in = e < p.E && k >= least;
+        const uint32_t b = __ballot_sync(0xffffffffu, in);
+        if (in) cand[n + __popc(b & ((1u << lane) - 1u))] = (uint64_t)k << 32 | (uint32_t)~e;  // equal logits: the lowest expert first
+        n += __popc(b);
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int i = lane; i < n; i += 32) {
+        const uint64_t k = cand[i];
+        int r = 0;
+#pragma unroll 2
+        for (int o = 0; o < n; ++o) r += cand[o] > k ? 1 : 0;
+        if (r < p.top_k) s_pick[warp][r] = k;
+      }
+      float denom = 0.f;
+      if (p.route == 0)  // softmax over all experts
+#pragma unroll 1
+        for (int e = lane; e < p.E; e += 32) denom += expf(logit_of(keys[e]) - top);
+      __syncwarp();
+      const uint64_t pick = s_pick[warp][lane < p.top_k ? lane : 0];
+      const uint32_t my_key = (uint32_t)(pick >> 32);
+      const int my_id = (int)~(uint32_t)pick;
+      __syncwarp();
       const float mine = logit_of(my_key);
       float num = 0.f;
       if (p.route == 2) {
@@ -503,12 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       }
     }
   }
-  if (ok && tid < p.M) s_unscale[tid] = __ldcg(p.x_unscale + tid);
-  if (ok && p.x_pitch != 0) {
-    const int per = spans_k * U::X_SPAN / 16;  // 16-byte chunks of a token
-    for (int i = tid; i < p.M * per; i += kThreads)
-      *reinterpret_cast<uint4*>(smem + p.off_x + i / per * p.x_pitch + i % per * 16) = __ldcg(reinterpret_cast<const uint4*>(p.xf) + i);
-  }
+  fence_proxy_async();  // the ring's use above precedes the copies into it
   __syncthreads();
   if (warp == 0) {
     int n = 0;
@@ -528,107 +580,110 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   const int KP = p.parts, team = warp / KP, part = warp % KP, teams = kWarps / KP;
   const int span0 = spans_k * part / KP, span1 = spans_k * (part + 1) / KP;  // this warp's spans of a gate/up tile
   const int per_expert = p.I / 8;                                          // gate/up tiles of an expert
-  const int gu_tiles = A * per_expert;                                     // dealt round robin over CTAs, then teams
-  const int first_gu = blockIdx.x + G * team;
-  const int tiles = p.K / kTileRows;
-  const int my_tiles = (int)blockIdx.x < tiles ? (tiles - (int)blockIdx.x + G - 1) / G : 0;
-  const int sd = (spans_i + U::NS - 1) / U::NS;                            // stages of an expert's rows in a down tile
-  const int u0 = warp * (A * sd) / kWarps, u1 = (warp + 1) * (A * sd) / kWarps;  // this warp's share of a down tile's stages
-  uint8_t* ring = smem + p.off_ring + (size_t)warp * p.stages * U::STAGE;
+  // A CTA's gate/up tiles [.., gu1) are neighbours, so that its warps share
+  // activations in L1; they go round its teams.
+  const int gu0 = (int)((int64_t)A * per_expert * blockIdx.x / G) + team, gu1 = (int)((int64_t)A * per_expert * (blockIdx.x + 1) / G);
+  // Down: a CTA takes 16-row tiles, and its warps share the stages of a tile
+  // (every chosen expert's rows) in equal runs.
+  const int ns = p.ns, sd = (spans_i + ns - 1) / ns;
+  const int tiles = p.K / kTileRows, my_tiles = (int)blockIdx.x < tiles ? (tiles - (int)blockIdx.x + G - 1) / G : 0;
+  const int u0 = warp * (A * sd) / kWarps, u1 = (warp + 1) * (A * sd) / kWarps;
+  uint8_t* ring = smem + p.off_ring + warp * p.stages * p.stage_bytes;
 
-  // Row r of a stage at the lane's unit of the stage's first span; further
-  // spans lie SPAN_STEP on.  Unaligned rows start at their own place within 16 bytes.
-  const int q = lane >> 2, c = lane & 3;
-  constexpr int SPAN_STEP = ALIGNED ? kTileRows * U::SPAN : U::SPAN;
-  auto unit_at = [&](const uint8_t* stage, int r, const uint8_t* src) {
-    if constexpr (ALIGNED) return stage + r * U::SPAN + c * U::BYTES;
-    else return stage + r * U::PITCH + mis16(src) + c * U::BYTES;
-  };
+  // Lane (q, c) reads rows q and q + 8 of a stage at unit c of each span.
+  // Unaligned rows start at their own place within 16 bytes.
+  const int q = lane >> 2, c = lane & 3, pitch = row_pitch<V, ALIGNED>(ns);
+  constexpr int STEP = span_step<V, ALIGNED>();
+  const int unit_a = q * pitch + c * U::BYTES, unit_b = unit_a + 8 * pitch;
   auto gu_row = [&](int e, int i0, int r) { return p.Wgu + ((int64_t)e * 2 * p.I + (r < 8 ? 0 : p.I) + i0 + (r & 7)) * rb_k; };
   auto dn_row = [&](int e, int n0, int r) { return p.Wd + ((int64_t)e * p.K + n0 + r) * rb_i; };
 
-  // Copies of spans [span, span + n) of a tile's 16 rows into a stage.
-  auto fill = [&](bool down, int e, int row0, int span, int n, int slot) {
-    uint8_t* dst = ring + (size_t)slot * U::STAGE;
+  // Copies of ns spans from `span` on of a tile's 16 rows into a stage (fewer at the row's end).
+  auto fill = [&](bool down, int e, int row0, int span, int slot) {
+    uint8_t* dst = ring + slot * p.stage_bytes;
     const uint32_t bar = smem_addr(&bars[slot]);
     if constexpr (ALIGNED) {
       if (lane == 0) {
+        const int n = min(ns, (down ? spans_i : span1) - span);
         mbar_arrive_expect_tx(bar, (uint32_t)(n * kTileRows * U::SPAN));
+#pragma unroll 1
         for (int k = 0; k < n; ++k) {
-          const uint32_t to = smem_addr(dst + k * kTileRows * U::SPAN);
+          const uint32_t to = smem_addr(dst) + k * (kTileRows * U::SPAN);
           if (down) tma_load_2d(to, &p.map_dn, (span + k) * (U::SPAN / 4), e * p.K + row0, bar);
           else tma_load_3d(to, &p.map_gu, (span + k) * (U::SPAN / 4), row0, 2 * e, bar);
         }
       }
     } else {
-      const int rb = down ? rb_i : rb_k, lo = span * U::SPAN, len = min(rb - lo, n * U::SPAN);
+      const int rb = down ? rb_i : rb_k, lo = span * U::SPAN, len = min(rb - lo, ns * U::SPAN);
       const uint8_t* src = (down ? dn_row(e, row0, lane & 15) : gu_row(e, row0, lane & 15)) + lo;
       const uint32_t bytes = __reduce_add_sync(0xffffffffu, lane < kTileRows ? span_bytes(src, len) : 0u);
       if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
       __syncwarp();
-      if (lane < kTileRows) copy_span(dst + lane * U::PITCH, src, len, bar);
+      if (lane < kTileRows) copy_span(dst + lane * pitch, src, len, bar);
     }
   };
-  // The next stage to fill.
+  // The next stage to fill: of a gate/up tile (its number, expert, first row
+  // and next span), then of a down tile (stage u of tile `id` of this CTA's).
   struct {
     bool gu, any;
-    int id, e, row0, span;  // gate/up: tile number, expert, first row, next span
-    int tile, u, a, s;      // down: tile of this CTA, unit, place in the list, stage of the row
+    int id, e, row0, span, u;
   } nx;
   auto start_gu = [&](int id) {
+    const int at = id / per_expert;
     nx.id = id;
-    nx.e = s_list[id / per_expert];
-    nx.row0 = id % per_expert * 8;
+    nx.e = s_list[at];
+    nx.row0 = (id - at * per_expert) * 8;
     nx.span = span0;
   };
-  auto start_dn = [&]() {
-    nx.u = u0;
-    nx.a = u0 / sd;
-    nx.s = u0 - nx.a * sd;
-  };
-  nx.tile = 0;
-  nx.gu = first_gu < gu_tiles;
+  nx.gu = gu0 < gu1;
   nx.any = nx.gu || (u0 < u1 && my_tiles > 0);
-  if (nx.gu) start_gu(first_gu);
-  if (u0 < u1) start_dn();
+  nx.id = 0;
+  nx.u = u0;
+  if (nx.gu) start_gu(gu0);
   int fill_slot = 0, filled = 0;
   auto fill_next = [&]() {
     if (!nx.any) return;
+    if (!nx.gu) {
+      const int at = nx.u / sd;
+      nx.e = s_list[at];
+      nx.row0 = (blockIdx.x + nx.id * G) * kTileRows;
+      nx.span = (nx.u - at * sd) * ns;
+    }
+    fill(!nx.gu, nx.e, nx.row0, nx.span, fill_slot);
     if (nx.gu) {
-      fill(false, nx.e, nx.row0, nx.span, min(U::NS, span1 - nx.span), fill_slot);
-      nx.span += U::NS;
+      nx.span += ns;
       if (nx.span >= span1) {
-        if (nx.id + G * teams < gu_tiles) {
-          start_gu(nx.id + G * teams);
+        if (nx.id + teams < gu1) {
+          start_gu(nx.id + teams);
         } else {
           nx.gu = false;
           nx.any = u0 < u1 && my_tiles > 0;
+          nx.id = 0;
         }
       }
-    } else {
-      fill(true, s_list[nx.a], (blockIdx.x + nx.tile * G) * kTileRows, nx.s * U::NS, min(U::NS, spans_i - nx.s * U::NS), fill_slot);
-      if (++nx.s == sd) nx.s = 0, ++nx.a;
-      if (++nx.u == u1) {
-        if (++nx.tile < my_tiles) start_dn();
-        else nx.any = false;
-      }
+    } else if (++nx.u == u1) {
+      nx.u = u0;
+      nx.any = ++nx.id < my_tiles;
     }
     if (++fill_slot == p.stages) fill_slot = 0;
     ++filled;
   };
   int slot = 0, used = 0;
   uint32_t parity = 0;
-  bool live = ok;
-  if (ok)
-    for (int i = 0; i < p.stages; ++i) fill_next();
-  auto wait_stage = [&]() {  // warp-uniform: every lane waits on the same barrier
-    const bool landed = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&bars[slot]), parity));
-    if (!landed && lane == 0) atomicOr(p.err, kErrWaitTimeout);
-    return landed;
-  };
+#pragma unroll 1
+  for (int i = 0; i < p.stages; ++i) fill_next();
   auto next_slot = [&]() {
     ++used;
     if (++slot == p.stages) slot = 0, parity ^= 1u;
+  };
+  // The next stage, once its copies have landed.  If a wait gives up, nothing
+  // more is copied or waited for: the outputs are invalid, and an error bit says so.
+  auto wait_stage = [&]() {
+    if (used < filled && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&bars[slot]), parity))) {
+      if (lane == 0) atomicOr(p.err, kErrWaitTimeout);
+      nx.any = false;
+    }
+    return ring + slot * p.stage_bytes;
   };
   auto release_stage = [&]() {
     __syncwarp();
@@ -638,100 +693,168 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   };
   // The token after `skip` others of a set, -1 for none.
   auto token_of = [&](uint32_t tokens, int skip) {
+#pragma unroll 1
     for (int i = 0; i < skip; ++i) tokens &= tokens - 1;
     return tokens ? __ffs(tokens) - 1 : -1;
   };
   float* acc_w = s_acc + (size_t)warp * p.acc_floats;
+  uint32_t* off_w = s_off + warp * 64;
+  int16_t* choice_w = s_choice + warp * 64;
+  float* un_w = s_un + warp * 64;
 
-  // ---- gate and up ----
-  const uint8_t* x_base = p.x_pitch != 0 ? smem + p.off_x : p.xf;
-  const int64_t x_row = p.x_pitch != 0 ? p.x_pitch : spans_k * U::X_SPAN;
-  auto gu_tile = [&](auto groups, int e, int i0, uint32_t tokens) {
-    constexpr int GROUPS = decltype(groups)::value;
-    const int ng = GROUPS == 1 ? 1 : (__popc(tokens) + 7) / 8;
-    int tok[GROUPS];
-    float acc[GROUPS][4];
-    Columns<GROUPS> col;
-#pragma unroll
-    for (int g = 0; g < GROUPS; ++g) {
-      tok[g] = g < ng ? token_of(tokens, 8 * g + q) : -1;
-      col.p[g] = x_base + (tok[g] >= 0 ? tok[g] : __ffs(tokens) - 1) * x_row + span0 * U::X_SPAN + c * 16;
-      acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
-    }
-    col.start();
-    for (int span = span0; span < span1 && live; span += U::NS) {
-      if (!wait_stage()) {
-        live = false;
-        break;
-      }
-      const uint8_t* st = ring + (size_t)slot * U::STAGE;
-      const uint8_t* ra = unit_at(st, q, gu_row(e, i0, q) + span * U::SPAN);
-      const uint8_t* rb = unit_at(st, q + 8, gu_row(e, i0, q + 8) + span * U::SPAN);
-      const int n = min(U::NS, span1 - span);
-      for (int k = 0; k < n; ++k)
-        span_products<V, ALIGNED, 0, GROUPS>(ra + k * SPAN_STEP, rb + k * SPAN_STEP, (span + k) * U::SPAN_BLOCKS + c * U::BLOCKS, nb_k, ng, col, acc);
-      release_stage();
-    }
-    if (KP > 1) {  // the parts' sums, in order
-      if (part > 0) {
-#pragma unroll
-        for (int g = 0; g < GROUPS; ++g)
-          if (g < ng) *reinterpret_cast<float4*>(acc_w + (g * 32 + lane) * 4) = make_float4(acc[g][0], acc[g][1], acc[g][2], acc[g][3]);
-      }
-      team_barrier(1 + team, KP * 32);
-      if (part == 0) {
-        for (int w = 1; w < KP; ++w) {
-          const float* other = acc_w + (size_t)w * p.acc_floats;
-#pragma unroll
-          for (int g = 0; g < GROUPS; ++g)
-            if (g < ng) {
-              const float4 v = *reinterpret_cast<const float4*>(other + (g * 32 + lane) * 4);
-              acc[g][0] += v.x, acc[g][1] += v.y, acc[g][2] += v.z, acc[g][3] += v.w;
-            }
-        }
-      }
-      team_barrier(1 + team, KP * 32);
-      if (part > 0) return;
-    }
-    // Lane (q, c): gate and up of hidden value i0 + q for columns 2 c and 2 c + 1.
-    const int i = i0 + q;
-    const int64_t place = h_place(i);
-#pragma unroll
-    for (int g = 0; g < GROUPS; ++g) {
-      if (g >= ng) break;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int m = __shfl_sync(0xffffffffu, tok[g], (2 * c + j) * 4);
-        float h = 0.f;
-        int a = 0;
-        if (m >= 0) {
-          const float un = s_unscale[m], gate = acc[g][j] * un, up = acc[g][2 + j] * un;
-          h = gate / (1.f + expf(-gate)) * up;
-          a = m * p.top_k + s_slot[m * p.E + e];
-          p.h[(int64_t)a * p.I + i] = h;
-          const float hs = h * (float)(1 << kFastExp);
-          const __half hi = __float2half_rn(hs);
-          *reinterpret_cast<__half*>(p.h_hi + a * h_row + place) = hi;
-          *reinterpret_cast<__half*>(p.h_lo + a * h_row + place) = __float2half_rn(hs - __half2float(hi));
-        }
-        uint32_t mx = __float_as_uint(h) & 0x7FFFFFFFu;
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        if (q == 0 && m >= 0) atomicMax(p.amax + a, mx);
-      }
-    }
+  // The h parts of an expert's first token on their way to L1, one expert ahead of use.
+  auto fetch_h = [&](int at) {
+    const int e = s_list[at], m = __ffs(s_mask[e]) - 1;
+    const int64_t row = (m * p.top_k + s_slot[m * p.E + e]) * h_row;
+    for (int64_t i = lane * 128; i < h_row && i < 4096; i += 4096) touch(p.h_hi + row + i), touch(p.h_lo + row + i);
   };
-  for (int id = first_gu; id < gu_tiles; id += G * teams) {
-    const int e = s_list[id / per_expert], i0 = id % per_expert * 8;
-    const uint32_t tokens = s_mask[e];
-    if (__popc(tokens) <= 8) gu_tile(std::integral_constant<int, 1>{}, e, i0, tokens);
-    else gu_tile(std::integral_constant<int, kGuGroups>{}, e, i0, tokens);
-  }
-  ok = grid_barrier(p.bars + 1) && ok;  // every h is written
+  // ---- the two products: gate and up (phase 0), then down (phase 1) ----------------------
+  // One loop for both, and one copy of its code: a launch meets most of it
+  // once, and instruction fetches are a good part of a short call.
+  float* y_w = s_y + warp * (kTileRows * p.M);  // down: the warp's part of a tile's outputs
+  float4* sums = reinterpret_cast<float4*>(acc_w) + lane;
+#pragma unroll 1
+  for (int phase = 0; phase < 2; ++phase) {
+    const bool down = phase == 1;
+    const int nb = down ? nb_i : nb_k;
+    // Columns: eight tokens; or the high parts of four tokens' h, then their remainders.
+    const int width = down ? 4 : 8;
+    const uint8_t* b0 = (down ? (q < 4 ? p.h_hi : p.h_lo) : p.xf) + c * 16;
+    const uint32_t b_row = (uint32_t)(down ? h_row : (int64_t)spans_k * U::X_SPAN);
+    const int rounds = !ok ? 0 : down ? my_tiles : 1;
+    int noted = -1, ng = 0;  // the place in the list whose columns are noted
+#pragma unroll 1
+    for (int round = 0; round < rounds; ++round) {
+      if (down) {
+        for (int i = lane; i < kTileRows * p.M; i += 32) y_w[i] = 0.f;
+        __syncwarp();
+      }
+      // gate/up: tile x and every span of this warp's part; down: stages from x on of one expert
+#pragma unroll 1
+      for (int x = down ? u0 : gu0; x < (down ? u1 : gu1);) {
+        const int at = x / (down ? sd : per_expert), e = s_list[at];
+        int row0, s0, s1;
+        if (down) {
+          const int last = min(u1, (at + 1) * sd);
+          row0 = (blockIdx.x + round * G) * kTileRows;
+          s0 = (x - at * sd) * ns;
+          s1 = min(spans_i, (last - at * sd) * ns);
+          x = last;
+        } else {
+          row0 = (x - at * per_expert) * 8;
+          s0 = span0, s1 = span1;
+          x += teams;
+        }
+        if (at != noted) {
+          if (down && x < u1) fetch_h(at + 1);
+          noted = at;
+          const uint32_t tokens = s_mask[e];
+          ng = (__popc(tokens) + width - 1) / width;
+          __syncwarp();
+#pragma unroll 1
+          for (int n = lane; n < 8 * ng; n += 32) {  // column n: token width * (n / 8) + n % width of the set
+            const int t = token_of(tokens, width * (n >> 3) + (n & (width - 1))), m = t >= 0 ? t : __ffs(tokens) - 1;
+            const int a = m * p.top_k + s_slot[m * p.E + e];
+            off_w[n] = (uint32_t)(down ? a : m) * b_row;
+            choice_w[n] = (int16_t)(t < 0 ? -1 : down ? m : a);
+            un_w[n] = down ? s_probs[a] : s_unscale[m];
+          }
+          __syncwarp();
+        }
+        int ma = 0, mb = 0;
+        if constexpr (!ALIGNED) {
+          ma = mis16(down ? dn_row(e, row0, q) : gu_row(e, row0, q));
+          mb = mis16(down ? dn_row(e, row0, q + 8) : gu_row(e, row0, q + 8));
+        }
+        auto stages = [&](auto& col) {
+#pragma unroll 1
+          for (int span = s0; span < s1; span += ns) {
+            const uint8_t* st = wait_stage();
+            const int n = min(ns, s1 - span);
+#pragma unroll 1
+            for (int k = 0; k < n; ++k)
+              col.template unit<V, ALIGNED, 0>(st + unit_a + ma + k * STEP, st + unit_b + mb + k * STEP, (span + k) * U::SPAN_BLOCKS + c * U::BLOCKS, nb);
+            release_stage();
+          }
+        };
+        if (ng == 1) {
+          Column col;
+          col.start(b0 + off_w[q] + s0 * U::X_SPAN);
+          stages(col);
+          sums[0] = make_float4(col.acc[0], col.acc[1], col.acc[2], col.acc[3]);
+        } else {
+          Columns col{b0 + s0 * U::X_SPAN, off_w + q, sums, ng};
+          for (int g = 0; g < ng; ++g) sums[32 * g] = make_float4(0.f, 0.f, 0.f, 0.f);
+          stages(col);
+        }
+        // Lane (q, c): rows q and q + 8, columns 2 c and 2 c + 1 of every group.
+        const int parts = down ? 1 : KP;
+        if (parts > 1) team_barrier(1 + team, KP * 32);
+        if (down) {
+#pragma unroll 1
+          for (int g = 0; g < ng; ++g) {
+            const float4 v = sums[32 * g];
+            const float s[4] = {v.x + __shfl_xor_sync(0xffffffffu, v.x, 2), v.y + __shfl_xor_sync(0xffffffffu, v.y, 2),
+                                v.z + __shfl_xor_sync(0xffffffffu, v.z, 2), v.w + __shfl_xor_sync(0xffffffffu, v.w, 2)};
+            if (c < 2) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int n = 8 * g + 2 * c + j, m = choice_w[n];
+                if (m >= 0) {
+                  float* y = y_w + m * kTileRows + q;
+                  y[0] += un_w[n] * s[j];
+                  y[8] += un_w[n] * s[2 + j];
+                }
+              }
+            }
+          }
+        } else if (part == 0) {
+          const int i = row0 + q;
+          const int64_t place = h_place(i);
+#pragma unroll 1
+          for (int g = 0; g < ng; ++g) {
+            float4 v = sums[32 * g];
+#pragma unroll 1
+            for (int w = 1; w < parts; ++w) {  // the parts' sums, in order
+              const float4 o = *reinterpret_cast<const float4*>(acc_w + (size_t)w * p.acc_floats + (32 * g + lane) * 4);
+              v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+            }
+            const float gates[2] = {v.x, v.y}, ups[2] = {v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int n = 8 * g + 2 * c + j, a = choice_w[n];
+              if (a >= 0) {
+                const float gate = gates[j] * un_w[n], up = ups[j] * un_w[n];
+                const float h = gate / (1.f + expf(-gate)) * up, hs = h * (float)(1 << kFastExp);
+                const __half hi = __float2half_rn(hs);
+                p.h[(int64_t)a * p.I + i] = h;
+                *reinterpret_cast<__half*>(p.h_hi + a * h_row + place) = hi;
+                *reinterpret_cast<__half*>(p.h_lo + a * h_row + place) = __float2half_rn(hs - __half2float(hi));
+                atomicMax(&s_amax[a], __float_as_uint(h) & 0x7FFFFFFFu);
+              }
+            }
+          }
+        }
+        if (parts > 1) team_barrier(1 + team, KP * 32);
+      }
+      if (down) {  // the warps' parts, in order
+        __syncthreads();
+        const int n0 = (blockIdx.x + round * G) * kTileRows;
+        for (int i = tid; i < kTileRows * p.M; i += kThreads) {
+          float y = 0.f;
+          for (int w = 0; w < kWarps; ++w) y += s_y[w * (kTileRows * p.M) + i];
+          p.Y[(int64_t)(i / kTileRows) * p.K + n0 + i % kTileRows] = y;
+        }
+        __syncthreads();
+      }
+    }
+    if (down) break;
 
-  // ---- h parts outside the fixed scale's range, made again; a choice's weight takes its scale ----
-  {
+    __syncthreads();
+    for (int a = tid; a < choices; a += kThreads)
+      if (s_amax[a] != 0) atomicMax(p.amax + a, s_amax[a]);
+    ok = grid_barrier(p.bars + 1) && ok;  // every h is written
+    // h parts outside the fixed scale's range are made again; a choice's weight takes its scale
     bool again = false;
     for (int a = tid; a < choices && ok; a += kThreads) {
       const uint32_t mx = __ldcg(p.amax + a);
@@ -740,10 +863,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       again = again || out;
     }
     if (__syncthreads_or(again)) {  // the same answer in every CTA
+#pragma unroll 1
       for (int a = blockIdx.x; a < choices; a += G) {
         const uint32_t mx = __ldcg(p.amax + a);
         if (fast_range(mx)) continue;
         const float scale = exp2i(scale_exp(mx));
+#pragma unroll 1
         for (int i = tid; i < p.I; i += kThreads) {
           const float hs = __ldcg(p.h + (int64_t)a * p.I + i) * scale;
           const __half hi = __float2half_rn(hs);
@@ -753,75 +878,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       }
       ok = grid_barrier(p.bars + 2) && ok;
     }
-  }
-  live = live && ok;
-
-  // ---- down: a tile of output rows at a time, its experts' stages shared by the warps ----
-  // column n < 4: the high part of the group's token n; n >= 4: the remainder of token n - 4
-  const uint8_t* h_base = (q < 4 ? p.h_hi : p.h_lo) + c * 16;
-  int u = 0;
-  auto dn_run = [&](auto groups, int e, int n0, int at, int end, uint32_t tokens) {  // stages [u, end) of one expert
-    constexpr int GROUPS = decltype(groups)::value;
-    const int ng = GROUPS == 1 ? 1 : (__popc(tokens) + 3) / 4;
-    int tok[GROUPS];
-    float acc[GROUPS][4];
-    Columns<GROUPS> col;
-#pragma unroll
-    for (int g = 0; g < GROUPS; ++g) {
-      tok[g] = g < ng ? token_of(tokens, 4 * g + (q & 3)) : -1;
-      const int m = tok[g] >= 0 ? tok[g] : __ffs(tokens) - 1;
-      col.p[g] = h_base + (m * p.top_k + s_slot[m * p.E + e]) * h_row + (u - at * sd) * (U::NS * U::X_SPAN);
-      acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
-    }
-    col.start();
-    for (; u < end; ++u) {
-      if (!wait_stage()) {
-        live = false;
-        break;
-      }
-      const uint8_t* st = ring + (size_t)slot * U::STAGE;
-      const int span = (u - at * sd) * U::NS, n = min(U::NS, spans_i - span);
-      const uint8_t* ra = unit_at(st, q, dn_row(e, n0, q) + span * U::SPAN);
-      const uint8_t* rb = unit_at(st, q + 8, dn_row(e, n0, q + 8) + span * U::SPAN);
-      for (int k = 0; k < n; ++k)
-        span_products<V, ALIGNED, 0, GROUPS>(ra + k * SPAN_STEP, rb + k * SPAN_STEP, (span + k) * U::SPAN_BLOCKS + c * U::BLOCKS, nb_i, ng, col, acc);
-      release_stage();
-    }
-    // columns 2 c, 2 c + 1 (c < 2) with their remainders, of rows q and q + 8
-#pragma unroll
-    for (int g = 0; g < GROUPS; ++g) {
-      if (g >= ng) break;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[g][i] += __shfl_xor_sync(0xffffffffu, acc[g][i], 2);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int m = __shfl_sync(0xffffffffu, tok[g], ((2 * c + j) & 3) * 4);
-        if (c < 2 && m >= 0) {
-          const float w = s_probs[m * p.top_k + s_slot[m * p.E + e]];
-          acc_w[q * p.M + m] += w * acc[g][j];
-          acc_w[(q + 8) * p.M + m] += w * acc[g][2 + j];
-        }
-      }
-    }
-  };
-  for (int tile = 0; tile < my_tiles && ok; ++tile) {
-    const int n0 = (blockIdx.x + tile * G) * kTileRows;
-    for (int i = lane; i < kTileRows * p.M; i += 32) acc_w[i] = 0.f;
-    __syncwarp();
-    for (u = u0; u < u1 && live;) {
-      const int at = u / sd, end = min(u1, (at + 1) * sd), e = s_list[at];
-      const uint32_t tokens = s_mask[e];
-      if (__popc(tokens) <= 4) dn_run(std::integral_constant<int, 1>{}, e, n0, at, end, tokens);
-      else dn_run(std::integral_constant<int, kDnGroups>{}, e, n0, at, end, tokens);
-    }
-    __syncthreads();
-    for (int i = tid; i < kTileRows * p.M; i += kThreads) {
-      const int m = i / kTileRows, r = i % kTileRows;
-      float y = 0.f;
-      for (int w = 0; w < kWarps; ++w) y += s_acc[(size_t)w * p.acc_floats + r * p.M + m];
-      p.Y[(int64_t)m * p.K + n0 + r] = y;
-    }
-    __syncthreads();
   }
   // copies that no one waited for (after a wait gave up) land before the CTA leaves
   for (; used < filled; next_slot()) (void)mbar_wait_bounded(smem_addr(&bars[slot]), parity);
@@ -838,7 +894,7 @@ MoeFn pick(int act, bool aligned) {
   return aligned ? moe_kernel<V, 1, true> : moe_kernel<V, 1, false>;
 }
 
-constexpr int kSmemMax = 227 * 1024 - 2560;  // dynamic; the rest is the kernel's static shared memory
+constexpr int kSmemMax = 227 * 1024 - (kWarps * 640 + 6144);  // dynamic; the rest is the kernel's static shared memory
 constexpr int kSlack = 32;                   // word reads past the last row slot
 
 int up16(int v) { return (v + 15) / 16 * 16; }
@@ -846,7 +902,7 @@ int up16(int v) { return (v + 15) / 16 * 16; }
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 template <int V>
-cudaError_t set_up(const MoeArgs& a, int sms, MoeParams* p, int* smem) {
+cudaError_t set_up(const MoeArgs& a, int sms, bool aligned, MoeParams* p, int* smem) {
   using U = Unit<V>;
   int at = up16(p->M * p->top_k * 4);
   p->off_mask = at;
@@ -857,32 +913,25 @@ cudaError_t set_up(const MoeArgs& a, int sms, MoeParams* p, int* smem) {
   at += up16(p->M * p->E);
   p->off_unscale = at;
   at += up16(p->M * 4);
-  p->off_keys = at;
-  at += kWarps * up16(p->E * 4);
+  p->off_y = at;
+  at += kWarps * kTileRows * p->M * 4;
   p->off_acc = at;
-  const int groups = (p->M + 7) / 8;
-  p->acc_floats = kTileRows * p->M > groups * 128 ? kTileRows * p->M : groups * 128;
+  p->acc_floats = (p->M + 3) / 4 * 128;  // a warp's sums of a tile, by group
   at += kWarps * p->acc_floats * 4;
-  const int64_t spans_k = (a.K / 32 + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS, spans_i = (a.I / 32 + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS;
-  // The activations go to shared memory where the ring keeps two stages next
-  // to them; rows 64 bytes off a multiple of 128, so that two tokens' loads
-  // meet no bank twice.  Else they are read through L1.
-  const int64_t x_bytes = a.M * (spans_k * U::X_SPAN + 64) + 256;
-  p->off_x = at;
-  if (x_bytes <= kSmemMax - kSlack - 128 - at - 2 * kWarps * U::STAGE) {
-    p->x_pitch = (int)(spans_k * U::X_SPAN + 64);
-    at += (int)x_bytes;
-  }
   p->off_ring = (at + 127) / 128 * 128;
-  const int room = (kSmemMax - p->off_ring - kSlack) / (kWarps * U::STAGE);
-  p->stages = room < kMaxStages ? room : kMaxStages;
-  if (p->stages < 1) return cudaErrorInvalidConfiguration;
-  *smem = p->off_ring + kWarps * p->stages * U::STAGE + kSlack;
   // Warps to a gate/up tile: one where every SM has tiles for its warps, more
   // where the (at most min(E, M top_k)) chosen experts give it fewer.
+  const int64_t spans_k = (a.K / 32 + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS, spans_i = (a.I / 32 + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS;
   const int64_t experts = a.M * a.top_k < a.E ? a.M * a.top_k : a.E;
   p->parts = 1;
-  while (kWarps % (2 * p->parts) == 0 && p->parts < 8 && 2 * p->parts <= spans_k && experts * (a.I / 8) * p->parts < 8 * (int64_t)sms) p->parts *= 2;
+  while (p->parts < 4 && 2 * p->parts <= spans_k && experts * (a.I / 8) * p->parts < 8 * (int64_t)sms) p->parts *= 2;
+  p->ns = V == 0 ? 2 : 1;  // spans of a stage
+  const int each = aligned ? p->ns * kTileRows * U::SPAN : kTileRows * row_pitch<V, false>(p->ns);
+  p->stage_bytes = (each + 127) / 128 * 128;
+  const int room = (kSmemMax - p->off_ring - kSlack) / (kWarps * p->stage_bytes);
+  p->stages = room < kMaxStages ? room : kMaxStages;
+  if (p->stages < 1) return cudaErrorInvalidConfiguration;
+  *smem = p->off_ring + kWarps * p->stages * p->stage_bytes + kSlack;
   // Workspace: logits, activation scales, largest |h|, then 16-byte aligned arrays.
   const int64_t choices = a.M * a.top_k;
   float* w = a.ws;
@@ -902,18 +951,17 @@ cudaError_t set_up(const MoeArgs& a, int sms, MoeParams* p, int* smem) {
 
 template <int V>
 cudaError_t encode_maps(const MoeArgs& a, MoeParams* p) {
-  using U = Unit<V>;
   const cuuint64_t rb_k = a.K / 32 * Fmt<V>::BB, rb_i = a.I / 32 * Fmt<V>::BB;
-  const cuuint32_t one[3] = {1, 1, 1};
+  const cuuint32_t one[3] = {1, 1, 1}, words = Unit<V>::SPAN / 4;
   {
     const cuuint64_t dims[3] = {rb_k / 4, (cuuint64_t)a.I, 2 * (cuuint64_t)a.E}, strides[2] = {rb_k, rb_k * a.I};
-    const cuuint32_t box[3] = {U::SPAN / 4, 8, 2};
+    const cuuint32_t box[3] = {words, 8, 2};
     if (g_encode(&p->map_gu, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(a.Wgu), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
   const cuuint64_t dims[2] = {rb_i / 4, (cuuint64_t)(a.E * a.K)}, strides[1] = {rb_i};
-  const cuuint32_t box[2] = {U::SPAN / 4, kTileRows};
+  const cuuint32_t box[2] = {words, kTileRows};
   if (g_encode(&p->map_dn, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(a.Wd), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
@@ -960,11 +1008,11 @@ cudaError_t launch_moe(int variant, int act, const MoeArgs& a, int sms, cudaStre
   p.router_type = a.router_type;
   p.route = a.route;
   p.route_scale = a.route_scale;
-  int smem = 0;
-  cudaError_t e = variant == 0 ? set_up<0>(a, sms, &p, &smem) : set_up<1>(a, sms, &p, &smem);
-  if (e != cudaSuccess) return e;
   const int ku = variant == 0 ? Fmt<0>::KU : Fmt<1>::KU;
-  const bool aligned = a.K % ku == 0 && a.I % ku == 0 && a.E * a.K < (int64_t(1) << 31);
+  const bool aligned = a.K % ku == 0 && a.I % ku == 0;
+  int smem = 0;
+  cudaError_t e = variant == 0 ? set_up<0>(a, sms, aligned, &p, &smem) : set_up<1>(a, sms, aligned, &p, &smem);
+  if (e != cudaSuccess) return e;
   if (aligned && (e = variant == 0 ? encode_maps<0>(a, &p) : encode_maps<1>(a, &p)) != cudaSuccess) return e;
   const MoeFn fn = variant == 0 ? pick<0>(act, aligned) : pick<1>(act, aligned);
   cudaLaunchConfig_t cfg = {};
