@@ -413,7 +413,7 @@ rocmfp4_status moe(MoeArgs a, int variant, int act, cudaStream_t s) {
 rocmfp4_status logprobs(LogprobsArgs a, int64_t top_n, cudaStream_t s) {
   if (!valid_dtype(a.type)) return fail(ROCMFP4_ERR_INVALID_ARG, "unknown type");
   if (a.M < 0 || a.V < 0 || top_n < 0) return fail(ROCMFP4_ERR_INVALID_ARG, "negative size");
-  if (!(a.scale > 0.f) || a.scale > 3.4e38f) return fail(ROCMFP4_ERR_INVALID_ARG, "scale must be finite and positive");
+  if (!(a.scale >= 1e-30f && a.scale <= 1e30f)) return fail(ROCMFP4_ERR_INVALID_ARG, "scale must be from 1e-30 to 1e30");
   if (a.M == 0) return ROCMFP4_OK;
   if (a.V == 0) return fail(ROCMFP4_ERR_INVALID_ARG, "V must be positive");
   if (a.ld < a.V) return fail(ROCMFP4_ERR_INVALID_ARG, "row stride below V");

@@ -14,11 +14,13 @@
 //
 // Top n.  Values are compared as 64-bit keys (order-preserving bits of the
 // logit, complement of the index), so ties go to the lowest index and keys
-// are distinct.  From a first tile of the range a threshold T is taken that
-// at least n of its values reach: the n-th largest of 64 disjoint groups'
-// maxima.  Values that reach T go to a candidate list in shared memory; later
-// tiles contribute only values above T, so almost every value costs one
-// comparison.  The list is cut back to n when it fills, which raises T.
+// are distinct.  From the first tile of the range a threshold is taken that at
+// least n of its values reach: the n-th largest of 64 disjoint groups' maxima.
+// Values that reach it go to a candidate list in shared memory; later tiles
+// contribute only values above it, so almost every value costs one comparison
+// and the tiles need no barrier.  Every eighth tile the list is cut back to n,
+// which raises the threshold.  A row that overfills the list all the same (one
+// that rises through the range) has its top n looked for again, tile by tile.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -26,12 +28,11 @@ namespace rocmfp4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVecs = 4;        // 16-byte vectors a thread takes of a tile
+constexpr int kVecs = 2;        // 16-byte vectors a thread takes of a tile
 constexpr int kGroups = 64;     // groups of 4 neighbouring threads
 constexpr int kCutAt = 256;     // candidates at which the list is cut back to n
+constexpr int kCap = 1024;      // room of the list: n threads' values of a tile and more
 constexpr float kLog2e = 1.4426950408889634f;
-
-constexpr int list_cap(int per_thread) { return kMaxTop * per_thread + 2 * kMaxTop; }
 
 // Order-preserving bits: a < b as floats iff key(a) < key(b); -0 counts as +0
 // and every NaN as the largest.
@@ -45,6 +46,10 @@ RF4_DEV float unordered(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 RF4_DEV uint64_t key_of(float f, uint32_t index) { return ((uint64_t)ordered(f) << 32) | (uint32_t)~index; }
+
+// A distance below the maximum at which exp(scale * distance) is 0 for every
+// accepted scale; takes the place of -inf, so that 0 * distance stays 0.
+constexpr float kFarBelow = -3.0e38f;
 
 RF4_DEV float ex2(float x) {
   float y;
@@ -127,7 +132,7 @@ struct Logit<2> {
 
 struct TopState {  // in shared memory
   int count;       // candidates pushed (may pass the capacity: then `over`)
-  int kept;        // candidates before the current tile
+  int kept;        // scratch of cut()
   uint64_t floor;  // values must have a larger key to become candidates
   uint64_t group[kGroups];
   uint64_t best[kMaxTop];
@@ -210,16 +215,17 @@ RF4_DEV void cut(TopState& st, uint64_t* list, uint64_t* spare, int count, int n
 constexpr int kRecordBytes = 16 + 8 * kMaxTop;
 
 template <int TYPE, bool TOP>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constant__ LogprobsArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_constant__ LogprobsArgs a) {
   using L = Logit<TYPE>;
   using E = typename L::type;
-  constexpr int PER = L::PER, N = kVecs * PER, CAP = list_cap(N);
+  constexpr int PER = L::PER, N = kVecs * PER, TILE = kThreads * kVecs;  // vectors of a tile
+  static_assert(kMaxTop * N + kMaxTop <= kCap && kCutAt + kThreads <= kCap, "what a search by tiles pushes has room");
   __shared__ TopState st;
-  __shared__ uint64_t lists[TOP ? 2 * CAP : 1];
+  __shared__ uint64_t lists[TOP ? 2 * kCap : 1];
   __shared__ Stats warp_stats[kThreads / 32];
   __shared__ int last;
   uint64_t* list = lists;
-  uint64_t* spare = lists + (TOP ? CAP : 0);
+  uint64_t* spare = lists + (TOP ? kCap : 0);
   grid_launch_dependents();
   grid_dependency_wait();
   const int tid = threadIdx.x, n = a.top_n, P = a.splits;
@@ -228,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
   const E* z = static_cast<const E*>(a.logits) + row * a.ld;
   const float c = a.scale * kLog2e;
   if (TOP && tid == 0) {
-    st.count = st.kept = 0;
+    st.count = 0;
     st.floor = 0;
   }
   __syncthreads();
@@ -239,110 +245,123 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
   const uint4* vz = reinterpret_cast<const uint4*>(z - lead);
   const int64_t vecs = (a.V + lead + PER - 1) / PER;
   const int64_t v0 = vecs * part / P, v1 = vecs * (part + 1) / P;
+  // A tile whose every vector is this range's and wholly inside the row: the same for all threads.
+  auto whole = [&](int64_t base) { return base + TILE <= v1 && base * PER >= lead && (base + TILE) * PER <= a.V + lead; };
+  auto fetch = [&](int64_t base, uint4 (&w)[kVecs]) {
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) w[k] = __ldcs(vz + base + k * kThreads + tid);
+  };
+  // index of value i of this thread's in a tile, and whether there is such a value
+  auto index = [&](int64_t base, int i) { return (base + (i / PER) * kThreads + tid) * PER - lead + i % PER; };
+  auto present = [&](int64_t base, int i) {
+    const int64_t e = index(base, i);
+    return base + (i / PER) * kThreads + tid < v1 && e >= 0 && e < a.V;
+  };
 
   Stats s;
-  bool first = true;
-  for (int64_t base = v0; base < v1; base += kThreads * kVecs) {
+  uint4 w[kVecs];
+  if (v0 < v1 && whole(v0)) fetch(v0, w);
+  int tiles = 0;
+  uint64_t floor = 0;  // candidates have larger keys
+#pragma unroll 1
+  for (int64_t base = v0; base < v1; base += TILE, ++tiles) {
     float v[N];
-    uint32_t idx[kVecs];  // index of the vector's first value
-    uint32_t have = 0;    // vectors that are wholly inside the row; others are read value by value
+    const bool full = whole(base);
+    if (full) {
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      const int64_t p = base + k * kThreads + tid;
-      const int64_t e = p * PER - lead;
-      idx[k] = (uint32_t)e;
-      if (p < v1 && e >= 0 && e + PER <= a.V) {
-        L::unpack(__ldg(vz + p), v + k * PER);
-        have |= 1u << k;
-      } else {
+      for (int k = 0; k < kVecs; ++k) L::unpack(w[k], v + k * PER);
+    } else {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) v[k * PER + j] = p < v1 && e + j >= 0 && e + j < a.V ? L::one(z[e + j]) : -INFINITY;
-      }
+      for (int i = 0; i < N; ++i) v[i] = present(base, i) ? L::one(z[index(base, i)]) : -INFINITY;
     }
-    float tm = -INFINITY;
+    if (whole(base + TILE)) fetch(base + TILE, w);  // the next tile is on its way while this one is summed
+    float tm = v[0];
 #pragma unroll
-    for (int i = 0; i < N; ++i) tm = fmaxf(tm, v[i]);
+    for (int i = 1; i < N; ++i) tm = fmaxf(tm, v[i]);
     const float m = fmaxf(s.m, tm);
-    rescale(s.S, s.A, s.m, m, c);
-    s.m = m;
+    if (m > s.m) {
+      rescale(s.S, s.A, s.m, m, c);
+      s.m = m;
+    }
     const float mm = m == -INFINITY ? 0.f : m;  // nothing but -inf yet: e = 0
     float S[2] = {0.f, 0.f}, A[2] = {0.f, 0.f};  // the tile's sums on their own: short chains
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float d = v[i] - mm, e = ex2(d * c);
+      const float d = max_nan(v[i] - mm, kFarBelow), e = ex2(d * c);
       S[i & 1] += e;
-      A[i & 1] = fmaf(e, max_nan(d, -3.4028235e38f), A[i & 1]);  // a finite factor: 0 * d stays 0
+      A[i & 1] = fmaf(e, d, A[i & 1]);
     }
     s.S += S[0] + S[1];
     s.A += A[0] + A[1];
     if constexpr (TOP) {
-      // whether value i of this thread is one of the row's
-      auto present = [&](int i) {
-        const int k = i / PER, j = i % PER;
-        if (have >> k & 1u) return true;
-        const int64_t p = base + k * kThreads + tid, e = p * PER - lead + j;
-        return p < v1 && e >= 0 && e < a.V;
-      };
-      auto key = [&](int i) { return key_of(v[i], idx[i / PER] + i % PER); };
-      auto largest = [&](uint64_t above) {  // the thread's largest key above a bound, 0 for none
-        uint64_t best = 0;
+      if (tiles == 0) {
+        uint64_t best = 0;  // the thread's largest key
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const uint64_t k = key(i);
-          if (k > best && k > above && present(i)) best = k;
+          const uint64_t k = key_of(v[i], (uint32_t)index(base, i));
+          if (k > best && present(base, i)) best = k;
         }
-        return best;
-      };
-      // NaN compares as the largest value: fmaxf skips it, the sum does not
-      uint64_t floor = st.floor;
-      if (first) {
-        const uint64_t t = group_threshold(st, largest(0), n);
+        const uint64_t t = group_threshold(st, best, n);
         floor = t > 0 ? t - 1 : 0;
-        first = false;
       }
+      // NaN compares as the largest value: fmaxf skips it, the sum does not
       const float fv = unordered((uint32_t)(floor >> 32));
-      if (!(tm < fv) || s.S != s.S || floor == 0) {
-#pragma unroll
+      if (!(tm < fv) || s.S != s.S) {
+#pragma unroll 1
         for (int i = 0; i < N; ++i) {
-          if (v[i] < fv && floor != 0) continue;
-          const uint64_t k = key(i);
-          if (k > floor && present(i)) {
+          if (!present(base, i)) continue;
+          const uint64_t k = key_of(L::one(z[index(base, i)]), (uint32_t)index(base, i));
+          if (k > floor) {
             const int at = atomicAdd(&st.count, 1);
-            if (at < CAP) list[at] = k;
+            if (at < kCap) list[at] = k;
           }
         }
       }
-      __syncthreads();
-      int count = st.count;
-      if (count > CAP) {
-        // More candidates than the list holds (a rising or constant row).
-        // Back to those before this tile; of the tile, the keys that reach
-        // the n-th largest of the threads' largest keys: at most n threads'.
-        const int kept = st.kept;
+      if ((tiles & 7) == 7) {
         __syncthreads();
-        cut(st, list, spare, kept, n);
-        const uint64_t t = thread_threshold(spare, largest(st.floor), n);
-        const uint64_t above = t > st.floor ? t - 1 : st.floor;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const uint64_t k = key(i);
-          if (k > above && present(i)) {
-            const int at = atomicAdd(&st.count, 1);
-            if (at < CAP) list[at] = k;
-          }
+        const int count = st.count;
+        __syncthreads();
+        if (count > kCutAt && count <= kCap) {
+          cut(st, list, spare, count, n);
+          floor = st.floor;
         }
-        __syncthreads();
-        count = st.count;
-      }
-      if (count > kCutAt) {
-        cut(st, list, spare, count, n);
-      } else {
-        if (tid == 0) st.kept = count;
-        __syncthreads();
       }
     }
   }
-
+  if constexpr (TOP) {
+    __syncthreads();
+    const int pushed = st.count;
+    __syncthreads();
+    if (pushed > kCap) {
+      // More candidates than the list holds.  Again over the range: of each
+      // tile the keys above the n-th that also reach the n-th largest of the
+      // threads' largest ones, at most n threads' values.
+      if (tid == 0) st.count = 0, st.floor = 0;
+      __syncthreads();
+#pragma unroll 1
+      for (int64_t base = v0; base < v1; base += TILE) {
+        const uint64_t least = st.floor;
+        uint64_t best = 0;
+#pragma unroll 1
+        for (int i = 0; i < N; ++i) {
+          const uint64_t k = present(base, i) ? key_of(L::one(z[index(base, i)]), (uint32_t)index(base, i)) : 0;
+          if (k > least && k > best) best = k;
+        }
+        if (__syncthreads_or(best != 0) == 0) continue;
+        const uint64_t t = thread_threshold(spare, best, n);
+        const uint64_t above = t > least ? t - 1 : least;
+#pragma unroll 1
+        for (int i = 0; i < N; ++i) {
+          const uint64_t k = present(base, i) ? key_of(L::one(z[index(base, i)]), (uint32_t)index(base, i)) : 0;
+          if (k > above) list[atomicAdd(&st.count, 1)] = k;
+        }
+        __syncthreads();
+        const int count = st.count;
+        __syncthreads();
+        cut(st, list, spare, count, n);
+      }
+    }
+  }
   // the CTA's statistics, joined in a fixed order
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) merge(s, shfl_xor(s, o), c);

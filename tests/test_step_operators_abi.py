@@ -52,7 +52,7 @@ def logprobs(L, **kw):
 
 @pytest.mark.parametrize("kw", [
     dict(type=3), dict(M=-1), dict(V=-1), dict(V=0, top_n=0), dict(top_n=-1), dict(top_n=101), dict(scale=0.0), dict(scale=-1.0), dict(scale=NAN),
-    dict(scale=INF), dict(ld=99), dict(logits=None), dict(logprob=None), dict(top_ids=None), dict(top_logprobs=None), dict(logits=PTR + 2),
+    dict(scale=INF), dict(scale=1e-31), dict(scale=1e31), dict(ld=99), dict(logits=None), dict(logprob=None), dict(top_ids=None), dict(top_logprobs=None), dict(logits=PTR + 2),
     dict(targets=PTR + 1), dict(top_ids=PTR + 2), dict(entropy=PTR + 2)])
 def test_logprobs_invalid(L, kw):
     assert logprobs(L, **kw) == INVALID
