@@ -18,7 +18,7 @@
 // least n of its values reach: the n-th largest of 64 disjoint groups' maxima.
 // Values that reach it go to a candidate list in shared memory; later tiles
 // contribute only values above it, so almost every value costs one comparison
-// and the tiles need no barrier.  Every eighth tile the list is cut back to n,
+// and the tiles need no barrier.  After 2, 4, 8, ... tiles the list is cut back to n,
 // which raises the threshold.  A row that overfills the list all the same (one
 // that rises through the range) has its top n looked for again, tile by tile.
 #include "common.cuh"
@@ -30,7 +30,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVecs = 2;        // 16-byte vectors a thread takes of a tile
 constexpr int kGroups = 64;     // groups of 4 neighbouring threads
-constexpr int kCutAt = 256;     // candidates at which the list is cut back to n
+constexpr int kCutAt = 256;     // candidates at which the join of a row's ranges cuts its list back to n
 constexpr int kCap = 1024;      // room of the list: n threads' values of a tile and more
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -307,8 +307,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
       // NaN compares as the largest value: fmaxf skips it, the sum does not
       const float fv = unordered((uint32_t)(floor >> 32));
       if (!(tm < fv) || s.S != s.S) {
-#pragma unroll 1
-        for (int i = 0; i < N; ++i) {
+        uint32_t hits = 0;  // values that may be candidates: seldom more than one
+#pragma unroll
+        for (int i = 0; i < N; ++i) hits |= (v[i] < fv ? 0u : 1u) << i;
+        for (; hits != 0; hits &= hits - 1) {
+          const int i = __ffs(hits) - 1;
           if (!present(base, i)) continue;
           const uint64_t k = key_of(L::one(z[index(base, i)]), (uint32_t)index(base, i));
           if (k > floor) {
@@ -317,11 +320,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
           }
         }
       }
-      if ((tiles & 7) == 7) {
+      // The threshold of t tiles lets about n / t values of the next one pass:
+      // it is raised after 2, 4, 8, ... tiles.
+      if (tiles > 0 && ((tiles & (tiles + 1)) == 0 || (tiles & 31) == 31)) {
         __syncthreads();
         const int count = st.count;
         __syncthreads();
-        if (count > kCutAt && count <= kCap) {
+        if (count > n && count <= kCap) {
           cut(st, list, spare, count, n);
           floor = st.floor;
         }
