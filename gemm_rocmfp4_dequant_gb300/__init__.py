@@ -259,22 +259,23 @@ def decode_attention(q, K, V, lens, Hkv: int, Tmax: int, scale: float, variant: 
 
 def _rows(t, name: str):
     """(rows, width, row stride) of a [rows, width] or [width] CUDA tensor whose rows are contiguous."""
-    d = t.dim()
-    if d == 2:
-        M, D = t.shape
-        ld, step = t.stride()
-    elif d == 1:
-        M, D = 1, t.shape[0]
-        ld, step = D, t.stride(0)
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        M, D = shape
+        ld, step = stride
+        if M == 1 and ld < D:
+            ld = D
+    elif len(shape) == 1:
+        M, D, ld, step = 1, shape[0], shape[0], stride[0]
     else:
         raise ValueError(f"{name} must be a [rows, width] or [width] tensor")
-    if not t.is_cuda or (step != 1 and D > 1):
+    if (step != 1 and D > 1) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor with contiguous rows")
-    return M, D, (ld if M > 1 else max(ld, D))
+    return M, D, ld
 
 
 def _dense(t, name: str, dtype, shape):
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
     return t
 
@@ -298,47 +299,49 @@ def add_rmsnorm(x, weight, residual=None, eps: float = 1e-6, dtype=None, y=None,
     ``residual``  h in the residual's type, into ``residual_out`` if given, else in place of ``residual``;
     ``q``, ``scales``  with group 32, 64 or 128 (or -1: the row), y in 8 bits: e4m3 values [M, D] and float32 scales
                   [M, groups], y being about q * scale; into ``q`` and ``scales`` if given."""
-    torch = _torch()
     codes = _DTYPES or _dtypes()
     M, D, ldx = _rows(x, "x")
-    ldr = ldro = 0
-    rtype = OUT_F32
+    shape = x.shape
+    ldr = ldro = rptr = roptr = yptr = qptr = sptr = size = 0
+    rtype, act = OUT_F32, ACT_F16
     if residual is not None:
+        _, _, ldr = _rows(residual, "residual")
+        dt = residual.dtype
+        rtype, rptr = codes.get(dt, -1), residual.data_ptr()
         if residual_out is None:
-            residual_out = residual
-        Mr, Dr, ldr = _rows(residual, "residual")
-        Mo, Do, ldro = _rows(residual_out, "residual_out")
-        if (Mr, Dr, Mo, Do) != (M, D, M, D) or residual.dtype is not residual_out.dtype:
+            residual_out, ldro, roptr = residual, ldr, rptr
+        else:
+            _, _, ldro = _rows(residual_out, "residual_out")
+            roptr = residual_out.data_ptr()
+        if residual.shape != shape or residual_out.shape != shape or residual_out.dtype is not dt:
             raise ValueError("residual and residual_out must have x's shape and one type")
-        rtype = codes.get(residual.dtype, -1)
     elif residual_out is not None:
         raise ValueError("residual_out without residual")
-    if not weight.is_cuda or not weight.is_contiguous() or weight.numel() != D:
+    if weight.numel() != D or not weight.is_contiguous() or not weight.is_cuda:
         raise ValueError("weight must be a contiguous CUDA tensor of D elements")
-    if y is None and (not group or dtype is not None):
-        y = torch.empty(x.shape, dtype=dtype or torch.float16, device=x.device)
-    act = ACT_F16
     if y is not None:
-        if not y.is_cuda or not y.is_contiguous() or y.shape != x.shape:
+        if y.shape != shape or not y.is_contiguous() or not y.is_cuda:
             raise ValueError("y must be a contiguous CUDA tensor of x's shape")
-        act = _act_of(y)
-    size = 0
+    elif not group or dtype is not None:
+        torch = _torch()
+        y = torch.empty(shape, dtype=dtype or torch.float16, device=x.device)
+    if y is not None:
+        act, yptr = _act_of(y), y.data_ptr()
     if group:
+        torch = _torch()
         size = 0 if group < 0 else group
-        groups = 1 if group < 0 else -(-D // group)
-        if q is None:
-            q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-        if scales is None:
-            scales = torch.empty((M, groups), dtype=torch.float32, device=x.device)
-        _dense(q, "q", torch.float8_e4m3fn, x.shape)
-        _dense(scales, "scales", torch.float32, (M, groups))
+        parts = (M, 1 if group < 0 else -(-D // group))
+        q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device) if q is None else _dense(q, "q", torch.float8_e4m3fn, shape)
+        scales = (torch.empty(parts, dtype=torch.float32, device=x.device) if scales is None
+                  else _dense(scales, "scales", torch.float32, parts))
+        qptr, sptr = q.data_ptr(), scales.data_ptr()
     elif q is not None or scales is not None:
         raise ValueError("q and scales need a group")
     if M:
-        _check(load().rocmfp4_add_rmsnorm(
-            x.data_ptr(), codes.get(x.dtype, -1), ldx, _ptr(residual), _ptr(residual_out), rtype, ldr, ldro, weight.data_ptr(),
-            codes.get(weight.dtype, -1), eps, _ptr(y), act, _ptr(q), _ptr(scales), size, M, D, _stream(stream)),
-            "rocmfp4_add_rmsnorm")
+        st = (_lib or load()).rocmfp4_add_rmsnorm(x.data_ptr(), codes.get(x.dtype, -1), ldx, rptr, roptr, rtype, ldr, ldro, weight.data_ptr(),
+                                                  codes.get(weight.dtype, -1), eps, yptr, act, qptr, sptr, size, M, D, _stream(stream))
+        if st:
+            _check(st, "rocmfp4_add_rmsnorm")
     return AddRmsNorm(y, residual_out, q, scales)
 
 
@@ -354,20 +357,24 @@ def moe(X, router, Wgu, Wd, I: int, top_k: int, variant: int = DUAL, route: int 
     codes = _DTYPES or _dtypes()
     if X.dim() == 1:
         X = X.view(1, -1)
-    if X.dim() != 2 or not X.is_cuda or not X.is_contiguous():
+    if X.dim() != 2 or not X.is_contiguous() or not X.is_cuda:
         raise ValueError("X must be a contiguous [M, K] CUDA tensor")
     M, K = X.shape
-    if router.dim() != 2 or not router.is_cuda or not router.is_contiguous() or router.shape[1] != K:
+    if router.dim() != 2 or not router.is_contiguous() or not router.is_cuda or router.shape[1] != K:
         raise ValueError("router must be a contiguous [E, K] CUDA tensor")
     E = router.shape[0]
     _check_w(Wgu, 2 * E * I, K, variant)
     _check_w(Wd, E * K, I, variant)
-    dev, shape = X.device, (M, top_k)
-    Y = torch.empty((M, K), dtype=torch.float32, device=dev) if Y is None else _dense(Y, "Y", torch.float32, (M, K))
-    ids = torch.empty(shape, dtype=torch.int32, device=dev) if ids is None else _dense(ids, "ids", torch.int32, shape)
-    probs = torch.empty(shape, dtype=torch.float32, device=dev) if probs is None else _dense(probs, "probs", torch.float32, shape)
-    _check(load().rocmfp4_moe(_ptr(X), _ptr(router), codes.get(router.dtype, -1), _ptr(Wgu), _ptr(Wd), _ptr(Y), _ptr(ids), _ptr(probs), M,
-                              E, top_k, K, I, route, route_scale, variant, _act_of(X), _stream(stream)), "rocmfp4_moe")
+    dev, shape, f32, i32 = X.device, (M, top_k), torch.float32, torch.int32
+    Y = torch.empty((M, K), dtype=f32, device=dev) if Y is None else _dense(Y, "Y", f32, (M, K))
+    ids = torch.empty(shape, dtype=i32, device=dev) if ids is None else _dense(ids, "ids", i32, shape)
+    probs = torch.empty(shape, dtype=f32, device=dev) if probs is None else _dense(probs, "probs", f32, shape)
+    if M:
+        st = (_lib or load()).rocmfp4_moe(X.data_ptr(), router.data_ptr(), codes.get(router.dtype, -1), Wgu.data_ptr(), Wd.data_ptr(), Y.data_ptr(),
+                                          ids.data_ptr(), probs.data_ptr(), M, E, top_k, K, I, route, route_scale, variant, _act_of(X),
+                                          _stream(stream))
+        if st:
+            _check(st, "rocmfp4_moe")
     return Y, ids, probs
 
 
@@ -380,21 +387,21 @@ def logprobs(logits, targets=None, top_n: int = 0, scale: float = 1.0, logprob=N
     torch = _torch()
     codes = _DTYPES or _dtypes()
     M, V, ld = _rows(logits, "logits")
-    dev = logits.device
+    dev, rows, shape, f32, tptr, lptr = logits.device, (M,), (M, top_n), torch.float32, 0, 0
     if targets is not None:
-        _dense(targets, "targets", torch.int32, (M,))
-        logprob = torch.empty(M, dtype=torch.float32, device=dev) if logprob is None else _dense(logprob, "logprob", torch.float32, (M,))
+        tptr = _dense(targets, "targets", torch.int32, rows).data_ptr()
+        logprob = torch.empty(rows, dtype=f32, device=dev) if logprob is None else _dense(logprob, "logprob", f32, rows)
+        lptr = logprob.data_ptr()
     elif logprob is not None:
         raise ValueError("logprob without targets")
-    entropy = torch.empty(M, dtype=torch.float32, device=dev) if entropy is None else _dense(entropy, "entropy", torch.float32, (M,))
-    shape = (M, top_n)
+    entropy = torch.empty(rows, dtype=f32, device=dev) if entropy is None else _dense(entropy, "entropy", f32, rows)
     top_ids = torch.empty(shape, dtype=torch.int32, device=dev) if top_ids is None else _dense(top_ids, "top_ids", torch.int32, shape)
-    top_logprobs = (torch.empty(shape, dtype=torch.float32, device=dev) if top_logprobs is None
-                    else _dense(top_logprobs, "top_logprobs", torch.float32, shape))
+    top_logprobs = torch.empty(shape, dtype=f32, device=dev) if top_logprobs is None else _dense(top_logprobs, "top_logprobs", f32, shape)
     if M:
-        _check(load().rocmfp4_logprobs(logits.data_ptr(), codes.get(logits.dtype, -1), ld, _ptr(targets), scale, _ptr(logprob),
-                                       _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs), top_n, M, V, _stream(stream)),
-               "rocmfp4_logprobs")
+        st = (_lib or load()).rocmfp4_logprobs(logits.data_ptr(), codes.get(logits.dtype, -1), ld, tptr, scale, lptr, entropy.data_ptr(),
+                                               top_ids.data_ptr(), top_logprobs.data_ptr(), top_n, M, V, _stream(stream))
+        if st:
+            _check(st, "rocmfp4_logprobs")
     return logprob, entropy, top_ids, top_logprobs
 
 

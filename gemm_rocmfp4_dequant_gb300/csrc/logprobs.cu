@@ -30,7 +30,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVecs = 2;        // 16-byte vectors a thread takes of a tile
 constexpr int kGroups = 64;     // groups of 4 neighbouring threads
-constexpr int kCutAt = 256;     // candidates at which the join of a row's ranges cuts its list back to n
 constexpr int kCap = 1024;      // room of the list: n threads' values of a tile and more
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -76,21 +75,31 @@ RF4_DEV void rescale(float& S, float& A, float from, float to, float c) {
   A = e > 0.f ? e * (A + d * S) : 0.f;
   S = e * S;
 }
-RF4_DEV void merge(Stats& a, const Stats& b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  float S = b.S, A = b.A;
-  rescale(a.S, a.A, a.m, m, c);
-  rescale(S, A, b.m, m, c);
-  a.m = m;
-  a.S += S;
-  a.A += A;
+// The statistics of the lanes together, in every lane; the sums in a fixed order.
+RF4_DEV Stats join(Stats s, float c) {
+  float m = s.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  rescale(s.S, s.A, s.m, m, c);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s.S += __shfl_xor_sync(0xffffffffu, s.S, o);
+    s.A += __shfl_xor_sync(0xffffffffu, s.A, o);
+  }
+  s.m = m;
+  return s;
 }
-RF4_DEV Stats shfl_xor(const Stats& s, int o) {
-  Stats r;
-  r.m = __shfl_xor_sync(0xffffffffu, s.m, o);
-  r.S = __shfl_xor_sync(0xffffffffu, s.S, o);
-  r.A = __shfl_xor_sync(0xffffffffu, s.A, o);
-  return r;
+// The statistics of the CTA's threads together, in every thread of warp 0 and
+// in all[0] behind the next barrier.  `all`: room for a warp's each.
+RF4_DEV void join_cta(Stats s, float c, Stats* all) {
+  s = join(s, c);
+  if ((threadIdx.x & 31) == 0) all[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    s = join(threadIdx.x < kThreads / 32 ? all[threadIdx.x] : Stats{}, c);
+    __syncwarp();
+    if (threadIdx.x == 0) all[0] = s;
+  }
 }
 
 template <int TYPE>
@@ -162,19 +171,27 @@ RF4_DEV uint64_t group_threshold(TopState& st, uint64_t mine, int n) {
   return threshold;
 }
 
+// The n-th largest of `count` (n < count <= kThreads) distinct keys; thread i
+// gives key i as `mine`, 0 for none (then there may be fewer: 0).
+RF4_DEV uint64_t nth_of(const uint64_t* keys, int count, uint64_t mine, int n) {
+  __shared__ uint64_t threshold;
+  if (threadIdx.x == 0) threshold = 0;
+  __syncthreads();
+  if (mine != 0) {
+    int rank = 0;
+#pragma unroll 8
+    for (int i = 0; i < count; ++i) rank += keys[i] > mine ? 1 : 0;
+    if (rank == n - 1) threshold = mine;
+  }
+  __syncthreads();
+  return threshold;
+}
+
 // As group_threshold, over single threads: at most n threads have keys that
 // reach it.  `keys` is room for kThreads keys.  Slower: for full lists only.
 RF4_DEV uint64_t thread_threshold(uint64_t* keys, uint64_t mine, int n) {
-  __shared__ uint64_t threshold;
   keys[threadIdx.x] = mine;
-  if (threadIdx.x == 0) threshold = 0;
-  __syncthreads();
-  int rank = 0;
-#pragma unroll 16
-  for (int i = 0; i < kThreads; ++i) rank += keys[i] > mine ? 1 : 0;
-  if (rank == n - 1 && mine != 0) threshold = mine;
-  __syncthreads();
-  return threshold;
+  return nth_of(keys, kThreads, mine, n);
 }
 
 // The n largest of the candidate list's `count` keys to the list's front, in
@@ -213,16 +230,18 @@ RF4_DEV void cut(TopState& st, uint64_t* list, uint64_t* spare, int count, int n
 
 // One record per range of a split row: m, S, A, the number of keys, then kMaxTop keys.
 constexpr int kRecordBytes = 16 + 8 * kMaxTop;
+constexpr int kMaxSplits = kThreads;  // one record a thread at the join
 
 template <int TYPE, bool TOP>
 __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_constant__ LogprobsArgs a) {
   using L = Logit<TYPE>;
   using E = typename L::type;
   constexpr int PER = L::PER, N = kVecs * PER, TILE = kThreads * kVecs;  // vectors of a tile
-  static_assert(kMaxTop * N + kMaxTop <= kCap && kCutAt + kThreads <= kCap, "what a search by tiles pushes has room");
+  static_assert(kMaxTop * N + kMaxTop <= kCap && kMaxTop * kMaxTop <= kCap, "what is pushed without a check has room");
   __shared__ TopState st;
   __shared__ uint64_t lists[TOP ? 2 * kCap : 1];
   __shared__ Stats warp_stats[kThreads / 32];
+  __shared__ int picked[kMaxTop];
   __shared__ int last;
   uint64_t* list = lists;
   uint64_t* spare = lists + (TOP ? kCap : 0);
@@ -257,6 +276,12 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     const int64_t e = index(base, i);
     return base + (i / PER) * kThreads + tid < v1 && e >= 0 && e < a.V;
   };
+
+  float given = __uint_as_float(0x7FC00000u);  // the target's logit, asked for ahead of use
+  if (tid == 0 && a.targets != nullptr) {
+    const int64_t t = a.targets[row];
+    if (t >= 0 && t < a.V) given = L::one(z[t]);
+  }
 
   Stats s;
   uint4 w[kVecs];
@@ -367,23 +392,15 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
       }
     }
   }
-  // the CTA's statistics, joined in a fixed order
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) merge(s, shfl_xor(s, o), c);
-  if ((tid & 31) == 0) warp_stats[tid >> 5] = s;
+  join_cta(s, c, warp_stats);
   if (TOP) cut(st, list, spare, st.count, n);
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kThreads / 32; ++w) merge(s, warp_stats[w], c);
-    warp_stats[0] = s;
-  }
   __syncthreads();
 
   if (P > 1) {
     uint8_t* records = reinterpret_cast<uint8_t*>(a.ws) + (size_t)row * P * kRecordBytes;
     uint8_t* mine = records + (size_t)part * kRecordBytes;
-    if (tid == 0) *reinterpret_cast<float4*>(mine) = make_float4(s.m, s.S, s.A, 0.f);
-    if (TOP && tid < n) reinterpret_cast<uint64_t*>(mine + 16)[tid] = tid < st.count ? list[tid] : 0;
+    if (tid == 0) *reinterpret_cast<float4*>(mine) = make_float4(warp_stats[0].m, warp_stats[0].S, warp_stats[0].A, 0.f);
+    if (TOP && tid < n) reinterpret_cast<uint64_t*>(mine + 16)[tid] = tid < st.count ? list[tid] : 0;  // 0: none
     __threadfence();
     __syncthreads();
     if (tid == 0) {
@@ -393,43 +410,36 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     }
     __syncthreads();
     if (!last) return;
+    // Thread p has record p (P is at most the CTA's threads).
+    const uint8_t* own = records + (size_t)(tid < P ? tid : 0) * kRecordBytes;
     s = Stats{};
-    for (int p = tid; p < P; p += kThreads) {
-      const float4 r = __ldcg(reinterpret_cast<const float4*>(records + (size_t)p * kRecordBytes));
-      merge(s, Stats{r.x, r.y, r.z}, c);
+    uint64_t first = 0;  // the record's largest key
+    if (tid < P) {
+      const float4 r = __ldcg(reinterpret_cast<const float4*>(own));
+      s = Stats{r.x, r.y, r.z};
+      if (TOP) first = __ldcg(reinterpret_cast<const unsigned long long*>(own + 16));
     }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) merge(s, shfl_xor(s, o), c);
-    if ((tid & 31) == 0) warp_stats[tid >> 5] = s;
     if constexpr (TOP) {
-      // key j of record p at place j * P + p: the records' largest keys first
-      auto at = [&](int i) { return __ldcg(reinterpret_cast<const unsigned long long*>(records + (size_t)(i % P) * kRecordBytes + 16) + i / P); };
-      const int total = P * n;
-      uint64_t mx = 0;
-      for (int i = tid; i < P; i += kThreads) {  // a record's first key is its largest
-        const uint64_t k = at(i);
-        mx = k > mx ? k : mx;
-      }
-      if (tid == 0) st.count = 0;
-      const uint64_t t = group_threshold(st, mx, n);
-      if (tid == 0) st.floor = t > 0 ? t - 1 : 0;
+      // The n-th largest of the records' largest keys is reached by at most n
+      // records; the top n are among the keys of these.
+      if (tid == 0) st.count = 0, st.floor = 0;
+      if (tid < P) spare[tid] = first;
       __syncthreads();
-      for (int base = 0; base < total; base += kThreads) {
-        const uint64_t k = base + tid < total ? at(base + tid) : 0;
-        if (k > st.floor) list[atomicAdd(&st.count, 1)] = k;  // at most kCutAt + kThreads of them
-        __syncthreads();
-        const int count = st.count;
-        __syncthreads();
-        if (count > kCutAt) cut(st, list, spare, count, n);
+      const uint64_t t = P > n ? nth_of(spare, P, first, n) : 0;
+      if (first != 0 && first >= t) picked[atomicAdd(&st.count, 1)] = tid;
+      __syncthreads();
+      const int records_in = st.count;
+      __syncthreads();
+      if (tid == 0) st.count = 0;
+      __syncthreads();
+      for (int i = tid; i < records_in * n; i += kThreads) {
+        const uint64_t k = __ldcg(reinterpret_cast<const unsigned long long*>(records + (size_t)picked[i / n] * kRecordBytes + 16) + i % n);
+        if (k != 0 && k >= t) list[atomicAdd(&st.count, 1)] = k;
       }
-      cut(st, list, spare, st.count, n);
     }
+    join_cta(s, c, warp_stats);
     __syncthreads();
-    if (tid == 0) {
-      for (int w = 1; w < kThreads / 32; ++w) merge(s, warp_stats[w], c);
-      warp_stats[0] = s;
-    }
-    __syncthreads();
+    if (TOP) cut(st, list, spare, st.count, n);
   }
 
   s = warp_stats[0];
@@ -438,8 +448,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   if (tid == 0) {
     if (a.targets != nullptr) {
       const int64_t t = a.targets[row];
-      const float x = t >= 0 && t < a.V ? L::one(z[t]) : __uint_as_float(0x7FC00000u);
-      a.logprob[row] = t >= 0 && t < a.V ? (empty ? -INFINITY : a.scale * (x - s.m) - ln) : x;
+      a.logprob[row] = t >= 0 && t < a.V ? (empty ? -INFINITY : a.scale * (given - s.m) - ln) : given;
     }
     if (a.entropy != nullptr) a.entropy[row] = empty ? 0.f : ln - a.scale * s.A / s.S;
   }
@@ -465,6 +474,7 @@ cudaError_t launch_logprobs(const LogprobsArgs& args, int sms, cudaStream_t s) {
   // About four CTAs per SM, each with at least one whole tile of its row.
   int64_t P = a.M >= 4 * (int64_t)sms ? 1 : (4 * (int64_t)sms + a.M - 1) / a.M;
   P = P < tiles ? P : tiles;
+  P = P < kMaxSplits ? P : kMaxSplits;
   a.splits = (int)P;
   LogprobsFn fn;
   if (a.top_n > 0) fn = a.type == 0 ? logprobs_kernel<0, true> : a.type == 1 ? logprobs_kernel<1, true> : logprobs_kernel<2, true>;

@@ -47,7 +47,7 @@ RF4_DEV typename Elem<T>::type from_f32(float f) {
 
 // Eight consecutive values starting at p; n of them exist (the rest read as 0).
 template <int T, bool VEC>
-RF4_DEV void load8(const void* base, int64_t off, int n, float (&v)[8]) {
+RF4_DEV void load8(const void* base, int off, int n, float (&v)[8]) {
   using E = typename Elem<T>::type;
   const E* p = static_cast<const E*>(base) + off;
   if constexpr (VEC) {
@@ -70,7 +70,7 @@ RF4_DEV void load8(const void* base, int64_t off, int n, float (&v)[8]) {
 }
 
 template <int T, bool VEC>
-RF4_DEV void store8(void* base, int64_t off, int n, const float (&v)[8]) {
+RF4_DEV void store8(void* base, int off, int n, const float (&v)[8]) {
   using E = typename Elem<T>::type;
   E* p = static_cast<E*>(base) + off;
   if constexpr (VEC) {
@@ -93,7 +93,7 @@ RF4_DEV void store8(void* base, int64_t off, int n, const float (&v)[8]) {
 // The types that are not template parameters (weight, y) are the same for the
 // whole launch: a uniform branch per vector.
 template <bool VEC>
-RF4_DEV void load8_any(int type, const void* base, int64_t off, int n, float (&v)[8]) {
+RF4_DEV void load8_any(int type, const void* base, int off, int n, float (&v)[8]) {
   if (type == kTypeF32) load8<kTypeF32, VEC>(base, off, n, v);
   else if (type == kTypeBF16) load8<kTypeBF16, VEC>(base, off, n, v);
   else load8<kTypeF16, VEC>(base, off, n, v);
@@ -114,24 +114,25 @@ RF4_DEV uint32_t e4m3_pair(float lo, float hi) {
 }
 
 // The 8-bit codes of eight values whose group's largest magnitude is amax.
-// The quotient y / s is y * (448 / amax), off by at most 1.5 ulp of fp32: far
-// below the 2^-4 steps of e4m3, and one product instead of a division a value.
-// A group below 1e-30 divides, as 448 / amax would leave fp32's range.
+// The quotient y / s is y * (448 / amax), off by a few ulp of fp32: far below
+// the 2^-4 steps of e4m3, and one product instead of a division a value.  A
+// group below 1e-30 divides, as 448 / amax would leave fp32's range.
 template <bool VEC>
-RF4_DEV void quantise8(const NormArgs& a, int64_t off, int n, const float (&v)[8], float amax) {
+RF4_DEV void quantise8(uint8_t* q, int n, const float (&v)[8], float amax) {
   float z[8];
   if (amax < 1e-30f) {
     const float s = amax / kFp8Max;
 #pragma unroll
     for (int j = 0; j < 8; ++j) z[j] = s > 0.f ? v[j] / s : 0.f;
   } else {
-    const float inv = kFp8Max / amax;
+    float inv;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(amax));
+    inv *= kFp8Max;
 #pragma unroll
     for (int j = 0; j < 8; ++j) z[j] = v[j] * inv;
   }
   const uint32_t c0 = e4m3_pair(z[0], z[1]) | (e4m3_pair(z[2], z[3]) << 16);
   const uint32_t c1 = e4m3_pair(z[4], z[5]) | (e4m3_pair(z[6], z[7]) << 16);
-  uint8_t* q = a.q + off;
   if constexpr (VEC) {
     *reinterpret_cast<uint2*>(q) = make_uint2(c0, c1);
   } else {
@@ -171,69 +172,82 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
   const int64_t row = (int64_t)blockIdx.x * rows_per_cta + tid / lanes;
   const bool live = row < a.M;
   const int nwarps = blockDim.x >> 5;
-  const int64_t D = a.D;
+  const int D = (int)a.D;
+  // the row of every operand (a row past the last one reads and writes nothing)
+  const int64_t r = live ? row : 0;
+  auto at = [](const void* p, int type, int64_t i) { return static_cast<const uint8_t*>(p) + i * (type == kTypeF32 ? 4 : 2); };
+  const void* x = at(a.x, XT, r * a.ldx);
+  const void* res = at(a.residual, RT, r * a.ldr);
+  void* res_out = const_cast<uint8_t*>(at(a.residual_out, RT, r * a.ldro));
+  auto values = [&](int e) { return !live || e >= D ? 0 : VEC || D - e >= 8 ? 8 : D - e; };  // of a vector from e on
   float h[NV][8];
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t e = 8 * ((int64_t)i * lanes + t);
-    const int n = !live || e >= D ? 0 : (D - e < 8 ? (int)(D - e) : 8);
+    const int e = 8 * (i * lanes + t), n = values(e);
     if (n > 0) {
-      load8<XT, VEC>(a.x, row * a.ldx + e, n, h[i]);
+      load8<XT, VEC>(x, e, n, h[i]);
       if constexpr (RT != kTypeNone) {
-        float r[8];
-        load8<RT, VEC>(a.residual, row * a.ldr + e, n, r);
+        float v[8];
+        load8<RT, VEC>(res, e, n, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] += r[j];
-        store8<RT, VEC>(a.residual_out, row * a.ldro + e, n, h[i]);
+        for (int j = 0; j < 8; ++j) h[i][j] += v[j];
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(h[i][j], h[i][j], ss);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
     }
   }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if constexpr (RT != kTypeNone) {
+      const int e = 8 * (i * lanes + t), n = values(e);
+      if (n > 0) store8<RT, VEC>(res_out, e, n, h[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(h[i][j], h[i][j], ss);
+  }
   ss = row_reduce<false>(ss, lanes, nwarps, red);
   const float rstd = rsqrtf(ss / (float)D + a.eps);
+  const int group = a.group, shift = 31 - __clz(group | 1), groups = group ? (D + group - 1) >> shift : 1;
+  void* y = a.y == nullptr ? nullptr : const_cast<uint8_t*>(at(a.y, kTypeF16, r * D));
+  uint8_t* q = a.q == nullptr ? nullptr : a.q + r * D;
+  float* scales = a.scales + r * groups;
   float rowmax = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t e = 8 * ((int64_t)i * lanes + t);
-    const int n = !live || e >= D ? 0 : (D - e < 8 ? (int)(D - e) : 8);
+    const int e = 8 * (i * lanes + t), n = values(e);
     if (n > 0) {
       float w[8];
       load8_any<VEC>(a.weight_type, a.weight, e, n, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[i][j] *= rstd * w[j];
-      if (a.y != nullptr) {
-        if (a.y_act == 1) store8<kTypeBF16, VEC>(a.y, row * D + e, n, h[i]);
-        else store8<kTypeF16, VEC>(a.y, row * D + e, n, h[i]);
+      if (y != nullptr) {
+        if (a.y_act == 1) store8<kTypeBF16, VEC>(y, e, n, h[i]);
+        else store8<kTypeF16, VEC>(y, e, n, h[i]);
       }
     }
-    if (a.q == nullptr) continue;
+    if (q == nullptr) continue;
     float m = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (VEC || j < n) m = max_nan(m, fabsf(h[i][j]));
     rowmax = max_nan(rowmax, m);
-    if (a.group == 0) continue;
+    if (group == 0) continue;
     // a group is group / 8 consecutive lanes (4, 8 or 16, aligned in the warp)
-    for (int o = a.group >> 4; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = group >> 4; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (n > 0) {
-      const int64_t groups = (D + a.group - 1) / a.group;
-      if (e % a.group == 0) a.scales[row * groups + e / a.group] = m / kFp8Max;
-      quantise8<VEC>(a, row * D + e, n, h[i], m);
+      if ((e & (group - 1)) == 0) scales[e >> shift] = m * (1.f / kFp8Max);
+      quantise8<VEC>(q + e, n, h[i], m);
     }
   }
-  if (a.q == nullptr || a.group != 0) return;
+  if (q == nullptr || group != 0) return;
   rowmax = row_reduce<true>(rowmax, lanes, nwarps, red);
-  if (live && t == 0) a.scales[row] = rowmax / kFp8Max;
+  if (live && t == 0) scales[0] = rowmax * (1.f / kFp8Max);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t e = 8 * ((int64_t)i * lanes + t);
-    const int n = !live || e >= D ? 0 : (D - e < 8 ? (int)(D - e) : 8);
-    if (n > 0) quantise8<VEC>(a, row * D + e, n, h[i], rowmax);
+    const int e = 8 * (i * lanes + t), n = values(e);
+    if (n > 0) quantise8<VEC>(q + e, n, h[i], rowmax);
   }
 }
 
