@@ -46,9 +46,36 @@ RF4_DEV float unordered(uint32_t k) {
 }
 RF4_DEV uint64_t key_of(float f, uint32_t index) { return ((uint64_t)ordered(f) << 32) | (uint32_t)~index; }
 
-// A distance below the maximum at which exp(scale * distance) is 0 for every
-// accepted scale; takes the place of -inf, so that 0 * distance stays 0.
+// A distance at which exp(scale * distance) is 0 for every accepted scale;
+// takes the place of -inf, so that 0 * distance stays 0.
 constexpr float kFarBelow = -3.0e38f;
+constexpr float kRise = 40.f;  // powers of two by which exp() may pass 1: sums of 2^31 stay far below fp32's range
+
+RF4_DEV uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+RF4_DEV float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+RF4_DEV uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+RF4_DEV uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+RF4_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
 
 RF4_DEV float ex2(float x) {
   float y;
@@ -61,13 +88,15 @@ RF4_DEV float max_nan(float a, float b) {
   return r;
 }
 
-// Running softmax of some of a row's logits: m is the largest logit, S and A
-// the sums of e and e * (logit - m) with e = exp(scale * (logit - m)).
+// Running softmax of some of a row's logits: S and A are the sums of e and
+// e * (logit - m) with e = exp(scale * (logit - m)).  The reference m is one of
+// the logits and within a factor of 2^kRise of the largest: moving it for
+// every new maximum would cost a rescaling in almost every tile.
 struct Stats {
   float m = -INFINITY, S = 0.f, A = 0.f;
 };
 
-// Moves (S, A) from the maximum `from` to `to` >= from; no values yet (m = -inf) stay nothing.
+// Moves (S, A) from the reference `from` to `to` >= from; no values yet (m = -inf) stay nothing.
 RF4_DEV void rescale(float& S, float& A, float from, float to, float c) {
   if (from == to || (S == 0.f && A == 0.f)) return;
   const float d = from - to, e = ex2(d * c);
@@ -109,6 +138,17 @@ struct Logit<0> {
   using type = float;
   static constexpr int PER = 4;
   static RF4_DEV float one(float v) { return v; }
+  // the largest value of some words (NaN only where there is nothing else)
+  template <int W>
+  static RF4_DEV float largest(const uint4 (&w)[W]) {
+    float m = __uint_as_float(w[0].x);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      m = fmaxf(fmaxf(m, __uint_as_float(w[i].x)), __uint_as_float(w[i].y));
+      m = fmaxf(fmaxf(m, __uint_as_float(w[i].z)), __uint_as_float(w[i].w));
+    }
+    return m;
+  }
   static RF4_DEV void unpack(const uint4& w, float* v) {
     v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y), v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
   }
@@ -118,6 +158,18 @@ struct Logit<1> {
   using type = uint16_t;
   static constexpr int PER = 8;
   static RF4_DEV float one(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+  static RF4_DEV uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  template <int W>
+  static RF4_DEV float largest(const uint4 (&w)[W]) {
+    uint32_t m = w[0].x;
+#pragma unroll
+    for (int i = 0; i < W; ++i) m = max2(max2(max2(max2(m, w[i].x), w[i].y), w[i].z), w[i].w);
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+  }
   static RF4_DEV void unpack(const uint4& w, float* v) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -129,6 +181,19 @@ struct Logit<2> {
   using type = uint16_t;
   static constexpr int PER = 8;
   static RF4_DEV float one(uint16_t v) { return __half2float(__ushort_as_half(v)); }
+  static RF4_DEV uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  template <int W>
+  static RF4_DEV float largest(const uint4 (&w)[W]) {
+    uint32_t m = w[0].x;
+#pragma unroll
+    for (int i = 0; i < W; ++i) m = max2(max2(max2(max2(m, w[i].x), w[i].y), w[i].z), w[i].w);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+    return fmaxf(f.x, f.y);
+  }
   static RF4_DEV void unpack(const uint4& w, float* v) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -262,17 +327,19 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   // its start: places before value 0 and past value V - 1 count as absent.
   const int lead = (int)((reinterpret_cast<uintptr_t>(z) & 15u) / sizeof(E));
   const uint4* vz = reinterpret_cast<const uint4*>(z - lead);
-  const int64_t vecs = (a.V + lead + PER - 1) / PER;
-  const int64_t v0 = vecs * part / P, v1 = vecs * (part + 1) / P;
-  // A tile whose every vector is this range's and wholly inside the row: the same for all threads.
-  auto whole = [&](int64_t base) { return base + TILE <= v1 && base * PER >= lead && (base + TILE) * PER <= a.V + lead; };
-  auto fetch = [&](int64_t base, uint4 (&w)[kVecs]) {
+  const int vecs = (int)((a.V + lead + PER - 1) / PER);
+  const int v0 = (int)((int64_t)vecs * part / P), v1 = (int)((int64_t)vecs * (part + 1) / P);
+  // A tile from `base` on whose every vector is this range's and wholly inside the row.
+  const int whole_from = v0 + (v0 * PER < lead ? 1 : 0);
+  const int whole_to = min(v1, (int)((a.V + lead) / PER)) - TILE;
+  auto whole = [&](int base) { return base >= whole_from && base <= whole_to; };
+  auto fetch = [&](int base, uint4 (&w)[kVecs]) {
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) w[k] = __ldcs(vz + base + k * kThreads + tid);
+    for (int k = 0; k < kVecs; ++k) w[k] = __ldcs(vz + (base + tid) + k * kThreads);
   };
   // index of value i of this thread's in a tile, and whether there is such a value
-  auto index = [&](int64_t base, int i) { return (base + (i / PER) * kThreads + tid) * PER - lead + i % PER; };
-  auto present = [&](int64_t base, int i) {
+  auto index = [&](int base, int i) { return (int64_t)(base + (i / PER) * kThreads + tid) * PER - lead + i % PER; };
+  auto present = [&](int base, int i) {
     const int64_t e = index(base, i);
     return base + (i / PER) * kThreads + tid < v1 && e >= 0 && e < a.V;
   };
@@ -289,35 +356,49 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   int tiles = 0;
   uint64_t floor = 0;  // candidates have larger keys
 #pragma unroll 1
-  for (int64_t base = v0; base < v1; base += TILE, ++tiles) {
-    float v[N];
+  for (int base = v0; base < v1; base += TILE, ++tiles) {
+    float v[N], tm;
     const bool full = whole(base);
     if (full) {
 #pragma unroll
       for (int k = 0; k < kVecs; ++k) L::unpack(w[k], v + k * PER);
+      tm = L::largest(w);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] = present(base, i) ? L::one(z[index(base, i)]) : -INFINITY;
+      tm = v[0];
+#pragma unroll
+      for (int i = 1; i < N; ++i) tm = fmaxf(tm, v[i]);
     }
     if (whole(base + TILE)) fetch(base + TILE, w);  // the next tile is on its way while this one is summed
-    float tm = v[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) tm = fmaxf(tm, v[i]);
-    const float m = fmaxf(s.m, tm);
-    if (m > s.m) {
-      rescale(s.S, s.A, s.m, m, c);
-      s.m = m;
+    if ((tm - s.m) * c > kRise || s.m == -INFINITY) {
+      rescale(s.S, s.A, s.m, tm, c);
+      s.m = tm;
     }
-    const float mm = m == -INFINITY ? 0.f : m;  // nothing but -inf yet: e = 0
-    float S[2] = {0.f, 0.f}, A[2] = {0.f, 0.f};  // the tile's sums on their own: short chains
+    const float mm = s.m == -INFINITY ? 0.f : s.m;  // nothing but -inf yet: e = 0
+    // the tile's sums on their own: short chains
+    uint64_t S[2] = {0, 0}, A[2] = {0, 0};
+    const uint64_t minus = pack2(-mm, -mm), cc = pack2(c, c);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float d = max_nan(v[i] - mm, kFarBelow), e = ex2(d * c);
-      S[i & 1] += e;
-      A[i & 1] = fmaf(e, d, A[i & 1]);
+    for (int i = 0; i < N / 2; ++i) {
+      const uint64_t d = add2(pack2(v[2 * i], v[2 * i + 1]), minus);
+      const float2 t = unpack2(mul2(d, cc));
+      const uint64_t e = pack2(ex2(t.x), ex2(t.y));
+      S[i & 1] = add2(S[i & 1], e);
+      A[i & 1] = fma2(e, d, A[i & 1]);
     }
-    s.S += S[0] + S[1];
-    s.A += A[0] + A[1];
+    const float2 sum = unpack2(add2(S[0], S[1])), part_a = unpack2(add2(A[0], A[1]));
+    float tile_a = part_a.x + part_a.y;
+    if (tile_a != tile_a) {  // a value of -inf (0 * -inf) or a NaN: again, with a finite factor for e = 0
+      tile_a = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float d = v[i] - mm;
+        tile_a = fmaf(ex2(d * c), max_nan(d, kFarBelow), tile_a);
+      }
+    }
+    s.S += sum.x + sum.y;
+    s.A += tile_a;
     if constexpr (TOP) {
       if (tiles == 0) {
         uint64_t best = 0;  // the thread's largest key
@@ -369,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
       if (tid == 0) st.count = 0, st.floor = 0;
       __syncthreads();
 #pragma unroll 1
-      for (int64_t base = v0; base < v1; base += TILE) {
+      for (int base = v0; base < v1; base += TILE) {
         const uint64_t least = st.floor;
         uint64_t best = 0;
 #pragma unroll 1
