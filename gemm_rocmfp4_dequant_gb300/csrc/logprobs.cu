@@ -365,7 +365,15 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
       tm = L::largest(w);
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = present(base, i) ? L::one(z[index(base, i)]) : -INFINITY;
+      for (int k = 0; k < kVecs; ++k) {
+        // a vector inside the row in one load, one at an end of it value by value
+        if (present(base, k * PER) && present(base, k * PER + PER - 1)) {
+          L::unpack(__ldg(vz + base + k * kThreads + tid), v + k * PER);
+        } else {
+#pragma unroll
+          for (int i = k * PER; i < k * PER + PER; ++i) v[i] = present(base, i) ? L::one(z[index(base, i)]) : -INFINITY;
+        }
+      }
       tm = v[0];
 #pragma unroll
       for (int i = 1; i < N; ++i) tm = fmaxf(tm, v[i]);

@@ -112,6 +112,13 @@ def test_matches_definition(shape, act, variant):
     run_and_check(*SHAPES[shape], variant, act, route=shape % 3, scale=(1.0, 2.5)[shape % 2], seed=100 + shape)
 
 
+@pytest.mark.parametrize("variant", [DUAL, FAST])
+@pytest.mark.parametrize("shape", [(8, 16, 4, 2560, 1536), (6, 12, 6, 512, 2048), (5, 24, 5, 96, 4096), (4, 20, 5, 2464, 1568)])
+def test_tile_counts(shape, variant):
+    """Output rows that do not deal out evenly over the SMs, and fewer tiles than SMs."""
+    run_and_check(*shape, variant, 0, seed=200)
+
+
 @pytest.mark.parametrize("rtype", ["float32", "float16"])
 def test_router_types_and_many_experts(rtype):
     t = torch()
