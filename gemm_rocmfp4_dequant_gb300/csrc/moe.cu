@@ -626,28 +626,29 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   // and next span), then of a down tile (stage u of tile `id` of this CTA's).
   struct {
     bool gu, any;
-    int id, e, row0, span, u;
+    int id, e, row0, span, u, at;  // at: place of e in the list
   } nx;
   auto start_gu = [&](int id) {
-    const int at = id / per_expert;
+    while (id >= (nx.at + 1) * per_expert) ++nx.at;
     nx.id = id;
-    nx.e = s_list[at];
-    nx.row0 = (id - at * per_expert) * 8;
+    nx.e = s_list[nx.at];
+    nx.row0 = (id - nx.at * per_expert) * 8;
     nx.span = span0;
   };
   nx.gu = gu0 < gu1;
   nx.any = nx.gu || (u0 < u1 && my_tiles > 0);
   nx.id = 0;
   nx.u = u0;
+  nx.at = nx.gu ? gu0 / per_expert : u0 / sd;
   if (nx.gu) start_gu(gu0);
   int fill_slot = 0, filled = 0;
   auto fill_next = [&]() {
     if (!nx.any) return;
     if (!nx.gu) {
-      const int at = nx.u / sd;
-      nx.e = s_list[at];
+      if (nx.u == (nx.at + 1) * sd) ++nx.at;
+      nx.e = s_list[nx.at];
       nx.row0 = (blockIdx.x + nx.id * G) * kTileRows;
-      nx.span = (nx.u - at * sd) * ns;
+      nx.span = (nx.u - nx.at * sd) * ns;
     }
     fill(!nx.gu, nx.e, nx.row0, nx.span, fill_slot);
     if (nx.gu) {
@@ -659,10 +660,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
           nx.gu = false;
           nx.any = u0 < u1 && my_tiles > 0;
           nx.id = 0;
+          nx.at = u0 / sd;
         }
       }
     } else if (++nx.u == u1) {
       nx.u = u0;
+      nx.at = u0 / sd;
       nx.any = ++nx.id < my_tiles;
     }
     if (++fill_slot == p.stages) fill_slot = 0;
@@ -730,9 +733,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         __syncwarp();
       }
       // gate/up: tile x and every span of this warp's part; down: stages from x on of one expert
+      const int per = down ? sd : per_expert;
+      int at = (down ? u0 : gu0) / max(per, 1);
 #pragma unroll 1
       for (int x = down ? u0 : gu0; x < (down ? u1 : gu1);) {
-        const int at = x / (down ? sd : per_expert), e = s_list[at];
+        while (x >= (at + 1) * per) ++at;
+        const int e = s_list[at];
         int row0, s0, s1;
         if (down) {
           const int last = min(u1, (at + 1) * sd);
