@@ -100,6 +100,7 @@ rocmfp4_status device_state(DeviceState** out) {
       return cuda_fail(e, "cudaMalloc");
     if ((e = cudaMemset(d.lp_cnt, 0, sizeof(uint32_t) * logprobs_cnt_words(d.sms))) != cudaSuccess)
       return cuda_fail(e, "cudaMemset");
+    if ((e = norm_prepare()) != cudaSuccess) return cuda_fail(e, "RMS norm kernel set-up");
     if ((e = moe_prepare()) != cudaSuccess) return cuda_fail(e, "mixture-of-experts kernel set-up");
     if ((e = cudaMalloc(&d.moe_ws, sizeof(float) * kMoeWsFloats)) != cudaSuccess) return cuda_fail(e, "cudaMalloc");
     if ((e = cudaMalloc(&d.moe_bars, sizeof(uint32_t) * kMoeBarWords)) != cudaSuccess) return cuda_fail(e, "cudaMalloc");
@@ -345,7 +346,7 @@ rocmfp4_status decode_attention(const void* q, const void* K, const void* V, con
   return ROCMFP4_OK;
 }
 
-rocmfp4_status add_rmsnorm(const NormArgs& a, int64_t group, cudaStream_t s) {
+rocmfp4_status add_rmsnorm(NormArgs a, int64_t group, cudaStream_t s) {
   if (!valid_dtype(a.x_type) || !valid_dtype(a.weight_type) || (a.residual && !valid_dtype(a.residual_type)))
     return fail(ROCMFP4_ERR_INVALID_ARG, "unknown type");
   if (!valid_act(a.y_act)) return fail(ROCMFP4_ERR_INVALID_ARG, "unknown activation type");
@@ -371,6 +372,7 @@ rocmfp4_status add_rmsnorm(const NormArgs& a, int64_t group, cudaStream_t s) {
   DeviceState* d = nullptr;
   rocmfp4_status st = device_state(&d);
   if (st != ROCMFP4_OK) return st;
+  a.err = d->err;
   cudaError_t e = launch_norm(a, d->sms, s);
   if (e != cudaSuccess) return cuda_fail(e, "RMS norm launch");
   g_launches.fetch_add(1);

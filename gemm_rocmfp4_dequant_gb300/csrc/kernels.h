@@ -96,8 +96,10 @@ struct NormArgs {
   int64_t M, D, ldx, ldr, ldro;
   int x_type, residual_type, weight_type, y_act, group;
   float eps;
+  uint32_t* err;
 };
 int64_t norm_max_width();  // largest D
+cudaError_t norm_prepare();  // sets the smem attributes
 cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t s);
 
 // Log probabilities, entropy and top alternatives of rows of logits (logprobs.cu).

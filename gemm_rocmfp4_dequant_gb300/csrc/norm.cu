@@ -11,6 +11,10 @@
 // scaling), so nothing is read twice: a group of threads owns a row, every
 // thread 1 to kMaxVec vectors of 8 consecutive values.  Rows of up to 256
 // values share a CTA (one warp or part of one per row).
+//
+// Many wide rows: a CTA per row leaves the memory idle while it sums and
+// scales (8.5 to 9 ns a row whatever its bytes).  There, persistent CTAs bring
+// whole rows to shared memory by bulk copies two rows ahead of use.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -158,46 +162,15 @@ RF4_DEV float row_reduce(float v, int lanes, int nwarps, float* red) {
   return v;
 }
 
-// XT, RT: types of x and of the residual (kTypeNone: no residual).  NV:
-// vectors a thread holds.  VEC: every row of every operand starts on a 16-byte
-// boundary and D is a multiple of 8.
-template <int XT, int RT, int NV, bool VEC>
-__global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormArgs a, int lanes) {
-  __shared__ float red[32];
-  grid_launch_dependents();
-  grid_dependency_wait();
-  const int tid = threadIdx.x;
-  const int rows_per_cta = blockDim.x / lanes;
-  const int t = tid % lanes;
-  const int64_t row = (int64_t)blockIdx.x * rows_per_cta + tid / lanes;
-  const bool live = row < a.M;
-  const int nwarps = blockDim.x >> 5;
+// The rest of a row once its threads hold h: residual, sum of squares, norm and
+// outputs.  `taken()` runs behind the first barrier of the row's sum, when
+// every thread has h.  values(e): how many values a vector from e on has.
+template <int RT, int NV, bool VEC, class Values, class Taken>
+RF4_DEV void finish_row(const NormArgs& a, int64_t row, bool live, int t, int lanes, int nwarps, float* red, float (&h)[NV][8], Values&& values,
+                        Taken&& taken) {
   const int D = (int)a.D;
-  // the row of every operand (a row past the last one reads and writes nothing)
-  const int64_t r = live ? row : 0;
-  auto at = [](const void* p, int type, int64_t i) { return static_cast<const uint8_t*>(p) + i * (type == kTypeF32 ? 4 : 2); };
-  const void* x = at(a.x, XT, r * a.ldx);
-  const void* res = at(a.residual, RT, r * a.ldr);
-  void* res_out = const_cast<uint8_t*>(at(a.residual_out, RT, r * a.ldro));
-  auto values = [&](int e) { return !live || e >= D ? 0 : VEC || D - e >= 8 ? 8 : D - e; };  // of a vector from e on
-  float h[NV][8];
   float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = 8 * (i * lanes + t), n = values(e);
-    if (n > 0) {
-      load8<XT, VEC>(x, e, n, h[i]);
-      if constexpr (RT != kTypeNone) {
-        float v[8];
-        load8<RT, VEC>(res, e, n, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] += v[j];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
-    }
-  }
+  uint8_t* res_out = RT == kTypeNone ? nullptr : static_cast<uint8_t*>(a.residual_out) + row * a.ldro * (RT == kTypeF32 ? 4 : 2);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     if constexpr (RT != kTypeNone) {
@@ -208,11 +181,12 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
     for (int j = 0; j < 8; ++j) ss = fmaf(h[i][j], h[i][j], ss);
   }
   ss = row_reduce<false>(ss, lanes, nwarps, red);
+  taken();
   const float rstd = rsqrtf(ss / (float)D + a.eps);
   const int group = a.group, shift = 31 - __clz(group | 1), groups = group ? (D + group - 1) >> shift : 1;
-  void* y = a.y == nullptr ? nullptr : const_cast<uint8_t*>(at(a.y, kTypeF16, r * D));
-  uint8_t* q = a.q == nullptr ? nullptr : a.q + r * D;
-  float* scales = a.scales + r * groups;
+  void* y = a.y == nullptr ? nullptr : static_cast<uint16_t*>(a.y) + row * D;
+  uint8_t* q = a.q == nullptr ? nullptr : a.q + row * D;
+  float* scales = a.scales + row * groups;
   float rowmax = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -251,7 +225,127 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
   }
 }
 
+// XT, RT: types of x and of the residual (kTypeNone: no residual).  NV:
+// vectors a thread holds.  VEC: every row of every operand starts on a 16-byte
+// boundary and D is a multiple of 8.
+template <int XT, int RT, int NV, bool VEC>
+__global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormArgs a, int lanes) {
+  __shared__ float red[32];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int tid = threadIdx.x;
+  const int rows_per_cta = blockDim.x / lanes;
+  const int t = tid % lanes;
+  const int64_t row = (int64_t)blockIdx.x * rows_per_cta + tid / lanes;
+  const bool live = row < a.M;
+  const int D = (int)a.D;
+  // the row of every operand (a row past the last one reads and writes nothing)
+  const int64_t r = live ? row : 0;
+  const uint8_t* x = static_cast<const uint8_t*>(a.x) + r * a.ldx * (XT == kTypeF32 ? 4 : 2);
+  const uint8_t* res = static_cast<const uint8_t*>(a.residual) + r * a.ldr * (RT == kTypeF32 ? 4 : 2);
+  auto values = [&](int e) { return !live || e >= D ? 0 : VEC || D - e >= 8 ? 8 : D - e; };
+  float h[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = 8 * (i * lanes + t), n = values(e);
+    if (n > 0) {
+      load8<XT, VEC>(x, e, n, h[i]);
+      if constexpr (RT != kTypeNone) {
+        float v[8];
+        load8<RT, VEC>(res, e, n, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] += v[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
+    }
+  }
+  finish_row<RT, NV, VEC>(a, r, live, t, lanes, blockDim.x >> 5, red, h, values, [] {});
+}
+
+constexpr int kStages = 2;
+
+// Bytes of a stage: a row of x, then a row of the residual.
+RF4_HOSTDEV constexpr int stage_bytes(int xt, int rt, int D) {
+  return D * (xt == kTypeF32 ? 4 : 2) + (rt == kTypeNone ? 0 : D * (rt == kTypeF32 ? 4 : 2));
+}
+
+// The persistent form: a CTA takes rows blockIdx.x, + gridDim.x, ...; thread t
+// its vectors t, t + blockDim.x, ... of each.
+template <int XT, int RT, int NV>
+__global__ void __launch_bounds__(512) norm_stream_kernel(const __grid_constant__ NormArgs a) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float red[32];
+  __shared__ uint64_t bars[kStages];
+  __shared__ int gave_up;
+  const int t = threadIdx.x, lanes = blockDim.x, D = (int)a.D;
+  const int xb = stage_bytes(XT, kTypeNone, D), bytes = stage_bytes(XT, RT, D);
+  if (t == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(smem_addr(&bars[i]), 1);
+    fence_mbar_init();
+    gave_up = 0;
+  }
+  __syncthreads();
+  grid_launch_dependents();
+  grid_dependency_wait();
+  auto issue = [&](int64_t row, int s) {  // thread 0
+    const uint32_t bar = smem_addr(&bars[s]);
+    uint8_t* dst = ring + s * bytes;
+    mbar_arrive_expect_tx(bar, (uint32_t)bytes);
+    bulk_g2s(smem_addr(dst), static_cast<const uint8_t*>(a.x) + row * a.ldx * (XT == kTypeF32 ? 4 : 2), (uint32_t)xb, bar);
+    if constexpr (RT != kTypeNone)
+      bulk_g2s(smem_addr(dst + xb), static_cast<const uint8_t*>(a.residual) + row * a.ldr * (RT == kTypeF32 ? 4 : 2), (uint32_t)(bytes - xb), bar);
+  };
+  if (t == 0)
+    for (int s = 0; s < kStages; ++s)
+      if (blockIdx.x + (int64_t)s * gridDim.x < a.M) issue(blockIdx.x + (int64_t)s * gridDim.x, s);
+  auto values = [&](int e) { return e < D ? 8 : 0; };
+  int s = 0;
+  uint32_t parity = 0;
+  int64_t row = blockIdx.x;
+  bool stopped = false;
+  for (; row < a.M && !stopped; row += gridDim.x) {
+    if (!mbar_wait_bounded(smem_addr(&bars[s]), parity)) gave_up = 1;
+    const uint8_t* st = ring + s * bytes;
+    float h[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = 8 * (i * lanes + t);
+      if (e < D) {
+        load8<XT, true>(st, e, 8, h[i]);
+        if constexpr (RT != kTypeNone) {
+          float v[8];
+          load8<RT, true>(st + xb, e, 8, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[i][j] += v[j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
+      }
+    }
+    // Behind the barrier every thread has read the stage: the row two ahead may
+    // come in.  A wait that gave up ends the loop, the same for all threads.
+    auto taken = [&] {
+      stopped = gave_up != 0;
+      if (t == 0 && !stopped && row + (int64_t)kStages * gridDim.x < a.M) {
+        fence_proxy_async();
+        issue(row + (int64_t)kStages * gridDim.x, s);
+      }
+    };
+    finish_row<RT, NV, true>(a, row, true, t, lanes, lanes >> 5, red, h, values, taken);
+    if (++s == kStages) s = 0, parity ^= 1u;
+  }
+  if (stopped && t == 0) {  // the copies under way land before the CTA leaves
+    atomicOr(a.err, kErrWaitTimeout);
+    for (int i = 0; i < kStages; ++i) (void)mbar_wait_bounded(smem_addr(&bars[i]), i < s ? parity ^ 1u : parity);
+  }
+}
+
 using NormFn = void (*)(NormArgs, int);
+
+using StreamFn = void (*)(NormArgs);
 
 template <int XT, int RT, bool VEC>
 NormFn pick_nv(int nv) {
@@ -281,20 +375,83 @@ NormFn pick(int xt, int rt, int nv) {
   }
 }
 
+template <int XT, int NV>
+StreamFn pick_stream_rt(int rt) {
+  switch (rt) {
+    case kTypeF32: return norm_stream_kernel<XT, kTypeF32, NV>;
+    case kTypeBF16: return norm_stream_kernel<XT, kTypeBF16, NV>;
+    case kTypeF16: return norm_stream_kernel<XT, kTypeF16, NV>;
+    default: return norm_stream_kernel<XT, kTypeNone, NV>;
+  }
+}
+
+template <int NV>
+StreamFn pick_stream(int xt, int rt) {
+  switch (xt) {
+    case kTypeF32: return pick_stream_rt<kTypeF32, NV>(rt);
+    case kTypeBF16: return pick_stream_rt<kTypeBF16, NV>(rt);
+    default: return pick_stream_rt<kTypeF16, NV>(rt);
+  }
+}
+
+constexpr int kStreamSmem = 96 * 1024;  // most a CTA of the persistent form takes
+
+template <class... Args>
+cudaError_t launch_dependent(void (*fn)(Args...), int64_t grid, int threads, int smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
 
 int64_t norm_max_width() { return (int64_t)1024 * 8 * kMaxVec; }
 
+cudaError_t norm_prepare() {
+  for (int xt = 0; xt < 3; ++xt)
+    for (int rt = 0; rt < 4; ++rt) {
+      for (const StreamFn fn : {pick_stream<2>(xt, rt), pick_stream<4>(xt, rt)}) {
+        cudaError_t e = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
+        if (e != cudaSuccess) return e;
+      }
+    }
+  return cudaSuccess;
+}
+
 cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t s) {
   const int rt = a.residual != nullptr ? a.residual_type : (int)kTypeNone;
   const bool vec = a.D % 8 == 0 && a.ldx % 8 == 0 && al16(a.x) && al16(a.weight) && al16(a.y) && al16(a.q) &&
                    (rt == kTypeNone || (a.ldr % 8 == 0 && a.ldro % 8 == 0 && al16(a.residual) && al16(a.residual_out)));
+  const int64_t vecs = (a.D + 7) / 8;
+  // Persistent CTAs for rows of 1024 values and more, from eight rows an SM on
+  // (fewer do not repay their start), where two rows fit a CTA's share.  Two
+  // vectors a thread for the 8-bit output, whose extra work wants more threads
+  // (4096 rows of 5120: 30.6 us against 35.7 with four), and for rows of up to
+  // 24 KB (8192 rows of 2048, fp32 into bf16: 28.6 us against 33.8); else four
+  // (23552 rows of 5120, fp32 into bf16: 193.5 us against 204.5 with two).
+  const int64_t smem = kStages * (int64_t)stage_bytes(a.x_type, rt, (int)a.D);
+  const int per = (a.q != nullptr || smem <= kStages * 24 * 1024) && vecs <= 1024 ? 2 : 4;
+  if (vec && vecs >= 128 && vecs <= 512 * per && a.M >= 8 * (int64_t)sms && smem <= kStreamSmem) {
+    const int threads = (int)(((vecs + per - 1) / per + 31) / 32 * 32);
+    const StreamFn fn = per == 2 ? pick_stream<2>(a.x_type, rt) : pick_stream<4>(a.x_type, rt);
+    int per_sm = 0;
+    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads, (size_t)smem);
+    if (e != cudaSuccess) return e;
+    if (per_sm > 0) return launch_dependent(fn, (int64_t)per_sm * sms, threads, (int)smem, s, a);
+  }
   // Vectors a thread holds: one where the rows are too few to fill the GPU (a
   // row's latency counts), four where they are many (fewer threads wait at
   // the row's reduction).
-  const int64_t vecs = (a.D + 7) / 8;
   int nv = a.M <= 2 * (int64_t)sms ? 1 : vecs >= 512 ? 4 : vecs >= 128 ? 2 : 1;
   while (nv < kMaxVec && (vecs + nv - 1) / nv > 1024) nv *= 2;
   int64_t lanes = (vecs + nv - 1) / nv;
@@ -307,16 +464,8 @@ cudaError_t launch_norm(const NormArgs& a, int sms, cudaStream_t s) {
   }
   const int threads = lanes <= 32 ? 128 : (int)lanes;
   const int64_t rows_per_cta = threads / lanes;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.M + rows_per_cta - 1) / rows_per_cta));
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, vec ? pick<true>(a.x_type, rt, nv) : pick<false>(a.x_type, rt, nv), a, (int)lanes);
+  return launch_dependent(vec ? pick<true>(a.x_type, rt, nv) : pick<false>(a.x_type, rt, nv), (a.M + rows_per_cta - 1) / rows_per_cta, threads, 0, s,
+                          a, (int)lanes);
 }
 
 }  // namespace rocmfp4

@@ -89,6 +89,29 @@ def test_matches_formula(M, D, pad):
                 assert (first.y is None or t.equal(first.y, again.y)) and (first.q is None or t.equal(first.scales, again.scales))
 
 
+@pytest.mark.parametrize("M,D", [(1217, 1024), (1300, 2056), (1999, 5120), (2500, 8192), (1217, 12288), (1400, 16384)])
+@pytest.mark.parametrize("pad", [0, 16])
+def test_many_wide_rows(M, D, pad):
+    """Rows enough for the persistent form (and too wide for it in some types), every pair of types, in place as well."""
+    t = torch()
+    g = t.Generator(device="cuda")
+    g.manual_seed(M + D + pad)
+    types = [t.float32, t.bfloat16, t.float16]
+    w = (1 + 0.3 * t.randn(D, generator=g, device="cuda")).bfloat16()
+    for k, xt in enumerate(types):
+        x = rows_of(t, M, D, xt, pad, 2.0, g)
+        for rt in [None] + types:
+            r = rows_of(t, M, D, rt, pad, 30.0, g) if rt is not None else None
+            group, yt = [(0, t.float16), (128, None), (-1, t.bfloat16), (32, t.float16)][(k + (types.index(rt) if rt else 3)) % 4]
+            ro = t.empty(M, D, dtype=rt, device="cuda") if r is not None else None
+            out = rf4.add_rmsnorm(x, w, residual=r, dtype=yt, residual_out=ro, group=group)
+            check(out, x, r, w, 1e-6, group)
+            if r is not None:
+                again = rf4.add_rmsnorm(x, w, residual=r, dtype=yt, group=group)
+                assert again.residual is r and t.equal(r, out.residual)
+                assert (out.y is None or t.equal(out.y, again.y)) and (out.q is None or t.equal(out.q.view(t.uint8), again.q.view(t.uint8)))
+
+
 @pytest.mark.parametrize("xoff,D", [(1, 512), (3, 514), (8, 512)])
 def test_unaligned_pointers(xoff, D):
     t = torch()
