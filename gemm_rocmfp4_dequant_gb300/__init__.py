@@ -259,19 +259,25 @@ def decode_attention(q, K, V, lens, Hkv: int, Tmax: int, scale: float, variant: 
 
 def _rows(t, name: str):
     """(rows, width, row stride) of a [rows, width] or [width] CUDA tensor whose rows are contiguous."""
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
     if len(shape) == 2:
         M, D = shape
-        ld, step = stride
-        if M == 1 and ld < D:
-            ld = D
     elif len(shape) == 1:
-        M, D, ld, step = 1, shape[0], shape[0], stride[0]
+        M, D = 1, shape[0]
     else:
         raise ValueError(f"{name} must be a [rows, width] or [width] tensor")
-    if (step != 1 and D > 1) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor with contiguous rows")
-    return M, D, ld
+    return M, D, _row_stride(t, name, M, D)
+
+
+def _row_stride(t, name: str, M: int, D: int) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.is_contiguous():
+        return D
+    stride = t.stride()
+    if stride[-1] != 1 and D > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return stride[0] if M > 1 else D
 
 
 def _dense(t, name: str, dtype, shape):
@@ -305,16 +311,16 @@ def add_rmsnorm(x, weight, residual=None, eps: float = 1e-6, dtype=None, y=None,
     ldr = ldro = rptr = roptr = yptr = qptr = sptr = size = 0
     rtype, act = OUT_F32, ACT_F16
     if residual is not None:
-        _, _, ldr = _rows(residual, "residual")
         dt = residual.dtype
-        rtype, rptr = codes.get(dt, -1), residual.data_ptr()
+        if residual.shape != shape:
+            raise ValueError("residual must have x's shape")
+        ldr, rtype, rptr = _row_stride(residual, "residual", M, D), codes.get(dt, -1), residual.data_ptr()
         if residual_out is None:
             residual_out, ldro, roptr = residual, ldr, rptr
+        elif residual_out.shape != shape or residual_out.dtype is not dt:
+            raise ValueError("residual_out must have x's shape and the residual's type")
         else:
-            _, _, ldro = _rows(residual_out, "residual_out")
-            roptr = residual_out.data_ptr()
-        if residual.shape != shape or residual_out.shape != shape or residual_out.dtype is not dt:
-            raise ValueError("residual and residual_out must have x's shape and one type")
+            ldro, roptr = _row_stride(residual_out, "residual_out", M, D), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out without residual")
     if weight.numel() != D or not weight.is_contiguous() or not weight.is_cuda:
