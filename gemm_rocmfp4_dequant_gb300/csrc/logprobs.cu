@@ -3,14 +3,19 @@
 //   z_v = scale * logit_v,  m = max z,  S = sum exp(z_v - m),
 //   logprob(t) = z_t - m - ln S,   entropy = ln S - (sum exp(z_v - m) (z_v - m)) / S,
 //   top n by (logit descending, index ascending) with their log probabilities.
-// Every thread keeps a running maximum, S and A = sum exp(z - m) (z - m) and
-// rescales them when its maximum grows; sums are fp32.
+// Every thread keeps a reference m and the sums S and A = sum exp(z - m) (z - m)
+// relative to it; sums are fp32.
 //
-// Bound: memory for many rows (each logit is read once: about 10
-// instructions a value, one of them a MUFU), latency for few.  A row is cut
-// into contiguous ranges, one per CTA, when there are too few rows to fill
-// the GPU; the last CTA of a row to finish joins the ranges' records in
-// range order, so the result does not depend on which that was.
+// Bound: memory for many rows (each logit is read once; about 13 instructions
+// a value, and at 59 % of the issue slots they are what holds it back),
+// latency for few.  A row is cut into contiguous ranges, one per CTA, when
+// there are too few rows to fill the GPU; the last CTA of a row to finish
+// joins the ranges' records in range order, so the result does not depend on
+// which that was.
+//
+// Measured on one GB300: 1024 rows of 152064 bf16 logits, 8 alternatives:
+// 81 us, 3.84 TB/s, 57 % of the copy bandwidth; 333 rows of 32001 fp16: 11.8 us;
+// one row of 152064 fp32, 5 alternatives: 8.4 us.
 //
 // Top n.  Values are compared as 64-bit keys (order-preserving bits of the
 // logit, complement of the index), so ties go to the lowest index and keys
