@@ -14,9 +14,9 @@
 //
 // Products.  A tile is 16 rows: 8 gate and the 8 up rows of the same hidden
 // values, or 16 output rows.  A span is 144 bytes (8 dual blocks) or 272 bytes
-// (16 single-scale blocks) of each row.  A warp takes tiles on its own (or
-// KP neighbouring warps share a tile's spans where tiles are few) and streams
-// their spans through a private ring of shared-memory stages, one tensor copy
+// (16 single-scale blocks) of each row.  A warp takes tiles on its own (the
+// last of a CTA's gate/up tiles, too few for a tile a warp, go to teams of two
+// or four warps that share a tile's spans) and streams their spans through a private ring of shared-memory stages, one tensor copy
 // of a 16-row box a span.  The down tasks are known as soon as the routing is,
 // so the ring runs on into them before the second barrier.
 // The arithmetic is mma.sync m16n8k16 on fp16 with fp32 accumulators: A is
@@ -110,7 +110,6 @@ struct MoeParams {
   int M, E, top_k, K, I;
   int router_type, route;
   float route_scale;
-  int parts;           // KP: warps that share a gate/up tile
   int ns;              // spans of a stage
   int stages, stage_bytes;  // ring of a warp
   // offsets in shared memory
@@ -586,12 +585,20 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 
   // ---- this warp's stages: gate/up tiles, then down tiles --------------------------------
   const int rb_k = nb_k * Fmt<V>::BB, rb_i = nb_i * Fmt<V>::BB;
-  const int KP = p.parts, team = warp / KP, part = warp % KP, teams = kWarps / KP;
-  const int span0 = spans_k * part / KP, span1 = spans_k * (part + 1) / KP;  // this warp's spans of a gate/up tile
-  const int per_expert = p.I / 8;                                          // gate/up tiles of an expert
-  // A CTA's gate/up tiles [.., gu1) are neighbours, so that its warps share
-  // activations in L1; they go round its teams.
-  const int gu0 = (int)((int64_t)A * per_expert * blockIdx.x / G) + team, gu1 = (int)((int64_t)A * per_expert * (blockIdx.x + 1) / G);
+  const int per_expert = p.I / 8;  // gate/up tiles of an expert
+  // A CTA's gate/up tiles are neighbours, so that its warps share activations
+  // in L1.  Rounds of a tile a warp; the tiles left over go to teams of KP
+  // warps, each with its part of the spans (a round of few tiles would leave
+  // most warps idle for as long as a whole tile takes: 34.6 against 29 us to
+  // the second barrier, where an SM had 33 tiles for its 16 warps).
+  const int g0 = (int)((int64_t)A * per_expert * blockIdx.x / G), n_gu = (int)((int64_t)A * per_expert * (blockIdx.x + 1) / G) - g0;
+  const int rounds_gu = n_gu / kWarps, left = n_gu - rounds_gu * kWarps;
+  int KP = left > 8 ? 1 : left > 4 ? 2 : 4;
+  while (KP > spans_k) KP /= 2;
+  const int team = warp / KP, part = warp - team * KP;
+  const int l0 = spans_k * part / KP, l1 = spans_k * (part + 1) / KP;  // spans of a tile left over
+  const int jobs_gu = rounds_gu + (team < left ? 1 : 0);              // this warp's
+  auto tile_of = [&](int j) { return g0 + rounds_gu * kWarps + (j < rounds_gu ? (j - rounds_gu) * kWarps + warp : team); };
   // Down: a CTA takes 16-row tiles, and its warps share the stages of a tile
   // (every chosen expert's rows) in equal runs.
   const int ns = p.ns, sd = (spans_i + ns - 1) / ns;
@@ -607,13 +614,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   auto gu_row = [&](int e, int i0, int r) { return p.Wgu + ((int64_t)e * 2 * p.I + (r < 8 ? 0 : p.I) + i0 + (r & 7)) * rb_k; };
   auto dn_row = [&](int e, int n0, int r) { return p.Wd + ((int64_t)e * p.K + n0 + r) * rb_i; };
 
-  // Copies of ns spans from `span` on of a tile's 16 rows into a stage (fewer at the row's end).
-  auto fill = [&](bool down, int e, int row0, int span, int slot) {
+  // Copies of ns spans from `span` on, up to `last`, of a tile's 16 rows into a stage.
+  auto fill = [&](bool down, int e, int row0, int span, int last, int slot) {
     uint8_t* dst = ring + slot * p.stage_bytes;
     const uint32_t bar = smem_addr(&bars[slot]);
     if constexpr (ALIGNED) {
       if (lane == 0) {
-        const int n = min(ns, (down ? spans_i : span1) - span);
+        const int n = min(ns, last - span);
         mbar_arrive_expect_tx(bar, (uint32_t)(n * kTileRows * U::SPAN));
 #pragma unroll 1
         for (int k = 0; k < n; ++k) {
@@ -623,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         }
       }
     } else {
-      const int rb = down ? rb_i : rb_k, lo = span * U::SPAN, len = min(rb - lo, ns * U::SPAN);
+      const int rb = down ? rb_i : rb_k, lo = span * U::SPAN, len = min(rb - lo, min(ns, last - span) * U::SPAN);
       const uint8_t* src = (down ? dn_row(e, row0, lane & 15) : gu_row(e, row0, lane & 15)) + lo;
       const uint32_t bytes = __reduce_add_sync(0xffffffffu, lane < kTileRows ? span_bytes(src, len) : 0u);
       if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
@@ -631,25 +638,32 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       if (lane < kTileRows) copy_span(dst + lane * pitch, src, len, bar);
     }
   };
-  // The next stage to fill: of a gate/up tile (its number, expert, first row
-  // and next span), then of a down tile (stage u of tile `id` of this CTA's).
+  // The next stage to fill: of gate/up job `id` (expert, first row, next span and
+  // the end), then of a down tile (stage u of tile `id` of this CTA's).
   struct {
     bool gu, any;
-    int id, e, row0, span, u, at;  // at: place of e in the list
+    int id, e, row0, span, last, u, at;  // at: place of e in the list
   } nx;
   auto start_gu = [&](int id) {
-    while (id >= (nx.at + 1) * per_expert) ++nx.at;
+    const int tile = tile_of(id);
+    while (tile >= (nx.at + 1) * per_expert) ++nx.at;
     nx.id = id;
     nx.e = s_list[nx.at];
-    nx.row0 = (id - nx.at * per_expert) * 8;
-    nx.span = span0;
+    nx.row0 = (tile - nx.at * per_expert) * 8;
+    nx.span = id < rounds_gu ? 0 : l0;
+    nx.last = id < rounds_gu ? spans_k : l1;
   };
-  nx.gu = gu0 < gu1;
-  nx.any = nx.gu || (u0 < u1 && my_tiles > 0);
-  nx.id = 0;
-  nx.u = u0;
-  nx.at = nx.gu ? gu0 / per_expert : u0 / sd;
-  if (nx.gu) start_gu(gu0);
+  auto start_dn = [&]() {
+    nx.gu = false;
+    nx.any = u0 < u1 && my_tiles > 0;
+    nx.id = 0;
+    nx.u = u0;
+    nx.at = u0 / max(sd, 1);
+    nx.last = spans_i;
+  };
+  nx.gu = nx.any = jobs_gu > 0;
+  if (nx.gu) nx.at = tile_of(0) / per_expert, start_gu(0);
+  else start_dn();
   int fill_slot = 0, filled = 0;
   auto fill_next = [&]() {
     if (!nx.any) return;
@@ -659,18 +673,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       nx.row0 = (blockIdx.x + nx.id * G) * kTileRows;
       nx.span = (nx.u - nx.at * sd) * ns;
     }
-    fill(!nx.gu, nx.e, nx.row0, nx.span, fill_slot);
+    fill(!nx.gu, nx.e, nx.row0, nx.span, nx.last, fill_slot);
     if (nx.gu) {
       nx.span += ns;
-      if (nx.span >= span1) {
-        if (nx.id + teams < gu1) {
-          start_gu(nx.id + teams);
-        } else {
-          nx.gu = false;
-          nx.any = u0 < u1 && my_tiles > 0;
-          nx.id = 0;
-          nx.at = u0 / sd;
-        }
+      if (nx.span >= nx.last) {
+        if (nx.id + 1 < jobs_gu) start_gu(nx.id + 1);
+        else start_dn();
       }
     } else if (++nx.u == u1) {
       nx.u = u0;
@@ -741,14 +749,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         for (int i = lane; i < kTileRows * p.M; i += 32) y_w[i] = 0.f;
         __syncwarp();
       }
-      // gate/up: tile x and every span of this warp's part; down: stages from x on of one expert
+      // gate/up: job x; down: stages from x on of one expert
       const int per = down ? sd : per_expert;
-      int at = (down ? u0 : gu0) / max(per, 1);
+      int at = (down ? u0 : tile_of(0)) / max(per, 1);
 #pragma unroll 1
-      for (int x = down ? u0 : gu0; x < (down ? u1 : gu1);) {
-        while (x >= (at + 1) * per) ++at;
+      for (int x = down ? u0 : 0; x < (down ? u1 : jobs_gu);) {
+        const int place = down ? x : tile_of(x);
+        while (place >= (at + 1) * per) ++at;
         const int e = s_list[at];
-        int row0, s0, s1;
+        int row0, s0, s1, parts = 1;
         if (down) {
           const int last = min(u1, (at + 1) * sd);
           row0 = (blockIdx.x + round * G) * kTileRows;
@@ -756,9 +765,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
           s1 = min(spans_i, (last - at * sd) * ns);
           x = last;
         } else {
-          row0 = (x - at * per_expert) * 8;
-          s0 = span0, s1 = span1;
-          x += teams;
+          row0 = (place - at * per_expert) * 8;
+          s0 = x < rounds_gu ? 0 : l0, s1 = x < rounds_gu ? spans_k : l1;
+          parts = x < rounds_gu ? 1 : KP;
+          ++x;
         }
         if (at != noted) {
           if (down && x < u1) fetch_h(at + 1);
@@ -803,7 +813,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
           stages(col);
         }
         // Lane (q, c): rows q and q + 8, columns 2 c and 2 c + 1 of every group.
-        const int parts = down ? 1 : KP;
         if (parts > 1) team_barrier(1 + team, KP * 32);
         if (down) {
 #pragma unroll 1
@@ -823,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
               }
             }
           }
-        } else if (part == 0) {
+        } else if (parts == 1 || part == 0) {
           const int i = row0 + q;
           const int64_t place = h_place(i);
 #pragma unroll 1
@@ -934,12 +943,7 @@ cudaError_t set_up(const MoeArgs& a, int sms, bool aligned, MoeParams* p, int* s
   p->acc_floats = (p->M + 3) / 4 * 128;  // a warp's sums of a tile, by group
   at += kWarps * p->acc_floats * 4;
   p->off_ring = (at + 127) / 128 * 128;
-  // Warps to a gate/up tile: one where every SM has tiles for its warps, more
-  // where the (at most min(E, M top_k)) chosen experts give it fewer.
   const int64_t spans_k = (a.K / 32 + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS, spans_i = (a.I / 32 + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS;
-  const int64_t experts = a.M * a.top_k < a.E ? a.M * a.top_k : a.E;
-  p->parts = 1;
-  while (p->parts < 4 && 2 * p->parts <= spans_k && experts * (a.I / 8) * p->parts < 8 * (int64_t)sms) p->parts *= 2;
   p->ns = V == 0 ? 2 : 1;  // spans of a stage
   const int each = aligned ? p->ns * kTileRows * U::SPAN : kTileRows * row_pitch<V, false>(p->ns);
   p->stage_bytes = (each + 127) / 128 * 128;
