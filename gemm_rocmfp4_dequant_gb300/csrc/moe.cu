@@ -16,8 +16,8 @@
 // values, or 16 output rows.  A span is 144 bytes (8 dual blocks) or 272 bytes
 // (16 single-scale blocks) of each row.  A warp takes tiles on its own (the
 // last of a CTA's gate/up tiles, too few for a tile a warp, go to teams of two
-// or four warps that share a tile's spans) and streams their spans through a private ring of shared-memory stages, one tensor copy
-// of a 16-row box a span.  The down tasks are known as soon as the routing is,
+// or four warps that share a tile's spans) and streams their spans through a
+// private ring of shared-memory stages, one tensor copy of a 16-row box a span.  The down tasks are known as soon as the routing is,
 // so the ring runs on into them before the second barrier.
 // The arithmetic is mma.sync m16n8k16 on fp16 with fp32 accumulators: A is
 // the decoded weights, exact in fp16, decoded once for all the tokens of the
@@ -43,8 +43,8 @@
 //
 // Measured on one GB300, dual, 128 experts of [2 x 768, 2048] + [2048, 768], 8
 // chosen: one token 20.5 us (21.8 MB; a cooperative launch starts every 2.048
-// us at best), eight tokens 52 to 56 us (137.6 MB, 2.5 TB/s); 64 experts of
-// [2 x 1536, 5120], single-scale, 6 chosen, four tokens: 88 us (2.97 TB/s).
+// us at best), eight tokens 51 to 53 us (137.6 MB, 2.6 TB/s); 64 experts of
+// [2 x 1536, 5120], single-scale, 6 chosen, four tokens: 81 to 88 us (3.1 TB/s).
 // 16 warps: with 12 (and 168 registers) the last ran 104 us.
 //
 // Rows whose length is no multiple of 16 bytes (K / 32 not a multiple of 8,
@@ -589,8 +589,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   // A CTA's gate/up tiles are neighbours, so that its warps share activations
   // in L1.  Rounds of a tile a warp; the tiles left over go to teams of KP
   // warps, each with its part of the spans (a round of few tiles would leave
-  // most warps idle for as long as a whole tile takes: 34.6 against 29 us to
-  // the second barrier, where an SM had 33 tiles for its 16 warps).
+  // most warps idle for as long as a whole tile takes.  Whole calls, a warp a
+  // tile always: 22.6, 51.4, 90.0 and 28.7 us; teams: 20.5, 50.6, 88.0 and
+  // 25.5, for the three sizes named on top and 13 tokens over 10 experts of
+  // width 352).
   const int g0 = (int)((int64_t)A * per_expert * blockIdx.x / G), n_gu = (int)((int64_t)A * per_expert * (blockIdx.x + 1) / G) - g0;
   const int rounds_gu = n_gu / kWarps, left = n_gu - rounds_gu * kWarps;
   int KP = left > 8 ? 1 : left > 4 ? 2 : 4;
