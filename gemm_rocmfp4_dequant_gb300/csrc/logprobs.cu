@@ -6,26 +6,29 @@
 // Every thread keeps a reference m and the sums S and A = sum exp(z - m) (z - m)
 // relative to it; sums are fp32.
 //
-// Bound: memory for many rows (each logit is read once; about 13 instructions
-// a value, and at 59 % of the issue slots they are what holds it back),
-// latency for few.  A row is cut into contiguous ranges, one per CTA, when
+// Bound: memory for many rows (each logit is read once; without
+// alternatives 5.2 TB/s at 1024 rows, 5.8 where the rows are a multiple of the
+// 608 CTAs that are resident at once), latency for few.  A row is cut into contiguous ranges, one per CTA, when
 // there are too few rows to fill the GPU; the last CTA of a row to finish
 // joins the ranges' records in range order, so the result does not depend on
 // which that was.
 //
 // Measured on one GB300: 1024 rows of 152064 bf16 logits, 8 alternatives:
-// 81 us, 3.84 TB/s, 57 % of the copy bandwidth; 333 rows of 32001 fp16: 11.8 us;
-// one row of 152064 fp32, 5 alternatives: 8.4 us.
+// 69.5 us, 4.48 TB/s, 66 % of the copy bandwidth; 333 rows of 32001 fp16, none:
+// 11.8 us; one row of 152064 fp32, 5: 8.7 us.
 //
 // Top n.  Values are compared as 64-bit keys (order-preserving bits of the
-// logit, complement of the index), so ties go to the lowest index and keys
-// are distinct.  From the first tile of the range a threshold is taken that at
-// least n of its values reach: the n-th largest of 64 disjoint groups' maxima.
-// Values that reach it go to a candidate list in shared memory; later tiles
-// contribute only values above it, so almost every value costs one comparison
-// and the tiles need no barrier.  After 2, 4, 8, ... tiles the list is cut back to n,
-// which raises the threshold.  A row that overfills the list all the same (one
-// that rises through the range) has its top n looked for again, tile by tile.
+// logit, complement of the index), so ties go to the lowest index and keys are
+// distinct.  In the pass a thread keeps the largest value of each of at most 8
+// runs of tiles, its chunks.  The n-th largest of 64 groups' largest values, as
+// a key with the last index that it can have, is a threshold that at least n
+// values reach; only chunks whose largest value reaches it can hold the top n,
+// little more than n as a rule, and their vectors alone are read again.  The
+// pass has no barrier and costs the same in whatever order the values come.
+// A candidate list filled during the pass, behind a threshold that was raised
+// after 2, 4, 8, ... tiles, took 80.8 against 69.5 us on the first case above
+// and 8.3 against 8.7 on the third.  One chunk a thread, and so all vectors of
+// the few threads read again, took 85.8.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -35,7 +38,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVecs = 2;        // 16-byte vectors a thread takes of a tile
 constexpr int kGroups = 64;     // groups of 4 neighbouring threads
-constexpr int kCap = 1024;      // room of the list: n threads' values of a tile and more
+constexpr int kChunks = 8;      // runs of tiles whose largest values a thread keeps
+constexpr int kCap = 1024;      // room of the candidate list
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Order-preserving bits: a < b as floats iff key(a) < key(b); -0 counts as +0
@@ -210,7 +214,8 @@ struct Logit<2> {
 };
 
 struct TopState {  // in shared memory
-  int count;       // candidates pushed (may pass the capacity: then `over`)
+  int count;       // candidates pushed (may pass the capacity)
+  int chunks;      // that may have some
   int kept;        // scratch of cut()
   uint64_t floor;  // values must have a larger key to become candidates
   uint64_t group[kGroups];
@@ -257,13 +262,6 @@ RF4_DEV uint64_t nth_of(const uint64_t* keys, int count, uint64_t mine, int n) {
   return threshold;
 }
 
-// As group_threshold, over single threads: at most n threads have keys that
-// reach it.  `keys` is room for kThreads keys.  Slower: for full lists only.
-RF4_DEV uint64_t thread_threshold(uint64_t* keys, uint64_t mine, int n) {
-  keys[threadIdx.x] = mine;
-  return nth_of(keys, kThreads, mine, n);
-}
-
 // The n largest of the candidate list's `count` keys to the list's front, in
 // order; floor becomes the n-th (if there are n).  Every thread calls it.
 RF4_DEV void cut(TopState& st, uint64_t* list, uint64_t* spare, int count, int n) {
@@ -307,11 +305,14 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   using L = Logit<TYPE>;
   using E = typename L::type;
   constexpr int PER = L::PER, N = kVecs * PER, TILE = kThreads * kVecs;  // vectors of a tile
-  static_assert(kMaxTop * N + kMaxTop <= kCap && kMaxTop * kMaxTop <= kCap, "what is pushed without a check has room");
+  constexpr int kPicked = 4 * kMaxTop;  // threads that may have some of the top n
+  static_assert(kThreads * kChunks * sizeof(float) <= kCap * sizeof(uint64_t), "the chunks' largest values fit the spare list");
+  static_assert(kThreads + kMaxTop <= kCap && kMaxTop * kMaxTop <= kCap, "what is pushed without a check has room");
   __shared__ TopState st;
   __shared__ uint64_t lists[TOP ? 2 * kCap : 1];
   __shared__ Stats warp_stats[kThreads / 32];
   __shared__ int picked[kMaxTop];
+  __shared__ uint16_t chunks[TOP ? kPicked * kChunks : 1];  // thread and chunk
   __shared__ int last;
   uint64_t* list = lists;
   uint64_t* spare = lists + (TOP ? kCap : 0);
@@ -324,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   const float c = a.scale * kLog2e;
   if (TOP && tid == 0) {
     st.count = 0;
+    st.chunks = 0;
     st.floor = 0;
   }
   __syncthreads();
@@ -349,6 +351,19 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     return base + (i / PER) * kThreads + tid < v1 && e >= 0 && e < a.V;
   };
 
+  auto values = [&](int base, float (&v)[N]) {  // of a tile at an end, absent ones -inf
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      // a vector inside the row in one load, one at an end of it value by value
+      if (present(base, k * PER) && present(base, k * PER + PER - 1)) {
+        L::unpack(__ldg(vz + base + k * kThreads + tid), v + k * PER);
+      } else {
+#pragma unroll
+        for (int i = k * PER; i < k * PER + PER; ++i) v[i] = present(base, i) ? L::one(z[index(base, i)]) : -INFINITY;
+      }
+    }
+  };
+
   float given = __uint_as_float(0x7FC00000u);  // the target's logit, asked for ahead of use
   if (tid == 0 && a.targets != nullptr) {
     const int64_t t = a.targets[row];
@@ -358,10 +373,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   Stats s;
   uint4 w[kVecs];
   if (v0 < v1 && whole(v0)) fetch(v0, w);
-  int tiles = 0;
-  uint64_t floor = 0;  // candidates have larger keys
+  // This thread's chunks' largest values; `spare` is not needed until they are done with.
+  float* top = reinterpret_cast<float*>(spare) + tid;
+  const int per_chunk = TOP ? ((v1 - v0 + TILE - 1) / TILE + kChunks - 1) / kChunks : 1;  // tiles
+  float chunk_top = -INFINITY;
+  int chunk = 0, in_chunk = 0;
 #pragma unroll 1
-  for (int base = v0; base < v1; base += TILE, ++tiles) {
+  for (int base = v0; base < v1; base += TILE) {
     float v[N], tm;
     const bool full = whole(base);
     if (full) {
@@ -369,16 +387,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
       for (int k = 0; k < kVecs; ++k) L::unpack(w[k], v + k * PER);
       tm = L::largest(w);
     } else {
-#pragma unroll
-      for (int k = 0; k < kVecs; ++k) {
-        // a vector inside the row in one load, one at an end of it value by value
-        if (present(base, k * PER) && present(base, k * PER + PER - 1)) {
-          L::unpack(__ldg(vz + base + k * kThreads + tid), v + k * PER);
-        } else {
-#pragma unroll
-          for (int i = k * PER; i < k * PER + PER; ++i) v[i] = present(base, i) ? L::one(z[index(base, i)]) : -INFINITY;
-        }
-      }
+      values(base, v);
       tm = v[0];
 #pragma unroll
       for (int i = 1; i < N; ++i) tm = fmaxf(tm, v[i]);
@@ -413,76 +422,124 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     s.S += sum.x + sum.y;
     s.A += tile_a;
     if constexpr (TOP) {
-      if (tiles == 0) {
-        uint64_t best = 0;  // the thread's largest key
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const uint64_t k = key_of(v[i], (uint32_t)index(base, i));
-          if (k > best && present(base, i)) best = k;
-        }
-        const uint64_t t = group_threshold(st, best, n);
-        floor = t > 0 ? t - 1 : 0;
-      }
-      // NaN compares as the largest value: fmaxf skips it, the sum does not
-      const float fv = unordered((uint32_t)(floor >> 32));
-      if (!(tm < fv) || s.S != s.S) {
-        uint32_t hits = 0;  // values that may be candidates: seldom more than one
-#pragma unroll
-        for (int i = 0; i < N; ++i) hits |= (v[i] < fv ? 0u : 1u) << i;
-        for (; hits != 0; hits &= hits - 1) {
-          const int i = __ffs(hits) - 1;
-          if (!present(base, i)) continue;
-          const uint64_t k = key_of(L::one(z[index(base, i)]), (uint32_t)index(base, i));
-          if (k > floor) {
-            const int at = atomicAdd(&st.count, 1);
-            if (at < kCap) list[at] = k;
-          }
-        }
-      }
-      // The threshold of t tiles lets about n / t values of the next one pass:
-      // it is raised after 2, 4, 8, ... tiles.
-      if (tiles > 0 && ((tiles & (tiles + 1)) == 0 || (tiles & 31) == 31)) {
-        __syncthreads();
-        const int count = st.count;
-        __syncthreads();
-        if (count > n && count <= kCap) {
-          cut(st, list, spare, count, n);
-          floor = st.floor;
-        }
+      chunk_top = fmaxf(chunk_top, tm);
+      if (++in_chunk == per_chunk) {
+        top[chunk++ * kThreads] = chunk_top;
+        chunk_top = -INFINITY;
+        in_chunk = 0;
       }
     }
   }
   if constexpr (TOP) {
+    if (in_chunk > 0) top[chunk++ * kThreads] = chunk_top;
+    const int count = chunk, vecs_chunk = per_chunk * kVecs;  // of a thread and chunk
+    auto vec_of = [&](int thread, int at, int r) { return v0 + (at * vecs_chunk + r) * kThreads + thread; };
+    // indices that values of a chunk lie between
+    auto from_index = [&](int thread, int at) { return (uint32_t)max((int64_t)vec_of(thread, at, 0) * PER - lead, (int64_t)0); };
+    auto to_index = [&](int thread, int at) { return (uint32_t)((int64_t)vec_of(thread, at, vecs_chunk - 1) * PER - lead + PER - 1); };
+
+    // Bounds of the thread's largest key, 0 for none.
+    uint64_t low = 0, high = 0;
+    int look_from = v0, look_to = v1;
+    const bool nan = s.S != s.S;  // perhaps: fmaxf() has passed over it, and it is the largest of values
+    if (nan) {
+      for (int k = 0; k < count; ++k) top[k * kThreads] = __uint_as_float(0x7FC00000u);
+    } else if (v0 + tid < v1) {
+      int at = 0;
+      float best = top[0];
+      for (int k = 1; k < count; ++k)
+        if (top[k * kThreads] > best) best = top[k * kThreads], at = k;
+      low = key_of(best, to_index(tid, at));
+      high = key_of(best, from_index(tid, at));
+      look_from = v0 + at * per_chunk * TILE;
+      look_to = min(v1, look_from + per_chunk * TILE);
+    }
+    uint64_t least = 0;
+    bool mine = false, look = nan;
+#pragma unroll 1
+    for (int round = 0; round < 2; ++round) {
+      if (look) {
+        low = 0;
+#pragma unroll 1
+        for (int base = look_from; base < look_to; base += TILE) {
+          float v[N];
+          values(base, v);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const uint64_t k = key_of(v[i], (uint32_t)index(base, i));
+            if (k > low && present(base, i)) low = k;
+          }
+        }
+        high = low;
+      }
+      least = group_threshold(st, low, n);
+      mine = high != 0 && high >= least;
+      if (__syncthreads_count(mine) <= kPicked) break;
+      // Many threads tie at the threshold: their keys themselves, of which at
+      // most 4 n reach their threshold.
+      look = mine && !nan;
+      if (!mine) low = high = 0;
+    }
+    if (mine)
+      for (int k = 0; k < count; ++k)
+        if (key_of(top[k * kThreads], from_index(tid, k)) >= least) chunks[atomicAdd(&st.chunks, 1)] = (uint16_t)(k * kThreads + tid);
+    __syncthreads();
+    const int items = st.chunks * vecs_chunk;
+    auto item_vec = [&](int item) {
+      const int k = item < items ? chunks[item / vecs_chunk] : 0;
+      return item < items ? vec_of(k % kThreads, k / kThreads, item % vecs_chunk) : v1;
+    };
+    auto push = [&](uint64_t k) {
+      const int at = atomicAdd(&st.count, 1);
+      if (at < kCap) list[at] = k;
+    };
+    const float lv = unordered((uint32_t)(least >> 32));  // a NaN if there is no threshold
+#pragma unroll 1
+    for (int item = tid; item < items; item += kThreads) {
+      const int x = item_vec(item);
+      if (x >= v1) continue;
+      const int64_t e = (int64_t)x * PER - lead;  // index of its first value
+      if (e >= 0 && e + PER <= a.V) {
+        float v[PER];
+        L::unpack(__ldg(vz + x), v);
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (!(v[i] < lv)) {
+            const uint64_t k = key_of(v[i], (uint32_t)(e + i));
+            if (k >= least) push(k);
+          }
+      } else {  // at an end of the row
+#pragma unroll 1
+        for (int i = 0; i < PER; ++i)
+          if (e + i >= 0 && e + i < a.V) {
+            const uint64_t k = key_of(L::one(z[e + i]), (uint32_t)(e + i));
+            if (k >= least) push(k);
+          }
+      }
+    }
     __syncthreads();
     const int pushed = st.count;
     __syncthreads();
     if (pushed > kCap) {
-      // More candidates than the list holds.  Again over the range: of each
-      // tile the keys above the n-th that also reach the n-th largest of the
-      // threads' largest ones, at most n threads' values.
-      if (tid == 0) st.count = 0, st.floor = 0;
+      // Few chunks with a thousand of the range's largest values.  Again, a
+      // value a thread at a time, cut to n each time.
+      if (tid == 0) st.count = 0, st.floor = least > 0 ? least - 1 : 0;
       __syncthreads();
 #pragma unroll 1
-      for (int base = v0; base < v1; base += TILE) {
-        const uint64_t least = st.floor;
-        uint64_t best = 0;
+      for (int from = 0; from < items; from += kThreads) {
+        const int x = item_vec(from + tid);
 #pragma unroll 1
-        for (int i = 0; i < N; ++i) {
-          const uint64_t k = present(base, i) ? key_of(L::one(z[index(base, i)]), (uint32_t)index(base, i)) : 0;
-          if (k > least && k > best) best = k;
+        for (int i = 0; i < PER; ++i) {
+          const int64_t e = x < v1 ? (int64_t)x * PER - lead + i : -1;
+          if (e >= 0 && e < a.V) {
+            const uint64_t k = key_of(L::one(z[e]), (uint32_t)e);
+            if (k > st.floor) push(k);
+          }
+          __syncthreads();
+          const int have = st.count;
+          __syncthreads();
+          cut(st, list, spare, have, n);
         }
-        if (__syncthreads_or(best != 0) == 0) continue;
-        const uint64_t t = thread_threshold(spare, best, n);
-        const uint64_t above = t > least ? t - 1 : least;
-#pragma unroll 1
-        for (int i = 0; i < N; ++i) {
-          const uint64_t k = present(base, i) ? key_of(L::one(z[index(base, i)]), (uint32_t)index(base, i)) : 0;
-          if (k > above) list[atomicAdd(&st.count, 1)] = k;
-        }
-        __syncthreads();
-        const int count = st.count;
-        __syncthreads();
-        cut(st, list, spare, count, n);
       }
     }
   }

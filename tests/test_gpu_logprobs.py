@@ -131,6 +131,44 @@ def test_special_rows(V, dtype, copies):
         assert all(t.equal(a, b) for a, b in zip(got, again))
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("M", [1, 620])
+@pytest.mark.parametrize("off", [0, 3])
+def test_large_values_in_few_places(M, dtype, off):
+    """Every large value of a row where a few threads read: more candidates than the list holds."""
+    t = torch()
+    V = 20000
+    g = t.Generator(device="cuda")
+    g.manual_seed(M + off)
+    dt = getattr(t, dtype)
+    per = 16 // dt.itemsize
+    buf = t.rand(M * V + 16, generator=g, device="cuda").to(dt)
+    z = buf[off:off + M * V].view(M, V)
+    place = (t.arange(V, device="cuda") + off) // per % 256
+    for n in (5, 20, 32):
+        large = (place % 8 == 0) & (place < 8 * (n - 1))
+        w = (z.float() + 20 * large).to(dt)
+        buf2 = t.empty_like(buf)
+        row = buf2[off:off + M * V].view(M, V)
+        row.copy_(w)
+        targets = t.randint(0, V, (M,), generator=g, device="cuda").int()
+        check(row, targets, n, 1.0, rf4.logprobs(row, targets, top_n=n))
+
+
+@pytest.mark.parametrize("M", [1, 620])
+def test_rows_with_many_nan(M):
+    """NaN ranks as the largest value, the lowest index first."""
+    t = torch()
+    z = t.randn(M, 9001, device="cuda")
+    z[:, 5::3] = float("nan")
+    z[M // 2:, :] = float("nan")
+    z[M // 2:, 8] = 1.0
+    _, _, ids, _ = rf4.logprobs(z, None, top_n=12)
+    first = t.tensor([list(range(5, 41, 3))], device="cuda", dtype=t.int32)
+    rest = t.tensor([[0, 1, 2, 3, 4, 5, 6, 7, 9, 10, 11, 12]], device="cuda", dtype=t.int32)
+    assert t.equal(ids, t.cat([first.expand(M // 2, -1), rest.expand(M - M // 2, -1)]))
+
+
 def test_nan_and_infinity():
     t = torch()
     z = t.randn(3, 5000, device="cuda")
