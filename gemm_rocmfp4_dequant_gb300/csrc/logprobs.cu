@@ -235,29 +235,33 @@ RF4_DEV uint64_t group_threshold(TopState& st, uint64_t mine, int n) {
   if ((threadIdx.x & 3) == 0) st.group[threadIdx.x >> 2] = mine;
   if (threadIdx.x == 0) threshold = 0;
   __syncthreads();
-  if (threadIdx.x < kGroups) {
-    const uint64_t k = st.group[threadIdx.x];
-    int rank = 0;
-#pragma unroll 16
-    for (int i = 0; i < kGroups; ++i) rank += st.group[i] > k ? 1 : 0;
-    if (rank == n - 1 && k != 0) threshold = k;  // distinct keys: one thread
-  }
+  // a group's four lanes compare with a quarter of the groups each
+  const int part = threadIdx.x & 3;
+  int rank = 0;
+#pragma unroll
+  for (int i = 0; i < kGroups; i += 4) rank += st.group[i + part] > mine ? 1 : 0;
+  rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+  rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+  if (part == 0 && rank == n - 1 && mine != 0) threshold = mine;  // distinct keys: one group
   __syncthreads();
   return threshold;
 }
 
-// The n-th largest of `count` (n < count <= kThreads) distinct keys; thread i
-// gives key i as `mine`, 0 for none (then there may be fewer: 0).
-RF4_DEV uint64_t nth_of(const uint64_t* keys, int count, uint64_t mine, int n) {
+// The n-th largest of `count` (n < count <= kThreads) distinct keys, of which
+// zeros are none (then there may be fewer: 0).  Every thread of the CTA calls it.
+RF4_DEV uint64_t nth_of(const uint64_t* keys, int count, int n) {
   __shared__ uint64_t threshold;
   if (threadIdx.x == 0) threshold = 0;
   __syncthreads();
-  if (mine != 0) {
-    int rank = 0;
+  const int lanes = count <= kThreads / 4 ? 4 : count <= kThreads / 2 ? 2 : 1;  // a key's
+  const int at = threadIdx.x / lanes, part = threadIdx.x % lanes;
+  const uint64_t mine = at < count ? keys[at] : 0;
+  int rank = 0;
 #pragma unroll 8
-    for (int i = 0; i < count; ++i) rank += keys[i] > mine ? 1 : 0;
-    if (rank == n - 1) threshold = mine;
-  }
+  for (int i = part; i < count; i += lanes) rank += keys[i] > mine ? 1 : 0;
+  if (lanes > 1) rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+  if (lanes > 2) rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+  if (part == 0 && mine != 0 && rank == n - 1) threshold = mine;
   __syncthreads();
   return threshold;
 }
@@ -576,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
       if (tid == 0) st.count = 0, st.floor = 0;
       if (tid < P) spare[tid] = first;
       __syncthreads();
-      const uint64_t t = P > n ? nth_of(spare, P, first, n) : 0;
+      const uint64_t t = P > n ? nth_of(spare, P, n) : 0;
       if (first != 0 && first >= t) picked[atomicAdd(&st.count, 1)] = tid;
       __syncthreads();
       const int records_in = st.count;
