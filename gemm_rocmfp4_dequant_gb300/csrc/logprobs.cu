@@ -14,8 +14,8 @@
 // which that was.
 //
 // Measured on one GB300: 1024 rows of 152064 bf16 logits, 8 alternatives:
-// 69.5 us, 4.48 TB/s, 66 % of the copy bandwidth; 333 rows of 32001 fp16, none:
-// 11.8 us; one row of 152064 fp32, 5: 8.7 us.
+// 69.2 us, 4.50 TB/s, 66 % of the copy bandwidth; 333 rows of 32001 fp16, none:
+// 8.5 to 9.5 us; one row of 152064 fp32, 5: 8.6 us.
 //
 // Top n.  Values are compared as 64-bit keys (order-preserving bits of the
 // logit, complement of the index), so ties go to the lowest index and keys are
@@ -618,8 +618,8 @@ using LogprobsFn = void (*)(LogprobsArgs);
 
 }  // namespace
 
-// A split row has at most 4 * sms + M records with M < 4 * sms.
-size_t logprobs_ws_bytes(int sms) { return (size_t)8 * sms * kRecordBytes; }
+// Split rows have at most 4 * sms parts together.
+size_t logprobs_ws_bytes(int sms) { return (size_t)4 * sms * kRecordBytes; }
 size_t logprobs_cnt_words(int sms) { return (size_t)4 * sms; }
 
 cudaError_t launch_logprobs(const LogprobsArgs& args, int sms, cudaStream_t s) {
