@@ -4,6 +4,8 @@
 #include <string>
 #include <cuda_runtime.h>
 
+#include "moe_layout.h"
+
 namespace rocmfp4 {
 
 // Host-side bookkeeping shared by the C entry points (api.cu).
@@ -126,14 +128,6 @@ cudaError_t launch_logprobs(const LogprobsArgs& a, int sms, cudaStream_t s);
 // Wgu and Wd 16-byte aligned; K and I multiples of 32, at most kMoeMaxWidth;
 // E <= kMoeMaxExperts; top_k <= min(E, kMoeMaxTop); M * top_k * I at most
 // kMoeMaxHidden.  One cooperative launch of one CTA per SM.
-constexpr int kMoeMaxTokens = 32, kMoeMaxExperts = 512, kMoeMaxTop = 16, kMoeMaxWidth = 32768;
-constexpr int64_t kMoeMaxHidden = int64_t(1) << 22;
-// router logits, activation scales, largest hidden values, hidden values in
-// fp32 and as two fp16 parts (rows padded to 512), activations (likewise),
-// room for a read past the last
-constexpr size_t kMoeWsFloats = (size_t)kMoeMaxTokens * (kMoeMaxExperts + 1 + kMoeMaxTop) + 2 * kMoeMaxHidden +
-                                (size_t)kMoeMaxTokens * kMoeMaxTop * 512 + (size_t)kMoeMaxTokens * (kMoeMaxWidth + 512) / 2 + 256;
-constexpr int kMoeBarWords = 4;
 struct MoeArgs {
   const uint16_t* X;   // M x K
   const void* router;  // E x K

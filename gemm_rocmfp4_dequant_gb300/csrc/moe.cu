@@ -62,10 +62,10 @@
 namespace rocmfp4 {
 namespace {
 
-constexpr int kWarps = 16;
+constexpr int kWarps = kMoeWarps;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTileRows = 16;
-constexpr int kMaxStages = 6;
+constexpr int kTileRows = kMoeTileRows;
+constexpr int kMaxStages = kMoeMaxStages;
 constexpr int kRouterTokens = 8;   // tokens a router pass holds
 constexpr int kTouchBytes = 32768;  // activations asked for ahead of use
 constexpr int kFastExp = 4;        // h times 2^4 in its fp16 pair
@@ -79,12 +79,10 @@ struct Unit {
   static constexpr int X_SPAN = SPAN_BLOCKS * 64;  // bytes of a span's fp16 activations
 };
 
-// A stage of ns spans: aligned rows as ns boxes of 16 rows x one span (36 or 68
-// words: rows an odd multiple of 16 bytes apart, whose reads meet no bank
-// twice), unaligned ones as 16 slots of ns spans, with room for their place
-// within 16 bytes and to end in.
-template <int V, bool ALIGNED>
-RF4_HOSTDEV constexpr int row_pitch(int ns) { return ALIGNED ? Unit<V>::SPAN : ns * Unit<V>::SPAN + 32; }
+static_assert(Unit<0>::SPAN == moe_span_bytes(0) && Unit<1>::SPAN == moe_span_bytes(1), "the layout's spans");
+static_assert(Unit<0>::SPAN_BLOCKS == moe_span_blocks(0) && Unit<1>::SPAN_BLOCKS == moe_span_blocks(1), "the layout's spans");
+
+// Bytes from span to span of a stage.
 template <int V, bool ALIGNED>
 RF4_HOSTDEV constexpr int span_step() { return ALIGNED ? kTileRows * Unit<V>::SPAN : Unit<V>::SPAN; }
 
@@ -110,11 +108,7 @@ struct MoeParams {
   int M, E, top_k, K, I;
   int router_type, route;
   float route_scale;
-  int ns;              // spans of a stage
-  int stages, stage_bytes;  // ring of a warp
-  // offsets in shared memory
-  int off_mask, off_list, off_slot, off_unscale, off_y, off_acc, off_ring;
-  int acc_floats;      // per warp
+  MoeLayout l;
 };
 
 template <int ACT>
@@ -333,13 +327,13 @@ template <int V, int ACT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant__ MoeParams p) {
   using U = Unit<V>;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* s_probs = reinterpret_cast<float*>(smem);                           // [M][top_k]
-  uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + p.off_mask);         // [E]: tokens of an expert
-  uint16_t* s_list = reinterpret_cast<uint16_t*>(smem + p.off_list);         // chosen experts, ascending
-  uint8_t* s_slot = smem + p.off_slot;                                       // [M][E]: which choice of the token
-  float* s_unscale = reinterpret_cast<float*>(smem + p.off_unscale);         // [M]: 1 / the activations' scale
-  float* s_y = reinterpret_cast<float*>(smem + p.off_y);                     // [kWarps][M][16]: outputs of a down tile
-  float* s_acc = reinterpret_cast<float*>(smem + p.off_acc);                 // [kWarps][acc_floats]
+  float* s_probs = reinterpret_cast<float*>(smem);                          // [M][top_k]
+  uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + p.l.off_mask);      // [E]: tokens of an expert
+  uint16_t* s_list = reinterpret_cast<uint16_t*>(smem + p.l.off_list);      // chosen experts, ascending
+  uint8_t* s_slot = smem + p.l.off_slot;                                    // [M][E]: which choice of the token
+  float* s_unscale = reinterpret_cast<float*>(smem + p.l.off_unscale);      // [M]: 1 / the activations' scale
+  float* s_y = reinterpret_cast<float*>(smem + p.l.off_y);                  // [kWarps][M][16]: outputs of a down tile
+  float* s_acc = reinterpret_cast<float*>(smem + p.l.off_acc);              // [kWarps][acc_floats]
   __shared__ uint64_t s_bars[kWarps * kMaxStages];
   __shared__ uint64_t s_pick[kWarps][kMoeMaxTop];
   __shared__ float s_red[kWarps][kRouterTokens];
@@ -354,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 
   uint64_t* bars = s_bars + warp * kMaxStages;
   if (lane == 0) {
-    for (int i = 0; i < p.stages; ++i) mbar_init(smem_addr(&bars[i]), 1);
+    for (int i = 0; i < p.l.stages; ++i) mbar_init(smem_addr(&bars[i]), 1);
     fence_mbar_init();
   }
   if (ALIGNED && tid == 0) {
@@ -497,9 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   for (int64_t i = (int64_t)tid * 128; ok && i < p.M * spans_k * U::X_SPAN && i < kTouchBytes; i += kThreads * 128) touch(p.xf + i);
   // ---- top k of every token (one warp per token), repeated by every CTA ----
   if (ok) {
-    // Room in the idle ring: the order of every expert's logit, then the
+    // Room in what is idle yet: the order of every expert's logit, then the
     // candidates: those that reach the top_k-th largest of the lanes' maxima.
-    uint32_t* keys = reinterpret_cast<uint32_t*>(smem + p.off_ring) + warp * 4 * p.E;
+    uint32_t* keys = reinterpret_cast<uint32_t*>(smem + p.l.off_select + warp * p.l.select_bytes);
     uint64_t* cand = reinterpret_cast<uint64_t*>(keys + 2 * p.E);
     for (int m = warp; m < p.M; m += kWarps) {
       uint32_t best = 0;
@@ -603,14 +597,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   auto tile_of = [&](int j) { return g0 + rounds_gu * kWarps + (j < rounds_gu ? (j - rounds_gu) * kWarps + warp : team); };
   // Down: a CTA takes 16-row tiles, and its warps share the stages of a tile
   // (every chosen expert's rows) in equal runs.
-  const int ns = p.ns, sd = (spans_i + ns - 1) / ns;
+  const int ns = p.l.ns, sd = (spans_i + ns - 1) / ns;
   const int tiles = p.K / kTileRows, my_tiles = (int)blockIdx.x < tiles ? (tiles - (int)blockIdx.x + G - 1) / G : 0;
   const int u0 = warp * (A * sd) / kWarps, u1 = (warp + 1) * (A * sd) / kWarps;
-  uint8_t* ring = smem + p.off_ring + warp * p.stages * p.stage_bytes;
+  uint8_t* ring = smem + p.l.off_ring + warp * p.l.stages * p.l.stage_bytes;
 
   // Lane (q, c) reads rows q and q + 8 of a stage at unit c of each span.
   // Unaligned rows start at their own place within 16 bytes.
-  const int q = lane >> 2, c = lane & 3, pitch = row_pitch<V, ALIGNED>(ns);
+  const int q = lane >> 2, c = lane & 3, pitch = moe_row_pitch(V, ALIGNED, ns);
   constexpr int STEP = span_step<V, ALIGNED>();
   const int unit_a = q * pitch + c * U::BYTES, unit_b = unit_a + 8 * pitch;
   auto gu_row = [&](int e, int i0, int r) { return p.Wgu + ((int64_t)e * 2 * p.I + (r < 8 ? 0 : p.I) + i0 + (r & 7)) * rb_k; };
@@ -618,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 
   // Copies of ns spans from `span` on, up to `last`, of a tile's 16 rows into a stage.
   auto fill = [&](bool down, int e, int row0, int span, int last, int slot) {
-    uint8_t* dst = ring + slot * p.stage_bytes;
+    uint8_t* dst = ring + slot * p.l.stage_bytes;
     const uint32_t bar = smem_addr(&bars[slot]);
     if constexpr (ALIGNED) {
       if (lane == 0) {
@@ -687,16 +681,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       nx.at = u0 / sd;
       nx.any = ++nx.id < my_tiles;
     }
-    if (++fill_slot == p.stages) fill_slot = 0;
+    if (++fill_slot == p.l.stages) fill_slot = 0;
     ++filled;
   };
   int slot = 0, used = 0;
   uint32_t parity = 0;
 #pragma unroll 1
-  for (int i = 0; i < p.stages; ++i) fill_next();
+  for (int i = 0; i < p.l.stages; ++i) fill_next();
   auto next_slot = [&]() {
     ++used;
-    if (++slot == p.stages) slot = 0, parity ^= 1u;
+    if (++slot == p.l.stages) slot = 0, parity ^= 1u;
   };
   // The next stage, once its copies have landed.  If a wait gives up, nothing
   // more is copied or waited for: the outputs are invalid, and an error bit says so.
@@ -705,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       if (lane == 0) atomicOr(p.err, kErrWaitTimeout);
       nx.any = false;
     }
-    return ring + slot * p.stage_bytes;
+    return ring + slot * p.l.stage_bytes;
   };
   auto release_stage = [&]() {
     __syncwarp();
@@ -719,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     for (int i = 0; i < skip; ++i) tokens &= tokens - 1;
     return tokens ? __ffs(tokens) - 1 : -1;
   };
-  float* acc_w = s_acc + (size_t)warp * p.acc_floats;
+  float* acc_w = s_acc + (size_t)warp * p.l.acc_floats;
   uint32_t* off_w = s_off + warp * 64;
   int16_t* choice_w = s_choice + warp * 64;
   float* un_w = s_un + warp * 64;
@@ -842,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             float4 v = sums[32 * g];
 #pragma unroll 1
             for (int w = 1; w < parts; ++w) {  // the parts' sums, in order
-              const float4 o = *reinterpret_cast<const float4*>(acc_w + (size_t)w * p.acc_floats + (32 * g + lane) * 4);
+              const float4 o = *reinterpret_cast<const float4*>(acc_w + (size_t)w * p.l.acc_floats + (32 * g + lane) * 4);
               v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
             }
             const float gates[2] = {v.x, v.y}, ups[2] = {v.z, v.w};
@@ -920,55 +914,7 @@ MoeFn pick(int act, bool aligned) {
   return aligned ? moe_kernel<V, 1, true> : moe_kernel<V, 1, false>;
 }
 
-constexpr int kSmemMax = 227 * 1024 - (kWarps * 640 + 6144);  // dynamic; the rest is the kernel's static shared memory
-constexpr int kSlack = 32;                   // word reads past the last row slot
-
-int up16(int v) { return (v + 15) / 16 * 16; }
-
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-
-template <int V>
-cudaError_t set_up(const MoeArgs& a, int sms, bool aligned, MoeParams* p, int* smem) {
-  using U = Unit<V>;
-  int at = up16(p->M * p->top_k * 4);
-  p->off_mask = at;
-  at += up16(p->E * 4);
-  p->off_list = at;
-  at += up16(p->E * 2);
-  p->off_slot = at;
-  at += up16(p->M * p->E);
-  p->off_unscale = at;
-  at += up16(p->M * 4);
-  p->off_y = at;
-  at += kWarps * kTileRows * p->M * 4;
-  p->off_acc = at;
-  p->acc_floats = (p->M + 3) / 4 * 128;  // a warp's sums of a tile, by group
-  at += kWarps * p->acc_floats * 4;
-  p->off_ring = (at + 127) / 128 * 128;
-  const int64_t spans_k = (a.K / 32 + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS, spans_i = (a.I / 32 + U::SPAN_BLOCKS - 1) / U::SPAN_BLOCKS;
-  p->ns = V == 0 ? 2 : 1;  // spans of a stage
-  const int each = aligned ? p->ns * kTileRows * U::SPAN : kTileRows * row_pitch<V, false>(p->ns);
-  p->stage_bytes = (each + 127) / 128 * 128;
-  const int room = (kSmemMax - p->off_ring - kSlack) / (kWarps * p->stage_bytes);
-  p->stages = room < kMaxStages ? room : kMaxStages;
-  if (p->stages < 1) return cudaErrorInvalidConfiguration;
-  *smem = p->off_ring + kWarps * p->stages * p->stage_bytes + kSlack;
-  // Workspace: logits, activation scales, largest |h|, then 16-byte aligned arrays.
-  const int64_t choices = a.M * a.top_k;
-  float* w = a.ws;
-  p->logits = w;
-  w += kMoeMaxTokens * kMoeMaxExperts;
-  p->x_unscale = w;
-  w += kMoeMaxTokens;
-  p->amax = reinterpret_cast<uint32_t*>(w);
-  w += kMoeMaxTokens * kMoeMaxTop;
-  p->h = w;
-  w += choices * a.I;
-  p->xf = reinterpret_cast<uint8_t*>(w);
-  p->h_hi = p->xf + a.M * spans_k * U::X_SPAN;
-  p->h_lo = p->h_hi + choices * spans_i * U::X_SPAN;
-  return cudaSuccess;
-}
 
 template <int V>
 cudaError_t encode_maps(const MoeArgs& a, MoeParams* p) {
@@ -1004,7 +950,7 @@ cudaError_t moe_prepare() {
     for (int act = 0; act < 2; ++act)
       for (int al = 0; al < 2; ++al) {
         const MoeFn fn = v == 0 ? pick<0>(act, al) : pick<1>(act, al);
-        cudaError_t e = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+        cudaError_t e = cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoeSmemMax);
         if (e != cudaSuccess) return e;
       }
   return cudaSuccess;
@@ -1031,15 +977,21 @@ cudaError_t launch_moe(int variant, int act, const MoeArgs& a, int sms, cudaStre
   p.route_scale = a.route_scale;
   const int ku = variant == 0 ? Fmt<0>::KU : Fmt<1>::KU;
   const bool aligned = a.K % ku == 0 && a.I % ku == 0;
-  int smem = 0;
-  cudaError_t e = variant == 0 ? set_up<0>(a, sms, aligned, &p, &smem) : set_up<1>(a, sms, aligned, &p, &smem);
-  if (e != cudaSuccess) return e;
+  if (!moe_layout(variant, aligned, a.M, a.E, a.top_k, a.K, a.I, &p.l)) return cudaErrorInvalidConfiguration;
+  p.logits = a.ws + p.l.ws_logits;
+  p.x_unscale = a.ws + p.l.ws_unscale;
+  p.amax = reinterpret_cast<uint32_t*>(a.ws + p.l.ws_amax);
+  p.h = a.ws + p.l.ws_h;
+  p.xf = reinterpret_cast<uint8_t*>(a.ws + p.l.ws_x);
+  p.h_hi = reinterpret_cast<uint8_t*>(a.ws + p.l.ws_hi);
+  p.h_lo = reinterpret_cast<uint8_t*>(a.ws + p.l.ws_lo);
+  cudaError_t e;
   if (aligned && (e = variant == 0 ? encode_maps<0>(a, &p) : encode_maps<1>(a, &p)) != cudaSuccess) return e;
   const MoeFn fn = variant == 0 ? pick<0>(act, aligned) : pick<1>(act, aligned);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)sms);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = p.l.bytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;  // its CTAs wait on one another: all resident
