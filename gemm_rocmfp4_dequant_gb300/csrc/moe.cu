@@ -542,7 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       const float mine = logit_of(my_key);
       float num = 0.f;
       if (p.route == 2) {
-        num = lane < p.top_k ? 1.f / (1.f + expf(-mine)) : 0.f;
+        // Below 0 the sigmoids times exp(-top), which cancels: all of them may be too small for fp32.
+        num = lane >= p.top_k ? 0.f : top < 0.f ? expf(mine - top) / (1.f + expf(mine)) : 1.f / (1.f + expf(-mine));
         denom = num;
       } else {
         num = lane < p.top_k ? expf(mine - top) : 0.f;
