@@ -33,7 +33,9 @@
 // remainder, 22 bits together.  The pair is made where h is, times 16, if the
 // choice's largest |h| proves to be in [2^-5, 2^11); a choice outside that
 // range has its pairs made again from the fp32 h, scaled like a bf16 token,
-// behind a third barrier that other calls do not meet.
+// behind a third barrier that other calls do not meet.  There an infinite h
+// (an overflow of its product) keeps a remainder of 0, so that its sign
+// reaches the outputs.
 //
 // Bound: memory (3 I K / 32 blocks per chosen expert) and, as close, the
 // decode: 387 cycles an SM quarter for 16 rows x 256 weights with everything in
@@ -125,10 +127,10 @@ RF4_DEV int scale_exp(uint32_t amax_bits) {
   if (e == 255 || amax_bits == 0) return 0;
   return max(-120, min(120, 141 - e));
 }
-// Whether the fp16 pair of h made with the fixed scale is good: 0, [2^-5, 2^11) or not finite (then so is the output).
+// Whether the fp16 pair of h made with the fixed scale is good: 0 or [2^-5, 2^11).
 RF4_DEV bool fast_range(uint32_t amax_bits) {
   const int e = (int)(amax_bits >> 23);
-  return amax_bits == 0 || e == 255 || (e >= 127 - 5 && e < 127 + 11);
+  return amax_bits == 0 || (e >= 127 - 5 && e < 127 + 11);
 }
 
 RF4_DEV uint32_t pack_half2(float lo, float hi) {
@@ -891,10 +893,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         const float scale = exp2i(scale_exp(mx));
 #pragma unroll 1
         for (int i = tid; i < p.I; i += kThreads) {
-          const float hs = __ldcg(p.h + (int64_t)a * p.I + i) * scale;
+          float hs = __ldcg(p.h + (int64_t)a * p.I + i) * scale;
+          // Beside an infinite h (or a NaN) every output is infinite or NaN,
+          // whatever the others are, as long as they stay finite.
+          if (mx >= 0x7F800000u && fabsf(hs) < INFINITY) hs = fminf(fmaxf(hs, -65504.f), 65504.f);
           const __half hi = __float2half_rn(hs);
           *reinterpret_cast<__half*>(p.h_hi + a * h_row + h_place(i)) = hi;
-          *reinterpret_cast<__half*>(p.h_lo + a * h_row + h_place(i)) = __float2half_rn(hs - __half2float(hi));
+          *reinterpret_cast<__half*>(p.h_lo + a * h_row + h_place(i)) = __float2half_rn(fabsf(hs) == INFINITY ? 0.f : hs - __half2float(hi));
         }
       }
       ok = grid_barrier(p.bars + 2) && ok;

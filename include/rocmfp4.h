@@ -223,6 +223,8 @@ typedef enum {
  *   - Logits, h and every sum are fp32; results are bitwise repeatable.  A NaN
  *     logit orders below every number; a token with a NaN or +inf logit, or
  *     with none above -inf, may get NaN weights, and then a NaN output.
+ *     An h beyond fp32's range is infinite: the outputs that it reaches are
+ *     infinite, or NaN where a weight of 0 meets it.
  *   - K and I positive multiples of 32; 1 <= top_k <= E.  M at most 32, E at
  *     most 512, top_k at most 16, K and I at most 32768, M * top_k * I at most
  *     2^22, and X, router, Wgu and Wd 16-byte aligned, else

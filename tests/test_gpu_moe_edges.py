@@ -1,4 +1,4 @@
-"""GPU tests of rocmfp4_moe at the ends of its arithmetic: sigmoid weights of very small logits."""
+"""GPU tests of rocmfp4_moe at the ends of its arithmetic: sigmoid weights of very small logits, hidden values beyond fp32."""
 import math
 
 import pytest
@@ -74,3 +74,58 @@ def test_sigmoid_weight_of_minus_infinity():
     assert ids.tolist() == [[0, 1, 3, 2]] and float(probs[0, 3]) == 0.0
     p = t.softmax(t.tensor([0.0, -1.0, -3.0], dtype=t.float64, device="cuda"), 0)
     assert bool(((probs[0, :3].double() - p).abs() <= 2.0 ** -19 * p).all()) and bool(Y.isfinite().all())
+
+
+@pytest.mark.parametrize("variant", [DUAL, FAST])
+@pytest.mark.parametrize("K,I", [(512, 512), (96, 64)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_infinite_hidden_value(K, I, variant, sign):
+    """h[0] = SiLU(2^71) * 2^71 is beyond fp32, h[1] = 2^100 beyond fp16 with the opposite sign in every output: outputs are
+    infinite with the sign of h[0]'s weight, and NaN where that weight is 0; a second expert adds finite values, and the other
+    tokens are as without the first."""
+    t = torch()
+    E, bb = 2, 18 if variant == DUAL else 17
+    g = t.Generator(device="cuda")
+    g.manual_seed(K)
+    X = t.randn(3, K, generator=g, device="cuda").bfloat16()
+    X[0] = 0.0
+    X[0, 0] = 2.0 ** 60
+    router = t.zeros(E, K, device="cuda")
+    Wgu, Wd = blocks(t, E * 2 * I, K, variant, g).view(E, 2, I, K // 32, bb), blocks(t, E * K, I, variant, g).view(E, K, I // 32, bb)
+    Wgu[0] = 0  # expert 0: byte 0's low nibble is column 0
+    Wgu[0, :, 0, 0, 0] = 7  # 10 * 224
+    Wgu[0, :, 0, 0, 16:] = 0x7E
+    Wgu[0, :, 1, 0, 0] = 1  # 2^-10
+    Wgu[0, :, 1, 0, 16:] = 1
+    if sign < 0:
+        Wgu[0, 1, :2, 0, 0] += 8
+    Wd[0] = 0
+    Wd[0, :, :, 16:] = 0x40
+    n = t.arange(K, device="cuda")
+    Wd[0, :, 0, 0] = t.where(n % 3 == 0, 1, t.where(n % 3 == 1, 9, 0)).to(t.uint8)  # 1, -1, 0
+    Wd[0, :, 0, 1] = t.where(n % 3 == 0, 15, 7).to(t.uint8)                        # -10, 10
+    args = (router, Wgu.reshape(-1), Wd.reshape(-1), I, 2, variant)
+    Y, ids, probs = rf4.moe(X, *args)
+    assert ids.tolist() == [[0, 1]] * 3 and bool((probs == 0.5).all())
+    inf = float("inf")
+    assert bool((Y[0, n % 3 == 0] == sign * inf).all()) and bool((Y[0, n % 3 == 1] == -sign * inf).all()) and bool(Y[0, n % 3 == 2].isnan().all())
+    assert bool(Y[1:].isfinite().all()) and t.equal(Y[1:], rf4.moe(X[1:].clone(), *args)[0])
+
+
+@pytest.mark.parametrize("variant", [DUAL, FAST])
+def test_infinite_hidden_values_of_both_signs(variant):
+    """Infinite hidden values of opposite signs: NaN where both have a weight, infinite where the products' signs agree."""
+    t = torch()
+    K = I = 32
+    bb = 18 if variant == DUAL else 17
+    X = t.zeros(1, K, device="cuda").bfloat16()
+    X[0, 0] = 2.0 ** 60
+    Wgu, Wd = t.zeros(2, I, 1, bb, dtype=t.uint8, device="cuda"), t.zeros(K, 1, bb, dtype=t.uint8, device="cuda")
+    Wgu[:, :2, 0, 0] = 7
+    Wgu[1, 1, 0, 0] = 15
+    Wgu[..., 16:] = 0x7E
+    Wd[..., 16:] = 0x40
+    Wd[:16, 0, 0], Wd[:16, 0, 1] = 1, 1   # inf - inf
+    Wd[16:, 0, 0], Wd[16:, 0, 1] = 1, 9   # inf + inf
+    Y, _, _ = rf4.moe(X, t.zeros(1, K, device="cuda"), Wgu.view(-1), Wd.view(-1), I, 1, variant)
+    assert bool(Y[0, :16].isnan().all()) and bool((Y[0, 16:] == float("inf")).all())
