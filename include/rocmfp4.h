@@ -256,6 +256,8 @@ rocmfp4_status rocmfp4_moe(const void *X, const void *router, rocmfp4_out_dtype 
  *     part in the entropy.  A row of nothing but -inf gives log probabilities
  *     -inf and entropy 0.  A row that holds a NaN or +inf gives NaN for all of
  *     its numbers; its top_ids order NaN first, then +inf.
+ *   - Log probabilities are at most 0 and entropies at least 0 (where they are
+ *     numbers).
  *   - scale from 1e-30 to 1e30.  V below 2^31.
  *   - One programmatic dependent launch on `stream`; sums are fp32, in a fixed
  *     order.  A row may be shared by several CTAs, whose records use the
