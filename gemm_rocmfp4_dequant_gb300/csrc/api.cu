@@ -27,8 +27,9 @@ struct DeviceState {
   unsigned long long* vfirst = nullptr;
   float* lp_ws = nullptr;            // log probabilities: records of split rows
   uint32_t* lp_cnt = nullptr;        // log probabilities: arrivals per split row
-  float* moe_ws = nullptr;           // mixture of experts: router logits and hidden values
+  bool norm_ready = false;           // RMS norm: kernels prepared
   uint32_t* moe_bars = nullptr;      // mixture of experts: barrier counters
+  float* moe_ws = nullptr;           // mixture of experts: router logits and hidden values, from its first call on
 };
 
 constexpr int kMaxDevices = 64;
@@ -57,9 +58,27 @@ bool valid_act(int a) { return a == ROCMFP4_ACT_F16 || a == ROCMFP4_ACT_BF16; }
 
 int64_t block_bytes_of(int v) { return v == ROCMFP4_DUAL ? 18 : 17; }
 
+// The mixture of experts' workspace (36 MiB) is made at its first call, not at
+// every user's first call.  That call may stand in a graph's capture, which
+// an allocation would end but for the relaxed mode (nothing here touches a stream).
+rocmfp4_status moe_set_up(DeviceState& d) {
+  cudaError_t e = moe_prepare();
+  if (e != cudaSuccess) return cuda_fail(e, "mixture-of-experts kernel set-up");
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return cuda_fail(e, "cudaThreadExchangeStreamCaptureMode");
+  float* ws = nullptr;
+  e = cudaMalloc(&ws, sizeof(float) * kMoeWsFloats);
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc");
+  d.moe_ws = ws;
+  return ROCMFP4_OK;
+}
+
+enum class Needs { kProducts, kNorm, kMoe };
+
 // Per-device set-up on first use: SM count, kernel attributes, occupancy and
-// the workspace of the split-tile reduction.
-rocmfp4_status device_state(DeviceState** out) {
+// the workspace of the split-tile reduction; and what `needs` has beside that.
+rocmfp4_status device_state(DeviceState** out, Needs needs = Needs::kProducts) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -100,14 +119,19 @@ rocmfp4_status device_state(DeviceState** out) {
       return cuda_fail(e, "cudaMalloc");
     if ((e = cudaMemset(d.lp_cnt, 0, sizeof(uint32_t) * logprobs_cnt_words(d.sms))) != cudaSuccess)
       return cuda_fail(e, "cudaMemset");
-    if ((e = norm_prepare()) != cudaSuccess) return cuda_fail(e, "RMS norm kernel set-up");
-    if ((e = moe_prepare()) != cudaSuccess) return cuda_fail(e, "mixture-of-experts kernel set-up");
-    if ((e = cudaMalloc(&d.moe_ws, sizeof(float) * kMoeWsFloats)) != cudaSuccess) return cuda_fail(e, "cudaMalloc");
     if ((e = cudaMalloc(&d.moe_bars, sizeof(uint32_t) * kMoeBarWords)) != cudaSuccess) return cuda_fail(e, "cudaMalloc");
     if ((e = cudaMemset(d.moe_bars, 0, sizeof(uint32_t) * kMoeBarWords)) != cudaSuccess) return cuda_fail(e, "cudaMemset");
     if ((e = cudaMemset(d.err, 0, sizeof(uint32_t))) != cudaSuccess) return cuda_fail(e, "cudaMemset");
     if ((e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
     d.ready = true;
+  }
+  if (needs == Needs::kNorm && !d.norm_ready) {
+    if ((e = norm_prepare()) != cudaSuccess) return cuda_fail(e, "RMS norm kernel set-up");
+    d.norm_ready = true;
+  }
+  if (needs == Needs::kMoe && d.moe_ws == nullptr) {
+    const rocmfp4_status st = moe_set_up(d);
+    if (st != ROCMFP4_OK) return st;
   }
   *out = &d;
   return ROCMFP4_OK;
@@ -370,7 +394,7 @@ rocmfp4_status add_rmsnorm(NormArgs a, int64_t group, cudaStream_t s) {
   if (a.D > norm_max_width()) return fail(ROCMFP4_ERR_UNSUPPORTED, "RMS norm: D at most 32768");
   if (a.M >= (int64_t(1) << 31)) return fail(ROCMFP4_ERR_UNSUPPORTED, "RMS norm: M too large");
   DeviceState* d = nullptr;
-  rocmfp4_status st = device_state(&d);
+  rocmfp4_status st = device_state(&d, Needs::kNorm);
   if (st != ROCMFP4_OK) return st;
   a.err = d->err;
   cudaError_t e = launch_norm(a, d->sms, s);
@@ -401,7 +425,7 @@ rocmfp4_status moe(MoeArgs a, int variant, int act, cudaStream_t s) {
   if (!aligned16(a.X) || !aligned16(a.router) || !aligned16(a.Wgu) || !aligned16(a.Wd))
     return fail(ROCMFP4_ERR_UNSUPPORTED, "mixture of experts: X, router, Wgu and Wd must be 16-byte aligned");
   DeviceState* d = nullptr;
-  rocmfp4_status st = device_state(&d);
+  rocmfp4_status st = device_state(&d, Needs::kMoe);
   if (st != ROCMFP4_OK) return st;
   a.ws = d->moe_ws;
   a.bars = d->moe_bars;
