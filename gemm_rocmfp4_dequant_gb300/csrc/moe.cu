@@ -17,8 +17,11 @@
 // (16 single-scale blocks) of each row.  A warp takes tiles on its own (the
 // last of a CTA's gate/up tiles, too few for a tile a warp, go to teams of two
 // or four warps that share a tile's spans) and streams their spans through a
-// private ring of shared-memory stages, one tensor copy of a 16-row box a span.  The down tasks are known as soon as the routing is,
-// so the ring runs on into them before the second barrier.
+// private ring of shared-memory stages, one tensor copy of a 16-row box a span.
+// The down tasks are known as soon as the routing is, so the ring runs on into
+// them before the second barrier.  The ring has two stages; one from 13 to 25
+// tokens on (by experts, layout and alignment), where the tokens' outputs and
+// sums take the room and a warp's next copy starts when it has done with the last.
 // The arithmetic is mma.sync m16n8k16 on fp16 with fp32 accumulators: A is
 // the decoded weights, exact in fp16, decoded once for all the tokens of the
 // expert; B's columns are tokens.  Lane (q, c) decodes blocks of rows q and
@@ -45,9 +48,11 @@
 //
 // Measured on one GB300, dual, 128 experts of [2 x 768, 2048] + [2048, 768], 8
 // chosen: one token 20.5 us (21.8 MB; a cooperative launch starts every 2.048
-// us at best), eight tokens 51 to 53 us (137.6 MB, 2.6 TB/s); 64 experts of
-// [2 x 1536, 5120], single-scale, 6 chosen, four tokens: 81 to 88 us (3.1 TB/s).
-// 16 warps: with 12 (and 168 registers) the last ran 104 us.
+// us at best), eight tokens 50 to 54 us (137.6 MB, 2.6 TB/s); 64 experts of
+// [2 x 1536, 5120], single-scale, 6 chosen, four tokens: 85 to 94 us (2.9 TB/s).
+// 16 warps: with 12 (and 168 registers) the last ran 104 us.  The first layer
+// at 16, 24 and 32 tokens: 74, 96 and 113 us, 2.9, 2.8 and 2.5 TB/s of the
+// blocks that they reach; the last two with one stage.
 //
 // Rows whose length is no multiple of 16 bytes (K / 32 not a multiple of 8,
 // dual, or 16, single-scale) cannot be boxes of a tensor copy.  They come by a
