@@ -6,8 +6,10 @@ fallback: if the library is missing or no GPU is present, calls raise.
 
 Entry points (names as in the C ABI, without the ``rocmfp4_`` prefix):
 ``gemv``, ``gemm``, ``gemv_gate_up``, ``gemv_chain``, ``decode_attention``,
-``add_rmsnorm``, ``moe``, ``logprobs``, ``quantize``, ``dequant``, ``validate``,
-``copy``, ``block_bytes``, ``row_bytes``.
+``add_rmsnorm``, ``moe``, ``logprobs``, ``rotary``, ``rope_append``, ``cache_read``,
+``paged_attention`` (over a ``PagedCache``), ``quantize``, ``dequant``, ``validate``,
+``copy``, ``block_bytes``, ``row_bytes``.  ``rotary_frequencies`` makes a table of
+frequencies on the host.
 Tensors are torch CUDA tensors; packed weights are ``uint8`` tensors holding
 ``N * row_bytes(K, variant)`` bytes; activations are ``float16`` or
 ``bfloat16``; outputs are ``float32``.  Calls are asynchronous on torch's
@@ -30,6 +32,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "librocmfp4.so")
 EXPORTS = ("rocmfp4_block_bytes", "rocmfp4_row_bytes", "rocmfp4_gemv", "rocmfp4_gemv_ex", "rocmfp4_gemm",
            "rocmfp4_gemm_ex", "rocmfp4_gemm_noalloc", "rocmfp4_gemv_gate_up", "rocmfp4_decode_attention", "rocmfp4_add_rmsnorm", "rocmfp4_moe", "rocmfp4_logprobs",
+           "rocmfp4_rotary", "rocmfp4_rope_append", "rocmfp4_cache_read", "rocmfp4_paged_attention",
            "rocmfp4_quantize", "rocmfp4_gemv_chain", "rocmfp4_gemv_chain_mixed", "rocmfp4_dequant", "rocmfp4_copy", "rocmfp4_validate", "rocmfp4_device_error_bits",
            "rocmfp4_status_string", "rocmfp4_last_error", "rocmfp4_launch_count", "rocmfp4_shutdown")
 
@@ -40,6 +43,12 @@ class GemvOp(ctypes.Structure):
     """rocmfp4_gemv_op: one product of a chain."""
     _fields_ = [("W", ctypes.c_void_p), ("X", ctypes.c_void_p), ("Y", ctypes.c_void_p),
                 ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
+
+
+class _PagedCacheStruct(ctypes.Structure):
+    """rocmfp4_paged_cache."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("K", "V", "table", "lens", "cu")]
+                + [(n, ctypes.c_int64) for n in ("B", "table_width", "table_stride", "num_pages", "page_size", "Hkv", "D")] + [("variant", ctypes.c_int)])
 
 
 class RocmFP4Error(RuntimeError):
@@ -73,6 +82,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "rocmfp4_moe": ([vp, vp, c_int, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, c_int, ctypes.c_float, c_int, c_int, vp],
                         c_int),
         "rocmfp4_logprobs": ([vp, c_int, i64, vp, ctypes.c_float, vp, vp, vp, vp, i64, i64, i64, vp], c_int),
+        "rocmfp4_rotary": ([vp, c_int, i64, vp, vp, i64, c_int, ctypes.c_float, vp, c_int, i64, i64, i64, vp], c_int),
+        "rocmfp4_rope_append": ([vp, vp, vp, vp, c_int, i64, i64, i64, vp, vp, i64, c_int, ctypes.c_float, vp, c_int, i64, i64, vp], c_int),
+        "rocmfp4_cache_read": ([vp, vp, vp, c_int, i64, vp], c_int),
+        "rocmfp4_paged_attention": ([vp, i64, vp, vp, i64, i64, ctypes.c_float, c_int, i64, c_int, vp], c_int),
         "rocmfp4_quantize": ([vp, c_int, vp, i64, i64, c_int, vp], c_int),
         "rocmfp4_gemv_chain": ([ctypes.POINTER(GemvOp), c_int, i64, c_int, c_int, vp], c_int),
         "rocmfp4_gemv_chain_mixed": ([ctypes.POINTER(GemvOp), ctypes.POINTER(c_int), c_int, i64, c_int, vp], c_int),
@@ -409,6 +422,220 @@ def logprobs(logits, targets=None, top_n: int = 0, scale: float = 1.0, logprob=N
         if st:
             _check(st, "rocmfp4_logprobs")
     return logprob, entropy, top_ids, top_logprobs
+
+
+class PagedCache:
+    """A paged K/V cache of ROCmFP4 rows and the batch of rows that calls deal with (rocmfp4_paged_cache).
+
+    K, V      uint8 tensors of num_pages x kv_heads x page_size rows of head / 32 blocks (page_size a multiple of 16);
+    table     int32 [B, pages]: token t of sequence b lies in page table[b, t // page_size], at t % page_size;
+    lens      int32 [B]: the tokens that each sequence holds, a call's new ones among them;
+    cu        int32 [B + 1], from 0 on: rows cu[b] .. cu[b + 1] - 1 of a call are the last tokens of sequence b (or its
+              queries, in a cross attention); rows from cu[B] on are padding, whose outputs stay as they are.
+
+    Make it once and keep it: calls read the tensors' contents when they run, so lens, cu and table are advanced in
+    place.  It holds the tensors alive.  A page number outside the cache is reported by device_error_bits (bit 1)."""
+
+    def __init__(self, K, V, table, lens, cu, *, kv_heads: int, head: int, page_size: int, variant: int = DUAL):
+        torch = _torch()
+        for t, name, dt in ((K, "K", torch.uint8), (V, "V", torch.uint8), (table, "table", torch.int32), (lens, "lens", torch.int32), (cu, "cu", torch.int32)):
+            if not t.is_cuda or t.dtype is not dt or t.device != K.device:
+                raise ValueError(f"{name} must be a {dt} CUDA tensor on K's device")
+            if name != "table" and not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        if kv_heads < 1 or head < 32 or page_size < 1:
+            raise ValueError("kv_heads, head and page_size must be positive, head at least 32")
+        page = kv_heads * page_size * row_bytes(head, variant)
+        if page == 0:
+            raise ValueError("head must be a multiple of 32, variant DUAL or FAST")
+        if K.numel() != V.numel() or K.numel() % page:
+            raise ValueError("K and V must hold the same whole number of pages")
+        B = lens.numel()
+        if table.dim() != 2 or table.shape[0] != B or cu.numel() != B + 1:
+            raise ValueError("table must be [B, pages], lens [B] and cu [B + 1]")
+        if table.shape[1] > 1 and table.stride(1) != 1:
+            raise ValueError("table must have contiguous rows")
+        width = table.shape[1]
+        self.K, self.V, self.table, self.lens, self.cu = K, V, table, lens, cu
+        self.kv_heads, self.head, self.page_size, self.variant, self.device = kv_heads, head, page_size, variant, K.device
+        self._index = K.device.index
+        self._struct = _PagedCacheStruct(_ptr(K), _ptr(V), _ptr(table), lens.data_ptr(), cu.data_ptr(), B, width,
+                                         max(width, table.stride(0)) if B > 1 else width, K.numel() // page, page_size, kv_heads, head, variant)
+        self._at = ctypes.addressof(self._struct)
+
+
+def _on_current(index: int):
+    if _raw_stream is None:
+        _current_stream()
+    now = _raw_stream[0]() if _raw_stream else _torch().cuda.current_device()
+    if index != now:
+        raise ValueError(f"the tensors lie on device {index}, the current device is {now}")
+
+
+def _new(shape, dtype, device, stream):
+    t = _torch().empty(shape, dtype=dtype, device=device)
+    if stream is not None:  # made on the current stream, used on another
+        torch = _torch()
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    return t
+
+
+def _heads(t, name: str, D: int):
+    """(rows, heads, row stride) of a [rows, heads, D] CUDA tensor whose rows are contiguous."""
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != D or not t.is_cuda:
+        raise ValueError(f"{name} must be a [rows, heads, {D}] CUDA tensor")
+    M, H = shape[0], shape[1]
+    if t.is_contiguous():
+        return M, H, H * D
+    stride = t.stride()
+    if stride[2] != 1 or (H > 1 and stride[1] != D):
+        raise ValueError(f"{name} must have contiguous rows of heads")
+    return M, H, stride[0] if M > 1 else H * D
+
+
+def _freq(freq, index: int) -> int:
+    if freq is None:
+        return 0
+    if freq.dtype is not _torch().float32 or freq.dim() != 1 or not freq.is_contiguous() or not freq.is_cuda or freq.device.index != index:
+        raise ValueError("freq must be a contiguous float32 CUDA tensor, one value per pair")
+    return freq.numel()
+
+
+def _positions(positions, M: int, index: int) -> int:
+    if positions is None:
+        return 0
+    if positions.dtype is not _torch().int32 or positions.shape != (M,) or not positions.is_contiguous() or not positions.is_cuda or positions.device.index != index:
+        raise ValueError("positions must be a contiguous int32 CUDA tensor, one value per row")
+    return _ptr(positions)
+
+
+def rotary_frequencies(rot: int, base: float = 10000.0, *, method: str = "none", factor: float = 1.0, original: int = 0, fast: float = 32.0,
+                       slow: float = 1.0, device="cuda"):
+    """(freq [rot / 2] float32, amplitude) of rotary positions: pair i turns by base ** (-2 i / rot) a token, in 64 bits
+    before the rounding.  For contexts longer than a model was trained on, ``factor`` times as long:
+    method "linear"  positions are divided by factor;
+    method "ntk"     the base grows by factor ** (rot / (rot - 2)), which leaves the fastest pair and divides the slowest;
+    method "parts"   pairs that turn more than ``fast`` times in ``original`` tokens stay, those that turn less than ``slow``
+                     times are divided by factor, the ones between in proportion to their turns; amplitude 0.1 ln(factor) + 1."""
+    torch = _torch()
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be even and positive")
+    if not base > 0 or not factor >= 1:
+        raise ValueError("base must be positive, factor at least 1")
+    if method not in ("none", "linear", "ntk", "parts"):
+        raise ValueError("method must be none, linear, ntk or parts")
+    if method == "ntk":
+        if rot == 2:
+            raise ValueError("ntk needs more than one pair")
+        base = base * factor ** (rot / (rot - 2))
+    f = torch.tensor([base ** (-2.0 * i / rot) for i in range(rot // 2)], dtype=torch.float64)
+    amplitude = 1.0
+    if method == "linear":
+        f = f / factor
+    elif method == "parts":
+        if original < 1 or not fast > slow:
+            raise ValueError("parts needs original, the tokens of the trained context, and fast above slow")
+        keep = ((original * f / (2 * torch.pi) - slow) / (fast - slow)).clamp(0.0, 1.0)
+        f = f * (keep + (1.0 - keep) / factor)
+        amplitude = 0.1 * float(torch.log(torch.tensor(factor, dtype=torch.float64))) + 1.0
+    return f.float().to(device), amplitude
+
+
+def rotary(x, freq, positions, *, interleaved: bool = False, amplitude: float = 1.0, dtype=None, out=None, stream=None):
+    """y [M, H, D] of the heads x [M, H, D] (float32, bfloat16 or float16, rows of contiguous heads) at positions [M]
+    (int32): the first 2 * len(freq) values of each head turned, pairs (i, i + rot / 2), or (2i, 2i + 1) if interleaved, by
+    positions * freq[i], times amplitude.  float16 or bfloat16, into ``out`` or a new tensor of ``dtype`` (float16)."""
+    torch = _torch()
+    codes = _DTYPES or _dtypes()
+    M, H, ld = _heads(x, "x", x.shape[-1])
+    D, index = x.shape[2], x.device.index
+    _on_current(index)
+    n, pos = _freq(freq, index), _positions(positions, M, index)
+    if out is None:
+        out = _new((M, H, D), dtype or torch.float16, x.device, stream)
+    elif out.shape != x.shape or not out.is_contiguous() or out.device != x.device:
+        raise ValueError("out must be a contiguous CUDA tensor of x's shape")
+    _check((_lib or load()).rocmfp4_rotary(_ptr(x), codes.get(x.dtype, -1), ld, pos, _ptr(freq), 2 * n, interleaved, amplitude, _ptr(out), _act_of(out),
+                                           M, H, D, _stream(stream)), "rocmfp4_rotary")
+    return out
+
+
+def rope_append(cache: PagedCache, q, k, v, freq=None, *, positions=None, interleaved: bool = False, amplitude: float = 1.0, dtype=None,
+                q_out=None, stream=None):
+    """Packs the batch's new tokens into the cache's pages and gives q [M, H, D] float16 / bfloat16.
+
+    q [M, H, D] (or None), k and v [M, kv_heads, D] float32, bfloat16 or float16, alike, with rows of contiguous heads (parts
+    of a QKV product's rows, say).  The first 2 * len(freq) values of q's and k's heads are turned as by rotary(), at
+    positions (int32 [M]; None: each token's place in its sequence); freq None turns nothing.  k and v are packed from
+    their float32 values by the quantiser's rule.  cache.lens counts the new tokens already."""
+    torch = _torch()
+    codes = _DTYPES or _dtypes()
+    D, index = cache.head, cache._index
+    M, Hkv, ldk = _heads(k, "k", D)
+    Mv, Hv, ldv = _heads(v, "v", D)
+    if Hkv != cache.kv_heads or Hv != Hkv or Mv != M or k.dtype is not v.dtype:
+        raise ValueError("k and v must be [M, kv_heads, head] tensors of one type")
+    if k.device.index != index or v.device.index != index:
+        raise ValueError("k and v must lie on the cache's device")
+    _on_current(index)
+    H, ldq, qptr, optr, act = 0, 0, 0, 0, ACT_F16
+    if q is not None:
+        Mq, H, ldq = _heads(q, "q", D)
+        if Mq != M or q.dtype is not k.dtype or q.device.index != index:
+            raise ValueError("q must have k's rows, type and device")
+        if q_out is None:
+            q_out = _new((M, H, D), dtype or torch.float16, q.device, stream)
+        elif q_out.shape != q.shape or not q_out.is_contiguous() or q_out.device != q.device:
+            raise ValueError("q_out must be a contiguous CUDA tensor of q's shape")
+        qptr, optr, act = _ptr(q), _ptr(q_out), _act_of(q_out)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    n, pos = _freq(freq, index), _positions(positions, M, index)
+    _check((_lib or load()).rocmfp4_rope_append(cache._at, qptr, _ptr(k), _ptr(v), codes.get(k.dtype, -1), ldq, ldk, ldv, pos, _ptr(freq), 2 * n, interleaved,
+                                                amplitude, optr, act, M, H, _stream(stream)), "rocmfp4_rope_append")
+    return q_out
+
+
+def cache_read(cache: PagedCache, rows=None, *, dtype=None, k_out=None, v_out=None, stream=None):
+    """(k, v) [M, kv_heads, head]: the values of the batch's tokens, exact (float32, bfloat16 or float16), into the tensors
+    given, or into new ones of ``rows`` rows and ``dtype`` (float16).  With only one of k_out and v_out, that one alone."""
+    torch = _torch()
+    codes = _DTYPES or _dtypes()
+    index = cache._index
+    if k_out is None and v_out is None:
+        if rows is None:
+            raise ValueError("rows or an output is needed")
+        k_out, v_out = (_new((rows, cache.kv_heads, cache.head), dtype or torch.float16, cache.device, stream) for _ in range(2))
+        rows = None
+    like = k_out if k_out is not None else v_out
+    M = like.shape[0]
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None and (t.shape != (M, cache.kv_heads, cache.head) or not t.is_contiguous() or t.dtype is not like.dtype or t.device != cache.device):
+            raise ValueError(f"{name} must be a contiguous [rows, kv_heads, head] tensor on the cache's device")
+    if rows is not None and rows != M:
+        raise ValueError("rows must be the outputs'")
+    _on_current(index)
+    _check((_lib or load()).rocmfp4_cache_read(cache._at, _ptr(k_out), _ptr(v_out), codes.get(like.dtype, -1), M, _stream(stream)), "rocmfp4_cache_read")
+    return k_out, v_out
+
+
+def paged_attention(q, cache: PagedCache, scale: float, *, causal: bool = True, window: int = 0, out=None, stream=None):
+    """out [M, H, D] of q's type: attention of the batch's rows q [M, H, D] (float16 or bfloat16, rows of contiguous heads)
+    over the pages of their sequences.  causal: row i of the n of sequence b sees the tokens up to lens[b] - n + i, with a
+    window only the last ``window`` of them; else every row sees all lens[b] tokens.  A row that sees none gives zeros."""
+    M, H, ldq = _heads(q, "q", cache.head)
+    index = cache._index
+    if q.device.index != index:
+        raise ValueError("q must lie on the cache's device")
+    _on_current(index)
+    if out is None:
+        out = _new((M, H, cache.head), q.dtype, q.device, stream)
+    elif out.shape != q.shape or not out.is_contiguous() or out.dtype is not q.dtype or out.device != q.device:
+        raise ValueError("out must be a contiguous CUDA tensor of q's shape and type")
+    _check((_lib or load()).rocmfp4_paged_attention(_ptr(q), ldq, cache._at, _ptr(out), M, H, scale, bool(causal), window, _act_of(q), _stream(stream)),
+           "rocmfp4_paged_attention")
+    return out
 
 
 def gemv_chain(ops, variant=DUAL, stream=None):

@@ -465,6 +465,131 @@ rocmfp4_status logprobs(LogprobsArgs a, int64_t top_n, cudaStream_t s) {
   return ROCMFP4_OK;
 }
 
+// The cache description of a call, checked, as the kernels see it.
+rocmfp4_status paged_args(const rocmfp4_paged_cache* c, PagedArgs* out) {
+  if (c == nullptr) return fail(ROCMFP4_ERR_INVALID_ARG, "cache is NULL");
+  if (!valid_variant(c->variant)) return fail(ROCMFP4_ERR_INVALID_ARG, "unknown variant");
+  if (c->B < 0 || c->table_width < 0 || c->num_pages < 0) return fail(ROCMFP4_ERR_INVALID_ARG, "negative size");
+  if (c->Hkv < 1 || c->D < 32 || c->page_size < 1) return fail(ROCMFP4_ERR_INVALID_ARG, "Hkv, D and page_size must be positive");
+  if (c->D % 32 != 0) return fail(ROCMFP4_ERR_INVALID_ARG, "D must be a multiple of 32");
+  if (c->table_stride < c->table_width) return fail(ROCMFP4_ERR_INVALID_ARG, "table_stride below table_width");
+  if (!c->cu || (c->B > 0 && !c->lens) || (c->table_width > 0 && !c->table) || (c->num_pages > 0 && (!c->K || !c->V)))
+    return fail(ROCMFP4_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned_to(c->cu, 0) || !aligned_to(c->lens, 0) || !aligned_to(c->table, 0))
+    return fail(ROCMFP4_ERR_INVALID_ARG, "misaligned pointer");
+  if (!aligned16(c->K) || !aligned16(c->V)) return fail(ROCMFP4_ERR_UNSUPPORTED, "paged cache: K and V must be 16-byte aligned");
+  const int64_t most = int64_t(1) << 31;
+  if (c->page_size % 16 != 0) return fail(ROCMFP4_ERR_UNSUPPORTED, "paged cache: page_size must be a multiple of 16");
+  if (c->D > 256) return fail(ROCMFP4_ERR_UNSUPPORTED, "paged cache: D at most 256");
+  if (c->B >= most || c->table_width >= most || c->num_pages >= most || c->page_size >= most || c->Hkv > 65536 ||
+      c->table_width > most / c->page_size)
+    return fail(ROCMFP4_ERR_UNSUPPORTED, "paged cache: sizes too large");
+  PagedArgs& p = *out;
+  p.K = static_cast<uint8_t*>(c->K);
+  p.V = static_cast<uint8_t*>(c->V);
+  p.table = c->table;
+  p.lens = c->lens;
+  p.cu = c->cu;
+  p.ldt = c->table_stride;
+  p.B = (int)c->B;
+  p.width = (int)c->table_width;
+  p.num_pages = (int)c->num_pages;
+  p.page_size = (int)c->page_size;
+  p.Hkv = (int)c->Hkv;
+  p.D = (int)c->D;
+  return ROCMFP4_OK;
+}
+
+// Shared by rocmfp4_rotary and rocmfp4_rope_append (`cache` not NULL).
+rocmfp4_status rope(RopeArgs a, const rocmfp4_paged_cache* cache, cudaStream_t s) {
+  rocmfp4_status st;
+  if (a.paged) {
+    if ((st = paged_args(cache, &a.cache)) != ROCMFP4_OK) return st;
+    a.D = cache->D;
+  }
+  if (!valid_dtype(a.type)) return fail(ROCMFP4_ERR_INVALID_ARG, "unknown type");
+  if (!valid_act(a.act)) return fail(ROCMFP4_ERR_INVALID_ARG, "unknown activation type");
+  if (a.M < 0 || a.H < 0) return fail(ROCMFP4_ERR_INVALID_ARG, "negative size");
+  if (a.D < 32 || a.D % 32 != 0) return fail(ROCMFP4_ERR_INVALID_ARG, "D must be a positive multiple of 32");
+  if (a.rot < 0 || a.rot > a.D || a.rot % 2 != 0) return fail(ROCMFP4_ERR_INVALID_ARG, "rot must be even, from 0 to D");
+  if (!(a.amplitude >= -3.4e38f && a.amplitude <= 3.4e38f)) return fail(ROCMFP4_ERR_INVALID_ARG, "amplitude must be finite");
+  if (a.M == 0 || (a.paged && a.cache.B == 0) || (!a.paged && a.H == 0)) return ROCMFP4_OK;
+  const int64_t widths[3] = {a.H * a.D, a.paged ? a.cache.Hkv * a.D : 0, a.paged ? a.cache.Hkv * a.D : 0};
+  for (int i = 0; i < 3; ++i) {
+    if (widths[i] == 0) {
+      a.x[i] = nullptr;
+      continue;
+    }
+    if (a.x[i] == nullptr) return fail(ROCMFP4_ERR_INVALID_ARG, "NULL pointer");
+    if (!aligned_to(a.x[i], a.type)) return fail(ROCMFP4_ERR_INVALID_ARG, "misaligned pointer");
+    if (a.ld[i] < widths[i]) return fail(ROCMFP4_ERR_INVALID_ARG, "row stride below the heads' width");
+  }
+  if ((a.H > 0 && a.q_out == nullptr) || (a.rot > 0 && a.freq == nullptr) || (!a.paged && a.rot > 0 && a.positions == nullptr))
+    return fail(ROCMFP4_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned_to(a.freq, 0) || !aligned_to(a.positions, 0) || !aligned_to(a.q_out, ROCMFP4_OUT_F16))
+    return fail(ROCMFP4_ERR_INVALID_ARG, "misaligned pointer");
+  if (a.D > 256) return fail(ROCMFP4_ERR_UNSUPPORTED, "rotary positions: D at most 256");
+  if (a.H > 65536 || a.M >= (int64_t(1) << 31)) return fail(ROCMFP4_ERR_UNSUPPORTED, "rotary positions: sizes too large");
+  if ((reinterpret_cast<uintptr_t>(a.q_out) & 7u) != 0)
+    return fail(ROCMFP4_ERR_UNSUPPORTED, "rotary positions: the output must be 8-byte aligned");
+  DeviceState* d = nullptr;
+  if ((st = device_state(&d)) != ROCMFP4_OK) return st;
+  a.cache.err = d->err;
+  cudaError_t e = launch_rope(a.paged ? cache->variant : 0, a, d->sms, s);
+  if (e != cudaSuccess) return cuda_fail(e, "rotary positions launch");
+  g_launches.fetch_add(1);
+  return ROCMFP4_OK;
+}
+
+rocmfp4_status cache_read(const rocmfp4_paged_cache* cache, CacheReadArgs a, int type, cudaStream_t s) {
+  rocmfp4_status st = paged_args(cache, &a.cache);
+  if (st != ROCMFP4_OK) return st;
+  if (!valid_dtype(type)) return fail(ROCMFP4_ERR_INVALID_ARG, "unknown type");
+  if (a.M < 0) return fail(ROCMFP4_ERR_INVALID_ARG, "negative size");
+  if (a.M == 0 || a.cache.B == 0) return ROCMFP4_OK;
+  if (a.k_out == nullptr && a.v_out == nullptr) return fail(ROCMFP4_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned_to(a.k_out, type) || !aligned_to(a.v_out, type)) return fail(ROCMFP4_ERR_INVALID_ARG, "misaligned pointer");
+  if (!aligned16(a.k_out) || !aligned16(a.v_out)) return fail(ROCMFP4_ERR_UNSUPPORTED, "reading a cache: outputs must be 16-byte aligned");
+  if (a.M >= (int64_t(1) << 31)) return fail(ROCMFP4_ERR_UNSUPPORTED, "reading a cache: M too large");
+  DeviceState* d = nullptr;
+  if ((st = device_state(&d)) != ROCMFP4_OK) return st;
+  a.cache.err = d->err;
+  cudaError_t e = launch_cache_read(cache->variant, type, a, d->sms, s);
+  if (e != cudaSuccess) return cuda_fail(e, "cache read launch");
+  g_launches.fetch_add(1);
+  return ROCMFP4_OK;
+}
+
+rocmfp4_status paged_attention(const rocmfp4_paged_cache* cache, PagedAttnArgs a, int64_t H, int64_t window, int act,
+                               cudaStream_t s) {
+  rocmfp4_status st = paged_args(cache, &a.cache);
+  if (st != ROCMFP4_OK) return st;
+  if (!valid_act(act)) return fail(ROCMFP4_ERR_INVALID_ARG, "unknown activation type");
+  if (a.M < 0 || H < 0 || window < 0) return fail(ROCMFP4_ERR_INVALID_ARG, "negative size");
+  if (H % cache->Hkv != 0) return fail(ROCMFP4_ERR_INVALID_ARG, "H must be a multiple of Hkv");
+  if (!(a.scale >= 1e-30f && a.scale <= 1e30f)) return fail(ROCMFP4_ERR_INVALID_ARG, "scale must be from 1e-30 to 1e30");
+  if (a.causal != 0 && a.causal != 1) return fail(ROCMFP4_ERR_INVALID_ARG, "causal is 0 or 1");
+  if (!a.causal && window != 0) return fail(ROCMFP4_ERR_INVALID_ARG, "a window needs causal");
+  if (a.M == 0 || H == 0 || a.cache.B == 0) return ROCMFP4_OK;
+  if (a.q == nullptr || a.out == nullptr) return fail(ROCMFP4_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned_to(a.q, ROCMFP4_OUT_F16) || !aligned_to(a.out, ROCMFP4_OUT_F16))
+    return fail(ROCMFP4_ERR_INVALID_ARG, "misaligned pointer");
+  if (a.ldq < H * cache->D) return fail(ROCMFP4_ERR_INVALID_ARG, "row stride below the heads' width");
+  if (cache->D != 64 && cache->D != 128) return fail(ROCMFP4_ERR_UNSUPPORTED, "paged attention: D must be 64 or 128");
+  if (!aligned16(a.q) || a.ldq % 8 != 0 || !aligned16(a.out))
+    return fail(ROCMFP4_ERR_UNSUPPORTED, "paged attention: q's rows and out must be 16-byte aligned");
+  if (a.M * H >= (int64_t(1) << 31) || H > 65536) return fail(ROCMFP4_ERR_UNSUPPORTED, "paged attention: sizes too large");
+  a.H = (int)H;
+  a.window = window >= (int64_t(1) << 31) ? 0 : (int)window;  // no sequence is as long
+  DeviceState* d = nullptr;
+  if ((st = device_state(&d)) != ROCMFP4_OK) return st;
+  a.cache.err = d->err;
+  cudaError_t e = launch_paged_attention(cache->variant, act, a, d->sms, s);
+  if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+  g_launches.fetch_add(1);
+  return ROCMFP4_OK;
+}
+
 }  // namespace
 
 namespace rocmfp4 {
@@ -581,6 +706,74 @@ rocmfp4_status rocmfp4_logprobs(const void* logits, rocmfp4_out_dtype type, int6
   a.scale = scale;
   a.type = type;
   return logprobs(a, top_n, reinterpret_cast<cudaStream_t>(stream));
+}
+
+rocmfp4_status rocmfp4_rotary(const void* x, rocmfp4_out_dtype x_type, int64_t ldx, const int32_t* positions,
+                              const float* freq, int64_t rot, int interleaved, float amplitude, void* y,
+                              rocmfp4_act y_type, int64_t M, int64_t H, int64_t D, rocmfp4_stream_t stream) {
+  RopeArgs a{};
+  a.x[0] = x;
+  a.ld[0] = ldx;
+  a.positions = positions;
+  a.freq = freq;
+  a.q_out = static_cast<uint16_t*>(y);
+  a.M = M;
+  a.H = H;
+  a.D = D;
+  a.rot = rot;
+  a.type = x_type;
+  a.act = y_type;
+  a.interleaved = interleaved;
+  a.amplitude = amplitude;
+  return rope(a, nullptr, reinterpret_cast<cudaStream_t>(stream));
+}
+
+rocmfp4_status rocmfp4_rope_append(const rocmfp4_paged_cache* cache, const void* q, const void* k, const void* v,
+                                   rocmfp4_out_dtype type, int64_t ldq, int64_t ldk, int64_t ldv,
+                                   const int32_t* positions, const float* freq, int64_t rot, int interleaved,
+                                   float amplitude, void* q_out, rocmfp4_act q_type, int64_t M, int64_t H,
+                                   rocmfp4_stream_t stream) {
+  RopeArgs a{};
+  a.x[0] = q;
+  a.x[1] = k;
+  a.x[2] = v;
+  a.ld[0] = ldq;
+  a.ld[1] = ldk;
+  a.ld[2] = ldv;
+  a.positions = positions;
+  a.freq = freq;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.M = M;
+  a.H = H;
+  a.rot = rot;
+  a.type = type;
+  a.act = q_type;
+  a.interleaved = interleaved;
+  a.paged = 1;
+  a.amplitude = amplitude;
+  return rope(a, cache, reinterpret_cast<cudaStream_t>(stream));
+}
+
+rocmfp4_status rocmfp4_cache_read(const rocmfp4_paged_cache* cache, void* k_out, void* v_out, rocmfp4_out_dtype type,
+                                  int64_t M, rocmfp4_stream_t stream) {
+  CacheReadArgs a{};
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.M = M;
+  return cache_read(cache, a, type, reinterpret_cast<cudaStream_t>(stream));
+}
+
+rocmfp4_status rocmfp4_paged_attention(const void* q, int64_t ldq, const rocmfp4_paged_cache* cache, void* out, int64_t M,
+                                       int64_t H, float scale, int causal, int64_t window, rocmfp4_act act,
+                                       rocmfp4_stream_t stream) {
+  PagedAttnArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.ldq = ldq;
+  a.out = static_cast<uint16_t*>(out);
+  a.M = M;
+  a.causal = causal;
+  a.scale = scale;
+  return paged_attention(cache, a, H, window, act, reinterpret_cast<cudaStream_t>(stream));
 }
 
 rocmfp4_status rocmfp4_gemv_chain(const rocmfp4_gemv_op* ops, int count, int64_t M, rocmfp4_variant variant,

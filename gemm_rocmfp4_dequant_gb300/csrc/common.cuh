@@ -26,7 +26,10 @@
 namespace rocmfp4 {
 
 // Error bits a kernel may record in the workspace error word.
-enum : uint32_t { kErrWaitTimeout = 1u };
+enum : uint32_t {
+  kErrWaitTimeout = 1u,
+  kErrBadPage = 2u,  // a token's page number was outside the cache
+};
 
 template <int V>
 struct Fmt {

@@ -9,6 +9,7 @@
 // it with the smallest covering scale and nearest codes, by exact comparisons.
 #include "common.cuh"
 #include "kernels.h"
+#include "quant.cuh"
 
 namespace rocmfp4 {
 namespace {
@@ -128,40 +129,6 @@ __global__ void gemm_generic_kernel(const GenericArgs a, int act) {
 // Codebook10 magnitude, ties to the smaller, by comparing |x| with the
 // midpoints times the half-scale.  Every product and comparison is exact in
 // fp32.  Non-finite inputs count as 0.
-
-// E4M3 value of a scale byte (bit 7 clear), exact.
-RF4_DEV float ue4m3_f32(uint32_t e) {
-  const uint32_t E = (e >> 3) & 15u, M = e & 7u;
-  return E ? __uint_as_float(((E + 120u) << 23) | (M << 20)) : (float)M * (1.0f / 512.0f);
-}
-
-// The scale byte of a group: E4M3 values increase with the byte, so this is
-// the smallest e with 5 * E4M3(e) >= amax.  A candidate comes from the fp32
-// bits of amax * 0.2 (E4M3 rounded up: within one step of the answer, as the
-// estimate is within a few ulp of amax / 5); one exact check each way (5 *
-// E4M3(e) is exact in fp32) then fixes it.
-RF4_DEV uint32_t quant_scale(float amax) {
-  if (!(amax > 0.f)) return 0u;
-  if (5.f * ue4m3_f32(0x7Eu) < amax) return 0x7Eu;
-  const float t = amax * 0.2f;
-  uint32_t e;
-  if (t >= 0.015625f) {  // 2^-6 and up: E4M3 exponent field E >= 1
-    const uint32_t b = __float_as_uint(t);
-    uint32_t E = (b >> 23) - 120u, M = (b >> 20) & 7u;
-    if (b & 0xFFFFFu) ++M;  // round the 3-bit mantissa up
-    if (M == 8u) {
-      M = 0u;
-      ++E;
-    }
-    e = E > 15u ? 0x7Eu : (E << 3) | M;
-  } else {  // subnormal E4M3: value M / 512
-    e = (uint32_t)ceilf(t * 512.f);  // at most 8, which is 2^-6 (E = 1, M = 0)
-  }
-  e = e > 0x7Eu ? 0x7Eu : (e == 0u ? 1u : e);
-  if (e > 1u && 5.f * ue4m3_f32(e - 1u) >= amax) --e;
-  else if (5.f * ue4m3_f32(e) < amax) ++e;
-  return e;
-}
 
 // The Codebook10 midpoints 0.5, 1.5, 2.5, 3.5, 5, 7, 9 as fp16 (ACT = 0) or
 // bf16 bits, in both lanes.

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "moe_layout.h"
+#include "paged.h"
 
 namespace rocmfp4 {
 
@@ -145,6 +146,42 @@ struct MoeArgs {
 };
 cudaError_t moe_prepare();
 cudaError_t launch_moe(int variant, int act, const MoeArgs& a, int sms, cudaStream_t s);
+
+// Rotary positions of rows of q, k and v heads; q to fp16 / bf16, k and v into
+// the pages (paged.cu).  Without `paged`, q alone, at `positions`.
+struct RopeArgs {
+  const void* x[3];          // q, k, v: rows of heads of D values
+  int64_t ld[3];             // row strides in elements
+  const int32_t* positions;  // [M], nullptr: the tokens' places in their sequences
+  const float* freq;         // [rot / 2]
+  uint16_t* q_out;           // [M][H][D]
+  int64_t M, H, D, rot;
+  int type, act, interleaved, paged;
+  float amplitude;
+  PagedArgs cache;
+};
+cudaError_t launch_rope(int variant, const RopeArgs& a, int sms, cudaStream_t s);
+
+struct CacheReadArgs {
+  void* k_out;  // [M][Hkv][D], nullptr: not wanted
+  void* v_out;
+  int64_t M;
+  PagedArgs cache;
+};
+cudaError_t launch_cache_read(int variant, int type, const CacheReadArgs& a, int sms, cudaStream_t s);
+
+// Attention of rows of queries over the pages of their sequences
+// (paged_attention.cu).  D is 64 or 128, page_size a multiple of 16.
+struct PagedAttnArgs {
+  const uint16_t* q;  // [M] rows of H heads, ldq apart
+  int64_t ldq;
+  uint16_t* out;      // [M][H][D]
+  int64_t M;
+  int H, causal, window;
+  float scale;
+  PagedArgs cache;
+};
+cudaError_t launch_paged_attention(int variant, int act, const PagedAttnArgs& a, int sms, cudaStream_t s);
 
 // Any K % 32 == 0, any alignment: one warp per (row, column chunk).
 struct GenericArgs {

@@ -267,6 +267,123 @@ rocmfp4_status rocmfp4_logprobs(const void *logits, rocmfp4_out_dtype type, int6
                                 float *entropy, int32_t *top_ids, float *top_logprobs,
                                 int64_t top_n, int64_t M, int64_t V, rocmfp4_stream_t stream);
 
+/* A paged K/V cache of ROCmFP4 rows and the batch of rows that a call deals
+ * with.  (The block format serves the K/V cache too: the "FlashAttention K/V
+ * cache optimization" item of "Feasibility Report: Porting ROCmFP4 to Atlas";
+ * the pages are this library's.)
+ *
+ *   - K, V   [num_pages][Hkv][page_size] rows of D / 32 packed blocks of
+ *            `variant` each, 16-byte aligned, device.  A contiguous cache
+ *            [B][Hkv][Tmax], as rocmfp4_decode_attention reads it, is one of
+ *            num_pages = B, page_size = Tmax, table[b] = {b};
+ *   - lens   [B] int32: the tokens that sequence b holds, a call's new tokens
+ *            among them;
+ *   - table  [B] rows of table_width int32 page numbers, table_stride apart:
+ *            token t of sequence b lies in page table[b][t / page_size], at
+ *            t % page_size.  Sequences may share pages that are read;
+ *   - cu     [B + 1] int32, cu[0] = 0, not decreasing: rows cu[b] ..
+ *            cu[b + 1] - 1 of a call belong to sequence b.  Where a row is a
+ *            token of its sequence, the rows are the last ones: row i of n is
+ *            token lens[b] - n + i.  Rows at or behind cu[B] are padding: they
+ *            are not read, and their outputs are left as they are.
+ *   - The struct is host memory, read during the call; table, lens and cu
+ *     are device memory, read by the kernels (a captured graph follows
+ *     their contents).
+ *   - page_size a multiple of 16, D at most 256, else ROCMFP4_ERR_UNSUPPORTED.
+ *   - No access leaves the buffers whatever table, lens and cu hold: a token
+ *     whose page number lies outside 0 .. num_pages - 1, or whose place lies
+ *     behind table_width pages, is no token (not written, not seen, read as
+ *     zeros), and bit 1 of rocmfp4_device_error_bits reports it. */
+typedef struct rocmfp4_paged_cache {
+  void *K;
+  void *V;
+  const int32_t *table;
+  const int32_t *lens;
+  const int32_t *cu;
+  int64_t B;
+  int64_t table_width;
+  int64_t table_stride;
+  int64_t num_pages;
+  int64_t page_size;
+  int64_t Hkv;
+  int64_t D;
+  rocmfp4_variant variant;
+} rocmfp4_paged_cache;
+
+/* Rotary positions: in the first rot values of each head the pairs
+ * (i, i + rot / 2), or (2i, 2i + 1) if interleaved, i < rot / 2, are turned:
+ *
+ *   y_a = amplitude * (x_a cos t - x_b sin t),
+ *   y_b = amplitude * (x_b cos t + x_a sin t),   t = position * freq[i];
+ *
+ * values rot .. D - 1 of a head pass unchanged.  A context that is stretched
+ * (by any rule) is a table of frequencies and an amplitude.  No counterpart in
+ * the format definition.
+ *   - x          [M] rows of H heads of D values of x_type, rows ldx apart;
+ *   - positions  [M] int32, of either sign;
+ *   - freq       [rot / 2] fp32.  rot even, 0 .. D (0: only the rounding);
+ *   - y          [M][H][D] of y_type, contiguous, 8-byte aligned.
+ *   - D a multiple of 32, at most 256.
+ *   - The angle is exact to about 2^-32 of a turn at any position; the turn is
+ *     fp32, and each output is rounded once.
+ *   - One programmatic dependent launch on `stream`. */
+rocmfp4_status rocmfp4_rotary(const void *x, rocmfp4_out_dtype x_type, int64_t ldx,
+                              const int32_t *positions, const float *freq, int64_t rot,
+                              int interleaved, float amplitude, void *y, rocmfp4_act y_type,
+                              int64_t M, int64_t H, int64_t D, rocmfp4_stream_t stream);
+
+/* New tokens of a batch: the heads of q and k turned as by rocmfp4_rotary, q
+ * to fp16 / bf16, k and v packed into the pages of their sequences by
+ * rocmfp4_quantize's rule (from the fp32 values: no other rounding between).
+ *   - q, k, v    [M] rows of H, Hkv and Hkv heads of D values of `type`, rows
+ *                ldq, ldk and ldv apart: parts of one product's rows, or
+ *                tensors of their own.  H may be 0 (no q, no q_out);
+ *   - positions  [M] int32, or NULL: a token's place in its sequence;
+ *   - freq, rot, interleaved, amplitude as for rocmfp4_rotary; v is not turned;
+ *   - q_out      [M][H][D] of q_type, contiguous, 8-byte aligned.
+ *   - A row whose place is before its sequence's first token (cu gives more
+ *     rows than lens tokens) goes to no page; its q is turned all the same.
+ *   - The rows of one call must lie in distinct slots: of two rows for one
+ *     slot, either may be found there, block by block.
+ *   - One programmatic dependent launch on `stream`. */
+rocmfp4_status rocmfp4_rope_append(const rocmfp4_paged_cache *cache, const void *q, const void *k,
+                                   const void *v, rocmfp4_out_dtype type, int64_t ldq, int64_t ldk,
+                                   int64_t ldv, const int32_t *positions, const float *freq,
+                                   int64_t rot, int interleaved, float amplitude, void *q_out,
+                                   rocmfp4_act q_type, int64_t M, int64_t H,
+                                   rocmfp4_stream_t stream);
+
+/* The values of the batch's tokens as dense rows: k_out and v_out [M][Hkv][D]
+ * of `type`, contiguous, 16-byte aligned; either may be NULL.  Exact, as
+ * rocmfp4_dequant.  With cu the running sum of lens, the whole cache.  A row
+ * before its sequence's first token reads as zeros.
+ *   - One programmatic dependent launch on `stream`. */
+rocmfp4_status rocmfp4_cache_read(const rocmfp4_paged_cache *cache, void *k_out, void *v_out,
+                                  rocmfp4_out_dtype type, int64_t M, rocmfp4_stream_t stream);
+
+/* Attention of the batch's rows over the pages of their sequences:
+ *
+ *   out[r][h] = sum_t p_t V[t],  p = softmax_t(scale * q[r][h] . K[t]),
+ *
+ * over the tokens t of KV head h / (H / Hkv) that row r, row i of the n of
+ * sequence b, sees:
+ *   causal, window 0   t <= lens[b] - n + i  (a chunk of new tokens, whose own
+ *                      rows rocmfp4_rope_append has written before);
+ *   causal, window w   also t > lens[b] - n + i - w;
+ *   causal 0           t < lens[b]  (a cross attention: the rows are queries
+ *                      of any number, the cache holds another's states).
+ * A row that sees nothing gives zeros.
+ *   - q    [M] rows of H heads of D values of type act, rows ldq apart, 16-byte
+ *          aligned; out [M][H][D] of type act, contiguous, 16-byte aligned.
+ *   - H a multiple of Hkv; D 64 or 128; scale from 1e-30 to 1e30.
+ *   - Scores, maxima, sums and the weighted sum are fp32; p is rounded to fp16
+ *     for the product with V, and the output once.  Results are bitwise
+ *     repeatable for the same inputs on the same device.
+ *   - Rows at or behind lens[b] of a page need not hold valid blocks. */
+rocmfp4_status rocmfp4_paged_attention(const void *q, int64_t ldq, const rocmfp4_paged_cache *cache,
+                                       void *out, int64_t M, int64_t H, float scale, int causal,
+                                       int64_t window, rocmfp4_act act, rocmfp4_stream_t stream);
+
 /* One product of a chain: Y = X . W^T with the layouts of rocmfp4_gemm_ex
  * (X is M x K of the chain's activation type, Y is M x N fp32). */
 typedef struct rocmfp4_gemv_op {
@@ -405,7 +522,7 @@ rocmfp4_status rocmfp4_copy(void *dst, const void *src, int64_t bytes, rocmfp4_s
 
 /* Error bits recorded by kernels on the current device since the last query
  * (bit 0: a kernel gave up waiting for its own bulk copies, so its outputs
- * are invalid), from the workspace of the allocating entry points and from
+ * are invalid; bit 1: a page number of a paged cache lay outside it), from the workspace of the allocating entry points and from
  * the fixed array of rocmfp4_gemm_noalloc, whichever exist on the device.
  * Synchronises with the stream, clears the bits, and on a non-zero result
  * also clears the split-reduction counters.  Allocates nothing: a device on
