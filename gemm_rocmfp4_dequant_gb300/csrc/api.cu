@@ -29,6 +29,8 @@ struct DeviceState {
   uint32_t* lp_cnt = nullptr;        // log probabilities: arrivals per split row
   bool norm_ready = false;           // RMS norm: kernels prepared
   uint32_t* moe_bars = nullptr;      // mixture of experts: barrier counters
+  float* paged_ws = nullptr;         // paged attention: parts of split row tiles, from its first call on
+  uint32_t* paged_cnt = nullptr;     // paged attention: arrivals per split row tile
   float* moe_ws = nullptr;           // mixture of experts: router logits and hidden values, from its first call on
 };
 
@@ -74,7 +76,21 @@ rocmfp4_status moe_set_up(DeviceState& d) {
   return ROCMFP4_OK;
 }
 
-enum class Needs { kProducts, kNorm, kMoe };
+// Paged attention's workspace (57 MiB on 152 SMs), made in the same manner.
+rocmfp4_status paged_set_up(DeviceState& d) {
+  cudaError_t e = paged_attn_prepare();
+  if (e != cudaSuccess) return cuda_fail(e, "paged attention kernel set-up");
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return cuda_fail(e, "cudaThreadExchangeStreamCaptureMode");
+  float* ws = nullptr;
+  e = cudaMalloc(&ws, sizeof(float) * paged_attn_ws_floats(d.sms));
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc");
+  d.paged_ws = ws;
+  return ROCMFP4_OK;
+}
+
+enum class Needs { kProducts, kNorm, kMoe, kPaged };
 
 // Per-device set-up on first use: SM count, kernel attributes, occupancy and
 // the workspace of the split-tile reduction; and what `needs` has beside that.
@@ -121,6 +137,8 @@ rocmfp4_status device_state(DeviceState** out, Needs needs = Needs::kProducts) {
       return cuda_fail(e, "cudaMemset");
     if ((e = cudaMalloc(&d.moe_bars, sizeof(uint32_t) * kMoeBarWords)) != cudaSuccess) return cuda_fail(e, "cudaMalloc");
     if ((e = cudaMemset(d.moe_bars, 0, sizeof(uint32_t) * kMoeBarWords)) != cudaSuccess) return cuda_fail(e, "cudaMemset");
+    if ((e = cudaMalloc(&d.paged_cnt, sizeof(uint32_t) * d.sms)) != cudaSuccess) return cuda_fail(e, "cudaMalloc");
+    if ((e = cudaMemset(d.paged_cnt, 0, sizeof(uint32_t) * d.sms)) != cudaSuccess) return cuda_fail(e, "cudaMemset");
     if ((e = cudaMemset(d.err, 0, sizeof(uint32_t))) != cudaSuccess) return cuda_fail(e, "cudaMemset");
     if ((e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
     d.ready = true;
@@ -131,6 +149,10 @@ rocmfp4_status device_state(DeviceState** out, Needs needs = Needs::kProducts) {
   }
   if (needs == Needs::kMoe && d.moe_ws == nullptr) {
     const rocmfp4_status st = moe_set_up(d);
+    if (st != ROCMFP4_OK) return st;
+  }
+  if (needs == Needs::kPaged && d.paged_ws == nullptr) {
+    const rocmfp4_status st = paged_set_up(d);
     if (st != ROCMFP4_OK) return st;
   }
   *out = &d;
@@ -482,7 +504,7 @@ rocmfp4_status paged_args(const rocmfp4_paged_cache* c, PagedArgs* out) {
   if (c->page_size % 16 != 0) return fail(ROCMFP4_ERR_UNSUPPORTED, "paged cache: page_size must be a multiple of 16");
   if (c->D > 256) return fail(ROCMFP4_ERR_UNSUPPORTED, "paged cache: D at most 256");
   if (c->B >= most || c->table_width >= most || c->num_pages >= most || c->page_size >= most || c->Hkv > 65536 ||
-      c->table_width > most / c->page_size)
+      c->table_width > (most >> 1) / c->page_size)
     return fail(ROCMFP4_ERR_UNSUPPORTED, "paged cache: sizes too large");
   PagedArgs& p = *out;
   p.K = static_cast<uint8_t*>(c->K);
@@ -582,8 +604,10 @@ rocmfp4_status paged_attention(const rocmfp4_paged_cache* cache, PagedAttnArgs a
   a.H = (int)H;
   a.window = window >= (int64_t(1) << 31) ? 0 : (int)window;  // no sequence is as long
   DeviceState* d = nullptr;
-  if ((st = device_state(&d)) != ROCMFP4_OK) return st;
+  if ((st = device_state(&d, Needs::kPaged)) != ROCMFP4_OK) return st;
   a.cache.err = d->err;
+  a.ws = d->paged_ws;
+  a.cnt = d->paged_cnt;
   cudaError_t e = launch_paged_attention(cache->variant, act, a, d->sms, s);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   g_launches.fetch_add(1);
@@ -914,6 +938,7 @@ uint32_t rocmfp4_device_error_bits(rocmfp4_stream_t stream) {
       cudaMemsetAsync(d->cnt, 0, sizeof(uint32_t) * d->wmax, s);
       cudaMemsetAsync(d->tccnt, 0, sizeof(uint32_t) * tc_cnt_words(d->sms), s);
       cudaMemsetAsync(d->moe_bars, 0, sizeof(uint32_t) * kMoeBarWords, s);
+      cudaMemsetAsync(d->paged_cnt, 0, sizeof(uint32_t) * d->sms, s);
       if (cudaStreamSynchronize(s) != cudaSuccess) return 0xFFFFFFFFu;
     }
   }
@@ -958,6 +983,8 @@ void rocmfp4_shutdown(void) {
     cudaFree(d.lp_cnt);
     cudaFree(d.moe_ws);
     cudaFree(d.moe_bars);
+    cudaFree(d.paged_ws);
+    cudaFree(d.paged_cnt);
     d = DeviceState{};
   }
   cudaSetDevice(cur);

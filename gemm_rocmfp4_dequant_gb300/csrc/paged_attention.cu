@@ -1,116 +1,932 @@
 // Attention of a chunk of rows of every sequence over a paged ROCmFP4 cache:
 //   out[r][h] = softmax_t(scale * q[r][h] . K[t]) . V[t]
-// over the tokens t that row r sees.  A CTA takes one (row, head); its warps
-// take alternate tokens and keep a running maximum and sum each.
+// over the tokens t that row r sees (causal, causal with a window, or all).
+//
+// Tiles.  The G query heads of a KV head share its tokens, so the (row, head)
+// pairs of a sequence and a KV head are the rows of one matrix, token-major:
+// row r is row r / G of the chunk, head r % G.  They are cut into tiles of up to
+// 256; a tile walks over the tokens it sees, 128 at a time:
+//   S = Q K^T    tcgen05.mma, 128 rows x 128 tokens, Q and K in shared memory
+//   P = 2^(S scale log2 e - m + 7), m a running maximum, into tensor memory
+//   O += P V     tcgen05.mma, P from tensor memory, V from shared memory
+// K and V are decoded from their blocks into shared memory, exact in fp16 (K in
+// q's type), once for all rows of the tile.
+//
+// Two chains.  A "wide" tile (more than 128 rows) is two halves of 128 rows
+// over the same tokens; a "narrow" one is one half whose even and odd token
+// tiles go to the two chains, merged at the end.  While one chain's softmax
+// runs, the tensor core works for the other.
+//
+// Softmax.  A thread owns a row (a lane of tensor memory), so maxima and sums
+// need no exchange; both are fp32.  The reference m follows the maximum only
+// when that has grown by more than 2^8 (the sum and O are scaled then), so
+// P <= 2^15 fits fp16; P is rounded to fp16, whose half step of 2^-11 is the
+// output type's own (fp16) or an eighth of it (bf16), and the sum keeps the
+// unrounded values.  The factor 2^7 keeps weights down to 2^-21 normal in fp16; it
+// cancels in O / l.
+//
+// Order of D.  Byte j of a block decodes to the pair (j, j + 16).  The
+// contraction of S does not care for the order of D, so Q is stored in that
+// order and K as it falls out; V's columns, and so O's, are in it too, and the
+// output puts them back.
+//
+// Work.  All token tiles of all row tiles are numbered in one row (sequence,
+// KV head, row tile, token tile; a wide one counts twice) and every CTA takes an
+// equal stretch of it, by the lengths on the device.  A row tile that falls to
+// several CTAs leaves unnormalised parts in the workspace; the CTA that arrives
+// last adds them in order.  Nothing waits for another CTA.
+//
+// Warps (512 threads):
+//   0-3, 4-7   softmax and output of chain 0 and 1
+//   8-11       decode: one token row a thread
+//   12         tensor-memory allocation, MMA issue (one thread)
+//   13         bulk copies of raw rows, 16 tokens each (a page is a multiple of 16)
+//   14-15      Q rows into shared memory
+// Every wait is bounded: a warp that gives up records kErrWaitTimeout and
+// goes on without waiting, so that all meet at the end.
+#include <cstring>
+
 #include "common.cuh"
 #include "kernels.h"
 
 namespace rocmfp4 {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kThreads = 512;
+constexpr int kTok = 128;     // tokens per tile
+constexpr int kHalf = 128;    // rows per chain
+constexpr int kMinShare = 4;  // least work of a CTA: narrow token tiles
+constexpr int kFlags = 16;
+constexpr int kSlots = 3;     // parts a CTA may hold: of its first, its last, and its current row tile
+constexpr float kGrow = 8.f;  // log2 of how far a maximum may lead its reference
+constexpr float kLift = 7.f;  // log2 of P's factor
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct Params {
-  PagedAttnArgs a;
+  const uint16_t* q;
+  uint16_t* out;
+  int64_t ldq;
+  int M, H, G, causal, window;
+  float scale_log2;
+  PagedArgs c;
+  float* ws;      // [ctas][kSlots][2][kHalf] rows of D, then as many pairs (m, l)
+  uint32_t* cnt;  // [ctas], zero between launches
 };
 
-RF4_DEV float act_f32(uint16_t bits, int act) {
-  return act == 0 ? __half2float(__ushort_as_half(bits)) : __uint_as_float((uint32_t)bits << 16);
-}
-
 template <int V, int D>
-RF4_DEV void row_values(const uint8_t* row, int lane, float (&v)[D / 32]) {
-  constexpr int N = D / 32;
-  const int d0 = lane * N, i = d0 & 31;
-  const uint8_t* blk = row + d0 / 32 * Fmt<V>::BB;
-  const float hs = halfscale_f32(blk[16 + (V == 0 ? i >> 4 : 0)]);
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const uint32_t byte = blk[(i + k) & 15], q = i >= 16 ? byte >> 4 : byte & 15u;
-    const int m = (int)(q & 7u), c = m <= 4 ? m : 2 * m - 4;
-    v[k] = (float)(q & 8u ? -c : c) * hs;
-  }
-}
+struct Plan {
+  static constexpr int RB = D / 32 * Fmt<V>::BB;  // raw bytes per token row
+  static constexpr int RAW = kTok * RB;           // raw bytes per tile of K or V
+  static constexpr int TILE = kTok * D * 2;       // decoded tile
+  static constexpr int PANEL = kTok * 128;        // 64 columns of a tile
+  static constexpr int STAGES = 2;
+  static constexpr int OFF_Q = 0;  // two halves
+  static constexpr int OFF_K = OFF_Q + 2 * TILE;
+  static constexpr int OFF_V = OFF_K + STAGES * TILE;
+  static constexpr int OFF_RAW = OFF_V + STAGES * TILE;
+  static constexpr int ROOM = 227 * 1024 - 1024 - 1024;  // less alignment and barriers
+  static constexpr int FIT = (ROOM - OFF_RAW) / RAW;
+  static constexpr int RSTAGES = FIT > 8 ? 8 : FIT;
+  static constexpr int OFF_BAR = (OFF_RAW + RSTAGES * RAW + 15) / 16 * 16;
+  static constexpr int SMEM = OFF_BAR + 1024 + 1024;
+  static_assert(RSTAGES >= 2 && SMEM <= 227 * 1024, "shared memory");
+  static_assert(RAW % 16 == 0, "bulk copies");
+};
 
-template <int V, int D>
-__global__ void __launch_bounds__(kWarps * 32) attend_kernel(const __grid_constant__ Params p, int act) {
-  constexpr int N = D / 32;
-  constexpr int RB = D / 32 * Fmt<V>::BB;
-  __shared__ float sm[kWarps][D + 2];
-  const PagedAttnArgs& a = p.a;
-  const PagedArgs& c = a.cache;
-  grid_dependency_wait();
-  const int64_t row = blockIdx.x / a.H;
-  const int h = (int)(blockIdx.x % a.H), hk = h / (a.H / c.Hkv), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (row >= c.cu[c.B] || row < c.cu[0]) return;
-  int b = 0;
-  for (int n = c.B; n > 1;) {
-    const int step = n / 2;
-    if (c.cu[b + step] <= row) b += step, n -= step;
-    else n = step;
+struct Control {  // at OFF_BAR
+  uint64_t raw_full[8], raw_empty[8];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t q_full, q_empty;
+  long long start, end, total;  // of this CTA's stretch; of all work
+  long long base;               // where the first row tile begins
+  long long scan[kThreads / 32];
+  int b, hk, k, ctas;
+  int last;
+  uint32_t tmem;
+  uint32_t bad[kFlags];  // per token tile: 16-token groups whose page lies outside the cache
+};
+static_assert(sizeof(Control) <= 1024, "control block");
+
+// ---- tensor-core instructions -------------------------------------------------
+RF4_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+RF4_DEV void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+RF4_DEV void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+RF4_DEV void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Shared-memory operand in the 128-byte swizzle: rows of 128 bytes, groups of
+// eight rows 1024 bytes apart (stride), 64-column panels `lead` bytes apart
+// (used where the columns are the operand's outer dimension).
+RF4_DEV uint64_t smem_desc(uint32_t saddr, uint32_t lead) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// kind::f16, fp32 accumulator, A and B both fp16 (type 0) or bf16 (type 1), M =
+// 128; `b_outer`: B's rows in memory are its contraction index.
+RF4_HOSTDEV constexpr uint32_t instr_desc(int type, int n, int b_outer) {
+  return (1u << 4) | ((uint32_t)type << 7) | ((uint32_t)type << 10) | ((uint32_t)b_outer << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kHalf >> 4) << 24);
+}
+RF4_DEV void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+RF4_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+RF4_DEV void tmem_ld32(uint32_t addr, float (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(addr));
+}
+RF4_DEV void tmem_st32(uint32_t addr, const float (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
+      "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]),
+      "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]), "f"(r[27]),
+      "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31])
+      : "memory");
+}
+RF4_DEV void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+RF4_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+RF4_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+RF4_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+RF4_DEV uint32_t pack_h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+RF4_DEV uint32_t pack_act(float lo, float hi, int act) {
+  if (act == 0) return pack_h2(lo, hi);
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+RF4_DEV void chains_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Waits that go on without waiting once one has given up.
+struct Waits {
+  bool ok = true;
+  RF4_DEV void one(const uint64_t* bar, uint32_t parity) {
+    if (ok) ok = mbar_wait_bounded(smem_addr(bar), parity);
   }
-  int64_t len = c.lens[b];
-  len = len < 0 ? 0 : len > (int64_t)c.width * c.page_size ? (int64_t)c.width * c.page_size : len;
-  int64_t hi = len, lo = 0;
-  if (a.causal) {
-    hi = (int64_t)c.lens[b] - (c.cu[b + 1] - row) + 1;
-    if (a.window > 0) lo = hi - a.window > 0 ? hi - a.window : 0;
-    if (hi > len) hi = len;
+  RF4_DEV void warp(const uint64_t* bar, uint32_t parity) {
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(bar), parity));
   }
-  float q[N], o[N], m = -INFINITY, sum = 0.f;
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    q[k] = act_f32(a.q[row * a.ldq + (int64_t)h * D + lane * N + k], act);
-    o[k] = 0.f;
-  }
-  for (int64_t t = lo + warp; t < hi; t += kWarps) {
-    const int page = c.table[b * c.ldt + t / c.page_size];
-    if (page < 0 || page >= c.num_pages) {
-      if (lane == 0) atomicOr(c.err, kErrBadPage);
-      continue;
+};
+
+struct Ring {
+  uint32_t stage = 0, phase = 0;
+  RF4_DEV void next(uint32_t n) {
+    if (++stage == n) {
+      stage = 0;
+      phase ^= 1u;
     }
-    const int64_t at = (((int64_t)page * c.Hkv + hk) * c.page_size + t % c.page_size) * RB;
-    float kv[N], s = 0.f;
-    row_values<V, D>(c.K + at, lane, kv);
-#pragma unroll
-    for (int k = 0; k < N; ++k) s = fmaf(q[k], kv[k], s);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= a.scale;
-    const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn, al = expf(m - ref), e = expf(s - ref);
-    row_values<V, D>(c.V + at, lane, kv);
-    sum = sum * al + e;
-#pragma unroll
-    for (int k = 0; k < N; ++k) o[k] = o[k] * al + e * kv[k];
-    m = mn;
   }
-  if (lane == 0) sm[warp][D] = m, sm[warp][D + 1] = sum;
+};
+
+// ---- work -----------------------------------------------------------------------
+struct Seq {
+  int row0, n;     // rows of the call
+  int len;         // tokens
+  int lim;         // tokens that the table has room for
+};
+
+RF4_DEV Seq sequence(const Params& p, int b) {
+  Seq s;
+  const int r0 = min(max(p.c.cu[b], 0), p.M), r1 = min(max(p.c.cu[b + 1], 0), p.M);
+  s.row0 = r0;
+  s.n = max(r1 - r0, 0);
+  s.len = max(p.c.lens[b], 0);
+  const long long room = (long long)p.c.width * p.c.page_size;
+  s.lim = (int)(s.len < room ? s.len : room);
+  return s;
+}
+
+// Tokens lo .. hi - 1 that row i of a sequence's chunk sees.
+RF4_DEV void seen(const Params& p, const Seq& s, int i, int& lo, int& hi) {
+  lo = 0;
+  hi = s.lim;
+  if (p.causal) {
+    const long long end = (long long)s.len - s.n + i + 1;
+    hi = (int)(end < 0 ? 0 : end < s.lim ? end : s.lim);
+    if (p.window > 0 && end > p.window) lo = (int)(end - p.window < hi ? end - p.window : hi);
+  }
+}
+
+struct RowTile {
+  int rows, weight;  // rows; work of one token tile
+  int c0, tiles;     // first token tile, and how many (at least one)
+};
+
+RF4_DEV RowTile row_tile(const Params& p, const Seq& s, int k) {
+  RowTile t;
+  const int r0 = k * 2 * kHalf;
+  t.rows = min(2 * kHalf, s.n * p.G - r0);
+  t.weight = t.rows > kHalf ? 2 : 1;
+  int lo, hi, x;
+  seen(p, s, r0 / p.G, lo, x);
+  seen(p, s, (r0 + t.rows - 1) / p.G, x, hi);
+  t.c0 = lo / kTok;
+  t.tiles = max(1, (hi + kTok - 1) / kTok - t.c0);
+  return t;
+}
+
+struct Item {
+  int b, hk, r0, rows, wide;
+  int c0, tiles;       // this CTA's token tiles
+  Seq s;
+  int first, last;     // CTAs that share the row tile
+  int slot;            // of this CTA's part
+};
+
+struct Walk {
+  int b, hk, k, ctas;
+  long long base, start, end, total;
+  Seq s;
+  RF4_DEV Walk(const Params& p, const Control& ctl)
+      : b(ctl.b), hk(ctl.hk), k(ctl.k), ctas(ctl.ctas), base(ctl.base), start(ctl.start), end(ctl.end), total(ctl.total) {
+    s = sequence(p, b);
+  }
+  RF4_DEV int owner(long long u) const { return (int)(((u + 1) * ctas - 1) / total); }
+  RF4_DEV bool next(const Params& p, Item& it) {
+    while (base < end) {
+      const RowTile t = row_tile(p, s, k);
+      const long long all = (long long)t.tiles * t.weight;
+      const int j0 = base >= start ? 0 : (int)((start - base + t.weight - 1) / t.weight);
+      const int j1 = end >= base + all ? t.tiles : (int)((end - base + t.weight - 1) / t.weight);
+      it.b = b;
+      it.hk = hk;
+      it.r0 = k * 2 * kHalf;
+      it.rows = t.rows;
+      it.wide = t.weight - 1;
+      it.c0 = t.c0 + j0;
+      it.tiles = j1 - j0;
+      it.s = s;
+      it.first = it.last = blockIdx.x;
+      it.slot = 2;
+      if (j0 > 0 || j1 < t.tiles) {
+        it.first = owner(base);
+        it.last = owner(base + (long long)(t.tiles - 1) * t.weight);
+        it.slot = j0 > 0 ? 0 : 1;
+      }
+      base += all;
+      if ((long long)(++k) * 2 * kHalf >= (long long)s.n * p.G) {
+        k = 0;
+        if (++hk == p.c.Hkv) {
+          hk = 0;
+          do {
+            if (++b >= p.c.B) {
+              base = total;
+              break;
+            }
+            s = sequence(p, b);
+          } while (s.n == 0);
+        }
+      }
+      if (j0 < j1) return true;
+    }
+    return false;
+  }
+};
+
+// Work of sequence b: row tiles lane, lane + step, ...
+RF4_DEV long long work_of(const Params& p, int b, int lane, int step) {
+  const Seq s = sequence(p, b);
+  const int tiles = (s.n * p.G + 2 * kHalf - 1) / (2 * kHalf);
+  long long w = 0;
+  for (int k = lane; k < tiles; k += step) {
+    const RowTile t = row_tile(p, s, k);
+    w += (long long)t.tiles * t.weight;
+  }
+  return w * p.c.Hkv;
+}
+
+// This CTA's stretch and where it begins; false if it has none.  All threads.
+RF4_DEV bool find_work(const Params& p, Control& ctl) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = p.c.B;
+  // few sequences: a warp each, its lanes over row tiles; many: a thread each, or several in a row
+  const bool by_warp = B <= kThreads / 32;
+  const int per = (B + kThreads - 1) / kThreads;
+  const int b0 = by_warp ? (lane == 0 ? min(warp, B) : B) : min(tid * per, B);
+  const int b1 = by_warp ? (lane == 0 ? min(warp + 1, B) : B) : min(b0 + per, B);
+  long long mine = 0;
+  if (by_warp) {
+    if (warp < B) mine = work_of(p, warp, lane, 32);
 #pragma unroll
-  for (int k = 0; k < N; ++k) sm[warp][lane * N + k] = o[k];
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane != 0) mine = 0;
+  } else {
+    for (int b = b0; b < b1; ++b) mine += work_of(p, b, 0, 1);
+  }
+  long long before = mine;  // inclusive within the warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  if (lane == 31) ctl.scan[warp] = before;
   __syncthreads();
-  for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-    float M = -INFINITY, O = 0.f, L = 0.f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w][D]);
-    if (M == -INFINITY) M = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      const float e = sm[w][D] == -INFINITY ? 1.f : expf(sm[w][D] - M);
-      O += e * sm[w][d];
-      L += e * sm[w][D + 1];
-    }
-    const float y = L > 0.f || L != L ? O / L : 0.f;
-    a.out[(row * a.H + h) * D + d] = act == 0 ? __half_as_ushort(__float2half_rn(y)) : __bfloat16_as_ushort(__float2bfloat16_rn(y));
+  long long total = 0, lower = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == warp) lower = total;
+    total += ctl.scan[w];
   }
+  before += lower - mine;
+  const long long most = total / kMinShare;
+  const int ctas = (int)(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
+  if (total == 0 || (int)blockIdx.x >= ctas) return false;
+  const long long start = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
+  if (start >= before && start < before + mine) {
+    int b = b0;
+    long long base = before, w = mine;
+    for (; b < b1; ++b) {
+      w = by_warp ? mine : work_of(p, b, 0, 1);
+      if (start < base + w) break;
+      base += w;
+    }
+    const long long head = w / p.c.Hkv;
+    const int hk = (int)((start - base) / head);
+    base += hk * head;
+    const Seq s = sequence(p, b);
+    int k = 0;
+    for (;; ++k) {
+      const RowTile t = row_tile(p, s, k);
+      const long long all = (long long)t.tiles * t.weight;
+      if (start < base + all) break;
+      base += all;
+    }
+    ctl.b = b;
+    ctl.hk = hk;
+    ctl.k = k;
+    ctl.base = base;
+    ctl.start = start;
+    ctl.end = end;
+    ctl.total = total;
+    ctl.ctas = ctas;
+  }
+  __syncthreads();
+  return true;
+}
+
+// ---- decode ---------------------------------------------------------------------
+template <int N>
+RF4_DEV uint32_t pair_at(const uint32_t (&w)[N], int pos) {
+  const uint32_t word = w[pos >> 2];
+  switch (pos & 3) {
+    case 0: return e2m1x2<0>(word);
+    case 1: return e2m1x2<1>(word);
+    case 2: return e2m1x2<2>(word);
+    default: return e2m1x2<3>(word);
+  }
+}
+template <int V, int N>
+RF4_DEV uint32_t scales_at(const uint32_t (&w)[N], int pos) {
+  if constexpr (V == 0) return (pos & 2) ? e4m3x2<1>(w[pos >> 2]) : e4m3x2<0>(w[pos >> 2]);
+  return e4m3x2<0>(__byte_perm(w[pos >> 2], 0u, (uint32_t)(pos & 3) * 0x11u));
+}
+
+// A token's raw row as words.
+template <int V, int D>
+RF4_DEV void load_row(const uint8_t* raw, int row, uint32_t (&w)[(D / 32 * Fmt<V>::BB + 3) / 4]) {
+  constexpr int RB = D / 32 * Fmt<V>::BB, N = (RB + 3) / 4;
+  if constexpr (RB % 8 == 0) {
+    const uint2* s = reinterpret_cast<const uint2*>(raw + row * RB);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const uint2 v = s[i];
+      w[2 * i] = v.x;
+      w[2 * i + 1] = v.y;
+    }
+  } else if constexpr (RB % 4 == 0) {
+    const uint32_t* s = reinterpret_cast<const uint32_t*>(raw + row * RB);
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = s[i];
+  } else {  // 34 bytes: odd rows begin in the middle of a word
+    static_assert(RB == 34, "row bytes");
+    const uint32_t* s = reinterpret_cast<const uint32_t*>(raw + (row >> 1) * 68 + (row & 1) * 32);
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = s[i];
+    if (row & 1) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = __funnelshift_r(w[i], i + 1 < N ? w[i + 1] : 0u, 16);
+    }
+  }
+}
+
+// The row's values into the swizzled tile: 64-column panels of 128-byte rows,
+// 16-byte chunk c of row r at c ^ (r % 8).
+template <int V, int D, bool BF16>
+RF4_DEV void decode_row(const uint8_t* raw, uint8_t* tile, int row, bool real) {
+  constexpr int BB = Fmt<V>::BB;
+  uint8_t* dst = tile + row * 128;
+  if (!real) {
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c)
+      *reinterpret_cast<uint4*>(dst + c / 8 * (kTok * 128) + (((c & 7) ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  uint32_t w[(D / 32 * BB + 3) / 4];
+  load_row<V, D>(raw, row, w);
+#pragma unroll
+  for (int kb = 0; kb < D / 32; ++kb) {
+    const uint32_t s2 = scales_at<V>(w, kb * BB + 16);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = hmul2(clamp5(pair_at(w, kb * BB + 4 * c + i)), s2);
+        if constexpr (BF16) v[i] = f16x2_to_bf16x2(v[i]);
+      }
+      const int chunk = (kb & 1) * 4 + c;
+      *reinterpret_cast<uint4*>(dst + kb / 2 * (kTok * 128) + ((chunk ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+}
+
+// ---- softmax of one tile's row -----------------------------------------------------
+struct Row {
+  float m = -INFINITY, l = 0.f;
+};
+
+template <bool MASK>
+RF4_DEV float masked(float x, int col, int a, uint32_t width, uint32_t bad) {
+  if constexpr (MASK) return (uint32_t)(col - a) < width && !(bad >> (col >> 4) & 1u) ? x : -INFINITY;
+  return x;
+}
+
+// S of this lane's row in tensor memory at `s` -> P at the same columns, O
+// (at `o`, D columns) scaled where the reference moves.  Tokens a .. a + width
+// - 1 of the tile are seen, but for `bad` groups of 16.
+template <int D, bool MASK>
+RF4_DEV void softmax_tile(uint32_t s, uint32_t o, Row& st, float scale_log2, bool first, bool used, int a, uint32_t width,
+                          uint32_t bad) {
+  float top = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < kTok; c += 32) {
+    float x[32];
+    tmem_ld32(s + c, x);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) top = fmaxf(top, masked<MASK>(x[i], c + i, a, width, bad));
+  }
+  top *= scale_log2;
+  if (first) {
+    st.m = top;
+  } else {
+    const bool grow = used && top > st.m + kGrow;
+    if (__any_sync(0xffffffffu, grow)) {
+      const float alpha = grow ? ex2(st.m - top) : 1.f;
+      if (grow) st.m = top;
+      st.l *= alpha;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float x[32];
+        tmem_ld32(o + c, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] *= alpha;
+        tmem_st32(o + c, x);
+      }
+    }
+  }
+  const float shift = kLift - (st.m == -INFINITY ? 0.f : st.m);
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < kTok; c += 32) {
+    float x[32];
+    tmem_ld32(s + c, x);
+    tmem_wait_ld();
+    uint32_t h[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float p0 = ex2(fmaf(masked<MASK>(x[2 * i], c + 2 * i, a, width, bad), scale_log2, shift));
+      const float p1 = ex2(fmaf(masked<MASK>(x[2 * i + 1], c + 2 * i + 1, a, width, bad), scale_log2, shift));
+      sum[i & 1] += p0;
+      sum[2 + (i & 1)] += p1;
+      h[i] = pack_h2(p0, p1);
+    }
+    tmem_st16(s + c / 2, h);
+  }
+  st.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  tmem_wait_st();
+}
+
+// Position p of O's columns is value d_of(p) of the head.
+RF4_DEV int d_of(int p) { return (p & ~31) + ((p & 31) >> 1) + ((p & 1) << 4); }
+
+template <int V, int D, int ACT>
+__global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __grid_constant__ Params p) {
+  using F = Plan<V, D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Control& ctl = *reinterpret_cast<Control*>(smem + F::OFF_BAR);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < F::RSTAGES; ++i) {
+      mbar_init(smem_addr(&ctl.raw_full[i]), 1);
+      mbar_init(smem_addr(&ctl.raw_empty[i]), 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&ctl.k_full[i]), 4);
+      mbar_init(smem_addr(&ctl.k_empty[i]), 1);
+      mbar_init(smem_addr(&ctl.v_full[i]), 4);
+      mbar_init(smem_addr(&ctl.v_empty[i]), 1);
+      mbar_init(smem_addr(&ctl.s_full[i]), 1);
+      mbar_init(smem_addr(&ctl.p_full[i]), 4);
+      mbar_init(smem_addr(&ctl.o_full[i]), 1);
+    }
+    mbar_init(smem_addr(&ctl.q_full), 2);
+    mbar_init(smem_addr(&ctl.q_empty), 1);
+    fence_mbar_init();
+  }
+  grid_dependency_wait();  // lengths, tables and everything else may be the preceding kernel's output
+  if (!find_work(p, ctl)) return;
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&ctl.tmem)), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  // columns: S (and P) of chain t at 128 t, O at 256 + D t
+  Waits wait;
+  Walk walk(p, ctl);
+  Item it;
+
+  if (warp < 8) {
+    // ---- softmax and output ----
+    const int t = warp >> 2, r = threadIdx.x & (kHalf - 1);
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + 128u * t, o_at = tmem + lanes + 256u + (uint32_t)D * t;
+    uint32_t n_s = 0, n_o = 0, tile = 0;  // uses of s_full and o_full; token tiles of this CTA so far
+    while (walk.next(p, it)) {
+      const int row = it.r0 + (it.wide ? t * kHalf : 0) + r;
+      const bool used = row < it.r0 + it.rows;
+      int lo = 0, hi = 0;
+      if (used) seen(p, it.s, row / p.G, lo, hi);
+      Row st;
+      bool first = true;
+      for (int j = it.wide ? 0 : t; j < it.tiles; j += it.wide ? 1 : 2) {
+        const int t0 = (it.c0 + j) * kTok;
+        const int a = max(lo - t0, 0), e = min(max(hi - t0, 0), kTok);
+        wait.warp(&ctl.s_full[t], n_s++ & 1u);
+        tc_fence_after();
+        const uint32_t bad = ctl.bad[(tile + j) % kFlags];
+        if (__any_sync(0xffffffffu, used && (a > 0 || e < kTok)) || bad)
+          softmax_tile<D, true>(s_at, o_at, st, p.scale_log2, first, used, a, (uint32_t)max(e - a, 0), bad);
+        else
+          softmax_tile<D, false>(s_at, o_at, st, p.scale_log2, first, used, 0, kTok, 0);
+        first = false;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&ctl.p_full[t]));
+      }
+      tile += it.tiles;
+      if (!first) {
+        wait.warp(&ctl.o_full[t], n_o++ & 1u);
+        tc_fence_after();
+      }
+      if (it.wide && it.first == it.last) {
+        // the whole of this row is here
+        const float inv = st.l == 0.f ? 0.f : 1.f / st.l;
+        const int token = row / p.G, g = row - token * p.G;
+        uint16_t* out = p.out + ((int64_t)(it.s.row0 + token) * p.H + (int64_t)it.hk * p.G + g) * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float x[32];
+          tmem_ld32(o_at + c, x);
+          tmem_wait_ld();
+          if (used) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = pack_act(x[4 * i + h] * inv, x[4 * i + 2 + h] * inv, ACT);
+              uint4* o4 = reinterpret_cast<uint4*>(out + c + 16 * h);
+              o4[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              o4[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
+        }
+        tc_fence_before();
+        continue;
+      }
+      // a part: into the workspace
+      const size_t records = (size_t)gridDim.x * kSlots * 2;
+      float2* ml = reinterpret_cast<float2*>(p.ws + records * kHalf * D);
+      auto record = [&](int cta, int slot, int chain) { return ((size_t)cta * kSlots + slot) * 2 + chain; };
+      const size_t mine = record(blockIdx.x, it.slot, t) * kHalf + r;
+      if (used) __stcg(&ml[mine], make_float2(st.m, st.l));
+      if (!first) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float x[32];
+          tmem_ld32(o_at + c, x);
+          tmem_wait_ld();
+          if (used) {
+            float4* w = reinterpret_cast<float4*>(p.ws + mine * D + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) __stcg(w + i, make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+          }
+        }
+        tc_fence_before();
+      }
+      __threadfence();
+      chains_sync();
+      bool merge = true;
+      if (it.first != it.last) {
+        if (threadIdx.x == 0) {
+          const uint32_t n = atomic_add_acq_rel_gpu(&p.cnt[it.first], 1u);
+          ctl.last = n == (uint32_t)(it.last - it.first);
+          if (ctl.last) store_relaxed_gpu(&p.cnt[it.first], 0u);
+        }
+        chains_sync();
+        merge = ctl.last;
+        if (merge) __threadfence();
+      }
+      if (merge) {
+        for (int i = threadIdx.x; i < it.rows * (D / 4); i += 256) {
+          const int rr = i / (D / 4), q4 = i - rr * (D / 4);
+          const int chain = it.wide ? rr / kHalf : 0, chains = it.wide ? 1 : 2, rw = it.wide ? rr % kHalf : rr;
+          auto part = [&](int c, int ch) {
+            return record(c, it.first == it.last ? 2 : c == it.first ? 1 : 0, chain + ch) * kHalf + rw;
+          };
+          float M = -INFINITY;
+          for (int c = it.first; c <= it.last; ++c)
+            for (int ch = 0; ch < chains; ++ch) M = fmaxf(M, __ldcg(&ml[part(c, ch)]).x);
+          if (M == -INFINITY) M = 0.f;
+          float L = 0.f;
+          float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int c = it.first; c <= it.last; ++c)
+            for (int ch = 0; ch < chains; ++ch) {
+              const size_t at = part(c, ch);
+              const float2 v = __ldcg(&ml[at]);
+              if (v.y == 0.f) continue;
+              const float e = exp2f(v.x - M);
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(p.ws + at * D) + q4);
+              L += e * v.y;
+              O.x += e * x.x;
+              O.y += e * x.y;
+              O.z += e * x.z;
+              O.w += e * x.w;
+            }
+          const float inv = L == 0.f ? 0.f : 1.f / L;
+          const int orow = it.r0 + rr, token = orow / p.G, g = orow - token * p.G;
+          uint16_t* out = p.out + ((int64_t)(it.s.row0 + token) * p.H + (int64_t)it.hk * p.G + g) * D + d_of(4 * q4);
+          *reinterpret_cast<uint32_t*>(out) = pack_act(O.x * inv, O.z * inv, ACT);
+          *reinterpret_cast<uint32_t*>(out + 16) = pack_act(O.y * inv, O.w * inv, ACT);
+        }
+      }
+      chains_sync();  // the records and ctl.last may be written again
+    }
+  } else if (warp < 12) {
+    // ---- decode ----
+    const int row = threadIdx.x - 8 * 32;
+    Ring raw, kv;
+    uint32_t tile = 0;
+    while (walk.next(p, it)) {
+      int lo, hi, x;
+      seen(p, it.s, it.r0 / p.G, lo, x);
+      seen(p, it.s, (it.r0 + it.rows - 1) / p.G, x, hi);
+      for (int j = 0; j < it.tiles; ++j, ++tile) {
+        const int tok = (it.c0 + j) * kTok + row;
+        for (int which = 0; which < 2; ++which) {
+          wait.warp(&ctl.raw_full[raw.stage], raw.phase);
+          wait.warp(which ? &ctl.v_empty[kv.stage] : &ctl.k_empty[kv.stage], kv.phase ^ 1u);
+          const uint8_t* src = smem + F::OFF_RAW + raw.stage * F::RAW;
+          // a row is there if its group of 16 was copied and it is a token
+          const int g0 = tok & ~15;
+          const bool real = tok < hi && g0 + 16 > lo && !(ctl.bad[tile % kFlags] >> (row >> 4) & 1u);
+          if (which == 0)
+            decode_row<V, D, ACT == 1>(src, smem + F::OFF_K + kv.stage * F::TILE, row, real);
+          else
+            decode_row<V, D, false>(src, smem + F::OFF_V + kv.stage * F::TILE, row, real);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_addr(&ctl.raw_empty[raw.stage]));
+            mbar_arrive(smem_addr(which ? &ctl.v_full[kv.stage] : &ctl.k_full[kv.stage]));
+          }
+          raw.next(F::RSTAGES);
+        }
+        kv.next(F::STAGES);
+      }
+    }
+  } else if (warp == 12) {
+    // ---- MMA issue ----
+    if (lane == 0) {
+      constexpr uint32_t id_s = instr_desc(ACT, kTok, 0), id_o = instr_desc(0, D, 1);
+      Ring kr, vr;
+      uint32_t n_q = 0, n_p[2] = {0, 0};
+      const uint64_t qd = smem_desc(smem_addr(smem + F::OFF_Q), 16), kd = smem_desc(smem_addr(smem + F::OFF_K), 16);
+      const uint64_t vd = smem_desc(smem_addr(smem + F::OFF_V), F::PANEL);
+      while (walk.next(p, it)) {
+        const int steps = it.wide ? 2 * it.tiles : it.tiles;
+        wait.one(&ctl.q_full, n_q++ & 1u);
+        tc_fence_after();
+        auto scores = [&](int s) {
+          const int t = s & 1;
+          if (!it.wide || t == 0) {
+            wait.one(&ctl.k_full[kr.stage], kr.phase);
+            tc_fence_after();
+          }
+          const uint64_t a = qd + (it.wide ? (uint64_t)(t * F::TILE >> 4) : 0), b = kd + (uint64_t)(kr.stage * F::TILE >> 4);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = (uint64_t)((k / 4) * (F::PANEL >> 4) + (k % 4) * 2);
+            mma_ss(tmem + 128u * t, a + off, b + off, id_s, k != 0);
+          }
+          mma_commit(smem_addr(&ctl.s_full[t]));
+          if (!it.wide || t == 1) {
+            mma_commit(smem_addr(&ctl.k_empty[kr.stage]));
+            kr.next(F::STAGES);
+          }
+          if (s == steps - 1) mma_commit(smem_addr(&ctl.q_empty));
+        };
+        scores(0);
+        if (steps > 1) scores(1);
+        for (int s = 0; s < steps; ++s) {
+          const int t = s & 1;
+          wait.one(&ctl.p_full[t], (t ? n_p[1]++ : n_p[0]++) & 1u);
+          if (!it.wide || t == 0) wait.one(&ctl.v_full[vr.stage], vr.phase);
+          tc_fence_after();
+          const uint64_t b = vd + (uint64_t)(vr.stage * F::TILE >> 4);
+#pragma unroll
+          for (int k = 0; k < kTok / 16; ++k)
+            mma_ts(tmem + 256u + (uint32_t)D * t, tmem + 128u * t + 8u * k, b + (uint64_t)(k * 2048 >> 4), id_o, s > 1 || k != 0);
+          if (!it.wide || t == 1) {
+            mma_commit(smem_addr(&ctl.v_empty[vr.stage]));
+            vr.next(F::STAGES);
+          }
+          if (s + 2 >= steps) mma_commit(smem_addr(&ctl.o_full[t]));
+          if (s + 2 < steps) scores(s + 2);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 13) {
+    // ---- raw rows ----
+    Ring raw;
+    uint32_t tile = 0, issued = 0;
+    const int group = lane & 7;
+    while (walk.next(p, it)) {
+      int lo, hi, x;
+      seen(p, it.s, it.r0 / p.G, lo, x);
+      seen(p, it.s, (it.r0 + it.rows - 1) / p.G, x, hi);
+      for (int j = 0; j < it.tiles; ++j, ++tile) {
+        const int t0 = (it.c0 + j) * kTok + 16 * group;
+        const bool want = lane < 8 && t0 < hi && t0 + 16 > lo;
+        int page = 0;
+        if (want) page = p.c.table[(int64_t)it.b * p.c.ldt + t0 / p.c.page_size];
+        const bool have = want && page >= 0 && page < p.c.num_pages;
+        const uint32_t bad = __ballot_sync(0xffffffffu, want && !have);
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, have)) * 16u * F::RB;
+        const int64_t at = (((int64_t)page * p.c.Hkv + it.hk) * p.c.page_size + t0 % p.c.page_size) * F::RB;
+        for (int which = 0; which < 2; ++which) {
+          wait.warp(&ctl.raw_empty[raw.stage], raw.phase ^ 1u);
+          if (!wait.ok) break;
+          const uint32_t bar = smem_addr(&ctl.raw_full[raw.stage]);
+          if (lane == 0) {
+            if (which == 0) {
+              ctl.bad[tile % kFlags] = bad;
+              if (bad) atomicOr(p.c.err, kErrBadPage);
+            }
+            mbar_arrive_expect_tx(bar, bytes);
+          }
+          __syncwarp();
+          if (have)
+            bulk_g2s(smem_addr(smem + F::OFF_RAW + raw.stage * F::RAW + group * 16 * F::RB), (which ? p.c.V : p.c.K) + at, 16 * F::RB,
+                     bar);
+          raw.next(F::RSTAGES);
+          ++issued;
+        }
+        if (!wait.ok) break;
+      }
+      if (!wait.ok) break;
+      if (lane == 0 && it.s.len > it.s.lim) atomicOr(p.c.err, kErrBadPage);
+    }
+    if (!wait.ok) {  // copies in flight land before the block ends
+      for (uint32_t i = issued > (uint32_t)F::RSTAGES ? issued - F::RSTAGES : 0; i < issued; ++i)
+        (void)mbar_wait_bounded(smem_addr(&ctl.raw_full[i % F::RSTAGES]), (i / F::RSTAGES) & 1u);
+    }
+  } else {
+    // ---- Q rows ----
+    const int id = threadIdx.x - 14 * 32;
+    uint32_t n_q = 0;
+    while (walk.next(p, it)) {
+      wait.warp(&ctl.q_empty, (n_q++ & 1u) ^ 1u);
+      // 16 positions of a row: values 8 i .. 8 i + 7 and 16 further of a block, interleaved
+      constexpr int PER = D / 16;
+#pragma unroll 4
+      for (int i = id; i < it.rows * PER; i += 64) {
+        const int rr = i / PER, u = i % PER, kb = u >> 1, half = u & 1;
+        const int row = it.r0 + rr, token = row / p.G, g = row - token * p.G;
+        const uint16_t* src = p.q + (int64_t)(it.s.row0 + token) * p.ldq + ((int64_t)it.hk * p.G + g) * D + kb * 32 + half * 8;
+        const uint4 x = *reinterpret_cast<const uint4*>(src), y = *reinterpret_cast<const uint4*>(src + 16);
+        uint8_t* dst = smem + F::OFF_Q + rr / kHalf * F::TILE + kb / 2 * F::PANEL + rr % kHalf * 128;
+        const int chunk = (kb & 1) * 4 + half * 2;
+        *reinterpret_cast<uint4*>(dst + ((chunk ^ (rr & 7)) << 4)) =
+            make_uint4(__byte_perm(x.x, y.x, 0x5410), __byte_perm(x.x, y.x, 0x7632), __byte_perm(x.y, y.y, 0x5410), __byte_perm(x.y, y.y, 0x7632));
+        *reinterpret_cast<uint4*>(dst + (((chunk + 1) ^ (rr & 7)) << 4)) =
+            make_uint4(__byte_perm(x.z, y.z, 0x5410), __byte_perm(x.z, y.z, 0x7632), __byte_perm(x.w, y.w, 0x5410), __byte_perm(x.w, y.w, 0x7632));
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&ctl.q_full));
+    }
+  }
+  if (!wait.ok && lane == 0) atomicOr(p.c.err, kErrWaitTimeout);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
+using Fn = void (*)(Params);
+template <int V, int D>
+Fn kernel_for(int act) {
+  return act == 0 ? paged_attention_kernel<V, D, 0> : paged_attention_kernel<V, D, 1>;
+}
+Fn kernel_for(int variant, int D, int act) {
+  if (variant == 0) return D == 64 ? kernel_for<0, 64>(act) : kernel_for<0, 128>(act);
+  return D == 64 ? kernel_for<1, 64>(act) : kernel_for<1, 128>(act);
+}
+int smem_for(int variant, int D) {
+  if (variant == 0) return D == 64 ? Plan<0, 64>::SMEM : Plan<0, 128>::SMEM;
+  return D == 64 ? Plan<1, 64>::SMEM : Plan<1, 128>::SMEM;
 }
 
 }  // namespace
 
+size_t paged_attn_ws_floats(int sms) { return (size_t)sms * kSlots * 2 * kHalf * (128 + 2); }
+
+cudaError_t paged_attn_prepare() {
+  for (int v = 0; v < 2; ++v)
+    for (int D : {64, 128})
+      for (int act = 0; act < 2; ++act) {
+        cudaError_t e = cudaFuncSetAttribute((const void*)kernel_for(v, D, act), cudaFuncAttributeMaxDynamicSharedMemorySize, smem_for(v, D));
+        if (e != cudaSuccess) return e;
+      }
+  return cudaSuccess;
+}
+
 cudaError_t launch_paged_attention(int variant, int act, const PagedAttnArgs& a, int sms, cudaStream_t s) {
-  Params p{a};
-  using Fn = void (*)(Params, int);
-  const Fn fn = variant == 0 ? (a.cache.D == 64 ? (Fn)attend_kernel<0, 64> : (Fn)attend_kernel<0, 128>)
-                             : (a.cache.D == 64 ? (Fn)attend_kernel<1, 64> : (Fn)attend_kernel<1, 128>);
-  fn<<<(unsigned)(a.M * a.H), kWarps * 32, 0, s>>>(p, act);
-  return cudaGetLastError();
+  Params p{};
+  p.q = a.q;
+  p.out = a.out;
+  p.ldq = a.ldq;
+  p.M = (int)a.M;
+  p.H = a.H;
+  p.G = a.H / a.cache.Hkv;
+  p.causal = a.causal;
+  p.window = a.window;
+  p.scale_log2 = a.scale * kLog2e;
+  p.c = a.cache;
+  p.ws = a.ws;
+  p.cnt = a.cnt;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)sms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_for(variant, a.cache.D);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel_for(variant, a.cache.D, act), p);
 }
 
 }  // namespace rocmfp4
