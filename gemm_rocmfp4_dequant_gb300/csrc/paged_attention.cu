@@ -36,12 +36,13 @@
 // several CTAs leaves unnormalised parts in the workspace; the CTA that arrives
 // last adds them in order.  Nothing waits for another CTA.
 //
-// Warps (512 threads):
+// Warps (640 threads), registers moved from the others to the softmax:
 //   0-3, 4-7   softmax and output of chain 0 and 1
-//   8-11       decode: one token row a thread
-//   12         tensor-memory allocation, MMA issue (one thread)
-//   13         bulk copies of raw rows, 16 tokens each (a page is a multiple of 16)
-//   14-15      Q rows into shared memory
+//   8-11       decode of K, one token row a thread;  12-15  of V
+//   16         tensor-memory allocation, MMA issue (one thread)
+//   17         the stretch's items, bulk copies of raw rows, 16 tokens each (a
+//              page is a multiple of 16)
+//   18-19      Q rows into shared memory
 // Every wait is bounded: a warp that gives up records kErrWaitTimeout and
 // goes on without waiting, so that all meet at the end.
 #include <cstring>
@@ -52,11 +53,12 @@
 namespace rocmfp4 {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kTok = 128;     // tokens per tile
 constexpr int kHalf = 128;    // rows per chain
 constexpr int kMinShare = 4;  // least work of a CTA: narrow token tiles
-constexpr int kFlags = 16;
+constexpr int kTiles = 16;    // token tiles described at a time
+constexpr int kItems = 4;     // row tiles described at a time
 constexpr int kSlots = 3;     // parts a CTA may hold: of its first, its last, and its current row tile
 constexpr float kGrow = 8.f;  // log2 of how far a maximum may lead its reference
 constexpr float kLift = 7.f;  // log2 of P's factor
@@ -84,29 +86,54 @@ struct Plan {
   static constexpr int OFF_K = OFF_Q + 2 * TILE;
   static constexpr int OFF_V = OFF_K + STAGES * TILE;
   static constexpr int OFF_RAW = OFF_V + STAGES * TILE;
-  static constexpr int ROOM = 227 * 1024 - 1024 - 1024;  // less alignment and barriers
+  static constexpr int ROOM = 227 * 1024 - 1024 - 1536;  // less alignment and barriers
   static constexpr int FIT = (ROOM - OFF_RAW) / RAW;
   static constexpr int RSTAGES = FIT > 8 ? 8 : FIT;
   static constexpr int OFF_BAR = (OFF_RAW + RSTAGES * RAW + 15) / 16 * 16;
-  static constexpr int SMEM = OFF_BAR + 1024 + 1024;
+  static constexpr int SMEM = OFF_BAR + 1536 + 1024;
   static_assert(RSTAGES >= 2 && SMEM <= 227 * 1024, "shared memory");
   static_assert(RAW % 16 == 0, "bulk copies");
 };
 
+struct Seq {
+  int row0, n;  // rows of the call
+  int len;      // tokens
+  int lim;      // tokens that the table has room for
+};
+
+// A row tile's share of this CTA.
+struct Item {
+  int b, hk, r0, rows, wide;  // rows 0: no more items
+  int c0, tiles;              // this CTA's token tiles
+  Seq s;
+  int first, last;  // CTAs that share the row tile
+  int slot;         // of this CTA's part
+  int tile;         // number of the first token tile among this CTA's
+};
+
+// A token tile: rows from .. to - 1 of it were copied, but for `bad` groups of 16.
+struct Tile {
+  int from, to;
+  uint32_t bad;
+  int stop;  // no more tiles
+};
+
 struct Control {  // at OFF_BAR
-  uint64_t raw_full[8], raw_empty[8];
+  uint64_t raw_full[2][8], raw_empty[8];  // full: of K's copies, of V's
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t q_full, q_empty;
+  uint64_t q_full, q_empty, drained;
+  uint64_t item_full[kItems], item_empty[kItems];
   long long start, end, total;  // of this CTA's stretch; of all work
   long long base;               // where the first row tile begins
   long long scan[kThreads / 32];
   int b, hk, k, ctas;
   int last;
   uint32_t tmem;
-  uint32_t bad[kFlags];  // per token tile: 16-token groups whose page lies outside the cache
+  Item items[kItems];
+  Tile tiles[kTiles];
 };
-static_assert(sizeof(Control) <= 1024, "control block");
+static_assert(sizeof(Control) <= 1536, "control block");
 
 // ---- tensor-core instructions -------------------------------------------------
 RF4_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -189,6 +216,18 @@ RF4_DEV uint32_t pack_act(float lo, float hi, int act) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Registers between warpgroups: the block was launched with 640 x 96; two
+// warpgroups take 144 a thread, three are left with 64.
+constexpr int kSoftmaxRegs = 144, kOtherRegs = 64;
+static_assert(256 * kSoftmaxRegs + 384 * kOtherRegs <= kThreads * 96, "register split");
+template <int N>
+RF4_DEV void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+RF4_DEV void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 RF4_DEV void chains_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // Waits that go on without waiting once one has given up.
@@ -202,6 +241,17 @@ struct Waits {
   }
 };
 
+// The raw ring holds K's and V's tiles in turn.  K's entries are waited for by
+// one set of warps and V's by another, so each kind has barriers of its own: a
+// set that shared them with the other's entries could take an earlier phase's
+// parity for the one it waits for.
+template <int STAGES>
+struct RawRing {
+  static constexpr uint32_t kUses = STAGES % 2 ? STAGES : STAGES / 2;  // entries of a kind until a stage comes again
+  static RF4_DEV uint32_t stage(uint32_t tile, uint32_t which) { return (2 * tile + which) % STAGES; }
+  static RF4_DEV uint32_t phase(uint32_t tile) { return tile / kUses & 1u; }
+};
+
 struct Ring {
   uint32_t stage = 0, phase = 0;
   RF4_DEV void next(uint32_t n) {
@@ -213,12 +263,6 @@ struct Ring {
 };
 
 // ---- work -----------------------------------------------------------------------
-struct Seq {
-  int row0, n;     // rows of the call
-  int len;         // tokens
-  int lim;         // tokens that the table has room for
-};
-
 RF4_DEV Seq sequence(const Params& p, int b) {
   Seq s;
   const int r0 = min(max(p.c.cu[b], 0), p.M), r1 = min(max(p.c.cu[b + 1], 0), p.M);
@@ -258,14 +302,6 @@ RF4_DEV RowTile row_tile(const Params& p, const Seq& s, int k) {
   t.tiles = max(1, (hi + kTok - 1) / kTok - t.c0);
   return t;
 }
-
-struct Item {
-  int b, hk, r0, rows, wide;
-  int c0, tiles;       // this CTA's token tiles
-  Seq s;
-  int first, last;     // CTAs that share the row tile
-  int slot;            // of this CTA's part
-};
 
 struct Walk {
   int b, hk, k, ctas;
@@ -365,33 +401,53 @@ RF4_DEV bool find_work(const Params& p, Control& ctl) {
   const int ctas = (int)(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
   if (total == 0 || (int)blockIdx.x >= ctas) return false;
   const long long start = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
-  if (start >= before && start < before + mine) {
+  const uint32_t hit = __ballot_sync(0xffffffffu, start >= before && start < before + mine);
+  if (hit) {  // one warp: the sequence of one of its lanes, then the row tile, 32 at a time
     int b = b0;
     long long base = before, w = mine;
-    for (; b < b1; ++b) {
-      w = by_warp ? mine : work_of(p, b, 0, 1);
-      if (start < base + w) break;
-      base += w;
-    }
+    if (!by_warp)
+      for (; b < b1; ++b) {
+        w = work_of(p, b, 0, 1);
+        if (start < base + w) break;
+        base += w;
+      }
+    const int from = __ffs(hit) - 1;
+    b = __shfl_sync(0xffffffffu, b, from);
+    base = __shfl_sync(0xffffffffu, base, from);
+    w = __shfl_sync(0xffffffffu, w, from);
     const long long head = w / p.c.Hkv;
     const int hk = (int)((start - base) / head);
     base += hk * head;
     const Seq s = sequence(p, b);
-    int k = 0;
-    for (;; ++k) {
-      const RowTile t = row_tile(p, s, k);
-      const long long all = (long long)t.tiles * t.weight;
-      if (start < base + all) break;
-      base += all;
+    for (int k0 = 0;; k0 += 32) {
+      const int k = k0 + lane;
+      long long all = 0;
+      if ((long long)k * 2 * kHalf < (long long)s.n * p.G) {
+        const RowTile t = row_tile(p, s, k);
+        all = (long long)t.tiles * t.weight;
+      }
+      long long upto = all;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      const uint32_t in = __ballot_sync(0xffffffffu, start < base + upto);
+      if (in) {
+        if (lane == __ffs(in) - 1) {
+          ctl.b = b;
+          ctl.hk = hk;
+          ctl.k = k;
+          ctl.base = base + upto - all;
+          ctl.start = start;
+          ctl.end = end;
+          ctl.total = total;
+          ctl.ctas = ctas;
+        }
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, upto, 31);
     }
-    ctl.b = b;
-    ctl.hk = hk;
-    ctl.k = k;
-    ctl.base = base;
-    ctl.start = start;
-    ctl.end = end;
-    ctl.total = total;
-    ctl.ctas = ctas;
   }
   __syncthreads();
   return true;
@@ -484,22 +540,75 @@ RF4_DEV float masked(float x, int col, int a, uint32_t width, uint32_t bad) {
   return x;
 }
 
+RF4_DEV uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+RF4_DEV void un2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+RF4_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+RF4_DEV uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+RF4_DEV float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+template <bool MASK>
+RF4_DEV float top_of(const float (&x)[32], int c, int a, uint32_t width, uint32_t bad) {
+  float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    t0 = max3(t0, masked<MASK>(x[i], c + i, a, width, bad), masked<MASK>(x[i + 1], c + i + 1, a, width, bad));
+    t1 = max3(t1, masked<MASK>(x[i + 2], c + i + 2, a, width, bad), masked<MASK>(x[i + 3], c + i + 3, a, width, bad));
+  }
+  return fmaxf(t0, t1);
+}
+
+// 32 columns of S to P at tensor-memory address `to`; their sum is added to `sum`.
+template <bool MASK>
+RF4_DEV void weights(const float (&x)[32], uint32_t to, uint64_t scale2, uint64_t shift2, uint64_t (&sum)[2], int c, int a,
+                     uint32_t width, uint32_t bad) {
+  uint32_t h[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint64_t y = fma2(f2(masked<MASK>(x[2 * i], c + 2 * i, a, width, bad), masked<MASK>(x[2 * i + 1], c + 2 * i + 1, a, width, bad)),
+                            scale2, shift2);
+    float y0, y1;
+    un2(y, y0, y1);
+    y0 = ex2(y0);
+    y1 = ex2(y1);
+    sum[i & 1] = add2(sum[i & 1], f2(y0, y1));
+    h[i] = pack_h2(y0, y1);
+  }
+  tmem_st16(to, h);
+}
+
 // S of this lane's row in tensor memory at `s` -> P at the same columns, O
 // (at `o`, D columns) scaled where the reference moves.  Tokens a .. a + width
-// - 1 of the tile are seen, but for `bad` groups of 16.
+// - 1 of the tile are seen, but for `bad` groups of 16.  S is read twice, 32
+// columns at a time, the next ones on their way while these are dealt with;
+// columns 0-31 are the last of the first pass and stay for the second.
 template <int D, bool MASK>
 RF4_DEV void softmax_tile(uint32_t s, uint32_t o, Row& st, float scale_log2, bool first, bool used, int a, uint32_t width,
                           uint32_t bad) {
-  float top = -INFINITY;
-#pragma unroll
-  for (int c = 0; c < kTok; c += 32) {
-    float x[32];
-    tmem_ld32(s + c, x);
-    tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) top = fmaxf(top, masked<MASK>(x[i], c + i, a, width, bad));
-  }
-  top *= scale_log2;
+  float x[32], y[32];
+  tmem_ld32(s + 96, x);
+  tmem_wait_ld();
+  tmem_ld32(s + 64, y);
+  float top = top_of<MASK>(x, 96, a, width, bad);
+  tmem_wait_ld();
+  tmem_ld32(s + 32, x);
+  top = fmaxf(top, top_of<MASK>(y, 64, a, width, bad));
+  tmem_wait_ld();
+  tmem_ld32(s, y);
+  top = fmaxf(top, top_of<MASK>(x, 32, a, width, bad));
+  tmem_wait_ld();
+  top = fmaxf(top, top_of<MASK>(y, 0, a, width, bad)) * scale_log2;
   if (first) {
     st.m = top;
   } else {
@@ -510,7 +619,6 @@ RF4_DEV void softmax_tile(uint32_t s, uint32_t o, Row& st, float scale_log2, boo
       st.l *= alpha;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
-        float x[32];
         tmem_ld32(o + c, x);
         tmem_wait_ld();
 #pragma unroll
@@ -520,29 +628,39 @@ RF4_DEV void softmax_tile(uint32_t s, uint32_t o, Row& st, float scale_log2, boo
     }
   }
   const float shift = kLift - (st.m == -INFINITY ? 0.f : st.m);
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int c = 0; c < kTok; c += 32) {
-    float x[32];
-    tmem_ld32(s + c, x);
-    tmem_wait_ld();
-    uint32_t h[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float p0 = ex2(fmaf(masked<MASK>(x[2 * i], c + 2 * i, a, width, bad), scale_log2, shift));
-      const float p1 = ex2(fmaf(masked<MASK>(x[2 * i + 1], c + 2 * i + 1, a, width, bad), scale_log2, shift));
-      sum[i & 1] += p0;
-      sum[2 + (i & 1)] += p1;
-      h[i] = pack_h2(p0, p1);
-    }
-    tmem_st16(s + c / 2, h);
-  }
-  st.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  const uint64_t scale2 = f2(scale_log2, scale_log2), shift2 = f2(shift, shift);
+  uint64_t sum[2] = {0, 0};
+  tmem_ld32(s + 32, x);
+  weights<MASK>(y, s, scale2, shift2, sum, 0, a, width, bad);
+  tmem_wait_ld();
+  tmem_ld32(s + 64, y);
+  weights<MASK>(x, s + 16, scale2, shift2, sum, 32, a, width, bad);
+  tmem_wait_ld();
+  tmem_ld32(s + 96, x);
+  weights<MASK>(y, s + 32, scale2, shift2, sum, 64, a, width, bad);
+  tmem_wait_ld();
+  weights<MASK>(x, s + 48, scale2, shift2, sum, 96, a, width, bad);
+  float s0, s1;
+  un2(add2(sum[0], sum[1]), s0, s1);
+  st.l += s0 + s1;
   tmem_wait_st();
 }
 
 // Position p of O's columns is value d_of(p) of the head.
 RF4_DEV int d_of(int p) { return (p & ~31) + ((p & 31) >> 1) + ((p & 1) << 4); }
+
+// Items in the order in which the scheduling warp wrote them; all lanes of a warp.
+struct Items {
+  uint32_t n = 0;
+  RF4_DEV bool next(Control& ctl, Waits& wait, Item& it) {
+    wait.warp(&ctl.item_full[n % kItems], (n / kItems) & 1u);
+    if (!wait.ok) return false;
+    it = ctl.items[n % kItems];
+    return it.rows > 0;
+  }
+  // one lane, after the warp's last use of the item
+  RF4_DEV void done(Control& ctl) { mbar_arrive(smem_addr(&ctl.item_empty[n++ % kItems])); }
+};
 
 template <int V, int D, int ACT>
 __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __grid_constant__ Params p) {
@@ -554,7 +672,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < F::RSTAGES; ++i) {
-      mbar_init(smem_addr(&ctl.raw_full[i]), 1);
+      mbar_init(smem_addr(&ctl.raw_full[0][i]), 1);
+      mbar_init(smem_addr(&ctl.raw_full[1][i]), 1);
       mbar_init(smem_addr(&ctl.raw_empty[i]), 4);
     }
     for (int i = 0; i < 2; ++i) {
@@ -566,13 +685,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
       mbar_init(smem_addr(&ctl.p_full[i]), 4);
       mbar_init(smem_addr(&ctl.o_full[i]), 1);
     }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(smem_addr(&ctl.item_full[i]), 1);
+      mbar_init(smem_addr(&ctl.item_empty[i]), 8 + 1 + 2);
+    }
     mbar_init(smem_addr(&ctl.q_full), 2);
     mbar_init(smem_addr(&ctl.q_empty), 1);
+    mbar_init(smem_addr(&ctl.drained), 1);
     fence_mbar_init();
   }
   grid_dependency_wait();  // lengths, tables and everything else may be the preceding kernel's output
   if (!find_work(p, ctl)) return;
-  if (warp == 12) {
+  if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&ctl.tmem)), "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -582,16 +706,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   const uint32_t tmem = ctl.tmem;
   // columns: S (and P) of chain t at 128 t, O at 256 + D t
   Waits wait;
-  Walk walk(p, ctl);
-  Item it;
 
   if (warp < 8) {
     // ---- softmax and output ----
+    take_registers<kSoftmaxRegs>();
     const int t = warp >> 2, r = threadIdx.x & (kHalf - 1);
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + 128u * t, o_at = tmem + lanes + 256u + (uint32_t)D * t;
-    uint32_t n_s = 0, n_o = 0, tile = 0;  // uses of s_full and o_full; token tiles of this CTA so far
-    while (walk.next(p, it)) {
+    uint32_t n_s = 0, n_o = 0;  // uses of s_full and o_full
+    Items items;
+    Item it;
+    while (items.next(ctl, wait, it)) {
+      __syncwarp();
+      if (lane == 0) items.done(ctl); else ++items.n;
       const int row = it.r0 + (it.wide ? t * kHalf : 0) + r;
       const bool used = row < it.r0 + it.rows;
       int lo = 0, hi = 0;
@@ -603,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         const int a = max(lo - t0, 0), e = min(max(hi - t0, 0), kTok);
         wait.warp(&ctl.s_full[t], n_s++ & 1u);
         tc_fence_after();
-        const uint32_t bad = ctl.bad[(tile + j) % kFlags];
+        const uint32_t bad = ctl.tiles[(it.tile + j) % kTiles].bad;
         if (__any_sync(0xffffffffu, used && (a > 0 || e < kTok)) || bad)
           softmax_tile<D, true>(s_at, o_at, st, p.scale_log2, first, used, a, (uint32_t)max(e - a, 0), bad);
         else
@@ -613,7 +740,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&ctl.p_full[t]));
       }
-      tile += it.tiles;
       if (!first) {
         wait.warp(&ctl.o_full[t], n_o++ & 1u);
         tc_fence_after();
@@ -644,10 +770,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         continue;
       }
       // a part: into the workspace
-      const size_t records = (size_t)gridDim.x * kSlots * 2;
-      float2* ml = reinterpret_cast<float2*>(p.ws + records * kHalf * D);
-      auto record = [&](int cta, int slot, int chain) { return ((size_t)cta * kSlots + slot) * 2 + chain; };
-      const size_t mine = record(blockIdx.x, it.slot, t) * kHalf + r;
+      float2* ml = reinterpret_cast<float2*>(p.ws + (size_t)gridDim.x * kSlots * 2 * kHalf * D);
+      const size_t mine = (((size_t)blockIdx.x * kSlots + it.slot) * 2 + t) * kHalf + r;
       if (used) __stcg(&ml[mine], make_float2(st.m, st.l));
       if (!first) {
 #pragma unroll 1
@@ -677,31 +801,35 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         if (merge) __threadfence();
       }
       if (merge) {
+        const int chains = it.wide ? 1 : 2, parts = (it.last - it.first + 1) * chains;
         for (int i = threadIdx.x; i < it.rows * (D / 4); i += 256) {
           const int rr = i / (D / 4), q4 = i - rr * (D / 4);
-          const int chain = it.wide ? rr / kHalf : 0, chains = it.wide ? 1 : 2, rw = it.wide ? rr % kHalf : rr;
-          auto part = [&](int c, int ch) {
-            return record(c, it.first == it.last ? 2 : c == it.first ? 1 : 0, chain + ch) * kHalf + rw;
+          const int chain = it.wide ? rr / kHalf : 0, rw = it.wide ? rr % kHalf : rr;
+          // part n: of CTA first + n / chains; the first CTA's in its slot 1, the others' in slot 0, a whole row tile's in slot 2
+          auto part = [&](int n) {
+            const int c = it.wide ? n : n >> 1, ch = it.wide ? chain : n & 1;
+            const int slot = it.first == it.last ? 2 : c == 0 ? 1 : 0;
+            return (((size_t)(it.first + c) * kSlots + slot) * 2 + ch) * kHalf + rw;
           };
           float M = -INFINITY;
-          for (int c = it.first; c <= it.last; ++c)
-            for (int ch = 0; ch < chains; ++ch) M = fmaxf(M, __ldcg(&ml[part(c, ch)]).x);
+#pragma unroll 8
+          for (int n = 0; n < parts; ++n) M = fmaxf(M, __ldcg(&ml[part(n)]).x);
           if (M == -INFINITY) M = 0.f;
           float L = 0.f;
           float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int c = it.first; c <= it.last; ++c)
-            for (int ch = 0; ch < chains; ++ch) {
-              const size_t at = part(c, ch);
-              const float2 v = __ldcg(&ml[at]);
-              if (v.y == 0.f) continue;
-              const float e = exp2f(v.x - M);
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(p.ws + at * D) + q4);
-              L += e * v.y;
-              O.x += e * x.x;
-              O.y += e * x.y;
-              O.z += e * x.z;
-              O.w += e * x.w;
-            }
+#pragma unroll 4
+          for (int n = 0; n < parts; ++n) {
+            const size_t at = part(n);
+            const float2 v = __ldcg(&ml[at]);
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(p.ws + at * D) + q4);
+            if (v.y == 0.f) continue;  // nothing seen: O may never have been written
+            const float e = exp2f(v.x - M);
+            L += e * v.y;
+            O.x += e * x.x;
+            O.y += e * x.y;
+            O.z += e * x.z;
+            O.w += e * x.w;
+          }
           const float inv = L == 0.f ? 0.f : 1.f / L;
           const int orow = it.r0 + rr, token = orow / p.G, g = orow - token * p.G;
           uint16_t* out = p.out + ((int64_t)(it.s.row0 + token) * p.H + (int64_t)it.hk * p.G + g) * D + d_of(4 * q4);
@@ -711,167 +839,217 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
       }
       chains_sync();  // the records and ctl.last may be written again
     }
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     // ---- decode ----
-    const int row = threadIdx.x - 8 * 32;
-    Ring raw, kv;
-    uint32_t tile = 0;
-    while (walk.next(p, it)) {
-      int lo, hi, x;
-      seen(p, it.s, it.r0 / p.G, lo, x);
-      seen(p, it.s, (it.r0 + it.rows - 1) / p.G, x, hi);
-      for (int j = 0; j < it.tiles; ++j, ++tile) {
-        const int tok = (it.c0 + j) * kTok + row;
-        for (int which = 0; which < 2; ++which) {
-          wait.warp(&ctl.raw_full[raw.stage], raw.phase);
-          wait.warp(which ? &ctl.v_empty[kv.stage] : &ctl.k_empty[kv.stage], kv.phase ^ 1u);
-          const uint8_t* src = smem + F::OFF_RAW + raw.stage * F::RAW;
-          // a row is there if its group of 16 was copied and it is a token
-          const int g0 = tok & ~15;
-          const bool real = tok < hi && g0 + 16 > lo && !(ctl.bad[tile % kFlags] >> (row >> 4) & 1u);
-          if (which == 0)
-            decode_row<V, D, ACT == 1>(src, smem + F::OFF_K + kv.stage * F::TILE, row, real);
-          else
-            decode_row<V, D, false>(src, smem + F::OFF_V + kv.stage * F::TILE, row, real);
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(smem_addr(&ctl.raw_empty[raw.stage]));
-            mbar_arrive(smem_addr(which ? &ctl.v_full[kv.stage] : &ctl.k_full[kv.stage]));
-          }
-          raw.next(F::RSTAGES);
-        }
-        kv.next(F::STAGES);
-      }
-    }
-  } else if (warp == 12) {
-    // ---- MMA issue ----
-    if (lane == 0) {
-      constexpr uint32_t id_s = instr_desc(ACT, kTok, 0), id_o = instr_desc(0, D, 1);
-      Ring kr, vr;
-      uint32_t n_q = 0, n_p[2] = {0, 0};
-      const uint64_t qd = smem_desc(smem_addr(smem + F::OFF_Q), 16), kd = smem_desc(smem_addr(smem + F::OFF_K), 16);
-      const uint64_t vd = smem_desc(smem_addr(smem + F::OFF_V), F::PANEL);
-      while (walk.next(p, it)) {
-        const int steps = it.wide ? 2 * it.tiles : it.tiles;
-        wait.one(&ctl.q_full, n_q++ & 1u);
-        tc_fence_after();
-        auto scores = [&](int s) {
-          const int t = s & 1;
-          if (!it.wide || t == 0) {
-            wait.one(&ctl.k_full[kr.stage], kr.phase);
-            tc_fence_after();
-          }
-          const uint64_t a = qd + (it.wide ? (uint64_t)(t * F::TILE >> 4) : 0), b = kd + (uint64_t)(kr.stage * F::TILE >> 4);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t off = (uint64_t)((k / 4) * (F::PANEL >> 4) + (k % 4) * 2);
-            mma_ss(tmem + 128u * t, a + off, b + off, id_s, k != 0);
-          }
-          mma_commit(smem_addr(&ctl.s_full[t]));
-          if (!it.wide || t == 1) {
-            mma_commit(smem_addr(&ctl.k_empty[kr.stage]));
-            kr.next(F::STAGES);
-          }
-          if (s == steps - 1) mma_commit(smem_addr(&ctl.q_empty));
-        };
-        scores(0);
-        if (steps > 1) scores(1);
-        for (int s = 0; s < steps; ++s) {
-          const int t = s & 1;
-          wait.one(&ctl.p_full[t], (t ? n_p[1]++ : n_p[0]++) & 1u);
-          if (!it.wide || t == 0) wait.one(&ctl.v_full[vr.stage], vr.phase);
-          tc_fence_after();
-          const uint64_t b = vd + (uint64_t)(vr.stage * F::TILE >> 4);
-#pragma unroll
-          for (int k = 0; k < kTok / 16; ++k)
-            mma_ts(tmem + 256u + (uint32_t)D * t, tmem + 128u * t + 8u * k, b + (uint64_t)(k * 2048 >> 4), id_o, s > 1 || k != 0);
-          if (!it.wide || t == 1) {
-            mma_commit(smem_addr(&ctl.v_empty[vr.stage]));
-            vr.next(F::STAGES);
-          }
-          if (s + 2 >= steps) mma_commit(smem_addr(&ctl.o_full[t]));
-          if (s + 2 < steps) scores(s + 2);
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp == 13) {
-    // ---- raw rows ----
-    Ring raw;
-    uint32_t tile = 0, issued = 0;
-    const int group = lane & 7;
-    while (walk.next(p, it)) {
-      int lo, hi, x;
-      seen(p, it.s, it.r0 / p.G, lo, x);
-      seen(p, it.s, (it.r0 + it.rows - 1) / p.G, x, hi);
-      for (int j = 0; j < it.tiles; ++j, ++tile) {
-        const int t0 = (it.c0 + j) * kTok + 16 * group;
-        const bool want = lane < 8 && t0 < hi && t0 + 16 > lo;
-        int page = 0;
-        if (want) page = p.c.table[(int64_t)it.b * p.c.ldt + t0 / p.c.page_size];
-        const bool have = want && page >= 0 && page < p.c.num_pages;
-        const uint32_t bad = __ballot_sync(0xffffffffu, want && !have);
-        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, have)) * 16u * F::RB;
-        const int64_t at = (((int64_t)page * p.c.Hkv + it.hk) * p.c.page_size + t0 % p.c.page_size) * F::RB;
-        for (int which = 0; which < 2; ++which) {
-          wait.warp(&ctl.raw_empty[raw.stage], raw.phase ^ 1u);
-          if (!wait.ok) break;
-          const uint32_t bar = smem_addr(&ctl.raw_full[raw.stage]);
-          if (lane == 0) {
-            if (which == 0) {
-              ctl.bad[tile % kFlags] = bad;
-              if (bad) atomicOr(p.c.err, kErrBadPage);
-            }
-            mbar_arrive_expect_tx(bar, bytes);
-          }
-          __syncwarp();
-          if (have)
-            bulk_g2s(smem_addr(smem + F::OFF_RAW + raw.stage * F::RAW + group * 16 * F::RB), (which ? p.c.V : p.c.K) + at, 16 * F::RB,
-                     bar);
-          raw.next(F::RSTAGES);
-          ++issued;
-        }
-        if (!wait.ok) break;
-      }
+    give_registers<kOtherRegs>();
+    const int which = warp >> 2 & 1;  // 0: K, 1: V
+    const int row = threadIdx.x & (kTok - 1);
+    uint64_t* full = which ? ctl.v_full : ctl.k_full;
+    uint64_t* empty = which ? ctl.v_empty : ctl.k_empty;
+    uint8_t* tiles = smem + (which ? F::OFF_V : F::OFF_K);
+    using Raw = RawRing<F::RSTAGES>;
+    Ring kv;
+    for (uint32_t n = 0;; ++n) {
+      const uint32_t stage = Raw::stage(n, which);
+      wait.warp(&ctl.raw_full[which][stage], Raw::phase(n));
       if (!wait.ok) break;
-      if (lane == 0 && it.s.len > it.s.lim) atomicOr(p.c.err, kErrBadPage);
-    }
-    if (!wait.ok) {  // copies in flight land before the block ends
-      for (uint32_t i = issued > (uint32_t)F::RSTAGES ? issued - F::RSTAGES : 0; i < issued; ++i)
-        (void)mbar_wait_bounded(smem_addr(&ctl.raw_full[i % F::RSTAGES]), (i / F::RSTAGES) & 1u);
-    }
-  } else {
-    // ---- Q rows ----
-    const int id = threadIdx.x - 14 * 32;
-    uint32_t n_q = 0;
-    while (walk.next(p, it)) {
-      wait.warp(&ctl.q_empty, (n_q++ & 1u) ^ 1u);
-      // 16 positions of a row: values 8 i .. 8 i + 7 and 16 further of a block, interleaved
-      constexpr int PER = D / 16;
-#pragma unroll 4
-      for (int i = id; i < it.rows * PER; i += 64) {
-        const int rr = i / PER, u = i % PER, kb = u >> 1, half = u & 1;
-        const int row = it.r0 + rr, token = row / p.G, g = row - token * p.G;
-        const uint16_t* src = p.q + (int64_t)(it.s.row0 + token) * p.ldq + ((int64_t)it.hk * p.G + g) * D + kb * 32 + half * 8;
-        const uint4 x = *reinterpret_cast<const uint4*>(src), y = *reinterpret_cast<const uint4*>(src + 16);
-        uint8_t* dst = smem + F::OFF_Q + rr / kHalf * F::TILE + kb / 2 * F::PANEL + rr % kHalf * 128;
-        const int chunk = (kb & 1) * 4 + half * 2;
-        *reinterpret_cast<uint4*>(dst + ((chunk ^ (rr & 7)) << 4)) =
-            make_uint4(__byte_perm(x.x, y.x, 0x5410), __byte_perm(x.x, y.x, 0x7632), __byte_perm(x.y, y.y, 0x5410), __byte_perm(x.y, y.y, 0x7632));
-        *reinterpret_cast<uint4*>(dst + (((chunk + 1) ^ (rr & 7)) << 4)) =
-            make_uint4(__byte_perm(x.z, y.z, 0x5410), __byte_perm(x.z, y.z, 0x7632), __byte_perm(x.w, y.w, 0x5410), __byte_perm(x.w, y.w, 0x7632));
-      }
+      const Tile tile = ctl.tiles[n % kTiles];
+      if (tile.stop) break;
+      wait.warp(&empty[kv.stage], kv.phase ^ 1u);
+      if (!wait.ok) break;
+      const uint8_t* src = smem + F::OFF_RAW + stage * F::RAW;
+      const bool real = row >= tile.from && row < tile.to && !(tile.bad >> (row >> 4) & 1u);
+      if (ACT == 1 && which == 0)
+        decode_row<V, D, true>(src, tiles + kv.stage * F::TILE, row, real);
+      else
+        decode_row<V, D, false>(src, tiles + kv.stage * F::TILE, row, real);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&ctl.q_full));
+      if (lane == 0) {
+        mbar_arrive(smem_addr(&ctl.raw_empty[stage]));
+        mbar_arrive(smem_addr(&full[kv.stage]));
+      }
+      kv.next(F::STAGES);
+    }
+  } else {
+    give_registers<kOtherRegs>();
+    if (warp == 16) {
+      // ---- MMA issue ----
+      constexpr uint32_t id_s = instr_desc(ACT, kTok, 0), id_o = instr_desc(0, D, 1);
+      Ring kr, vr;
+      uint32_t n_q = 0, n_p0 = 0, n_p1 = 0;
+      const uint64_t qd = smem_desc(smem_addr(smem + F::OFF_Q), 16), kd = smem_desc(smem_addr(smem + F::OFF_K), 16);
+      const uint64_t vd = smem_desc(smem_addr(smem + F::OFF_V), F::PANEL);
+      Items items;
+      Item it;
+      while (items.next(ctl, wait, it)) {
+        __syncwarp();
+        if (lane == 0) items.done(ctl); else ++items.n;
+        const int steps = it.wide ? 2 * it.tiles : it.tiles;
+        if (lane == 0) {
+          wait.one(&ctl.q_full, n_q++ & 1u);
+          tc_fence_after();
+          auto scores = [&](int s) {
+            const int t = s & 1;
+            if (!it.wide || t == 0) {
+              wait.one(&ctl.k_full[kr.stage], kr.phase);
+              tc_fence_after();
+            }
+            const uint64_t a = qd + (it.wide ? (uint64_t)(t * F::TILE >> 4) : 0), b = kd + (uint64_t)(kr.stage * F::TILE >> 4);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint64_t off = (uint64_t)((k / 4) * (F::PANEL >> 4) + (k % 4) * 2);
+              mma_ss(tmem + 128u * t, a + off, b + off, id_s, k != 0);
+            }
+            mma_commit(smem_addr(&ctl.s_full[t]));
+            if (!it.wide || t == 1) {
+              mma_commit(smem_addr(&ctl.k_empty[kr.stage]));
+              kr.next(F::STAGES);
+            }
+            if (s == steps - 1) mma_commit(smem_addr(&ctl.q_empty));
+          };
+          scores(0);
+          if (steps > 1) scores(1);
+          for (int s = 0; s < steps; ++s) {
+            const int t = s & 1;
+            wait.one(&ctl.p_full[t], (t ? n_p1++ : n_p0++) & 1u);
+            if (!it.wide || t == 0) wait.one(&ctl.v_full[vr.stage], vr.phase);
+            tc_fence_after();
+            const uint64_t b = vd + (uint64_t)(vr.stage * F::TILE >> 4);
+#pragma unroll
+            for (int k = 0; k < kTok / 16; ++k)
+              mma_ts(tmem + 256u + (uint32_t)D * t, tmem + 128u * t + 8u * k, b + (uint64_t)(k * 2048 >> 4), id_o, s > 1 || k != 0);
+            if (!it.wide || t == 1) {
+              mma_commit(smem_addr(&ctl.v_empty[vr.stage]));
+              vr.next(F::STAGES);
+            }
+            if (s + 2 >= steps) mma_commit(smem_addr(&ctl.o_full[t]));
+            if (s + 2 < steps) scores(s + 2);
+          }
+        }
+        wait.ok = __all_sync(0xffffffffu, wait.ok);
+      }
+      if (!wait.ok && lane == 0) {  // products in flight end before the tensor memory goes
+        mma_commit(smem_addr(&ctl.drained));
+        (void)mbar_wait_bounded(smem_addr(&ctl.drained), 0);
+      }
+      __syncwarp();
+    } else if (warp == 17) {
+      // ---- items and raw rows ----
+      Walk walk(p, ctl);
+      Ring raw;
+      uint32_t tile = 0, issued = 0, n_items = 0;
+      const int group = lane & 7;
+      Item it;
+      bool more = true;
+      while (more && wait.ok) {
+        more = walk.next(p, it);
+        wait.warp(&ctl.item_empty[n_items % kItems], ((n_items / kItems) & 1u) ^ 1u);
+        if (!wait.ok) break;
+        if (!more) it.rows = 0;
+        it.tile = tile;
+        if (lane == 0) {
+          ctl.items[n_items % kItems] = it;
+          mbar_arrive(smem_addr(&ctl.item_full[n_items % kItems]));
+        }
+        ++n_items;
+        int lo = 0, hi = 0, x;
+        if (more) {
+          if (lane == 0 && it.s.len > it.s.lim) atomicOr(p.c.err, kErrBadPage);
+          seen(p, it.s, it.r0 / p.G, lo, x);
+          seen(p, it.s, (it.r0 + it.rows - 1) / p.G, x, hi);
+        }
+        // the end is one more tile, of no rows
+        const int tiles = more ? it.tiles : 1;
+        for (int j = 0; j < tiles && wait.ok; ++j, ++tile) {
+          const int t0 = (it.c0 + j) * kTok, g0 = t0 + 16 * group;
+          const bool want = more && lane < 8 && g0 < hi && g0 + 16 > lo;
+          int page = 0;
+          if (want) page = p.c.table[(int64_t)it.b * p.c.ldt + g0 / p.c.page_size];
+          const bool have = want && page >= 0 && page < p.c.num_pages;
+          const uint32_t bad = __ballot_sync(0xffffffffu, want && !have);
+          const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, have)) * 16u * F::RB;
+          const int64_t at = (((int64_t)page * p.c.Hkv + it.hk) * p.c.page_size + g0 % p.c.page_size) * F::RB;
+          for (int which = 0; which < 2; ++which) {
+            wait.warp(&ctl.raw_empty[raw.stage], raw.phase ^ 1u);
+            if (!wait.ok) break;
+            const uint32_t bar = smem_addr(&ctl.raw_full[which][raw.stage]);
+            if (lane == 0) {
+              if (which == 0) {
+                ctl.tiles[tile % kTiles] = Tile{max((lo & ~15) - t0, 0), hi - t0, bad, !more};
+                if (bad) atomicOr(p.c.err, kErrBadPage);
+              }
+              mbar_arrive_expect_tx(bar, bytes);
+            }
+            __syncwarp();
+            if (have)
+              bulk_g2s(smem_addr(smem + F::OFF_RAW + raw.stage * F::RAW + group * 16 * F::RB), (which ? p.c.V : p.c.K) + at, 16 * F::RB,
+                       bar);
+            raw.next(F::RSTAGES);
+            ++issued;
+          }
+        }
+      }
+      if (!wait.ok) {  // copies in flight land before the block ends
+        for (uint32_t i = issued > (uint32_t)F::RSTAGES ? issued - F::RSTAGES : 0; i < issued; ++i)
+          (void)mbar_wait_bounded(smem_addr(&ctl.raw_full[i & 1][i % F::RSTAGES]), RawRing<F::RSTAGES>::phase(i / 2));
+      }
+    } else {
+      // ---- Q rows ----
+      const int id = threadIdx.x - 18 * 32;
+      uint32_t n_q = 0;
+      Items items;
+      Item it;
+      while (items.next(ctl, wait, it)) {
+        __syncwarp();
+        if (lane == 0) items.done(ctl); else ++items.n;
+        wait.warp(&ctl.q_empty, (n_q++ & 1u) ^ 1u);
+        // a thread brings 32-value blocks of rows as they are, then puts each in order in its place
+        constexpr int NB = D / 32;
+        const int blocks = it.rows * NB;
+        for (int i = id; i < blocks; i += 64) {
+          const int rr = i / NB, kb = i % NB, row = it.r0 + rr, token = row / p.G, g = row - token * p.G;
+          const uint16_t* src = p.q + (int64_t)(it.s.row0 + token) * p.ldq + ((int64_t)it.hk * p.G + g) * D + kb * 32;
+          const uint32_t dst = smem_addr(smem + F::OFF_Q + rr / kHalf * F::TILE + kb / 2 * F::PANEL + rr % kHalf * 128);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + ((((kb & 1) * 4 + c) ^ (rr & 7)) << 4)), "l"(src + 8 * c)
+                         : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        for (int i = id; i < blocks; i += 64) {
+          const int rr = i / NB, kb = i % NB;
+          uint8_t* dst = smem + F::OFF_Q + rr / kHalf * F::TILE + kb / 2 * F::PANEL + rr % kHalf * 128;
+          uint4 q_lo, q_up;
+          auto chunk = [&](int c) { return reinterpret_cast<uint4*>(dst + ((((kb & 1) * 4 + c) ^ (rr & 7)) << 4)); };
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // chunks h and h + 2 hold values 8 h .. and 16 + 8 h ..
+            const uint4 x = *chunk(h), y = *chunk(h + 2);
+            const uint4 lo = make_uint4(__byte_perm(x.x, y.x, 0x5410), __byte_perm(x.x, y.x, 0x7632), __byte_perm(x.y, y.y, 0x5410),
+                                        __byte_perm(x.y, y.y, 0x7632));
+            const uint4 up = make_uint4(__byte_perm(x.z, y.z, 0x5410), __byte_perm(x.z, y.z, 0x7632), __byte_perm(x.w, y.w, 0x5410),
+                                        __byte_perm(x.w, y.w, 0x7632));
+            if (h == 0) {
+              q_lo = lo, q_up = up;
+            } else {
+              *chunk(0) = q_lo;
+              *chunk(1) = q_up;
+              *chunk(2) = lo;
+              *chunk(3) = up;
+            }
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&ctl.q_full));
+      }
     }
   }
   if (!wait.ok && lane == 0) atomicOr(p.c.err, kErrWaitTimeout);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
 using Fn = void (*)(Params);

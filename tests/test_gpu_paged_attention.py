@@ -212,3 +212,20 @@ def test_refusals_and_empty():
     with pytest.raises(rf4.RocmFP4Error):
         rf4.paged_attention(q[:, :3], p.cache, 0.1)  # three heads over two
     assert rf4.paged_attention(q[:0], p.cache, 0.1).shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("ns,ts,H,hkv,D,variant,name", [([1], [32768], 40, 8, 128, rf4.DUAL, "f16"), ([1] * 16, [4000 + 7 * i for i in range(16)], 40, 8, 128, rf4.FAST, "bf16"),
+                                                        ([1] * 40, [1500 + 11 * i for i in range(40)], 16, 16, 64, rf4.DUAL, "bf16"), ([60] * 3, [6000, 9001, 12345], 16, 8, 64, rf4.FAST, "f16")])
+def test_many_token_tiles_a_block(ns, ts, H, hkv, D, variant, name):
+    """Stretches of more token tiles than any ring holds, over caches that are not in the L2, launch after launch: every one alike."""
+    t = torch()
+    p = pu.Paged(ns, ts, hkv, D, 32, variant, seed=H)
+    q = p.queries(H, act(name))
+    flush = t.empty(200 << 20, dtype=t.uint8, device="cuda")
+    out = check(p, q)
+    for _ in range(10):
+        flush.fill_(1)
+        assert t.equal(rf4.paged_attention(q, p.cache, D ** -0.5), out)
+    for _ in range(10):
+        again = rf4.paged_attention(q, p.cache, D ** -0.5)
+    assert t.equal(again, out)
