@@ -144,31 +144,34 @@ RF4_DEV void mbar_arrive(uint32_t bar) {
 RF4_DEV void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// Shared-memory operand in the 128-byte swizzle: rows of 128 bytes, groups of
-// eight rows 1024 bytes apart (stride), 64-column panels `lead` bytes apart
-// (used where the columns are the operand's outer dimension).
-RF4_DEV uint64_t smem_desc(uint32_t saddr, uint32_t lead) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
+// Shared-memory operands are in the 128-byte swizzle: rows of 128 bytes,
+// groups of eight rows 1024 bytes apart (stride, in the descriptor's high word),
+// 64-column panels the low word's upper half apart (used where the columns are
+// the operand's outer dimension), address / 16 in its lower half.
+//
 // kind::f16, fp32 accumulator, A and B both fp16 (type 0) or bf16 (type 1), M =
 // 128; `b_outer`: B's rows in memory are its contraction index.
 RF4_HOSTDEV constexpr uint32_t instr_desc(int type, int n, int b_outer) {
   return (1u << 4) | ((uint32_t)type << 7) | ((uint32_t)type << 10) | ((uint32_t)b_outer << 16) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kHalf >> 4) << 24);
 }
-RF4_DEV void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+RF4_DEV bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
+RF4_DEV void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-RF4_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+RF4_DEV void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 RF4_DEV void tmem_ld32(uint32_t addr, float (&r)[32]) {
@@ -233,9 +236,6 @@ RF4_DEV void chains_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 // Waits that go on without waiting once one has given up.
 struct Waits {
   bool ok = true;
-  RF4_DEV void one(const uint64_t* bar, uint32_t parity) {
-    if (ok) ok = mbar_wait_bounded(smem_addr(bar), parity);
-  }
   RF4_DEV void warp(const uint64_t* bar, uint32_t parity) {
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(bar), parity));
   }
@@ -649,6 +649,73 @@ RF4_DEV void softmax_tile(uint32_t s, uint32_t o, Row& st, float scale_log2, boo
 // Position p of O's columns is value d_of(p) of the head.
 RF4_DEV int d_of(int p) { return (p & ~31) + ((p & 31) >> 1) + ((p & 1) << 4); }
 
+// Adds the parts of a row tile in order and writes its rows; 256 threads.  A
+// thread deals with several places of O at a time, so that loads of many
+// parts are on their way together.
+template <int D, int ACT>
+RF4_DEV void merge_parts(const Params& p, const Item& it, const float2* ml) {
+  constexpr int U = 4, Q4 = D / 4;
+  const int parts = (it.last - it.first + 1) << (it.wide ? 0 : 1), work = it.rows * Q4;
+  const bool whole = it.first == it.last;
+  // part n of row rr: of CTA first + n / chains; the first CTA's in its slot 1, the others' in slot 0, a whole row tile's in slot 2
+  auto record = [&](int n, int rr) {
+    const int c = it.wide ? n : n >> 1, ch = it.wide ? rr / kHalf : n & 1;
+    const int slot = whole ? 2 : c == 0 ? 1 : 0;
+    return (((it.first + c) * kSlots + slot) * 2 + ch) * kHalf + rr % kHalf;
+  };
+  for (int i0 = threadIdx.x; i0 < work; i0 += U * 256) {
+    int rr[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) rr[u] = min(i0 + u * 256, work - 1) / Q4;
+    float M[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) M[u] = -INFINITY;
+#pragma unroll 4
+    for (int n = 0; n < parts; ++n) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) M[u] = fmaxf(M[u], __ldcg(&ml[record(n, rr[u])]).x);
+    }
+    float L[U];
+    float4 O[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (M[u] == -INFINITY) M[u] = 0.f;
+      L[u] = 0.f;
+      O[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 2
+    for (int n = 0; n < parts; ++n) {
+      float2 v[U];
+      float4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int at = record(n, rr[u]);
+        v[u] = __ldcg(&ml[at]);
+        x[u] = __ldcg(reinterpret_cast<const float4*>(p.ws + (size_t)at * D) + (i0 + u * 256) % Q4);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        // a sum of zero: nothing seen, O may never have been written
+        const float e = v[u].y == 0.f ? 0.f : ex2(v[u].x - M[u]);
+        L[u] += e * v[u].y;
+        O[u].x += v[u].y == 0.f ? 0.f : e * x[u].x;
+        O[u].y += v[u].y == 0.f ? 0.f : e * x[u].y;
+        O[u].z += v[u].y == 0.f ? 0.f : e * x[u].z;
+        O[u].w += v[u].y == 0.f ? 0.f : e * x[u].w;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u * 256 >= work) break;
+      const float inv = L[u] == 0.f ? 0.f : 1.f / L[u];
+      const int row = it.r0 + rr[u], token = row / p.G, g = row - token * p.G;
+      uint16_t* out = p.out + ((int64_t)(it.s.row0 + token) * p.H + (int64_t)it.hk * p.G + g) * D + d_of(4 * ((i0 + u * 256) % Q4));
+      *reinterpret_cast<uint32_t*>(out) = pack_act(O[u].x * inv, O[u].z * inv, ACT);
+      *reinterpret_cast<uint32_t*>(out + 16) = pack_act(O[u].y * inv, O[u].w * inv, ACT);
+    }
+  }
+}
+
 // Items in the order in which the scheduling warp wrote them; all lanes of a warp.
 struct Items {
   uint32_t n = 0;
@@ -801,41 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         if (merge) __threadfence();
       }
       if (merge) {
-        const int chains = it.wide ? 1 : 2, parts = (it.last - it.first + 1) * chains;
-        for (int i = threadIdx.x; i < it.rows * (D / 4); i += 256) {
-          const int rr = i / (D / 4), q4 = i - rr * (D / 4);
-          const int chain = it.wide ? rr / kHalf : 0, rw = it.wide ? rr % kHalf : rr;
-          // part n: of CTA first + n / chains; the first CTA's in its slot 1, the others' in slot 0, a whole row tile's in slot 2
-          auto part = [&](int n) {
-            const int c = it.wide ? n : n >> 1, ch = it.wide ? chain : n & 1;
-            const int slot = it.first == it.last ? 2 : c == 0 ? 1 : 0;
-            return (((size_t)(it.first + c) * kSlots + slot) * 2 + ch) * kHalf + rw;
-          };
-          float M = -INFINITY;
-#pragma unroll 8
-          for (int n = 0; n < parts; ++n) M = fmaxf(M, __ldcg(&ml[part(n)]).x);
-          if (M == -INFINITY) M = 0.f;
-          float L = 0.f;
-          float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int n = 0; n < parts; ++n) {
-            const size_t at = part(n);
-            const float2 v = __ldcg(&ml[at]);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(p.ws + at * D) + q4);
-            if (v.y == 0.f) continue;  // nothing seen: O may never have been written
-            const float e = exp2f(v.x - M);
-            L += e * v.y;
-            O.x += e * x.x;
-            O.y += e * x.y;
-            O.z += e * x.z;
-            O.w += e * x.w;
-          }
-          const float inv = L == 0.f ? 0.f : 1.f / L;
-          const int orow = it.r0 + rr, token = orow / p.G, g = orow - token * p.G;
-          uint16_t* out = p.out + ((int64_t)(it.s.row0 + token) * p.H + (int64_t)it.hk * p.G + g) * D + d_of(4 * q4);
-          *reinterpret_cast<uint32_t*>(out) = pack_act(O.x * inv, O.z * inv, ACT);
-          *reinterpret_cast<uint32_t*>(out + 16) = pack_act(O.y * inv, O.w * inv, ACT);
-        }
+        merge_parts<D, ACT>(p, it, ml);
       }
       chains_sync();  // the records and ctl.last may be written again
     }
@@ -875,59 +908,61 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
     give_registers<kOtherRegs>();
     if (warp == 16) {
       // ---- MMA issue ----
+      // The whole warp walks along, one elected lane issues: what the
+      // instructions take is then uniform and stays in uniform registers.
       constexpr uint32_t id_s = instr_desc(ACT, kTok, 0), id_o = instr_desc(0, D, 1);
+      constexpr uint32_t desc_hi = (1024u >> 4) | 1u << 14 | 2u << 29;
+      const uint32_t q_lo = (smem_addr(smem + F::OFF_Q) >> 4) | 1u << 16, k_lo = (smem_addr(smem + F::OFF_K) >> 4) | 1u << 16;
+      const uint32_t v_lo = (smem_addr(smem + F::OFF_V) >> 4) | (uint32_t)(F::PANEL >> 4) << 16;
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       Ring kr, vr;
       uint32_t n_q = 0, n_p0 = 0, n_p1 = 0;
-      const uint64_t qd = smem_desc(smem_addr(smem + F::OFF_Q), 16), kd = smem_desc(smem_addr(smem + F::OFF_K), 16);
-      const uint64_t vd = smem_desc(smem_addr(smem + F::OFF_V), F::PANEL);
       Items items;
       Item it;
       while (items.next(ctl, wait, it)) {
         __syncwarp();
         if (lane == 0) items.done(ctl); else ++items.n;
-        const int steps = it.wide ? 2 * it.tiles : it.tiles;
-        if (lane == 0) {
-          wait.one(&ctl.q_full, n_q++ & 1u);
+        const uint32_t wide = __shfl_sync(0xffffffffu, it.wide, 0);
+        const int steps = __shfl_sync(0xffffffffu, it.tiles, 0) << wide;
+        wait.warp(&ctl.q_full, n_q++ & 1u);
+        auto scores = [&](int s) {
+          const uint32_t t = s & 1;
+          if (!wide || t == 0) wait.warp(&ctl.k_full[kr.stage], kr.phase);
           tc_fence_after();
-          auto scores = [&](int s) {
-            const int t = s & 1;
-            if (!it.wide || t == 0) {
-              wait.one(&ctl.k_full[kr.stage], kr.phase);
-              tc_fence_after();
-            }
-            const uint64_t a = qd + (it.wide ? (uint64_t)(t * F::TILE >> 4) : 0), b = kd + (uint64_t)(kr.stage * F::TILE >> 4);
+          const uint32_t a = q_lo + (wide & t) * (F::TILE >> 4), b = k_lo + kr.stage * (F::TILE >> 4);
+          if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-              const uint64_t off = (uint64_t)((k / 4) * (F::PANEL >> 4) + (k % 4) * 2);
-              mma_ss(tmem + 128u * t, a + off, b + off, id_s, k != 0);
+              const uint32_t off = (k / 4) * (F::PANEL >> 4) + (k % 4) * 2;
+              mma_ss(tm + 128u * t, a + off, b + off, desc_hi, id_s, k != 0);
             }
             mma_commit(smem_addr(&ctl.s_full[t]));
-            if (!it.wide || t == 1) {
-              mma_commit(smem_addr(&ctl.k_empty[kr.stage]));
-              kr.next(F::STAGES);
-            }
+            if (!wide || t == 1) mma_commit(smem_addr(&ctl.k_empty[kr.stage]));
             if (s == steps - 1) mma_commit(smem_addr(&ctl.q_empty));
-          };
-          scores(0);
-          if (steps > 1) scores(1);
-          for (int s = 0; s < steps; ++s) {
-            const int t = s & 1;
-            wait.one(&ctl.p_full[t], (t ? n_p1++ : n_p0++) & 1u);
-            if (!it.wide || t == 0) wait.one(&ctl.v_full[vr.stage], vr.phase);
-            tc_fence_after();
-            const uint64_t b = vd + (uint64_t)(vr.stage * F::TILE >> 4);
+          }
+          __syncwarp();
+          if (!wide || t == 1) kr.next(F::STAGES);
+        };
+        scores(0);
+        if (steps > 1) scores(1);
+#pragma unroll 1
+        for (int s = 0; s < steps; ++s) {
+          const uint32_t t = s & 1;
+          wait.warp(&ctl.p_full[t], (t ? n_p1++ : n_p0++) & 1u);
+          if (!wide || t == 0) wait.warp(&ctl.v_full[vr.stage], vr.phase);
+          tc_fence_after();
+          const uint32_t b = v_lo + vr.stage * (F::TILE >> 4);
+          if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < kTok / 16; ++k)
-              mma_ts(tmem + 256u + (uint32_t)D * t, tmem + 128u * t + 8u * k, b + (uint64_t)(k * 2048 >> 4), id_o, s > 1 || k != 0);
-            if (!it.wide || t == 1) {
-              mma_commit(smem_addr(&ctl.v_empty[vr.stage]));
-              vr.next(F::STAGES);
-            }
+              mma_ts(tm + 256u + (uint32_t)D * t, tm + 128u * t + 8u * k, b + k * (2048 >> 4), desc_hi, id_o, s > 1 || k != 0);
+            if (!wide || t == 1) mma_commit(smem_addr(&ctl.v_empty[vr.stage]));
             if (s + 2 >= steps) mma_commit(smem_addr(&ctl.o_full[t]));
-            if (s + 2 < steps) scores(s + 2);
           }
+          __syncwarp();
+          if (!wide || t == 1) vr.next(F::STAGES);
+          if (s + 2 < steps) scores(s + 2);
         }
-        wait.ok = __all_sync(0xffffffffu, wait.ok);
       }
       if (!wait.ok && lane == 0) {  // products in flight end before the tensor memory goes
         mma_commit(smem_addr(&ctl.drained));
