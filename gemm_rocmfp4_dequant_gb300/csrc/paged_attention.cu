@@ -39,10 +39,10 @@
 // Warps (640 threads), registers moved from the others to the softmax:
 //   0-3, 4-7   softmax and output of chain 0 and 1
 //   8-11       decode of K, one token row a thread;  12-15  of V
-//   16         tensor-memory allocation, MMA issue (one thread)
-//   17         the stretch's items, bulk copies of raw rows, 16 tokens each (a
-//              page is a multiple of 16)
-//   18-19      Q rows into shared memory
+//   16, 19     MMA issue of chain 0 (and tensor-memory allocation) and 1
+//   17         the stretch's items; bulk copies of K's raw rows, one for each run
+//              within a page
+//   18         Q rows into shared memory; bulk copies of V's raw rows
 // Every wait is bounded: a warp that gives up records kErrWaitTimeout and
 // goes on without waiting, so that all meet at the end.
 #include <cstring>
@@ -56,7 +56,7 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int kTok = 128;     // tokens per tile
 constexpr int kHalf = 128;    // rows per chain
-constexpr int kMinShare = 4;  // least work of a CTA: narrow token tiles
+constexpr int kMinShare = 4;  // narrow token tiles that are worth a CTA
 constexpr int kTiles = 16;    // token tiles described at a time
 constexpr int kItems = 4;     // row tiles described at a time
 constexpr int kSlots = 3;     // parts a CTA may hold: of its first, its last, and its current row tile
@@ -86,11 +86,11 @@ struct Plan {
   static constexpr int OFF_K = OFF_Q + 2 * TILE;
   static constexpr int OFF_V = OFF_K + STAGES * TILE;
   static constexpr int OFF_RAW = OFF_V + STAGES * TILE;
-  static constexpr int ROOM = 227 * 1024 - 1024 - 1536;  // less alignment and barriers
+  static constexpr int ROOM = 227 * 1024 - 1024 - 2048;  // less alignment and barriers
   static constexpr int FIT = (ROOM - OFF_RAW) / RAW;
   static constexpr int RSTAGES = FIT > 8 ? 8 : FIT;
   static constexpr int OFF_BAR = (OFF_RAW + RSTAGES * RAW + 15) / 16 * 16;
-  static constexpr int SMEM = OFF_BAR + 1536 + 1024;
+  static constexpr int SMEM = OFF_BAR + 2048 + 1024;
   static_assert(RSTAGES >= 2 && SMEM <= 227 * 1024, "shared memory");
   static_assert(RAW % 16 == 0, "bulk copies");
 };
@@ -119,21 +119,22 @@ struct Tile {
 };
 
 struct Control {  // at OFF_BAR
-  uint64_t raw_full[2][8], raw_empty[8];  // full: of K's copies, of V's
+  uint64_t raw_full[2][8], raw_empty[2][8];  // of K's copies, of V's
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t q_full, q_empty, drained;
+  uint64_t s_full[2], p_full[2], o_full[2], turn[2];
+  uint64_t q_full[2], q_empty, drained[2];  // full: by halves of a row tile
   uint64_t item_full[kItems], item_empty[kItems];
   long long start, end, total;  // of this CTA's stretch; of all work
   long long base;               // where the first row tile begins
   long long scan[kThreads / 32];
+  int scan_items[kThreads / 32];
   int b, hk, k, ctas;
   int last;
   uint32_t tmem;
   Item items[kItems];
-  Tile tiles[kTiles];
+  Tile tiles[2][kTiles];  // K's, V's
 };
-static_assert(sizeof(Control) <= 1536, "control block");
+static_assert(sizeof(Control) <= 2048, "control block");
 
 // ---- tensor-core instructions -------------------------------------------------
 RF4_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -237,19 +238,20 @@ RF4_DEV void chains_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 struct Waits {
   bool ok = true;
   RF4_DEV void warp(const uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(smem_addr(bar), parity))) return;
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(bar), parity));
   }
 };
 
-// The raw ring holds K's and V's tiles in turn.  K's entries are waited for by
-// one set of warps and V's by another, so each kind has barriers of its own: a
-// set that shared them with the other's entries could take an earlier phase's
-// parity for the one it waits for.
+// The raw ring holds K's and V's tiles in turn, entry 2 tile + kind at stage
+// entry % STAGES.  Each kind's entries are filled and emptied by warps of their
+// own, so each has barriers of its own: a warp that shared them with the other
+// kind could take an earlier phase's parity for the one it waits for.
 template <int STAGES>
 struct RawRing {
   static constexpr uint32_t kUses = STAGES % 2 ? STAGES : STAGES / 2;  // entries of a kind until a stage comes again
-  static RF4_DEV uint32_t stage(uint32_t tile, uint32_t which) { return (2 * tile + which) % STAGES; }
-  static RF4_DEV uint32_t phase(uint32_t tile) { return tile / kUses & 1u; }
+  static RF4_DEV uint32_t stage(uint32_t entry) { return entry % STAGES; }
+  static RF4_DEV uint32_t phase(uint32_t entry) { return (entry >> 1) / kUses & 1u; }
 };
 
 struct Ring {
@@ -311,7 +313,10 @@ struct Walk {
       : b(ctl.b), hk(ctl.hk), k(ctl.k), ctas(ctl.ctas), base(ctl.base), start(ctl.start), end(ctl.end), total(ctl.total) {
     s = sequence(p, b);
   }
-  RF4_DEV int owner(long long u) const { return (int)(((u + 1) * ctas - 1) / total); }
+  RF4_DEV int owner(long long u) const {
+    if (total < 1 << 22) return (int)(((uint32_t)(u + 1) * ctas - 1) / (uint32_t)total);
+    return (int)(((u + 1) * ctas - 1) / total);
+  }
   RF4_DEV bool next(const Params& p, Item& it) {
     while (base < end) {
       const RowTile t = row_tile(p, s, k);
@@ -353,14 +358,16 @@ struct Walk {
   }
 };
 
-// Work of sequence b: row tiles lane, lane + step, ...
-RF4_DEV long long work_of(const Params& p, int b, int lane, int step) {
+// Work of sequence b: row tiles lane, lane + step, ...; `items` grows by their number.
+RF4_DEV long long work_of(const Params& p, int b, int lane, int step, int& items, bool& wide) {
   const Seq s = sequence(p, b);
   const int tiles = (s.n * p.G + 2 * kHalf - 1) / (2 * kHalf);
   long long w = 0;
   for (int k = lane; k < tiles; k += step) {
     const RowTile t = row_tile(p, s, k);
     w += (long long)t.tiles * t.weight;
+    items += p.c.Hkv;
+    wide |= t.weight > 1;
   }
   return w * p.c.Hkv;
 }
@@ -374,13 +381,15 @@ RF4_DEV bool find_work(const Params& p, Control& ctl) {
   const int b0 = by_warp ? (lane == 0 ? min(warp, B) : B) : min(tid * per, B);
   const int b1 = by_warp ? (lane == 0 ? min(warp + 1, B) : B) : min(b0 + per, B);
   long long mine = 0;
+  int items = 0;
+  bool wide = false;
   if (by_warp) {
-    if (warp < B) mine = work_of(p, warp, lane, 32);
+    if (warp < B) mine = work_of(p, warp, lane, 32, items, wide);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     if (lane != 0) mine = 0;
   } else {
-    for (int b = b0; b < b1; ++b) mine += work_of(p, b, 0, 1);
+    for (int b = b0; b < b1; ++b) mine += work_of(p, b, 0, 1, items, wide);
   }
   long long before = mine;  // inclusive within the warp
 #pragma unroll
@@ -388,26 +397,46 @@ RF4_DEV bool find_work(const Params& p, Control& ctl) {
     const long long v = __shfl_up_sync(0xffffffffu, before, o);
     if (lane >= o) before += v;
   }
-  if (lane == 31) ctl.scan[warp] = before;
-  __syncthreads();
+  items = __reduce_add_sync(0xffffffffu, items);
+  if (lane == 31) {
+    ctl.scan[warp] = before;
+    ctl.scan_items[warp] = items;
+  }
+  const int any_wide = __syncthreads_or(wide);
   long long total = 0, lower = 0;
+  items = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w == warp) lower = total;
     total += ctl.scan[w];
+    items += ctl.scan_items[w];
   }
   before += lower - mine;
-  const long long most = total / kMinShare;
-  const int ctas = (int)(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
+  // A CTA for every row tile, or for every kMinShare token tiles where that
+  // is more.  A wide token tile counts 2, and a CTA's stretch is never
+  // shorter than one, so that every CTA between the first and the last of a
+  // shared row tile has a part of it.
+  long long most = total / kMinShare;
+  most = most > items ? most : items;
+  if (any_wide) most = most < total / 2 ? most : total / 2;
+  const int ctas = (int)(most < (long long)gridDim.x ? most : (long long)gridDim.x);
   if (total == 0 || (int)blockIdx.x >= ctas) return false;
-  const long long start = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
+  long long start, end;
+  if (total < 1 << 22) {  // the 32-bit division is the short one
+    start = (uint32_t)total * blockIdx.x / (uint32_t)ctas;
+    end = (uint32_t)total * (blockIdx.x + 1) / (uint32_t)ctas;
+  } else {
+    start = total * blockIdx.x / ctas;
+    end = total * (blockIdx.x + 1) / ctas;
+  }
   const uint32_t hit = __ballot_sync(0xffffffffu, start >= before && start < before + mine);
   if (hit) {  // one warp: the sequence of one of its lanes, then the row tile, 32 at a time
     int b = b0;
     long long base = before, w = mine;
     if (!by_warp)
       for (; b < b1; ++b) {
-        w = work_of(p, b, 0, 1);
+        int ignored = 0;
+        w = work_of(p, b, 0, 1, ignored, wide);
         if (start < base + w) break;
         base += w;
       }
@@ -415,8 +444,15 @@ RF4_DEV bool find_work(const Params& p, Control& ctl) {
     b = __shfl_sync(0xffffffffu, b, from);
     base = __shfl_sync(0xffffffffu, base, from);
     w = __shfl_sync(0xffffffffu, w, from);
-    const long long head = w / p.c.Hkv;
-    const int hk = (int)((start - base) / head);
+    int hk;
+    long long head;
+    if (w < 1ll << 31) {
+      head = (uint32_t)w / (uint32_t)p.c.Hkv;
+      hk = (int)((uint32_t)(start - base) / (uint32_t)head);
+    } else {
+      head = w / p.c.Hkv;
+      hk = (int)((start - base) / head);
+    }
     base += hk * head;
     const Seq s = sequence(p, b);
     for (int k0 = 0;; k0 += 32) {
@@ -534,10 +570,19 @@ struct Row {
   float m = -INFINITY, l = 0.f;
 };
 
+// Column i of a group of 32, or -inf where bit i of `keep` is clear.
 template <bool MASK>
-RF4_DEV float masked(float x, int col, int a, uint32_t width, uint32_t bad) {
-  if constexpr (MASK) return (uint32_t)(col - a) < width && !(bad >> (col >> 4) & 1u) ? x : -INFINITY;
+RF4_DEV float masked(float x, int i, uint32_t keep) {
+  if constexpr (MASK) return keep & (1u << i) ? x : -INFINITY;
   return x;
+}
+
+// Which of the 32 tokens from column c on a row sees: a .. e - 1 of the tile, but for `bad` groups of 16.
+RF4_DEV uint32_t kept(int c, int a, int e, uint32_t bad) {
+  const int lo = min(max(a - c, 0), 32), hi = min(max(e - c, 0), 32);
+  const uint32_t from = lo < 32 ? 0xffffffffu << lo : 0u, to = hi < 32 ? ~(0xffffffffu << hi) : 0xffffffffu;
+  const uint32_t two = bad >> (c >> 4);
+  return from & to & ~((two & 1u ? 0xffffu : 0u) | (two & 2u ? 0xffff0000u : 0u));
 }
 
 RF4_DEV uint64_t f2(float a, float b) {
@@ -559,56 +604,53 @@ RF4_DEV uint64_t add2(uint64_t a, uint64_t b) {
 RF4_DEV float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 template <bool MASK>
-RF4_DEV float top_of(const float (&x)[32], int c, int a, uint32_t width, uint32_t bad) {
+RF4_DEV float top_of(const float (&x)[32], uint32_t keep) {
   float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
-    t0 = max3(t0, masked<MASK>(x[i], c + i, a, width, bad), masked<MASK>(x[i + 1], c + i + 1, a, width, bad));
-    t1 = max3(t1, masked<MASK>(x[i + 2], c + i + 2, a, width, bad), masked<MASK>(x[i + 3], c + i + 3, a, width, bad));
+    t0 = max3(t0, masked<MASK>(x[i], i, keep), masked<MASK>(x[i + 1], i + 1, keep));
+    t1 = max3(t1, masked<MASK>(x[i + 2], i + 2, keep), masked<MASK>(x[i + 3], i + 3, keep));
   }
   return fmaxf(t0, t1);
 }
 
-// 32 columns of S to P at tensor-memory address `to`; their sum is added to `sum`.
+// 32 columns of S to P, packed; their sum is added to `sum`.
 template <bool MASK>
-RF4_DEV void weights(const float (&x)[32], uint32_t to, uint64_t scale2, uint64_t shift2, uint64_t (&sum)[2], int c, int a,
-                     uint32_t width, uint32_t bad) {
-  uint32_t h[16];
+RF4_DEV void weights(const float (&x)[32], uint32_t (&h)[16], uint64_t scale2, uint64_t shift2, uint64_t (&sum)[2], uint32_t keep) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const uint64_t y = fma2(f2(masked<MASK>(x[2 * i], c + 2 * i, a, width, bad), masked<MASK>(x[2 * i + 1], c + 2 * i + 1, a, width, bad)),
-                            scale2, shift2);
     float y0, y1;
-    un2(y, y0, y1);
+    un2(fma2(f2(masked<MASK>(x[2 * i], 2 * i, keep), masked<MASK>(x[2 * i + 1], 2 * i + 1, keep)), scale2, shift2), y0, y1);
     y0 = ex2(y0);
     y1 = ex2(y1);
     sum[i & 1] = add2(sum[i & 1], f2(y0, y1));
     h[i] = pack_h2(y0, y1);
   }
-  tmem_st16(to, h);
 }
 
 // S of this lane's row in tensor memory at `s` -> P at the same columns, O
-// (at `o`, D columns) scaled where the reference moves.  Tokens a .. a + width
-// - 1 of the tile are seen, but for `bad` groups of 16.  S is read twice, 32
-// columns at a time, the next ones on their way while these are dealt with;
-// columns 0-31 are the last of the first pass and stay for the second.
+// (at `o`, D columns) scaled where the reference moves.  Tokens a .. e - 1 of
+// the tile are seen, but for `bad` groups of 16.  S is read twice, 32 columns at
+// a time, the next ones on their way while these are dealt with; columns 0-31
+// are the last of the first pass and stay for the second.
 template <int D, bool MASK>
-RF4_DEV void softmax_tile(uint32_t s, uint32_t o, Row& st, float scale_log2, bool first, bool used, int a, uint32_t width,
-                          uint32_t bad) {
+RF4_DEV void softmax_tile(uint32_t s, uint32_t o, Row& st, float scale_log2, bool first, bool used, int a, int e, uint32_t bad) {
+  uint32_t keep[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) keep[c] = MASK ? kept(32 * c, a, e, bad) : 0xffffffffu;
   float x[32], y[32];
   tmem_ld32(s + 96, x);
   tmem_wait_ld();
   tmem_ld32(s + 64, y);
-  float top = top_of<MASK>(x, 96, a, width, bad);
+  float top = top_of<MASK>(x, keep[3]);
   tmem_wait_ld();
   tmem_ld32(s + 32, x);
-  top = fmaxf(top, top_of<MASK>(y, 64, a, width, bad));
+  top = fmaxf(top, top_of<MASK>(y, keep[2]));
   tmem_wait_ld();
   tmem_ld32(s, y);
-  top = fmaxf(top, top_of<MASK>(x, 32, a, width, bad));
+  top = fmaxf(top, top_of<MASK>(x, keep[1]));
   tmem_wait_ld();
-  top = fmaxf(top, top_of<MASK>(y, 0, a, width, bad)) * scale_log2;
+  top = fmaxf(top, top_of<MASK>(y, keep[0])) * scale_log2;
   if (first) {
     st.m = top;
   } else {
@@ -630,16 +672,60 @@ RF4_DEV void softmax_tile(uint32_t s, uint32_t o, Row& st, float scale_log2, boo
   const float shift = kLift - (st.m == -INFINITY ? 0.f : st.m);
   const uint64_t scale2 = f2(scale_log2, scale_log2), shift2 = f2(shift, shift);
   uint64_t sum[2] = {0, 0};
+  uint32_t h[16];
   tmem_ld32(s + 32, x);
-  weights<MASK>(y, s, scale2, shift2, sum, 0, a, width, bad);
+  weights<MASK>(y, h, scale2, shift2, sum, keep[0]);
+  tmem_st16(s, h);
   tmem_wait_ld();
   tmem_ld32(s + 64, y);
-  weights<MASK>(x, s + 16, scale2, shift2, sum, 32, a, width, bad);
+  weights<MASK>(x, h, scale2, shift2, sum, keep[1]);
+  tmem_st16(s + 16, h);
   tmem_wait_ld();
   tmem_ld32(s + 96, x);
-  weights<MASK>(y, s + 32, scale2, shift2, sum, 64, a, width, bad);
+  weights<MASK>(y, h, scale2, shift2, sum, keep[2]);
+  tmem_st16(s + 32, h);
   tmem_wait_ld();
-  weights<MASK>(x, s + 48, scale2, shift2, sum, 96, a, width, bad);
+  weights<MASK>(x, h, scale2, shift2, sum, keep[3]);
+  tmem_st16(s + 48, h);
+  float s0, s1;
+  un2(add2(sum[0], sum[1]), s0, s1);
+  st.l += s0 + s1;
+  tmem_wait_st();
+}
+
+// The same for a tile that is seen whole and is not the row's first: P by the
+// reference as it stands, in one pass, with the maximum beside it; P waits in
+// registers until that shows whether the reference holds, and where it does
+// not (a maximum that has grown by more than 2^8, seldom) the tile is done again.
+template <int D>
+RF4_DEV void softmax_next(uint32_t s, uint32_t o, Row& st, float scale_log2, bool used) {
+  const float shift = kLift - (st.m == -INFINITY ? 0.f : st.m);
+  const uint64_t scale2 = f2(scale_log2, scale_log2), shift2 = f2(shift, shift);
+  uint64_t sum[2] = {0, 0};
+  uint32_t h[4][16];
+  float x[32], y[32];
+  tmem_ld32(s, x);
+  tmem_wait_ld();
+  tmem_ld32(s + 32, y);
+  float top = top_of<false>(x, 0);
+  weights<false>(x, h[0], scale2, shift2, sum, 0);
+  tmem_wait_ld();
+  tmem_ld32(s + 64, x);
+  top = fmaxf(top, top_of<false>(y, 0));
+  weights<false>(y, h[1], scale2, shift2, sum, 0);
+  tmem_wait_ld();
+  tmem_ld32(s + 96, y);
+  top = fmaxf(top, top_of<false>(x, 0));
+  weights<false>(x, h[2], scale2, shift2, sum, 0);
+  tmem_wait_ld();
+  top = fmaxf(top, top_of<false>(y, 0));
+  weights<false>(y, h[3], scale2, shift2, sum, 0);
+  if (__any_sync(0xffffffffu, used && top * scale_log2 > st.m + kGrow)) {
+    softmax_tile<D, false>(s, o, st, scale_log2, false, used, 0, kTok, 0);
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_st16(s + 16 * c, h[c]);
   float s0, s1;
   un2(add2(sum[0], sum[1]), s0, s1);
   st.l += s0 + s1;
@@ -729,6 +815,115 @@ struct Items {
   RF4_DEV void done(Control& ctl) { mbar_arrive(smem_addr(&ctl.item_empty[n++ % kItems])); }
 };
 
+// Bulk copies of K's (WHICH 0) or V's raw rows; one warp.  Lanes 0-7 follow a
+// group of 16 tokens each through the pages; the first of a run of groups that
+// lie in one page copies the run.
+template <int V, int D, int WHICH>
+struct Loader {
+  using F = Plan<V, D>;
+  using Raw = RawRing<F::RSTAGES>;
+  uint32_t tile = 0;
+
+  // The next entry's stage, free of its last one.
+  RF4_DEV uint32_t acquire(Control& ctl, Waits& wait) const {
+    const uint32_t entry = 2 * tile + WHICH;
+    if (entry >= F::RSTAGES) {
+      const uint32_t old = entry - F::RSTAGES;
+      wait.warp(&ctl.raw_empty[old & 1][Raw::stage(old)], Raw::phase(old));
+    }
+    return Raw::stage(entry);
+  }
+
+  RF4_DEV void item(const Params& p, Control& ctl, Waits& wait, const Item& it, uint8_t* smem) {
+    const int lane = threadIdx.x & 31, group = lane & 7, ps = p.c.page_size;
+    int lo, hi, x;
+    seen(p, it.s, it.r0 / p.G, lo, x);
+    seen(p, it.s, (it.r0 + it.rows - 1) / p.G, x, hi);
+    const int32_t* row = p.c.table + (int64_t)it.b * p.c.ldt;
+    const uint8_t* base = (WHICH ? p.c.V : p.c.K) + (int64_t)it.hk * ps * F::RB;
+    const int64_t page_bytes = (int64_t)p.c.Hkv * ps * F::RB;
+    int g0 = it.c0 * kTok + 16 * group, at = g0 / ps, off = g0 - at * ps;
+    const int step = kTok / ps, rest = kTok - step * ps;
+    auto look_up = [&](int g) { return lane < 8 && g < hi && g + 16 > lo ? row[at] : -1; };
+    int page = look_up(g0);
+    for (int j = 0; j < it.tiles; ++j, ++tile) {
+      const int t0 = (it.c0 + j) * kTok;
+      const bool want = lane < 8 && g0 < hi && g0 + 16 > lo, have = want && page >= 0 && page < p.c.num_pages;
+      const uint8_t* src = base + page * page_bytes + off * F::RB;
+      const uint32_t bad = __ballot_sync(0xffffffffu, want && !have), there = __ballot_sync(0xffffffffu, have);
+      const bool lead = have && (lane == 0 || off == 0 || !(there >> (lane - 1) & 1u));
+      const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+      const uint32_t run = __ffs((leads | ~there) >> (lane + 1 & 31)) * 16 * F::RB;
+      // the next tile's page, on its way meanwhile
+      g0 += kTok;
+      at += step;
+      off += rest;
+      if (off >= ps) off -= ps, ++at;
+      const int place = group * 16 * F::RB;
+      page = j + 1 < it.tiles ? look_up(g0) : -1;
+      const uint32_t stage = acquire(ctl, wait);
+      if (!wait.ok) return;
+      const uint32_t bar = smem_addr(&ctl.raw_full[WHICH][stage]);
+      if (lane == 0) {
+        ctl.tiles[WHICH][tile % kTiles] = Tile{max((lo & ~15) - t0, 0), hi - t0, bad, 0};
+        if (bad) atomicOr(p.c.err, kErrBadPage);
+        mbar_arrive_expect_tx(bar, (uint32_t)__popc(there) * 16u * F::RB);
+      }
+      __syncwarp();
+      if (lead) bulk_g2s(smem_addr(smem + F::OFF_RAW + stage * F::RAW + place), src, run, bar);
+    }
+  }
+
+  // No more tiles.
+  RF4_DEV void stop(Control& ctl, Waits& wait) {
+    const uint32_t stage = acquire(ctl, wait);
+    if (!wait.ok) return;
+    if ((threadIdx.x & 31) == 0) {
+      ctl.tiles[WHICH][tile % kTiles] = Tile{0, 0, 0, 1};
+      mbar_arrive(smem_addr(&ctl.raw_full[WHICH][stage]));
+    }
+    ++tile;
+  }
+
+  // Where a wait gave up: copies in flight land before the block ends.
+  RF4_DEV void drain(Control& ctl, const Waits& wait) const {
+    if (wait.ok) return;
+    for (uint32_t t = tile > (uint32_t)F::RSTAGES ? tile - F::RSTAGES : 0; t < tile; ++t)
+      (void)mbar_wait_bounded(smem_addr(&ctl.raw_full[WHICH][Raw::stage(2 * t + WHICH)]), Raw::phase(2 * t + WHICH));
+  }
+};
+
+// Up to 128 rows of q into a swizzled tile; one warp.  A lane brings 32-value
+// blocks of rows as they are, then puts each in order (j, j + 16) in its place.
+template <int D>
+RF4_DEV void load_q(const Params& p, const Item& it, int half, uint8_t* tile, int lane) {
+  constexpr int NB = D / 32, PANEL = kTok * 128;
+  const int blocks = min(it.rows - half * kHalf, kHalf) * NB;
+  for (int i = lane; i < blocks; i += 32) {
+    const int rr = i / NB, kb = i % NB, row = it.r0 + half * kHalf + rr, token = row / p.G, g = row - token * p.G;
+    const uint16_t* src = p.q + (int64_t)(it.s.row0 + token) * p.ldq + ((int64_t)it.hk * p.G + g) * D + kb * 32;
+    const uint32_t dst = smem_addr(tile + kb / 2 * PANEL + rr * 128);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + ((((kb & 1) * 4 + c) ^ (rr & 7)) << 4)), "l"(src + 8 * c) : "memory");
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 2
+  for (int i = lane; i < blocks; i += 32) {
+    const int rr = i / NB, kb = i % NB;
+    uint8_t* dst = tile + kb / 2 * PANEL + rr * 128;
+    uint4* c[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[k] = reinterpret_cast<uint4*>(dst + ((((kb & 1) * 4 + k) ^ (rr & 7)) << 4));
+    // values 0-7 with 16-23, and 8-15 with 24-31
+    const uint4 w = *c[0], x = *c[1], y = *c[2], z = *c[3];
+    *c[0] = make_uint4(__byte_perm(w.x, y.x, 0x5410), __byte_perm(w.x, y.x, 0x7632), __byte_perm(w.y, y.y, 0x5410), __byte_perm(w.y, y.y, 0x7632));
+    *c[1] = make_uint4(__byte_perm(w.z, y.z, 0x5410), __byte_perm(w.z, y.z, 0x7632), __byte_perm(w.w, y.w, 0x5410), __byte_perm(w.w, y.w, 0x7632));
+    *c[2] = make_uint4(__byte_perm(x.x, z.x, 0x5410), __byte_perm(x.x, z.x, 0x7632), __byte_perm(x.y, z.y, 0x5410), __byte_perm(x.y, z.y, 0x7632));
+    *c[3] = make_uint4(__byte_perm(x.z, z.z, 0x5410), __byte_perm(x.z, z.z, 0x7632), __byte_perm(x.w, z.w, 0x5410), __byte_perm(x.w, z.w, 0x7632));
+  }
+}
+
 template <int V, int D, int ACT>
 __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __grid_constant__ Params p) {
   using F = Plan<V, D>;
@@ -739,26 +934,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < F::RSTAGES; ++i) {
-      mbar_init(smem_addr(&ctl.raw_full[0][i]), 1);
-      mbar_init(smem_addr(&ctl.raw_full[1][i]), 1);
-      mbar_init(smem_addr(&ctl.raw_empty[i]), 4);
+      for (int w = 0; w < 2; ++w) {
+        mbar_init(smem_addr(&ctl.raw_full[w][i]), 1);
+        mbar_init(smem_addr(&ctl.raw_empty[w][i]), 4);
+      }
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&ctl.k_full[i]), 4);
-      mbar_init(smem_addr(&ctl.k_empty[i]), 1);
+      mbar_init(smem_addr(&ctl.k_empty[i]), 2);
       mbar_init(smem_addr(&ctl.v_full[i]), 4);
-      mbar_init(smem_addr(&ctl.v_empty[i]), 1);
+      mbar_init(smem_addr(&ctl.v_empty[i]), 2);
       mbar_init(smem_addr(&ctl.s_full[i]), 1);
       mbar_init(smem_addr(&ctl.p_full[i]), 4);
       mbar_init(smem_addr(&ctl.o_full[i]), 1);
+      mbar_init(smem_addr(&ctl.turn[i]), 1);
+      mbar_init(smem_addr(&ctl.q_full[i]), 1);
+      mbar_init(smem_addr(&ctl.drained[i]), 1);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(smem_addr(&ctl.item_full[i]), 1);
-      mbar_init(smem_addr(&ctl.item_empty[i]), 8 + 1 + 2);
+      mbar_init(smem_addr(&ctl.item_empty[i]), 8 + 2 + 1);
     }
-    mbar_init(smem_addr(&ctl.q_full), 2);
-    mbar_init(smem_addr(&ctl.q_empty), 1);
-    mbar_init(smem_addr(&ctl.drained), 1);
+    mbar_init(smem_addr(&ctl.q_empty), 2);
     fence_mbar_init();
   }
   grid_dependency_wait();  // lengths, tables and everything else may be the preceding kernel's output
@@ -797,11 +994,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         const int a = max(lo - t0, 0), e = min(max(hi - t0, 0), kTok);
         wait.warp(&ctl.s_full[t], n_s++ & 1u);
         tc_fence_after();
-        const uint32_t bad = ctl.tiles[(it.tile + j) % kTiles].bad;
+        const uint32_t bad = ctl.tiles[0][(it.tile + j) % kTiles].bad;
         if (__any_sync(0xffffffffu, used && (a > 0 || e < kTok)) || bad)
-          softmax_tile<D, true>(s_at, o_at, st, p.scale_log2, first, used, a, (uint32_t)max(e - a, 0), bad);
+          softmax_tile<D, true>(s_at, o_at, st, p.scale_log2, first, used, a, e, bad);
+        else if (first)
+          softmax_tile<D, false>(s_at, o_at, st, p.scale_log2, true, used, 0, kTok, 0);
         else
-          softmax_tile<D, false>(s_at, o_at, st, p.scale_log2, first, used, 0, kTok, 0);
+          softmax_next<D>(s_at, o_at, st, p.scale_log2, used);
         first = false;
         tc_fence_before();
         __syncwarp();
@@ -883,10 +1082,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
     using Raw = RawRing<F::RSTAGES>;
     Ring kv;
     for (uint32_t n = 0;; ++n) {
-      const uint32_t stage = Raw::stage(n, which);
-      wait.warp(&ctl.raw_full[which][stage], Raw::phase(n));
+      const uint32_t entry = 2 * n + which, stage = Raw::stage(entry);
+      wait.warp(&ctl.raw_full[which][stage], Raw::phase(entry));
       if (!wait.ok) break;
-      const Tile tile = ctl.tiles[n % kTiles];
+      const Tile tile = ctl.tiles[which][n % kTiles];
       if (tile.stop) break;
       wait.warp(&empty[kv.stage], kv.phase ^ 1u);
       if (!wait.ok) break;
@@ -899,139 +1098,136 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(smem_addr(&ctl.raw_empty[stage]));
+        mbar_arrive(smem_addr(&ctl.raw_empty[which][stage]));
         mbar_arrive(smem_addr(&full[kv.stage]));
       }
       kv.next(F::STAGES);
     }
   } else {
     give_registers<kOtherRegs>();
-    if (warp == 16) {
+    if (warp == 16 || warp == 19) {
       // ---- MMA issue ----
       // The whole warp walks along, one elected lane issues: what the
-      // instructions take is then uniform and stays in uniform registers.
+      // instructions take is then uniform and stays in uniform registers.  A
+      // chain's products are issued by one warp, so that they run in order: S of
+      // its next token tile comes after the product that reads P in its place.
       constexpr uint32_t id_s = instr_desc(ACT, kTok, 0), id_o = instr_desc(0, D, 1);
       constexpr uint32_t desc_hi = (1024u >> 4) | 1u << 14 | 2u << 29;
+      const uint32_t t = warp == 19;
       const uint32_t q_lo = (smem_addr(smem + F::OFF_Q) >> 4) | 1u << 16, k_lo = (smem_addr(smem + F::OFF_K) >> 4) | 1u << 16;
       const uint32_t v_lo = (smem_addr(smem + F::OFF_V) >> 4) | (uint32_t)(F::PANEL >> 4) << 16;
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t s_at = tm + 128u * t, o_at = tm + 256u + (uint32_t)D * t;
       Ring kr, vr;
-      uint32_t n_q = 0, n_p0 = 0, n_p1 = 0;
+      uint32_t n_q0 = 0, n_q1 = 0, n_p = 0, n_turn = 0;
       Items items;
       Item it;
       while (items.next(ctl, wait, it)) {
         __syncwarp();
         if (lane == 0) items.done(ctl); else ++items.n;
         const uint32_t wide = __shfl_sync(0xffffffffu, it.wide, 0);
-        const int steps = __shfl_sync(0xffffffffu, it.tiles, 0) << wide;
-        wait.warp(&ctl.q_full, n_q++ & 1u);
-        auto scores = [&](int s) {
-          const uint32_t t = s & 1;
-          if (!wide || t == 0) wait.warp(&ctl.k_full[kr.stage], kr.phase);
+        const int tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
+        int left = wide ? tiles : (tiles + 1 - (int)t) >> 1;  // scores of this chain to come
+        int kj = 0, vj = 0;
+        // Goes on to this chain's next tile of K (or V) and waits for it; the other chain's tiles are let go.
+        auto next_own = [&](Ring& r, int& j, uint64_t* full, uint64_t* empty) {
+          for (; j < tiles; ++j) {
+            wait.warp(&full[r.stage], r.phase);
+            if (wide || (j & 1) == (int)t) return true;
+            if (lane == 0) mbar_arrive(smem_addr(&empty[r.stage]));
+            r.next(F::STAGES);
+          }
+          return false;
+        };
+        auto scores = [&]() {
           tc_fence_after();
           const uint32_t a = q_lo + (wide & t) * (F::TILE >> 4), b = k_lo + kr.stage * (F::TILE >> 4);
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t off = (k / 4) * (F::PANEL >> 4) + (k % 4) * 2;
-              mma_ss(tm + 128u * t, a + off, b + off, desc_hi, id_s, k != 0);
+              mma_ss(s_at, a + off, b + off, desc_hi, id_s, k != 0);
             }
             mma_commit(smem_addr(&ctl.s_full[t]));
-            if (!wide || t == 1) mma_commit(smem_addr(&ctl.k_empty[kr.stage]));
-            if (s == steps - 1) mma_commit(smem_addr(&ctl.q_empty));
+            mma_commit(smem_addr(&ctl.k_empty[kr.stage]));
+            if (left == 1) mma_commit(smem_addr(&ctl.q_empty));
           }
           __syncwarp();
-          if (!wide || t == 1) kr.next(F::STAGES);
+          --left;
+          ++kj;
+          kr.next(F::STAGES);
         };
-        scores(0);
-        if (steps > 1) scores(1);
+        bool have = next_own(kr, kj, ctl.k_full, ctl.k_empty);
+        wait.warp(&ctl.q_full[0], n_q0++ & 1u);
+        if (wide) {
+          if (t == 1) wait.warp(&ctl.q_full[1], n_q1 & 1u);
+          ++n_q1;
+        }
+        if (have) scores();
+        else if (lane == 0) mbar_arrive(smem_addr(&ctl.q_empty));
+        uint32_t again = 0;  // O holds something already
+        // The chains take turns at the tensor core, product and next scores in
+        // one go: left to themselves they fall into step, both at their softmax
+        // and then both at half the core's rate (4.8k cycles a token tile).
 #pragma unroll 1
-        for (int s = 0; s < steps; ++s) {
-          const uint32_t t = s & 1;
-          wait.warp(&ctl.p_full[t], (t ? n_p1++ : n_p0++) & 1u);
-          if (!wide || t == 0) wait.warp(&ctl.v_full[vr.stage], vr.phase);
+        for (int round = wide ? tiles : (tiles + 1) >> 1; round > 0; --round) {
+          if (!have) {  // an odd tile, the other chain's
+            wait.warp(&ctl.turn[t], (n_turn++ & 1u) ^ (t ^ 1u));
+            if (lane == 0) mbar_arrive(smem_addr(&ctl.turn[t ^ 1]));
+            break;
+          }
+          // K's and V's next tiles are there before P, mostly: only that wait counts
+          next_own(vr, vj, ctl.v_full, ctl.v_empty);
+          const bool more = next_own(kr, kj, ctl.k_full, ctl.k_empty);
+          wait.warp(&ctl.turn[t], (n_turn++ & 1u) ^ (t ^ 1u));
+          wait.warp(&ctl.p_full[t], n_p++ & 1u);
           tc_fence_after();
           const uint32_t b = v_lo + vr.stage * (F::TILE >> 4);
           if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kTok / 16; ++k)
-              mma_ts(tm + 256u + (uint32_t)D * t, tm + 128u * t + 8u * k, b + k * (2048 >> 4), desc_hi, id_o, s > 1 || k != 0);
-            if (!wide || t == 1) mma_commit(smem_addr(&ctl.v_empty[vr.stage]));
-            if (s + 2 >= steps) mma_commit(smem_addr(&ctl.o_full[t]));
+            for (int k = 0; k < kTok / 16; ++k) mma_ts(o_at, s_at + 8u * k, b + k * (2048 >> 4), desc_hi, id_o, again | (k != 0));
+            mma_commit(smem_addr(&ctl.v_empty[vr.stage]));
+            if (!more) mma_commit(smem_addr(&ctl.o_full[t]));
           }
           __syncwarp();
-          if (!wide || t == 1) vr.next(F::STAGES);
-          if (s + 2 < steps) scores(s + 2);
+          again = 1;
+          ++vj;
+          vr.next(F::STAGES);
+          if (more) scores();
+          if (lane == 0) mbar_arrive(smem_addr(&ctl.turn[t ^ 1]));
+          have = more;
         }
+        next_own(vr, vj, ctl.v_full, ctl.v_empty);  // the other chain's last tile, perhaps
       }
       if (!wait.ok && lane == 0) {  // products in flight end before the tensor memory goes
-        mma_commit(smem_addr(&ctl.drained));
-        (void)mbar_wait_bounded(smem_addr(&ctl.drained), 0);
+        mma_commit(smem_addr(&ctl.drained[t]));
+        (void)mbar_wait_bounded(smem_addr(&ctl.drained[t]), 0);
       }
       __syncwarp();
     } else if (warp == 17) {
-      // ---- items and raw rows ----
+      // ---- items, K's raw rows ----
       Walk walk(p, ctl);
-      Ring raw;
-      uint32_t tile = 0, issued = 0, n_items = 0;
-      const int group = lane & 7;
+      Loader<V, D, 0> load;
+      uint32_t n_items = 0;
       Item it;
-      bool more = true;
-      while (more && wait.ok) {
+      for (bool more = true; more && wait.ok; ++n_items) {
         more = walk.next(p, it);
         wait.warp(&ctl.item_empty[n_items % kItems], ((n_items / kItems) & 1u) ^ 1u);
         if (!wait.ok) break;
         if (!more) it.rows = 0;
-        it.tile = tile;
+        it.tile = load.tile;
         if (lane == 0) {
           ctl.items[n_items % kItems] = it;
           mbar_arrive(smem_addr(&ctl.item_full[n_items % kItems]));
+          if (more && it.s.len > it.s.lim) atomicOr(p.c.err, kErrBadPage);
         }
-        ++n_items;
-        int lo = 0, hi = 0, x;
-        if (more) {
-          if (lane == 0 && it.s.len > it.s.lim) atomicOr(p.c.err, kErrBadPage);
-          seen(p, it.s, it.r0 / p.G, lo, x);
-          seen(p, it.s, (it.r0 + it.rows - 1) / p.G, x, hi);
-        }
-        // the end is one more tile, of no rows
-        const int tiles = more ? it.tiles : 1;
-        for (int j = 0; j < tiles && wait.ok; ++j, ++tile) {
-          const int t0 = (it.c0 + j) * kTok, g0 = t0 + 16 * group;
-          const bool want = more && lane < 8 && g0 < hi && g0 + 16 > lo;
-          int page = 0;
-          if (want) page = p.c.table[(int64_t)it.b * p.c.ldt + g0 / p.c.page_size];
-          const bool have = want && page >= 0 && page < p.c.num_pages;
-          const uint32_t bad = __ballot_sync(0xffffffffu, want && !have);
-          const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, have)) * 16u * F::RB;
-          const int64_t at = (((int64_t)page * p.c.Hkv + it.hk) * p.c.page_size + g0 % p.c.page_size) * F::RB;
-          for (int which = 0; which < 2; ++which) {
-            wait.warp(&ctl.raw_empty[raw.stage], raw.phase ^ 1u);
-            if (!wait.ok) break;
-            const uint32_t bar = smem_addr(&ctl.raw_full[which][raw.stage]);
-            if (lane == 0) {
-              if (which == 0) {
-                ctl.tiles[tile % kTiles] = Tile{max((lo & ~15) - t0, 0), hi - t0, bad, !more};
-                if (bad) atomicOr(p.c.err, kErrBadPage);
-              }
-              mbar_arrive_expect_tx(bar, bytes);
-            }
-            __syncwarp();
-            if (have)
-              bulk_g2s(smem_addr(smem + F::OFF_RAW + raw.stage * F::RAW + group * 16 * F::RB), (which ? p.c.V : p.c.K) + at, 16 * F::RB,
-                       bar);
-            raw.next(F::RSTAGES);
-            ++issued;
-          }
-        }
+        if (more) load.item(p, ctl, wait, it, smem);
+        else load.stop(ctl, wait);
       }
-      if (!wait.ok) {  // copies in flight land before the block ends
-        for (uint32_t i = issued > (uint32_t)F::RSTAGES ? issued - F::RSTAGES : 0; i < issued; ++i)
-          (void)mbar_wait_bounded(smem_addr(&ctl.raw_full[i & 1][i % F::RSTAGES]), RawRing<F::RSTAGES>::phase(i / 2));
-      }
+      load.drain(ctl, wait);
     } else {
-      // ---- Q rows ----
-      const int id = threadIdx.x - 18 * 32;
+      // ---- Q rows, V's raw rows ----
+      Loader<V, D, 1> load;
       uint32_t n_q = 0;
       Items items;
       Item it;
@@ -1039,45 +1235,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         __syncwarp();
         if (lane == 0) items.done(ctl); else ++items.n;
         wait.warp(&ctl.q_empty, (n_q++ & 1u) ^ 1u);
-        // a thread brings 32-value blocks of rows as they are, then puts each in order in its place
-        constexpr int NB = D / 32;
-        const int blocks = it.rows * NB;
-        for (int i = id; i < blocks; i += 64) {
-          const int rr = i / NB, kb = i % NB, row = it.r0 + rr, token = row / p.G, g = row - token * p.G;
-          const uint16_t* src = p.q + (int64_t)(it.s.row0 + token) * p.ldq + ((int64_t)it.hk * p.G + g) * D + kb * 32;
-          const uint32_t dst = smem_addr(smem + F::OFF_Q + rr / kHalf * F::TILE + kb / 2 * F::PANEL + rr % kHalf * 128);
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + ((((kb & 1) * 4 + c) ^ (rr & 7)) << 4)), "l"(src + 8 * c)
-                         : "memory");
+#pragma unroll 1
+        for (int half = 0; half <= it.wide; ++half) {
+          load_q<D>(p, it, half, smem + F::OFF_Q + half * F::TILE, lane);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&ctl.q_full[half]));
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        for (int i = id; i < blocks; i += 64) {
-          const int rr = i / NB, kb = i % NB;
-          uint8_t* dst = smem + F::OFF_Q + rr / kHalf * F::TILE + kb / 2 * F::PANEL + rr % kHalf * 128;
-          uint4 q_lo, q_up;
-          auto chunk = [&](int c) { return reinterpret_cast<uint4*>(dst + ((((kb & 1) * 4 + c) ^ (rr & 7)) << 4)); };
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {  // chunks h and h + 2 hold values 8 h .. and 16 + 8 h ..
-            const uint4 x = *chunk(h), y = *chunk(h + 2);
-            const uint4 lo = make_uint4(__byte_perm(x.x, y.x, 0x5410), __byte_perm(x.x, y.x, 0x7632), __byte_perm(x.y, y.y, 0x5410),
-                                        __byte_perm(x.y, y.y, 0x7632));
-            const uint4 up = make_uint4(__byte_perm(x.z, y.z, 0x5410), __byte_perm(x.z, y.z, 0x7632), __byte_perm(x.w, y.w, 0x5410),
-                                        __byte_perm(x.w, y.w, 0x7632));
-            if (h == 0) {
-              q_lo = lo, q_up = up;
-            } else {
-              *chunk(0) = q_lo;
-              *chunk(1) = q_up;
-              *chunk(2) = lo;
-              *chunk(3) = up;
-            }
-          }
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&ctl.q_full));
+        load.item(p, ctl, wait, it, smem);
       }
+      if (wait.ok) load.stop(ctl, wait);
+      load.drain(ctl, wait);
     }
   }
   if (!wait.ok && lane == 0) atomicOr(p.c.err, kErrWaitTimeout);
