@@ -36,15 +36,18 @@
 // several CTAs leaves unnormalised parts in the workspace; the CTA that arrives
 // last adds them in order.  Nothing waits for another CTA.
 //
-// Warps (640 threads), registers moved from the others to the softmax:
-//   0-3, 4-7   softmax and output of chain 0 and 1
-//   8-11       decode of K, one token row a thread;  12-15  of V
-//   16, 19     MMA issue of chain 0 (and tensor-memory allocation) and 1
-//   17         the stretch's items; bulk copies of K's raw rows, one for each run
+// Warps (512 threads), registers moved from the others to the softmax:
+//   0-3, 4-7   Q rows, softmax and output of chain 0 and 1
+//   8-11       decode of K and V, one token row a thread
+//   12, 13     MMA issue of chain 0 (and tensor-memory allocation) and 1
+//   14         the stretch's row tiles; bulk copies of raw rows, one for each run
 //              within a page
-//   18         Q rows into shared memory; bulk copies of V's raw rows
+// (Two sets of decode warps leave the softmax 144 registers, in which its loop
+// spills: 322 us where this takes 286 for 512 rows over 33280 tokens.  Decode
+// warps that fetch their own rows: 376.)
 // Every wait is bounded: a warp that gives up records kErrWaitTimeout and
 // goes on without waiting, so that all meet at the end.
+#include <cstddef>
 #include <cstring>
 
 #include "common.cuh"
@@ -53,13 +56,16 @@
 namespace rocmfp4 {
 namespace {
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 512;
 constexpr int kTok = 128;     // tokens per tile
 constexpr int kHalf = 128;    // rows per chain
+constexpr int kWideCost = 3, kNarrowCost = 1;  // fixed work of a row tile
 constexpr int kMinShare = 4;  // narrow token tiles that are worth a CTA
+constexpr int kMaxRaw = 8;    // stages of the raw ring
 constexpr int kTiles = 16;    // token tiles described at a time
 constexpr int kItems = 4;     // row tiles described at a time
 constexpr int kSlots = 3;     // parts a CTA may hold: of its first, its last, and its current row tile
+constexpr uint32_t kSuspendNs = 1000000;
 constexpr float kGrow = 8.f;  // log2 of how far a maximum may lead its reference
 constexpr float kLift = 7.f;  // log2 of P's factor
 constexpr float kLog2e = 1.4426950408889634f;
@@ -82,16 +88,18 @@ struct Plan {
   static constexpr int TILE = kTok * D * 2;       // decoded tile
   static constexpr int PANEL = kTok * 128;        // 64 columns of a tile
   static constexpr int STAGES = 2;
-  static constexpr int OFF_Q = 0;  // two halves
-  static constexpr int OFF_K = OFF_Q + 2 * TILE;
+  static constexpr int OFF_K = 0;
   static constexpr int OFF_V = OFF_K + STAGES * TILE;
-  static constexpr int OFF_RAW = OFF_V + STAGES * TILE;
+  static constexpr int OFF_Q0 = OFF_V + STAGES * TILE;
+  static constexpr int OFF_Q1 = OFF_Q0 + TILE;  // raw stages where no row tile is wide
+  static constexpr int OFF_RAW = OFF_Q1 + TILE;
   static constexpr int ROOM = 227 * 1024 - 1024 - 2048;  // less alignment and barriers
-  static constexpr int FIT = (ROOM - OFF_RAW) / RAW;
-  static constexpr int RSTAGES = FIT > 8 ? 8 : FIT;
-  static constexpr int OFF_BAR = (OFF_RAW + RSTAGES * RAW + 15) / 16 * 16;
+  static constexpr int most(int n) { return n > kMaxRaw ? kMaxRaw : n; }
+  static constexpr int RSTAGES = most((ROOM - OFF_RAW) / RAW), RSTAGES_NARROW = most((ROOM - OFF_Q1) / RAW);
+  static constexpr int END = OFF_RAW + RSTAGES * RAW, END_NARROW = OFF_Q1 + RSTAGES_NARROW * RAW;
+  static constexpr int OFF_BAR = END > END_NARROW ? END : END_NARROW;
   static constexpr int SMEM = OFF_BAR + 2048 + 1024;
-  static_assert(RSTAGES >= 2 && SMEM <= 227 * 1024, "shared memory");
+  static_assert(RSTAGES >= 3 && OFF_BAR <= ROOM && SMEM <= 227 * 1024, "shared memory");
   static_assert(RAW % 16 == 0, "bulk copies");
 };
 
@@ -119,11 +127,15 @@ struct Tile {
 };
 
 struct Control {  // at OFF_BAR
-  uint64_t raw_full[2][8], raw_empty[2][8];  // of K's copies, of V's
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2], o_full[2], turn[2];
-  uint64_t q_full[2], q_empty, drained[2];  // full: by halves of a row tile
-  uint64_t item_full[kItems], item_empty[kItems];
+  // barriers, each with the number of its arrivals
+  uint64_t k_full[2], v_full[2];    // 4: decode warps
+  uint64_t k_empty[2], v_empty[2];  // 2: chains
+  uint64_t s_full[2], o_full[2], turn[2], drained[2];  // 1
+  uint64_t p_full[2], q_full[2];                       // 4: softmax warps
+  uint64_t raw_full[kMaxRaw];                          // 1, and the copies' bytes
+  uint64_t raw_empty[kMaxRaw];                         // 4: decode warps
+  uint64_t item_full[kItems];                          // 1
+  uint64_t item_empty[kItems];                         // 8 + 2: softmax and MMA warps
   long long start, end, total;  // of this CTA's stretch; of all work
   long long base;               // where the first row tile begins
   long long scan[kThreads / 32];
@@ -132,9 +144,10 @@ struct Control {  // at OFF_BAR
   int last;
   uint32_t tmem;
   Item items[kItems];
-  Tile tiles[2][kTiles];  // K's, V's
+  Tile tiles[kTiles];
 };
-static_assert(sizeof(Control) <= 2048, "control block");
+constexpr int kBars = 20 + 2 * kMaxRaw + 2 * kItems;
+static_assert(offsetof(Control, start) == 8 * kBars && sizeof(Control) <= 2048, "control block");
 
 // ---- tensor-core instructions -------------------------------------------------
 RF4_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -202,7 +215,13 @@ RF4_DEV void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
-RF4_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for the loads; the registers pass through, so that no use of theirs comes before.
+RF4_DEV void tmem_wait_ld(float (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])
+               :
+               : "memory");
+}
 RF4_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 RF4_DEV float ex2(float x) {
@@ -220,10 +239,10 @@ RF4_DEV uint32_t pack_act(float lo, float hi, int act) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Registers between warpgroups: the block was launched with 640 x 96; two
-// warpgroups take 144 a thread, three are left with 64.
-constexpr int kSoftmaxRegs = 144, kOtherRegs = 64;
-static_assert(256 * kSoftmaxRegs + 384 * kOtherRegs <= kThreads * 96, "register split");
+// Registers between warpgroups: the block was launched with 512 x 128; two
+// warpgroups take 176 a thread, two are left with 80.
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
+static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= kThreads * 128, "register split");
 template <int N>
 RF4_DEV void take_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -234,26 +253,35 @@ RF4_DEV void give_registers() {
 }
 RF4_DEV void chains_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
+// A wait for a phase that the hardware may suspend the warp in: a loop of plain
+// polls took half of the SM's issue slots from the warps that had work.  Gives
+// up after about 2^32 cycles.
+RF4_DEV bool wait_suspended(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    if (ok) return true;
+    if (clock64() - t0 > (1ll << 32)) return false;
+  }
+}
+
 // Waits that go on without waiting once one has given up.
 struct Waits {
   bool ok = true;
   RF4_DEV void warp(const uint64_t* bar, uint32_t parity) {
     if (__all_sync(0xffffffffu, mbar_try_wait(smem_addr(bar), parity))) return;
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(bar), parity));
+    if (ok) ok = __all_sync(0xffffffffu, wait_suspended(smem_addr(bar), parity));
   }
 };
 
-// The raw ring holds K's and V's tiles in turn, entry 2 tile + kind at stage
-// entry % STAGES.  Each kind's entries are filled and emptied by warps of their
-// own, so each has barriers of its own: a warp that shared them with the other
-// kind could take an earlier phase's parity for the one it waits for.
-template <int STAGES>
-struct RawRing {
-  static constexpr uint32_t kUses = STAGES % 2 ? STAGES : STAGES / 2;  // entries of a kind until a stage comes again
-  static RF4_DEV uint32_t stage(uint32_t entry) { return entry % STAGES; }
-  static RF4_DEV uint32_t phase(uint32_t entry) { return (entry >> 1) / kUses & 1u; }
-};
-
+// A place in a ring of stages and the parity of its use.  One set of warps waits
+// for each of a ring's barriers, use by use: a set that left uses out could take an
+// earlier phase's parity for the one it waits for.
 struct Ring {
   uint32_t stage = 0, phase = 0;
   RF4_DEV void next(uint32_t n) {
@@ -290,6 +318,10 @@ RF4_DEV void seen(const Params& p, const Seq& s, int i, int& lo, int& hi) {
 struct RowTile {
   int rows, weight;  // rows; work of one token tile
   int c0, tiles;     // first token tile, and how many (at least one)
+  // Work of the whole: its token tiles behind a fixed part, for what a row
+  // tile costs whatever its length (queries, output).
+  RF4_DEV int fixed() const { return weight == 2 ? kWideCost : kNarrowCost; }
+  RF4_DEV long long all() const { return fixed() + (long long)tiles * weight; }
 };
 
 RF4_DEV RowTile row_tile(const Params& p, const Seq& s, int k) {
@@ -320,9 +352,11 @@ struct Walk {
   RF4_DEV bool next(const Params& p, Item& it) {
     while (base < end) {
       const RowTile t = row_tile(p, s, k);
-      const long long all = (long long)t.tiles * t.weight;
-      const int j0 = base >= start ? 0 : (int)((start - base + t.weight - 1) / t.weight);
-      const int j1 = end >= base + all ? t.tiles : (int)((end - base + t.weight - 1) / t.weight);
+      // token tiles whose places lie in start .. end - 1
+      const long long at = base + t.fixed();
+      const long long from = start - at + t.weight - 1, to = end - at + t.weight - 1;
+      const int j0 = from <= 0 ? 0 : from >> (t.weight - 1) < t.tiles ? (int)(from >> (t.weight - 1)) : t.tiles;
+      const int j1 = to <= 0 ? 0 : to >> (t.weight - 1) < t.tiles ? (int)(to >> (t.weight - 1)) : t.tiles;
       it.b = b;
       it.hk = hk;
       it.r0 = k * 2 * kHalf;
@@ -334,11 +368,11 @@ struct Walk {
       it.first = it.last = blockIdx.x;
       it.slot = 2;
       if (j0 > 0 || j1 < t.tiles) {
-        it.first = owner(base);
-        it.last = owner(base + (long long)(t.tiles - 1) * t.weight);
+        it.first = owner(at);
+        it.last = owner(at + (long long)(t.tiles - 1) * t.weight);
         it.slot = j0 > 0 ? 0 : 1;
       }
-      base += all;
+      base += t.all();
       if ((long long)(++k) * 2 * kHalf >= (long long)s.n * p.G) {
         k = 0;
         if (++hk == p.c.Hkv) {
@@ -358,41 +392,56 @@ struct Walk {
   }
 };
 
-// Work of sequence b: row tiles lane, lane + step, ...; `items` grows by their number.
-RF4_DEV long long work_of(const Params& p, int b, int lane, int step, int& items, bool& wide) {
+struct Work {
+  long long cost;
+  int tiles;  // row tiles; negative: some is wide
+};
+
+// Work of sequence b for one KV head: row tiles lane, lane + step, ...
+RF4_DEV Work work_of(const Params& p, int b, int lane, int step) {
   const Seq s = sequence(p, b);
   const int tiles = (s.n * p.G + 2 * kHalf - 1) / (2 * kHalf);
-  long long w = 0;
+  Work w{0, 0};
+  bool wide = false;
   for (int k = lane; k < tiles; k += step) {
     const RowTile t = row_tile(p, s, k);
-    w += (long long)t.tiles * t.weight;
-    items += p.c.Hkv;
+    w.cost += t.all();
+    ++w.tiles;
     wide |= t.weight > 1;
   }
-  return w * p.c.Hkv;
+  if (wide) w.tiles = -w.tiles;
+  return w;
 }
 
-// This CTA's stretch and where it begins; false if it has none.  All threads.
-RF4_DEV bool find_work(const Params& p, Control& ctl) {
+RF4_DEV long long divide(long long a, long long b) {
+  if ((a | b) >> 31 == 0) return (uint32_t)a / (uint32_t)b;  // the short division
+  return a / b;
+}
+
+// This CTA's stretch and where it begins; false if it has none.  `any`: whether
+// some row tile of the call is wide.  All threads.
+RF4_DEV bool find_work(const Params& p, Control& ctl, bool& any) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = p.c.B;
   // few sequences: a warp each, its lanes over row tiles; many: a thread each, or several in a row
   const bool by_warp = B <= kThreads / 32;
   const int per = (B + kThreads - 1) / kThreads;
-  const int b0 = by_warp ? (lane == 0 ? min(warp, B) : B) : min(tid * per, B);
-  const int b1 = by_warp ? (lane == 0 ? min(warp + 1, B) : B) : min(b0 + per, B);
+  const int b0 = by_warp ? min(warp, B) : min(tid * per, B), b1 = by_warp ? min(warp + 1, B) : min(b0 + per, B);
   long long mine = 0;
   int items = 0;
   bool wide = false;
+  for (int b = b0; b < b1; ++b) {
+    const Work w = work_of(p, b, by_warp ? lane : 0, by_warp ? 32 : 1);
+    mine += w.cost * p.c.Hkv;
+    items += abs(w.tiles) * p.c.Hkv;
+    wide |= w.tiles < 0;
+  }
   if (by_warp) {
-    if (warp < B) mine = work_of(p, warp, lane, 32, items, wide);
-#pragma unroll
+#pragma unroll 1
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     if (lane != 0) mine = 0;
-  } else {
-    for (int b = b0; b < b1; ++b) mine += work_of(p, b, 0, 1, items, wide);
   }
   long long before = mine;  // inclusive within the warp
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const long long v = __shfl_up_sync(0xffffffffu, before, o);
     if (lane >= o) before += v;
@@ -403,9 +452,10 @@ RF4_DEV bool find_work(const Params& p, Control& ctl) {
     ctl.scan_items[warp] = items;
   }
   const int any_wide = __syncthreads_or(wide);
+  any = any_wide;
   long long total = 0, lower = 0;
   items = 0;
-#pragma unroll
+#pragma unroll 4
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w == warp) lower = total;
     total += ctl.scan[w];
@@ -419,24 +469,17 @@ RF4_DEV bool find_work(const Params& p, Control& ctl) {
   long long most = total / kMinShare;
   most = most > items ? most : items;
   if (any_wide) most = most < total / 2 ? most : total / 2;
+  if (most < 1) most = 1;
   const int ctas = (int)(most < (long long)gridDim.x ? most : (long long)gridDim.x);
   if (total == 0 || (int)blockIdx.x >= ctas) return false;
-  long long start, end;
-  if (total < 1 << 22) {  // the 32-bit division is the short one
-    start = (uint32_t)total * blockIdx.x / (uint32_t)ctas;
-    end = (uint32_t)total * (blockIdx.x + 1) / (uint32_t)ctas;
-  } else {
-    start = total * blockIdx.x / ctas;
-    end = total * (blockIdx.x + 1) / ctas;
-  }
+  const long long start = divide(total * blockIdx.x, ctas), end = divide(total * (blockIdx.x + 1), ctas);
   const uint32_t hit = __ballot_sync(0xffffffffu, start >= before && start < before + mine);
   if (hit) {  // one warp: the sequence of one of its lanes, then the row tile, 32 at a time
     int b = b0;
     long long base = before, w = mine;
     if (!by_warp)
       for (; b < b1; ++b) {
-        int ignored = 0;
-        w = work_of(p, b, 0, 1, ignored, wide);
+        w = work_of(p, b, 0, 1).cost * p.c.Hkv;
         if (start < base + w) break;
         base += w;
       }
@@ -444,15 +487,8 @@ RF4_DEV bool find_work(const Params& p, Control& ctl) {
     b = __shfl_sync(0xffffffffu, b, from);
     base = __shfl_sync(0xffffffffu, base, from);
     w = __shfl_sync(0xffffffffu, w, from);
-    int hk;
-    long long head;
-    if (w < 1ll << 31) {
-      head = (uint32_t)w / (uint32_t)p.c.Hkv;
-      hk = (int)((uint32_t)(start - base) / (uint32_t)head);
-    } else {
-      head = w / p.c.Hkv;
-      hk = (int)((start - base) / head);
-    }
+    const long long head = divide(w, p.c.Hkv);
+    const int hk = (int)divide(start - base, head);
     base += hk * head;
     const Seq s = sequence(p, b);
     for (int k0 = 0;; k0 += 32) {
@@ -460,10 +496,10 @@ RF4_DEV bool find_work(const Params& p, Control& ctl) {
       long long all = 0;
       if ((long long)k * 2 * kHalf < (long long)s.n * p.G) {
         const RowTile t = row_tile(p, s, k);
-        all = (long long)t.tiles * t.weight;
+        all = t.all();
       }
       long long upto = all;
-#pragma unroll
+#pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
         const long long v = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += v;
@@ -630,27 +666,20 @@ RF4_DEV void weights(const float (&x)[32], uint32_t (&h)[16], uint64_t scale2, u
 
 // S of this lane's row in tensor memory at `s` -> P at the same columns, O
 // (at `o`, D columns) scaled where the reference moves.  Tokens a .. e - 1 of
-// the tile are seen, but for `bad` groups of 16.  S is read twice, 32 columns at
-// a time, the next ones on their way while these are dealt with; columns 0-31
-// are the last of the first pass and stay for the second.
-template <int D, bool MASK>
+// the tile are seen, but for `bad` groups of 16.  S is read twice, in loops that
+// are kept short: this serves a row tile's first and last token tiles, and code
+// that runs seldom had better not push the rest out of the instruction cache.
+template <int D>
 RF4_DEV void softmax_tile(uint32_t s, uint32_t o, Row& st, float scale_log2, bool first, bool used, int a, int e, uint32_t bad) {
-  uint32_t keep[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) keep[c] = MASK ? kept(32 * c, a, e, bad) : 0xffffffffu;
-  float x[32], y[32];
-  tmem_ld32(s + 96, x);
-  tmem_wait_ld();
-  tmem_ld32(s + 64, y);
-  float top = top_of<MASK>(x, keep[3]);
-  tmem_wait_ld();
-  tmem_ld32(s + 32, x);
-  top = fmaxf(top, top_of<MASK>(y, keep[2]));
-  tmem_wait_ld();
-  tmem_ld32(s, y);
-  top = fmaxf(top, top_of<MASK>(x, keep[1]));
-  tmem_wait_ld();
-  top = fmaxf(top, top_of<MASK>(y, keep[0])) * scale_log2;
+  float x[32], top = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < kTok; c += 32) {
+    tmem_ld32(s + c, x);
+    const uint32_t keep = kept(c, a, e, bad);
+    tmem_wait_ld(x);
+    top = fmaxf(top, top_of<true>(x, keep));
+  }
+  top *= scale_log2;
   if (first) {
     st.m = top;
   } else {
@@ -662,7 +691,7 @@ RF4_DEV void softmax_tile(uint32_t s, uint32_t o, Row& st, float scale_log2, boo
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         tmem_ld32(o + c, x);
-        tmem_wait_ld();
+        tmem_wait_ld(x);
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[i] *= alpha;
         tmem_st32(o + c, x);
@@ -672,21 +701,15 @@ RF4_DEV void softmax_tile(uint32_t s, uint32_t o, Row& st, float scale_log2, boo
   const float shift = kLift - (st.m == -INFINITY ? 0.f : st.m);
   const uint64_t scale2 = f2(scale_log2, scale_log2), shift2 = f2(shift, shift);
   uint64_t sum[2] = {0, 0};
-  uint32_t h[16];
-  tmem_ld32(s + 32, x);
-  weights<MASK>(y, h, scale2, shift2, sum, keep[0]);
-  tmem_st16(s, h);
-  tmem_wait_ld();
-  tmem_ld32(s + 64, y);
-  weights<MASK>(x, h, scale2, shift2, sum, keep[1]);
-  tmem_st16(s + 16, h);
-  tmem_wait_ld();
-  tmem_ld32(s + 96, x);
-  weights<MASK>(y, h, scale2, shift2, sum, keep[2]);
-  tmem_st16(s + 32, h);
-  tmem_wait_ld();
-  weights<MASK>(x, h, scale2, shift2, sum, keep[3]);
-  tmem_st16(s + 48, h);
+#pragma unroll 1
+  for (int c = 0; c < kTok; c += 32) {
+    uint32_t h[16];
+    tmem_ld32(s + c, x);
+    const uint32_t keep = kept(c, a, e, bad);
+    tmem_wait_ld(x);
+    weights<true>(x, h, scale2, shift2, sum, keep);
+    tmem_st16(s + c / 2, h);
+  }
   float s0, s1;
   un2(add2(sum[0], sum[1]), s0, s1);
   st.l += s0 + s1;
@@ -698,31 +721,30 @@ RF4_DEV void softmax_tile(uint32_t s, uint32_t o, Row& st, float scale_log2, boo
 // registers until that shows whether the reference holds, and where it does
 // not (a maximum that has grown by more than 2^8, seldom) the tile is done again.
 template <int D>
-RF4_DEV void softmax_next(uint32_t s, uint32_t o, Row& st, float scale_log2, bool used) {
+RF4_DEV bool softmax_next(uint32_t s, Row& st, float scale_log2, bool used) {
   const float shift = kLift - (st.m == -INFINITY ? 0.f : st.m);
   const uint64_t scale2 = f2(scale_log2, scale_log2), shift2 = f2(shift, shift);
   uint64_t sum[2] = {0, 0};
   uint32_t h[4][16];
   float x[32], y[32];
   tmem_ld32(s, x);
-  tmem_wait_ld();
+  tmem_wait_ld(x);
   tmem_ld32(s + 32, y);
   float top = top_of<false>(x, 0);
   weights<false>(x, h[0], scale2, shift2, sum, 0);
-  tmem_wait_ld();
+  tmem_wait_ld(y);
   tmem_ld32(s + 64, x);
   top = fmaxf(top, top_of<false>(y, 0));
   weights<false>(y, h[1], scale2, shift2, sum, 0);
-  tmem_wait_ld();
+  tmem_wait_ld(x);
   tmem_ld32(s + 96, y);
   top = fmaxf(top, top_of<false>(x, 0));
   weights<false>(x, h[2], scale2, shift2, sum, 0);
-  tmem_wait_ld();
+  tmem_wait_ld(y);
   top = fmaxf(top, top_of<false>(y, 0));
   weights<false>(y, h[3], scale2, shift2, sum, 0);
   if (__any_sync(0xffffffffu, used && top * scale_log2 > st.m + kGrow)) {
-    softmax_tile<D, false>(s, o, st, scale_log2, false, used, 0, kTok, 0);
-    return;
+    return false;
   }
 #pragma unroll
   for (int c = 0; c < 4; ++c) tmem_st16(s + 16 * c, h[c]);
@@ -730,6 +752,7 @@ RF4_DEV void softmax_next(uint32_t s, uint32_t o, Row& st, float scale_log2, boo
   un2(add2(sum[0], sum[1]), s0, s1);
   st.l += s0 + s1;
   tmem_wait_st();
+  return true;
 }
 
 // Position p of O's columns is value d_of(p) of the head.
@@ -744,7 +767,7 @@ RF4_DEV void merge_parts(const Params& p, const Item& it, const float2* ml) {
   const int parts = (it.last - it.first + 1) << (it.wide ? 0 : 1), work = it.rows * Q4;
   const bool whole = it.first == it.last;
   // part n of row rr: of CTA first + n / chains; the first CTA's in its slot 1, the others' in slot 0, a whole row tile's in slot 2
-  auto record = [&](int n, int rr) {
+  auto record = [&](int n, int rr) __attribute__((always_inline)) {
     const int c = it.wide ? n : n >> 1, ch = it.wide ? rr / kHalf : n & 1;
     const int slot = whole ? 2 : c == 0 ? 1 : 0;
     return (((it.first + c) * kSlots + slot) * 2 + ch) * kHalf + rr % kHalf;
@@ -756,7 +779,7 @@ RF4_DEV void merge_parts(const Params& p, const Item& it, const float2* ml) {
     float M[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) M[u] = -INFINITY;
-#pragma unroll 4
+#pragma unroll 2
     for (int n = 0; n < parts; ++n) {
 #pragma unroll
       for (int u = 0; u < U; ++u) M[u] = fmaxf(M[u], __ldcg(&ml[record(n, rr[u])]).x);
@@ -769,7 +792,7 @@ RF4_DEV void merge_parts(const Params& p, const Item& it, const float2* ml) {
       L[u] = 0.f;
       O[u] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-#pragma unroll 2
+#pragma unroll 1
     for (int n = 0; n < parts; ++n) {
       float2 v[U];
       float4 x[U];
@@ -802,54 +825,51 @@ RF4_DEV void merge_parts(const Params& p, const Item& it, const float2* ml) {
   }
 }
 
-// Items in the order in which the scheduling warp wrote them; all lanes of a warp.
+// Items in the order in which the scheduling warp wrote them; all lanes of a
+// warp.  An item is read where it lies, until the warp is done with it.
 struct Items {
   uint32_t n = 0;
-  RF4_DEV bool next(Control& ctl, Waits& wait, Item& it) {
-    wait.warp(&ctl.item_full[n % kItems], (n / kItems) & 1u);
-    if (!wait.ok) return false;
-    it = ctl.items[n % kItems];
-    return it.rows > 0;
+  // The item `ahead` of the next one to be done with, or nullptr behind the last.
+  RF4_DEV const Item* get(const Control& ctl, Waits& wait, uint32_t ahead = 0) {
+    const uint32_t i = n + ahead;
+    wait.warp(&ctl.item_full[i % kItems], (i / kItems) & 1u);
+    const Item* it = &ctl.items[i % kItems];
+    return wait.ok && it->rows > 0 ? it : nullptr;
   }
-  // one lane, after the warp's last use of the item
-  RF4_DEV void done(Control& ctl) { mbar_arrive(smem_addr(&ctl.item_empty[n++ % kItems])); }
+  RF4_DEV void done(Control& ctl) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&ctl.item_empty[n % kItems]));
+    ++n;
+  }
 };
 
-// Bulk copies of K's (WHICH 0) or V's raw rows; one warp.  Lanes 0-7 follow a
-// group of 16 tokens each through the pages; the first of a run of groups that
-// lie in one page copies the run.
-template <int V, int D, int WHICH>
+// Bulk copies of raw rows, K's and V's tiles in turn; one warp.  Lanes 0-7
+// follow a group of 16 tokens each through the pages; the first of a run of
+// groups that lie in one page copies the run.
+template <int V, int D>
 struct Loader {
   using F = Plan<V, D>;
-  using Raw = RawRing<F::RSTAGES>;
-  uint32_t tile = 0;
+  int stages;
+  uint8_t* raw;
+  Ring ring;
+  int tile = 0;
+  uint32_t issued = 0;
+  RF4_DEV Loader(int stages, uint8_t* raw) : stages(stages), raw(raw) {}
 
-  // The next entry's stage, free of its last one.
-  RF4_DEV uint32_t acquire(Control& ctl, Waits& wait) const {
-    const uint32_t entry = 2 * tile + WHICH;
-    if (entry >= F::RSTAGES) {
-      const uint32_t old = entry - F::RSTAGES;
-      wait.warp(&ctl.raw_empty[old & 1][Raw::stage(old)], Raw::phase(old));
-    }
-    return Raw::stage(entry);
-  }
-
-  RF4_DEV void item(const Params& p, Control& ctl, Waits& wait, const Item& it, uint8_t* smem) {
+  RF4_DEV void item(const Params& p, Control& ctl, Waits& wait, const Item& it) {
     const int lane = threadIdx.x & 31, group = lane & 7, ps = p.c.page_size;
     int lo, hi, x;
     seen(p, it.s, it.r0 / p.G, lo, x);
     seen(p, it.s, (it.r0 + it.rows - 1) / p.G, x, hi);
     const int32_t* row = p.c.table + (int64_t)it.b * p.c.ldt;
-    const uint8_t* base = (WHICH ? p.c.V : p.c.K) + (int64_t)it.hk * ps * F::RB;
-    const int64_t page_bytes = (int64_t)p.c.Hkv * ps * F::RB;
-    int g0 = it.c0 * kTok + 16 * group, at = g0 / ps, off = g0 - at * ps;
+    const int64_t head = (int64_t)it.hk * ps * F::RB, page_bytes = (int64_t)p.c.Hkv * ps * F::RB;
+    int t0 = it.c0 * kTok, g0 = t0 + 16 * group, at = g0 / ps, off = g0 - at * ps;
     const int step = kTok / ps, rest = kTok - step * ps;
-    auto look_up = [&](int g) { return lane < 8 && g < hi && g + 16 > lo ? row[at] : -1; };
+    auto look_up = [&](int g) __attribute__((always_inline)) { return lane < 8 && g < hi && g + 16 > lo ? row[at] : -1; };
     int page = look_up(g0);
-    for (int j = 0; j < it.tiles; ++j, ++tile) {
-      const int t0 = (it.c0 + j) * kTok;
+    for (int j = 0; j < it.tiles; ++j, ++tile, t0 += kTok) {
       const bool want = lane < 8 && g0 < hi && g0 + 16 > lo, have = want && page >= 0 && page < p.c.num_pages;
-      const uint8_t* src = base + page * page_bytes + off * F::RB;
+      const int64_t src = head + page * page_bytes + (int64_t)off * F::RB;
       const uint32_t bad = __ballot_sync(0xffffffffu, want && !have), there = __ballot_sync(0xffffffffu, have);
       const bool lead = have && (lane == 0 || off == 0 || !(there >> (lane - 1) & 1u));
       const uint32_t leads = __ballot_sync(0xffffffffu, lead);
@@ -859,68 +879,83 @@ struct Loader {
       at += step;
       off += rest;
       if (off >= ps) off -= ps, ++at;
-      const int place = group * 16 * F::RB;
       page = j + 1 < it.tiles ? look_up(g0) : -1;
-      const uint32_t stage = acquire(ctl, wait);
-      if (!wait.ok) return;
-      const uint32_t bar = smem_addr(&ctl.raw_full[WHICH][stage]);
-      if (lane == 0) {
-        ctl.tiles[WHICH][tile % kTiles] = Tile{max((lo & ~15) - t0, 0), hi - t0, bad, 0};
-        if (bad) atomicOr(p.c.err, kErrBadPage);
-        mbar_arrive_expect_tx(bar, (uint32_t)__popc(there) * 16u * F::RB);
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        wait.warp(&ctl.raw_empty[ring.stage], ring.phase ^ 1u);
+        if (!wait.ok) return;
+        const uint32_t bar = smem_addr(&ctl.raw_full[ring.stage]);
+        if (lane == 0) {
+          if (which == 0) {
+            ctl.tiles[tile % kTiles] = Tile{max((lo & ~15) - t0, 0), hi - t0, bad, 0};
+            if (bad) atomicOr(p.c.err, kErrBadPage);
+          }
+          mbar_arrive_expect_tx(bar, (uint32_t)__popc(there) * 16u * F::RB);
+        }
+        __syncwarp();
+        if (lead) bulk_g2s(smem_addr(raw + ring.stage * F::RAW + group * 16 * F::RB), (which ? p.c.V : p.c.K) + src, run, bar);
+        ring.next(stages);
+        ++issued;
       }
-      __syncwarp();
-      if (lead) bulk_g2s(smem_addr(smem + F::OFF_RAW + stage * F::RAW + place), src, run, bar);
     }
   }
 
   // No more tiles.
   RF4_DEV void stop(Control& ctl, Waits& wait) {
-    const uint32_t stage = acquire(ctl, wait);
+    wait.warp(&ctl.raw_empty[ring.stage], ring.phase ^ 1u);
     if (!wait.ok) return;
     if ((threadIdx.x & 31) == 0) {
-      ctl.tiles[WHICH][tile % kTiles] = Tile{0, 0, 0, 1};
-      mbar_arrive(smem_addr(&ctl.raw_full[WHICH][stage]));
+      ctl.tiles[tile % kTiles] = Tile{0, 0, 0, 1};
+      mbar_arrive(smem_addr(&ctl.raw_full[ring.stage]));
     }
-    ++tile;
   }
 
   // Where a wait gave up: copies in flight land before the block ends.
   RF4_DEV void drain(Control& ctl, const Waits& wait) const {
     if (wait.ok) return;
-    for (uint32_t t = tile > (uint32_t)F::RSTAGES ? tile - F::RSTAGES : 0; t < tile; ++t)
-      (void)mbar_wait_bounded(smem_addr(&ctl.raw_full[WHICH][Raw::stage(2 * t + WHICH)]), Raw::phase(2 * t + WHICH));
+    for (uint32_t i = issued > (uint32_t)stages ? issued - stages : 0; i < issued; ++i)
+      (void)mbar_wait_bounded(smem_addr(&ctl.raw_full[i % stages]), i / stages & 1u);
   }
 };
 
-// Up to 128 rows of q into a swizzled tile; one warp.  A lane brings 32-value
-// blocks of rows as they are, then puts each in order (j, j + 16) in its place.
+// Up to 128 rows of q into a swizzled tile, each 32-value block in the order (j, j + 16); 128 threads.
 template <int D>
-RF4_DEV void load_q(const Params& p, const Item& it, int half, uint8_t* tile, int lane) {
-  constexpr int NB = D / 32, PANEL = kTok * 128;
-  const int blocks = min(it.rows - half * kHalf, kHalf) * NB;
-  for (int i = lane; i < blocks; i += 32) {
-    const int rr = i / NB, kb = i % NB, row = it.r0 + half * kHalf + rr, token = row / p.G, g = row - token * p.G;
-    const uint16_t* src = p.q + (int64_t)(it.s.row0 + token) * p.ldq + ((int64_t)it.hk * p.G + g) * D + kb * 32;
-    const uint32_t dst = smem_addr(tile + kb / 2 * PANEL + rr * 128);
+__device__ __noinline__ void load_q(const Params& p, const Item& it, int half, uint8_t* tile, int tid) {
+  constexpr int NB = D / 32, PANEL = kTok * 128, PASS = 128 / NB;  // rows a pass
+  const int rows = min(it.rows - half * kHalf, kHalf), kb = tid % NB;
+  int rr = tid / NB;
+#pragma unroll 1
+  for (int pass = 0; pass < kHalf / PASS; pass += 2) {
+    uint4 x[2][4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + ((((kb & 1) * 4 + c) ^ (rr & 7)) << 4)), "l"(src + 8 * c) : "memory");
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 2
-  for (int i = lane; i < blocks; i += 32) {
-    const int rr = i / NB, kb = i % NB;
-    uint8_t* dst = tile + kb / 2 * PANEL + rr * 128;
-    uint4* c[4];
+    for (int u = 0; u < 2; ++u) {
+      const int r = rr + u * PASS;
+      if (r < rows) {
+        const int row = it.r0 + half * kHalf + r, token = row / p.G, g = row - token * p.G;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(it.s.row0 + token) * p.ldq + ((int64_t)it.hk * p.G + g) * D + kb * 32);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) c[k] = reinterpret_cast<uint4*>(dst + ((((kb & 1) * 4 + k) ^ (rr & 7)) << 4));
-    // values 0-7 with 16-23, and 8-15 with 24-31
-    const uint4 w = *c[0], x = *c[1], y = *c[2], z = *c[3];
-    *c[0] = make_uint4(__byte_perm(w.x, y.x, 0x5410), __byte_perm(w.x, y.x, 0x7632), __byte_perm(w.y, y.y, 0x5410), __byte_perm(w.y, y.y, 0x7632));
-    *c[1] = make_uint4(__byte_perm(w.z, y.z, 0x5410), __byte_perm(w.z, y.z, 0x7632), __byte_perm(w.w, y.w, 0x5410), __byte_perm(w.w, y.w, 0x7632));
-    *c[2] = make_uint4(__byte_perm(x.x, z.x, 0x5410), __byte_perm(x.x, z.x, 0x7632), __byte_perm(x.y, z.y, 0x5410), __byte_perm(x.y, z.y, 0x7632));
-    *c[3] = make_uint4(__byte_perm(x.z, z.z, 0x5410), __byte_perm(x.z, z.z, 0x7632), __byte_perm(x.w, z.w, 0x5410), __byte_perm(x.w, z.w, 0x7632));
+        for (int c = 0; c < 4; ++c) x[u][c] = src[c];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = rr + u * PASS;
+      if (r < rows) {
+        uint8_t* dst = tile + kb / 2 * PANEL + r * 128;
+        // values 0-7 with 16-23, and 8-15 with 24-31
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 a = x[u][h], b = x[u][h + 2];
+          const int chunk = (kb & 1) * 4 + 2 * h;
+          *reinterpret_cast<uint4*>(dst + ((chunk ^ (r & 7)) << 4)) =
+              make_uint4(__byte_perm(a.x, b.x, 0x5410), __byte_perm(a.x, b.x, 0x7632), __byte_perm(a.y, b.y, 0x5410), __byte_perm(a.y, b.y, 0x7632));
+          *reinterpret_cast<uint4*>(dst + (((chunk + 1) ^ (r & 7)) << 4)) =
+              make_uint4(__byte_perm(a.z, b.z, 0x5410), __byte_perm(a.z, b.z, 0x7632), __byte_perm(a.w, b.w, 0x5410), __byte_perm(a.w, b.w, 0x7632));
+        }
+      }
+    }
+    rr += 2 * PASS;
+    if (rr >= rows) break;
   }
 }
 
@@ -932,43 +967,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   Control& ctl = *reinterpret_cast<Control*>(smem + F::OFF_BAR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < F::RSTAGES; ++i) {
-      for (int w = 0; w < 2; ++w) {
-        mbar_init(smem_addr(&ctl.raw_full[w][i]), 1);
-        mbar_init(smem_addr(&ctl.raw_empty[w][i]), 4);
-      }
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_addr(&ctl.k_full[i]), 4);
-      mbar_init(smem_addr(&ctl.k_empty[i]), 2);
-      mbar_init(smem_addr(&ctl.v_full[i]), 4);
-      mbar_init(smem_addr(&ctl.v_empty[i]), 2);
-      mbar_init(smem_addr(&ctl.s_full[i]), 1);
-      mbar_init(smem_addr(&ctl.p_full[i]), 4);
-      mbar_init(smem_addr(&ctl.o_full[i]), 1);
-      mbar_init(smem_addr(&ctl.turn[i]), 1);
-      mbar_init(smem_addr(&ctl.q_full[i]), 1);
-      mbar_init(smem_addr(&ctl.drained[i]), 1);
-    }
-    for (int i = 0; i < kItems; ++i) {
-      mbar_init(smem_addr(&ctl.item_full[i]), 1);
-      mbar_init(smem_addr(&ctl.item_empty[i]), 8 + 2 + 1);
-    }
-    mbar_init(smem_addr(&ctl.q_empty), 2);
+  if (threadIdx.x < kBars) {
+    const int i = threadIdx.x;
+    const uint32_t arrivals = i < 4 ? 4 : i < 8 ? 2 : i < 16 ? 1 : i < 20 ? 4 : i < 20 + kMaxRaw ? 1 : i < 20 + 2 * kMaxRaw ? 4 : i < 20 + 2 * kMaxRaw + kItems ? 1 : 8 + 2;
+    mbar_init(smem_addr(reinterpret_cast<uint64_t*>(&ctl) + i), arrivals);
     fence_mbar_init();
   }
-  grid_dependency_wait();  // lengths, tables and everything else may be the preceding kernel's output
-  if (!find_work(p, ctl)) return;
-  if (warp == 16) {
+  if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&ctl.tmem)), "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   tc_fence_before();
+  grid_dependency_wait();  // lengths, tables and everything else may be the preceding kernel's output
+  bool any_wide;
+  const bool busy = find_work(p, ctl, any_wide);
   __syncthreads();
   tc_fence_after();
+  if (!busy) {
+    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(ctl.tmem), "r"(512));
+    return;
+  }
   const uint32_t tmem = ctl.tmem;
   // columns: S (and P) of chain t at 128 t, O at 256 + D t
+  const int raw_stages = any_wide ? F::RSTAGES : F::RSTAGES_NARROW;
+  uint8_t* raw = smem + (any_wide ? F::OFF_RAW : F::OFF_Q1);
   Waits wait;
 
   if (warp < 8) {
@@ -979,38 +1001,52 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
     const uint32_t s_at = tmem + lanes + 128u * t, o_at = tmem + lanes + 256u + (uint32_t)D * t;
     uint32_t n_s = 0, n_o = 0;  // uses of s_full and o_full
     Items items;
-    Item it;
-    while (items.next(ctl, wait, it)) {
+    // Chain t's half of a row tile's queries; a narrow tile's one half is chain 0's to bring.
+    auto bring_q = [&](const Item& of) __attribute__((always_inline)) {
+      if (t == 1 && !of.wide) return;
+      load_q<D>(p, of, t, smem + (t ? F::OFF_Q1 : F::OFF_Q0), r);
+      fence_proxy_async();
       __syncwarp();
-      if (lane == 0) items.done(ctl); else ++items.n;
-      const int row = it.r0 + (it.wide ? t * kHalf : 0) + r;
-      const bool used = row < it.r0 + it.rows;
+      if (lane == 0) mbar_arrive(smem_addr(&ctl.q_full[t]));
+    };
+    const Item* at = items.get(ctl, wait);
+    if (at) bring_q(*at);
+    for (const Item* nx; at; at = nx, items.done(ctl)) {
+      const Item& it = *at;
+      const int wide = it.wide, tiles = it.tiles, tile0 = it.tile, c0 = it.c0;
+      const bool whole = it.first == it.last;
+      const int row = it.r0 + (wide ? t * kHalf : 0) + r;
+      const bool used = row < it.r0 + it.rows, idle = row - lane >= it.r0 + it.rows;  // idle: none of the warp's rows is used
       int lo = 0, hi = 0;
       if (used) seen(p, it.s, row / p.G, lo, hi);
       Row st;
       bool first = true;
-      for (int j = it.wide ? 0 : t; j < it.tiles; j += it.wide ? 1 : 2) {
-        const int t0 = (it.c0 + j) * kTok;
+      for (int j = wide ? 0 : t; j < tiles; j += wide ? 1 : 2) {
+        const int t0 = (c0 + j) * kTok;
         const int a = max(lo - t0, 0), e = min(max(hi - t0, 0), kTok);
         wait.warp(&ctl.s_full[t], n_s++ & 1u);
         tc_fence_after();
-        const uint32_t bad = ctl.tiles[0][(it.tile + j) % kTiles].bad;
-        if (__any_sync(0xffffffffu, used && (a > 0 || e < kTok)) || bad)
-          softmax_tile<D, true>(s_at, o_at, st, p.scale_log2, first, used, a, e, bad);
-        else if (first)
-          softmax_tile<D, false>(s_at, o_at, st, p.scale_log2, true, used, 0, kTok, 0);
-        else
-          softmax_next<D>(s_at, o_at, st, p.scale_log2, used);
+        const uint32_t bad = ctl.tiles[(tile0 + j) % kTiles].bad;
+        const bool part = __any_sync(0xffffffffu, used && (a > 0 || e < kTok)) || bad;
+        // (P of rows that nobody reads may be anything)
+        if (!idle && (part || first || !softmax_next<D>(s_at, st, p.scale_log2, used)))
+          softmax_tile<D>(s_at, o_at, st, p.scale_log2, first, used, a, e, bad);
         first = false;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&ctl.p_full[t]));
       }
+      // The last scores are there, so this chain's products are done with its
+      // queries: the next row tile's take their place while the output of this
+      // one is dealt with.  A narrow tile's queries are the other chain's as
+      // well, whose end the synchronisation below tells.
+      nx = items.get(ctl, wait, 1);
+      if (nx && wide) bring_q(*nx);
       if (!first) {
         wait.warp(&ctl.o_full[t], n_o++ & 1u);
         tc_fence_after();
       }
-      if (it.wide && it.first == it.last) {
+      if (wide && whole) {
         // the whole of this row is here
         const float inv = st.l == 0.f ? 0.f : 1.f / st.l;
         const int token = row / p.G, g = row - token * p.G;
@@ -1019,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         for (int c = 0; c < D; c += 32) {
           float x[32];
           tmem_ld32(o_at + c, x);
-          tmem_wait_ld();
+          tmem_wait_ld(x);
           if (used) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -1044,7 +1080,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         for (int c = 0; c < D; c += 32) {
           float x[32];
           tmem_ld32(o_at + c, x);
-          tmem_wait_ld();
+          tmem_wait_ld(x);
           if (used) {
             float4* w = reinterpret_cast<float4*>(p.ws + mine * D + c);
 #pragma unroll
@@ -1056,7 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
       __threadfence();
       chains_sync();
       bool merge = true;
-      if (it.first != it.last) {
+      if (!whole) {
         if (threadIdx.x == 0) {
           const uint32_t n = atomic_add_acq_rel_gpu(&p.cnt[it.first], 1u);
           ctl.last = n == (uint32_t)(it.last - it.first);
@@ -1070,42 +1106,45 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         merge_parts<D, ACT>(p, it, ml);
       }
       chains_sync();  // the records and ctl.last may be written again
+      if (nx && !wide) bring_q(*nx);
     }
-  } else if (warp < 16) {
+  } else if (warp < 12) {
     // ---- decode ----
     give_registers<kOtherRegs>();
-    const int which = warp >> 2 & 1;  // 0: K, 1: V
     const int row = threadIdx.x & (kTok - 1);
-    uint64_t* full = which ? ctl.v_full : ctl.k_full;
-    uint64_t* empty = which ? ctl.v_empty : ctl.k_empty;
-    uint8_t* tiles = smem + (which ? F::OFF_V : F::OFF_K);
-    using Raw = RawRing<F::RSTAGES>;
-    Ring kv;
-    for (uint32_t n = 0;; ++n) {
-      const uint32_t entry = 2 * n + which, stage = Raw::stage(entry);
-      wait.warp(&ctl.raw_full[which][stage], Raw::phase(entry));
-      if (!wait.ok) break;
-      const Tile tile = ctl.tiles[which][n % kTiles];
-      if (tile.stop) break;
-      wait.warp(&empty[kv.stage], kv.phase ^ 1u);
-      if (!wait.ok) break;
-      const uint8_t* src = smem + F::OFF_RAW + stage * F::RAW;
-      const bool real = row >= tile.from && row < tile.to && !(tile.bad >> (row >> 4) & 1u);
-      if (ACT == 1 && which == 0)
-        decode_row<V, D, true>(src, tiles + kv.stage * F::TILE, row, real);
-      else
-        decode_row<V, D, false>(src, tiles + kv.stage * F::TILE, row, real);
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_addr(&ctl.raw_empty[which][stage]));
-        mbar_arrive(smem_addr(&full[kv.stage]));
+    Ring ring, kv;
+    for (uint32_t n = 0;; ++n, kv.next(F::STAGES)) {
+      bool real = false;
+#pragma unroll 1
+      for (int which = 0; which < 2; ++which) {
+        wait.warp(&ctl.raw_full[ring.stage], ring.phase);
+        if (!wait.ok) break;
+        if (which == 0) {
+          const Tile tile = ctl.tiles[n % kTiles];
+          if (tile.stop) break;
+          real = row >= tile.from && row < tile.to && !(tile.bad >> (row >> 4) & 1u);
+        }
+        wait.warp(which ? &ctl.v_empty[kv.stage] : &ctl.k_empty[kv.stage], kv.phase ^ 1u);
+        if (!wait.ok) break;
+        const uint8_t* src = raw + ring.stage * F::RAW;
+        uint8_t* dst = smem + (which ? F::OFF_V : F::OFF_K) + kv.stage * F::TILE;
+        if (ACT == 1 && which == 0)
+          decode_row<V, D, true>(src, dst, row, real);
+        else
+          decode_row<V, D, false>(src, dst, row, real);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_addr(&ctl.raw_empty[ring.stage]));
+          mbar_arrive(smem_addr(which ? &ctl.v_full[kv.stage] : &ctl.k_full[kv.stage]));
+        }
+        ring.next(raw_stages);
       }
-      kv.next(F::STAGES);
+      if (!wait.ok || ctl.tiles[n % kTiles].stop) break;
     }
   } else {
     give_registers<kOtherRegs>();
-    if (warp == 16 || warp == 19) {
+    if (warp < 14) {
       // ---- MMA issue ----
       // The whole warp walks along, one elected lane issues: what the
       // instructions take is then uniform and stays in uniform registers.  A
@@ -1113,24 +1152,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
       // its next token tile comes after the product that reads P in its place.
       constexpr uint32_t id_s = instr_desc(ACT, kTok, 0), id_o = instr_desc(0, D, 1);
       constexpr uint32_t desc_hi = (1024u >> 4) | 1u << 14 | 2u << 29;
-      const uint32_t t = warp == 19;
-      const uint32_t q_lo = (smem_addr(smem + F::OFF_Q) >> 4) | 1u << 16, k_lo = (smem_addr(smem + F::OFF_K) >> 4) | 1u << 16;
+      const uint32_t t = warp == 13;
+      const uint32_t q_lo = (smem_addr(smem + F::OFF_Q0) >> 4) | 1u << 16, k_lo = (smem_addr(smem + F::OFF_K) >> 4) | 1u << 16;
       const uint32_t v_lo = (smem_addr(smem + F::OFF_V) >> 4) | (uint32_t)(F::PANEL >> 4) << 16;
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t s_at = tm + 128u * t, o_at = tm + 256u + (uint32_t)D * t;
       Ring kr, vr;
       uint32_t n_q0 = 0, n_q1 = 0, n_p = 0, n_turn = 0;
       Items items;
-      Item it;
-      while (items.next(ctl, wait, it)) {
-        __syncwarp();
-        if (lane == 0) items.done(ctl); else ++items.n;
-        const uint32_t wide = __shfl_sync(0xffffffffu, it.wide, 0);
-        const int tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
-        int left = wide ? tiles : (tiles + 1 - (int)t) >> 1;  // scores of this chain to come
+      while (const Item* it = items.get(ctl, wait)) {
+        const uint32_t wide = __shfl_sync(0xffffffffu, it->wide, 0);
+        const int tiles = __shfl_sync(0xffffffffu, it->tiles, 0);
+        items.done(ctl);
         int kj = 0, vj = 0;
         // Goes on to this chain's next tile of K (or V) and waits for it; the other chain's tiles are let go.
-        auto next_own = [&](Ring& r, int& j, uint64_t* full, uint64_t* empty) {
+        auto next_own = [&](Ring& r, int& j, uint64_t* full, uint64_t* empty) __attribute__((always_inline)) {
           for (; j < tiles; ++j) {
             wait.warp(&full[r.stage], r.phase);
             if (wide || (j & 1) == (int)t) return true;
@@ -1139,7 +1175,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
           }
           return false;
         };
-        auto scores = [&]() {
+        auto scores = [&]() __attribute__((always_inline)) {
           tc_fence_after();
           const uint32_t a = q_lo + (wide & t) * (F::TILE >> 4), b = k_lo + kr.stage * (F::TILE >> 4);
           if (elect_one()) {
@@ -1150,52 +1186,52 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
             }
             mma_commit(smem_addr(&ctl.s_full[t]));
             mma_commit(smem_addr(&ctl.k_empty[kr.stage]));
-            if (left == 1) mma_commit(smem_addr(&ctl.q_empty));
           }
           __syncwarp();
-          --left;
           ++kj;
           kr.next(F::STAGES);
         };
-        bool have = next_own(kr, kj, ctl.k_full, ctl.k_empty);
-        wait.warp(&ctl.q_full[0], n_q0++ & 1u);
-        if (wide) {
-          if (t == 1) wait.warp(&ctl.q_full[1], n_q1 & 1u);
-          ++n_q1;
-        }
-        if (have) scores();
-        else if (lane == 0) mbar_arrive(smem_addr(&ctl.q_empty));
-        uint32_t again = 0;  // O holds something already
         // The chains take turns at the tensor core, product and next scores in
         // one go: left to themselves they fall into step, both at their softmax
         // and then both at half the core's rate (4.8k cycles a token tile).
+        bool have = false;  // scores of a tile are on their way, or P of it
+        uint32_t again = 0;  // O holds something already
 #pragma unroll 1
-        for (int round = wide ? tiles : (tiles + 1) >> 1; round > 0; --round) {
-          if (!have) {  // an odd tile, the other chain's
-            wait.warp(&ctl.turn[t], (n_turn++ & 1u) ^ (t ^ 1u));
-            if (lane == 0) mbar_arrive(smem_addr(&ctl.turn[t ^ 1]));
-            break;
-          }
+        for (;;) {
           // K's and V's next tiles are there before P, mostly: only that wait counts
-          next_own(vr, vj, ctl.v_full, ctl.v_empty);
+          // (V's first, for a tile of the other chain's to be let go that K's may wait for)
+          if (have) next_own(vr, vj, ctl.v_full, ctl.v_empty);
           const bool more = next_own(kr, kj, ctl.k_full, ctl.k_empty);
-          wait.warp(&ctl.turn[t], (n_turn++ & 1u) ^ (t ^ 1u));
-          wait.warp(&ctl.p_full[t], n_p++ & 1u);
-          tc_fence_after();
-          const uint32_t b = v_lo + vr.stage * (F::TILE >> 4);
-          if (elect_one()) {
+          if (!have) {
+            // a chain waits for its own queries alone: the other half's barrier may be two phases ahead
+            const uint32_t half = wide & t;
+            wait.warp(&ctl.q_full[half], (half ? n_q1 : n_q0) & 1u);
+            ++n_q0;
+            n_q1 += wide;
+          } else {
+            wait.warp(&ctl.turn[t], (n_turn++ & 1u) ^ (t ^ 1u));
+            wait.warp(&ctl.p_full[t], n_p++ & 1u);
+            tc_fence_after();
+            const uint32_t b = v_lo + vr.stage * (F::TILE >> 4);
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kTok / 16; ++k) mma_ts(o_at, s_at + 8u * k, b + k * (2048 >> 4), desc_hi, id_o, again | (k != 0));
-            mma_commit(smem_addr(&ctl.v_empty[vr.stage]));
-            if (!more) mma_commit(smem_addr(&ctl.o_full[t]));
+              for (int k = 0; k < kTok / 16; ++k) mma_ts(o_at, s_at + 8u * k, b + k * (2048 >> 4), desc_hi, id_o, again | (k != 0));
+              mma_commit(smem_addr(&ctl.v_empty[vr.stage]));
+              if (!more) mma_commit(smem_addr(&ctl.o_full[t]));
+            }
+            __syncwarp();
+            again = 1;
+            ++vj;
+            vr.next(F::STAGES);
           }
-          __syncwarp();
-          again = 1;
-          ++vj;
-          vr.next(F::STAGES);
           if (more) scores();
-          if (lane == 0) mbar_arrive(smem_addr(&ctl.turn[t ^ 1]));
-          have = more;
+          if (have && lane == 0) mbar_arrive(smem_addr(&ctl.turn[t ^ 1]));
+          if (!more) break;
+          have = true;
+        }
+        if (t == 1 && !wide && (tiles & 1)) {  // an odd tile, the other chain's
+          wait.warp(&ctl.turn[1], n_turn++ & 1u);
+          if (lane == 0) mbar_arrive(smem_addr(&ctl.turn[0]));
         }
         next_own(vr, vj, ctl.v_full, ctl.v_empty);  // the other chain's last tile, perhaps
       }
@@ -1204,47 +1240,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         (void)mbar_wait_bounded(smem_addr(&ctl.drained[t]), 0);
       }
       __syncwarp();
-    } else if (warp == 17) {
-      // ---- items, K's raw rows ----
+    } else if (warp == 14) {
+      // ---- row tiles, raw rows ----
       Walk walk(p, ctl);
-      Loader<V, D, 0> load;
-      uint32_t n_items = 0;
+      Loader<V, D> load(raw_stages, raw);
+      uint32_t n = 0;
       Item it;
-      for (bool more = true; more && wait.ok; ++n_items) {
+      for (bool more = true; more && wait.ok; ++n) {
         more = walk.next(p, it);
-        wait.warp(&ctl.item_empty[n_items % kItems], ((n_items / kItems) & 1u) ^ 1u);
+        wait.warp(&ctl.item_empty[n % kItems], ((n / kItems) & 1u) ^ 1u);
         if (!wait.ok) break;
         if (!more) it.rows = 0;
         it.tile = load.tile;
         if (lane == 0) {
-          ctl.items[n_items % kItems] = it;
-          mbar_arrive(smem_addr(&ctl.item_full[n_items % kItems]));
+          ctl.items[n % kItems] = it;
+          mbar_arrive(smem_addr(&ctl.item_full[n % kItems]));
           if (more && it.s.len > it.s.lim) atomicOr(p.c.err, kErrBadPage);
         }
-        if (more) load.item(p, ctl, wait, it, smem);
+        if (more) load.item(p, ctl, wait, it);
         else load.stop(ctl, wait);
       }
-      load.drain(ctl, wait);
-    } else {
-      // ---- Q rows, V's raw rows ----
-      Loader<V, D, 1> load;
-      uint32_t n_q = 0;
-      Items items;
-      Item it;
-      while (items.next(ctl, wait, it)) {
-        __syncwarp();
-        if (lane == 0) items.done(ctl); else ++items.n;
-        wait.warp(&ctl.q_empty, (n_q++ & 1u) ^ 1u);
-#pragma unroll 1
-        for (int half = 0; half <= it.wide; ++half) {
-          load_q<D>(p, it, half, smem + F::OFF_Q + half * F::TILE, lane);
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&ctl.q_full[half]));
-        }
-        load.item(p, ctl, wait, it, smem);
-      }
-      if (wait.ok) load.stop(ctl, wait);
       load.drain(ctl, wait);
     }
   }
@@ -1252,7 +1267,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
 using Fn = void (*)(Params);
