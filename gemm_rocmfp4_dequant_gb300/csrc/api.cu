@@ -79,6 +79,7 @@ rocmfp4_status moe_set_up(DeviceState& d) {
 // Paged attention's workspace (57 MiB on 152 SMs), made in the same manner.
 rocmfp4_status paged_set_up(DeviceState& d) {
   cudaError_t e = paged_attn_prepare();
+  if (e == cudaSuccess) e = paged_few_prepare();
   if (e != cudaSuccess) return cuda_fail(e, "paged attention kernel set-up");
   cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
   if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return cuda_fail(e, "cudaThreadExchangeStreamCaptureMode");
@@ -137,8 +138,8 @@ rocmfp4_status device_state(DeviceState** out, Needs needs = Needs::kProducts) {
       return cuda_fail(e, "cudaMemset");
     if ((e = cudaMalloc(&d.moe_bars, sizeof(uint32_t) * kMoeBarWords)) != cudaSuccess) return cuda_fail(e, "cudaMalloc");
     if ((e = cudaMemset(d.moe_bars, 0, sizeof(uint32_t) * kMoeBarWords)) != cudaSuccess) return cuda_fail(e, "cudaMemset");
-    if ((e = cudaMalloc(&d.paged_cnt, sizeof(uint32_t) * d.sms)) != cudaSuccess) return cuda_fail(e, "cudaMalloc");
-    if ((e = cudaMemset(d.paged_cnt, 0, sizeof(uint32_t) * d.sms)) != cudaSuccess) return cuda_fail(e, "cudaMemset");
+    if ((e = cudaMalloc(&d.paged_cnt, sizeof(uint32_t) * 2 * d.sms)) != cudaSuccess) return cuda_fail(e, "cudaMalloc");
+    if ((e = cudaMemset(d.paged_cnt, 0, sizeof(uint32_t) * 2 * d.sms)) != cudaSuccess) return cuda_fail(e, "cudaMemset");
     if ((e = cudaMemset(d.err, 0, sizeof(uint32_t))) != cudaSuccess) return cuda_fail(e, "cudaMemset");
     if ((e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
     d.ready = true;
@@ -608,7 +609,11 @@ rocmfp4_status paged_attention(const rocmfp4_paged_cache* cache, PagedAttnArgs a
   a.cache.err = d->err;
   a.ws = d->paged_ws;
   a.cnt = d->paged_cnt;
-  cudaError_t e = launch_paged_attention(cache->variant, act, a, d->sms, s);
+  // At most eight (row, head) pairs a sequence and KV head, on the average: the
+  // kernel of few rows; else 128-row tiles.  (The lengths of the chunks are on
+  // the device; either kernel is right for any.)
+  const bool few = a.M * (H / cache->Hkv) <= 8 * cache->B;
+  cudaError_t e = few ? launch_paged_few(cache->variant, act, a, d->sms, s) : launch_paged_attention(cache->variant, act, a, d->sms, s);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   g_launches.fetch_add(1);
   return ROCMFP4_OK;
@@ -938,7 +943,7 @@ uint32_t rocmfp4_device_error_bits(rocmfp4_stream_t stream) {
       cudaMemsetAsync(d->cnt, 0, sizeof(uint32_t) * d->wmax, s);
       cudaMemsetAsync(d->tccnt, 0, sizeof(uint32_t) * tc_cnt_words(d->sms), s);
       cudaMemsetAsync(d->moe_bars, 0, sizeof(uint32_t) * kMoeBarWords, s);
-      cudaMemsetAsync(d->paged_cnt, 0, sizeof(uint32_t) * d->sms, s);
+      cudaMemsetAsync(d->paged_cnt, 0, sizeof(uint32_t) * 2 * d->sms, s);
       if (cudaStreamSynchronize(s) != cudaSuccess) return 0xFFFFFFFFu;
     }
   }

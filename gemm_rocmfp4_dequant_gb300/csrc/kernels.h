@@ -180,11 +180,14 @@ struct PagedAttnArgs {
   int H, causal, window;
   float scale;
   float* ws;          // paged_attn_ws_floats(sms) floats
-  uint32_t* cnt;      // sms words, zero between launches
+  uint32_t* cnt;      // 2 * sms words, zero between launches
   PagedArgs cache;
 };
 size_t paged_attn_ws_floats(int sms);
 cudaError_t paged_attn_prepare();
+// The same for few rows (paged_few.cu).
+cudaError_t paged_few_prepare();
+cudaError_t launch_paged_few(int variant, int act, const PagedAttnArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_paged_attention(int variant, int act, const PagedAttnArgs& a, int sms, cudaStream_t s);
 
 // Any K % 32 == 0, any alignment: one warp per (row, column chunk).

@@ -30,11 +30,7 @@
 // order and K as it falls out; V's columns, and so O's, are in it too, and the
 // output puts them back.
 //
-// Work.  All token tiles of all row tiles are numbered in one row (sequence,
-// KV head, row tile, token tile; a wide one counts twice) and every CTA takes an
-// equal stretch of it, by the lengths on the device.  A row tile that falls to
-// several CTAs leaves unnormalised parts in the workspace; the CTA that arrives
-// last adds them in order.  Nothing waits for another CTA.
+// Work: see paged_work.cuh; a wide tile's token tile counts twice.
 //
 // Warps (512 threads), registers moved from the others to the softmax:
 //   0-3, 4-7   Q rows, softmax and output of chain 0 and 1
@@ -52,6 +48,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "paged_work.cuh"
 
 namespace rocmfp4 {
 namespace {
@@ -59,8 +56,6 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kTok = 128;     // tokens per tile
 constexpr int kHalf = 128;    // rows per chain
-constexpr int kWideCost = 3, kNarrowCost = 1;  // fixed work of a row tile
-constexpr int kMinShare = 4;  // narrow token tiles that are worth a CTA
 constexpr int kMaxRaw = 8;    // stages of the raw ring
 constexpr int kTiles = 16;    // token tiles described at a time
 constexpr int kItems = 4;     // row tiles described at a time
@@ -70,13 +65,12 @@ constexpr float kGrow = 8.f;  // log2 of how far a maximum may lead its referenc
 constexpr float kLift = 7.f;  // log2 of P's factor
 constexpr float kLog2e = 1.4426950408889634f;
 
-struct Params {
+struct Params : Batch {
   const uint16_t* q;
   uint16_t* out;
   int64_t ldq;
-  int M, H, G, causal, window;
+  int H;
   float scale_log2;
-  PagedArgs c;
   float* ws;      // [ctas][kSlots][2][kHalf] rows of D, then as many pairs (m, l)
   uint32_t* cnt;  // [ctas], zero between launches
 };
@@ -103,22 +97,6 @@ struct Plan {
   static_assert(RAW % 16 == 0, "bulk copies");
 };
 
-struct Seq {
-  int row0, n;  // rows of the call
-  int len;      // tokens
-  int lim;      // tokens that the table has room for
-};
-
-// A row tile's share of this CTA.
-struct Item {
-  int b, hk, r0, rows, wide;  // rows 0: no more items
-  int c0, tiles;              // this CTA's token tiles
-  Seq s;
-  int first, last;  // CTAs that share the row tile
-  int slot;         // of this CTA's part
-  int tile;         // number of the first token tile among this CTA's
-};
-
 // A token tile: rows from .. to - 1 of it were copied, but for `bad` groups of 16.
 struct Tile {
   int from, to;
@@ -136,18 +114,19 @@ struct Control {  // at OFF_BAR
   uint64_t raw_empty[kMaxRaw];                         // 4: decode warps
   uint64_t item_full[kItems];                          // 1
   uint64_t item_empty[kItems];                         // 8 + 2: softmax and MMA warps
-  long long start, end, total;  // of this CTA's stretch; of all work
-  long long base;               // where the first row tile begins
-  long long scan[kThreads / 32];
-  int scan_items[kThreads / 32];
-  int b, hk, k, ctas;
+  Stretch work;
   int last;
   uint32_t tmem;
   Item items[kItems];
   Tile tiles[kTiles];
 };
 constexpr int kBars = 20 + 2 * kMaxRaw + 2 * kItems;
-static_assert(offsetof(Control, start) == 8 * kBars && sizeof(Control) <= 2048, "control block");
+static_assert(offsetof(Control, work) == 8 * kBars && sizeof(Control) <= 2048, "control block");
+
+struct Shape {
+  static constexpr int kRows = 2 * kHalf, kNarrow = kHalf, kTok = 128, kMinShare = 4;
+  static RF4_DEV int fixed(int weight) { return weight == 2 ? 3 : 1; }
+};
 
 // ---- tensor-core instructions -------------------------------------------------
 RF4_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -291,239 +270,6 @@ struct Ring {
     }
   }
 };
-
-// ---- work -----------------------------------------------------------------------
-RF4_DEV Seq sequence(const Params& p, int b) {
-  Seq s;
-  const int r0 = min(max(p.c.cu[b], 0), p.M), r1 = min(max(p.c.cu[b + 1], 0), p.M);
-  s.row0 = r0;
-  s.n = max(r1 - r0, 0);
-  s.len = max(p.c.lens[b], 0);
-  const long long room = (long long)p.c.width * p.c.page_size;
-  s.lim = (int)(s.len < room ? s.len : room);
-  return s;
-}
-
-// Tokens lo .. hi - 1 that row i of a sequence's chunk sees.
-RF4_DEV void seen(const Params& p, const Seq& s, int i, int& lo, int& hi) {
-  lo = 0;
-  hi = s.lim;
-  if (p.causal) {
-    const long long end = (long long)s.len - s.n + i + 1;
-    hi = (int)(end < 0 ? 0 : end < s.lim ? end : s.lim);
-    if (p.window > 0 && end > p.window) lo = (int)(end - p.window < hi ? end - p.window : hi);
-  }
-}
-
-struct RowTile {
-  int rows, weight;  // rows; work of one token tile
-  int c0, tiles;     // first token tile, and how many (at least one)
-  // Work of the whole: its token tiles behind a fixed part, for what a row
-  // tile costs whatever its length (queries, output).
-  RF4_DEV int fixed() const { return weight == 2 ? kWideCost : kNarrowCost; }
-  RF4_DEV long long all() const { return fixed() + (long long)tiles * weight; }
-};
-
-RF4_DEV RowTile row_tile(const Params& p, const Seq& s, int k) {
-  RowTile t;
-  const int r0 = k * 2 * kHalf;
-  t.rows = min(2 * kHalf, s.n * p.G - r0);
-  t.weight = t.rows > kHalf ? 2 : 1;
-  int lo, hi, x;
-  seen(p, s, r0 / p.G, lo, x);
-  seen(p, s, (r0 + t.rows - 1) / p.G, x, hi);
-  t.c0 = lo / kTok;
-  t.tiles = max(1, (hi + kTok - 1) / kTok - t.c0);
-  return t;
-}
-
-struct Walk {
-  int b, hk, k, ctas;
-  long long base, start, end, total;
-  Seq s;
-  RF4_DEV Walk(const Params& p, const Control& ctl)
-      : b(ctl.b), hk(ctl.hk), k(ctl.k), ctas(ctl.ctas), base(ctl.base), start(ctl.start), end(ctl.end), total(ctl.total) {
-    s = sequence(p, b);
-  }
-  RF4_DEV int owner(long long u) const {
-    if (total < 1 << 22) return (int)(((uint32_t)(u + 1) * ctas - 1) / (uint32_t)total);
-    return (int)(((u + 1) * ctas - 1) / total);
-  }
-  RF4_DEV bool next(const Params& p, Item& it) {
-    while (base < end) {
-      const RowTile t = row_tile(p, s, k);
-      // token tiles whose places lie in start .. end - 1
-      const long long at = base + t.fixed();
-      const long long from = start - at + t.weight - 1, to = end - at + t.weight - 1;
-      const int j0 = from <= 0 ? 0 : from >> (t.weight - 1) < t.tiles ? (int)(from >> (t.weight - 1)) : t.tiles;
-      const int j1 = to <= 0 ? 0 : to >> (t.weight - 1) < t.tiles ? (int)(to >> (t.weight - 1)) : t.tiles;
-      it.b = b;
-      it.hk = hk;
-      it.r0 = k * 2 * kHalf;
-      it.rows = t.rows;
-      it.wide = t.weight - 1;
-      it.c0 = t.c0 + j0;
-      it.tiles = j1 - j0;
-      it.s = s;
-      it.first = it.last = blockIdx.x;
-      it.slot = 2;
-      if (j0 > 0 || j1 < t.tiles) {
-        it.first = owner(at);
-        it.last = owner(at + (long long)(t.tiles - 1) * t.weight);
-        it.slot = j0 > 0 ? 0 : 1;
-      }
-      base += t.all();
-      if ((long long)(++k) * 2 * kHalf >= (long long)s.n * p.G) {
-        k = 0;
-        if (++hk == p.c.Hkv) {
-          hk = 0;
-          do {
-            if (++b >= p.c.B) {
-              base = total;
-              break;
-            }
-            s = sequence(p, b);
-          } while (s.n == 0);
-        }
-      }
-      if (j0 < j1) return true;
-    }
-    return false;
-  }
-};
-
-struct Work {
-  long long cost;
-  int tiles;  // row tiles; negative: some is wide
-};
-
-// Work of sequence b for one KV head: row tiles lane, lane + step, ...
-RF4_DEV Work work_of(const Params& p, int b, int lane, int step) {
-  const Seq s = sequence(p, b);
-  const int tiles = (s.n * p.G + 2 * kHalf - 1) / (2 * kHalf);
-  Work w{0, 0};
-  bool wide = false;
-  for (int k = lane; k < tiles; k += step) {
-    const RowTile t = row_tile(p, s, k);
-    w.cost += t.all();
-    ++w.tiles;
-    wide |= t.weight > 1;
-  }
-  if (wide) w.tiles = -w.tiles;
-  return w;
-}
-
-RF4_DEV long long divide(long long a, long long b) {
-  if ((a | b) >> 31 == 0) return (uint32_t)a / (uint32_t)b;  // the short division
-  return a / b;
-}
-
-// This CTA's stretch and where it begins; false if it has none.  `any`: whether
-// some row tile of the call is wide.  All threads.
-RF4_DEV bool find_work(const Params& p, Control& ctl, bool& any) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, B = p.c.B;
-  // few sequences: a warp each, its lanes over row tiles; many: a thread each, or several in a row
-  const bool by_warp = B <= kThreads / 32;
-  const int per = (B + kThreads - 1) / kThreads;
-  const int b0 = by_warp ? min(warp, B) : min(tid * per, B), b1 = by_warp ? min(warp + 1, B) : min(b0 + per, B);
-  long long mine = 0;
-  int items = 0;
-  bool wide = false;
-  for (int b = b0; b < b1; ++b) {
-    const Work w = work_of(p, b, by_warp ? lane : 0, by_warp ? 32 : 1);
-    mine += w.cost * p.c.Hkv;
-    items += abs(w.tiles) * p.c.Hkv;
-    wide |= w.tiles < 0;
-  }
-  if (by_warp) {
-#pragma unroll 1
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane != 0) mine = 0;
-  }
-  long long before = mine;  // inclusive within the warp
-#pragma unroll 1
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += v;
-  }
-  items = __reduce_add_sync(0xffffffffu, items);
-  if (lane == 31) {
-    ctl.scan[warp] = before;
-    ctl.scan_items[warp] = items;
-  }
-  const int any_wide = __syncthreads_or(wide);
-  any = any_wide;
-  long long total = 0, lower = 0;
-  items = 0;
-#pragma unroll 4
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w == warp) lower = total;
-    total += ctl.scan[w];
-    items += ctl.scan_items[w];
-  }
-  before += lower - mine;
-  // A CTA for every row tile, or for every kMinShare token tiles where that
-  // is more.  A wide token tile counts 2, and a CTA's stretch is never
-  // shorter than one, so that every CTA between the first and the last of a
-  // shared row tile has a part of it.
-  long long most = total / kMinShare;
-  most = most > items ? most : items;
-  if (any_wide) most = most < total / 2 ? most : total / 2;
-  if (most < 1) most = 1;
-  const int ctas = (int)(most < (long long)gridDim.x ? most : (long long)gridDim.x);
-  if (total == 0 || (int)blockIdx.x >= ctas) return false;
-  const long long start = divide(total * blockIdx.x, ctas), end = divide(total * (blockIdx.x + 1), ctas);
-  const uint32_t hit = __ballot_sync(0xffffffffu, start >= before && start < before + mine);
-  if (hit) {  // one warp: the sequence of one of its lanes, then the row tile, 32 at a time
-    int b = b0;
-    long long base = before, w = mine;
-    if (!by_warp)
-      for (; b < b1; ++b) {
-        w = work_of(p, b, 0, 1).cost * p.c.Hkv;
-        if (start < base + w) break;
-        base += w;
-      }
-    const int from = __ffs(hit) - 1;
-    b = __shfl_sync(0xffffffffu, b, from);
-    base = __shfl_sync(0xffffffffu, base, from);
-    w = __shfl_sync(0xffffffffu, w, from);
-    const long long head = divide(w, p.c.Hkv);
-    const int hk = (int)divide(start - base, head);
-    base += hk * head;
-    const Seq s = sequence(p, b);
-    for (int k0 = 0;; k0 += 32) {
-      const int k = k0 + lane;
-      long long all = 0;
-      if ((long long)k * 2 * kHalf < (long long)s.n * p.G) {
-        const RowTile t = row_tile(p, s, k);
-        all = t.all();
-      }
-      long long upto = all;
-#pragma unroll 1
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-      }
-      const uint32_t in = __ballot_sync(0xffffffffu, start < base + upto);
-      if (in) {
-        if (lane == __ffs(in) - 1) {
-          ctl.b = b;
-          ctl.hk = hk;
-          ctl.k = k;
-          ctl.base = base + upto - all;
-          ctl.start = start;
-          ctl.end = end;
-          ctl.total = total;
-          ctl.ctas = ctas;
-        }
-        break;
-      }
-      base += __shfl_sync(0xffffffffu, upto, 31);
-    }
-  }
-  __syncthreads();
-  return true;
-}
 
 // ---- decode ---------------------------------------------------------------------
 template <int N>
@@ -980,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
   tc_fence_before();
   grid_dependency_wait();  // lengths, tables and everything else may be the preceding kernel's output
   bool any_wide;
-  const bool busy = find_work(p, ctl, any_wide);
+  const bool busy = find_work<Shape, kThreads>(p, ctl.work, any_wide);
   __syncthreads();
   tc_fence_after();
   if (!busy) {
@@ -1242,7 +988,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
       __syncwarp();
     } else if (warp == 14) {
       // ---- row tiles, raw rows ----
-      Walk walk(p, ctl);
+      Walk<Shape> walk(p, ctl.work);
       Loader<V, D> load(raw_stages, raw);
       uint32_t n = 0;
       Item it;
