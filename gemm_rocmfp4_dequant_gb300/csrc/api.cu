@@ -552,7 +552,7 @@ rocmfp4_status rope(RopeArgs a, const rocmfp4_paged_cache* cache, cudaStream_t s
   if (!aligned_to(a.freq, 0) || !aligned_to(a.positions, 0) || !aligned_to(a.q_out, ROCMFP4_OUT_F16))
     return fail(ROCMFP4_ERR_INVALID_ARG, "misaligned pointer");
   if (a.D > 256) return fail(ROCMFP4_ERR_UNSUPPORTED, "rotary positions: D at most 256");
-  if (a.H > 65536 || a.M >= (int64_t(1) << 31)) return fail(ROCMFP4_ERR_UNSUPPORTED, "rotary positions: sizes too large");
+  if (a.H > 65536 || a.M * (a.D / 32) >= (int64_t(1) << 31)) return fail(ROCMFP4_ERR_UNSUPPORTED, "rotary positions: sizes too large");
   if ((reinterpret_cast<uintptr_t>(a.q_out) & 7u) != 0)
     return fail(ROCMFP4_ERR_UNSUPPORTED, "rotary positions: the output must be 8-byte aligned");
   DeviceState* d = nullptr;
