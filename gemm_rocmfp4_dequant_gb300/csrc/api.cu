@@ -138,8 +138,8 @@ rocmfp4_status device_state(DeviceState** out, Needs needs = Needs::kProducts) {
       return cuda_fail(e, "cudaMemset");
     if ((e = cudaMalloc(&d.moe_bars, sizeof(uint32_t) * kMoeBarWords)) != cudaSuccess) return cuda_fail(e, "cudaMalloc");
     if ((e = cudaMemset(d.moe_bars, 0, sizeof(uint32_t) * kMoeBarWords)) != cudaSuccess) return cuda_fail(e, "cudaMemset");
-    if ((e = cudaMalloc(&d.paged_cnt, sizeof(uint32_t) * 2 * d.sms)) != cudaSuccess) return cuda_fail(e, "cudaMalloc");
-    if ((e = cudaMemset(d.paged_cnt, 0, sizeof(uint32_t) * 2 * d.sms)) != cudaSuccess) return cuda_fail(e, "cudaMemset");
+    if ((e = cudaMalloc(&d.paged_cnt, sizeof(uint32_t) * kPagedCtas * d.sms)) != cudaSuccess) return cuda_fail(e, "cudaMalloc");
+    if ((e = cudaMemset(d.paged_cnt, 0, sizeof(uint32_t) * kPagedCtas * d.sms)) != cudaSuccess) return cuda_fail(e, "cudaMemset");
     if ((e = cudaMemset(d.err, 0, sizeof(uint32_t))) != cudaSuccess) return cuda_fail(e, "cudaMemset");
     if ((e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
     d.ready = true;
@@ -609,10 +609,11 @@ rocmfp4_status paged_attention(const rocmfp4_paged_cache* cache, PagedAttnArgs a
   a.cache.err = d->err;
   a.ws = d->paged_ws;
   a.cnt = d->paged_cnt;
-  // At most eight (row, head) pairs a sequence and KV head, on the average: the
-  // kernel of few rows; else 128-row tiles.  (The lengths of the chunks are on
-  // the device; either kernel is right for any.)
-  const bool few = a.M * (H / cache->Hkv) <= 8 * cache->B;
+  // At most 16 (row, head) pairs a sequence and KV head, on the average: the kernel of few rows, tiles of 8; else tiles of 128
+  // and 256.  Measured, few against many: 16 rows: 41 / 62 us (32768 tokens), 68 / 69 (16 sequences of 4096), 71 / 86 (64 of 1000),
+  // 19 / 27 (9 of 3001, D = 64); 20 to 24 rows: 52 / 62, 90 / 70, 100 / 89, 23 / 28.  The lengths of the chunks are on the device:
+  // either kernel is right for any.
+  const bool few = a.M * (H / cache->Hkv) <= 16 * (int64_t)cache->B;
   cudaError_t e = few ? launch_paged_few(cache->variant, act, a, d->sms, s) : launch_paged_attention(cache->variant, act, a, d->sms, s);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   g_launches.fetch_add(1);
@@ -943,7 +944,7 @@ uint32_t rocmfp4_device_error_bits(rocmfp4_stream_t stream) {
       cudaMemsetAsync(d->cnt, 0, sizeof(uint32_t) * d->wmax, s);
       cudaMemsetAsync(d->tccnt, 0, sizeof(uint32_t) * tc_cnt_words(d->sms), s);
       cudaMemsetAsync(d->moe_bars, 0, sizeof(uint32_t) * kMoeBarWords, s);
-      cudaMemsetAsync(d->paged_cnt, 0, sizeof(uint32_t) * 2 * d->sms, s);
+      cudaMemsetAsync(d->paged_cnt, 0, sizeof(uint32_t) * kPagedCtas * d->sms, s);
       if (cudaStreamSynchronize(s) != cudaSuccess) return 0xFFFFFFFFu;
     }
   }

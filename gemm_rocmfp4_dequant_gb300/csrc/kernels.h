@@ -180,9 +180,10 @@ struct PagedAttnArgs {
   int H, causal, window;
   float scale;
   float* ws;          // paged_attn_ws_floats(sms) floats
-  uint32_t* cnt;      // 2 * sms words, zero between launches
+  uint32_t* cnt;      // kPagedCtas * sms words, zero between launches
   PagedArgs cache;
 };
+constexpr int kPagedCtas = 2;  // CTAs an SM of a launch, at most
 size_t paged_attn_ws_floats(int sms);
 cudaError_t paged_attn_prepare();
 // The same for few rows (paged_few.cu).

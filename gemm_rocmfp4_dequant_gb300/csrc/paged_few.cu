@@ -15,6 +15,16 @@
 // until the CTA's part of the row tile is done.  The work is cut as in
 // paged_work.cuh, over two CTAs an SM; the CTA that arrives last at a shared row
 // tile adds the parts, its warps a quarter of them each.
+//
+// Measured (40 query heads over 8 of D = 128, in a graph): one token over 32768
+// 24.6 us (38 MB, 1.5 TB/s), 16 over 4096 40.4 us (71 MB, 1.8 TB/s), 64 over 2000
+// 64.3 us (147 MB, 2.3 TB/s), one over 100 7.2 us.  What bounds it is the decode and its
+// latencies (about 1400 warp instructions a chunk, half of the issue slots used);
+// of the 40.4 us, copies and the joining of parts alone take 20.  Tried
+// and not better: three CTAs an SM (40.9 / 66.9 us), V transposed by byte permutes instead of movmatrix
+// with rows in conflict-free order (41.7 / 71.0), one CTA of twelve warps an SM (22.6 / 40.5
+// but 8.1 for 100 tokens and 74 for 64 x 2000), the same with copies that run on into the next row tile
+// (24.1 / 43.7).
 #include "attn_frag.cuh"
 #include "kernels.h"
 #include "paged_work.cuh"
@@ -25,7 +35,7 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kChunk = 32;   // tokens a warp takes at a time
 constexpr int kStages = 3;   // chunks under way per warp
-constexpr int kCtasPerSm = 2;
+constexpr int kCtasPerSm = kPagedCtas;
 constexpr int kCols = 8;     // rows of a row tile
 constexpr float kPScale = 32768.0f, kPUnscale = 1.0f / 32768.0f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -102,21 +112,27 @@ RF4_DEV void add_parts(const Params& p, const Item& it, const float2* ml, float*
     for (int n = lane; n < parts; n += 32) weight[row * parts + n] *= inv;
   }
   __syncthreads();
+  // warp w: parts w, w + kWarps, ...; a lane's places are four values each
+  constexpr int K = kCols * Q4 / 32;
   const int places = it.rows * Q4;
-  for (int i0 = lane; i0 < places; i0 += 64) {
-    const int i1 = min(i0 + 32, places - 1), r0 = i0 / Q4, r1 = i1 / Q4;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-#pragma unroll 4
-    for (int n = warp; n < parts; n += kWarps) {
-      const float4* base = reinterpret_cast<const float4*>(p.ws + record(n) * D);
-      const float4 x = __ldcg(base + i0), y = __ldcg(base + i1);
-      const float u = weight[r0 * parts + n], v = weight[r1 * parts + n];
-      a.x += u * x.x, a.y += u * x.y, a.z += u * x.z, a.w += u * x.w;
-      b.x += v * y.x, b.y += v * y.y, b.z += v * y.z, b.w += v * y.w;
+  float4 a[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int n = warp; n < parts; n += kWarps) {
+    const float4* base = reinterpret_cast<const float4*>(p.ws + record(n) * D);
+    float4 x[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] = lane + 32 * k < places ? __ldcg(base + lane + 32 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const float u = weight[min((lane + 32 * k) / Q4, it.rows - 1) * parts + n];
+      a[k].x += u * x[k].x, a[k].y += u * x[k].y, a[k].z += u * x[k].z, a[k].w += u * x[k].w;
     }
-    reinterpret_cast<float4*>(sums + warp * kCols * D)[i0] = a;
-    if (i0 + 32 < places) reinterpret_cast<float4*>(sums + warp * kCols * D)[i0 + 32] = b;
   }
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    if (lane + 32 * k < places) reinterpret_cast<float4*>(sums + warp * kCols * D)[lane + 32 * k] = a[k];
   __syncthreads();
   for (int i = threadIdx.x; i < it.rows * D / 2; i += kThreads) {
     float x = 0.f, y = 0.f;
