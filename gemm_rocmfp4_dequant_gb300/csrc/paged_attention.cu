@@ -38,9 +38,16 @@
 //   12, 13     MMA issue of chain 0 (and tensor-memory allocation) and 1
 //   14         the stretch's row tiles; bulk copies of raw rows, one for each run
 //              within a page
-// (Two sets of decode warps leave the softmax 144 registers, in which its loop
-// spills: 322 us where this takes 286 for 512 rows over 33280 tokens.  Decode
-// warps that fetch their own rows: 376.)
+// (Measured when 512 rows over 33280 tokens took 286 us: two sets of decode
+// warps, which leave the softmax 144 registers, 322; decode warps that fetch
+// their own rows 376.)
+//
+// Measured (40 query heads over 8 of D = 128, in a graph): a prompt of 4096 245 us
+// in bf16 (700 TFLOP/s of the products a causal mask asks for), 229 in fp16; 512 rows
+// over 33280 tokens 290 us (1190 TFLOP/s, fp16).  Bound by shared memory: a wide token tile stores
+// 64 KB of decoded K and V, reads their raw rows, and the four products read Q, K
+// and V again, 2336 cycles at 128 bytes a cycle, and the 512 rows take about 4000 a
+// wide token tile.  In bf16 K needs a second conversion.
 // Every wait is bounded: a warp that gives up records kErrWaitTimeout and
 // goes on without waiting, so that all meet at the end.
 #include <cstddef>
@@ -232,9 +239,8 @@ RF4_DEV void give_registers() {
 }
 RF4_DEV void chains_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// A wait for a phase that the hardware may suspend the warp in: a loop of plain
-// polls took half of the SM's issue slots from the warps that had work.  Gives
-// up after about 2^32 cycles.
+// A wait for a phase that the hardware may suspend the warp in (plain polls
+// measured the same).  Gives up after about 2^32 cycles.
 RF4_DEV bool wait_suspended(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
   for (;;) {
