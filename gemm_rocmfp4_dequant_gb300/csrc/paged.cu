@@ -22,17 +22,20 @@
 // cosines are computed once for all heads of a walk.  Where the pairs are
 // halves of whole blocks (rot = D, a multiple of 64) they own the partners' block
 // too.  Few rows: one head a walk, for latency; many rows: one wave of walks.
-// Measured, 4096 tokens of 40 + 8 + 8 heads of 128 in fp32: 44 us (163 MB in and out,
-// 3.7 TB/s; 82 us with its reading back, now 55, before the integers, the pairs of blocks and the single
-// wave); 512 x 40 x 128 5.8 us in a graph.  Bound by issue and latency together: 24
-// warps an SM, half of the issue slots, a third of them the quantiser's.
+// Measured, 4096 tokens of 40 + 8 + 8 heads of 128 in fp32, in a graph with their
+// reading back: 53 us, about 42 of them here (163 MB in and out, 3.9 TB/s).  82 with a
+// block a thread, angles in fp64 and five walks; 64 with angles in integers and four
+// heads' loads in flight; 56 with pairs of blocks; 55 with one wave of walks, in CTAs
+// of 256 threads, four an SM, which leave some SMs three.  Six CTAs an SM: 60.  512 x
+// 40 x 128 alone: 5.5 us.  Bound by issue and latency together: 24 warps an SM, 41 %
+// of the issue slots.
 //
 // cache_read_kernel.  The rows' blocks back as dense values, exact in every
 // output type; four threads a block, one or four tokens a warp.  Measured,
-// 16 x 4096 tokens of 8 heads of 128 in bf16: 76.5 us (344 MB, 4.5 TB/s; 198 us with the place of every block
-// looked up by itself, 98 with a token a warp, 78 with one block's loads in
-// flight a thread, 89 with three).  Bound by issue (about 100 instructions a
-// warp's eight blocks) and the latency of the places.
+// 16 x 4096 tokens of 8 heads of 128 in bf16: 75 us (344 MB, 4.6 TB/s).  198 with
+// every block's place looked up by itself; 98 with a token a warp; 77 with one
+// block's loads in flight a thread, 89 with three.  Bound by the ALU (58 %) and the
+// latency of the places.
 #include "common.cuh"
 #include "kernels.h"
 #include "quant.cuh"
@@ -40,9 +43,9 @@
 namespace rocmfp4 {
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeCtas = 4;  // CTAs an SM, at least: bounds the registers
-constexpr int kBatch = 4;  // heads whose loads a thread has in flight
+constexpr int kRopeThreads = 128;
+constexpr int kRopeCtas = 7;  // CTAs an SM, at least: bounds the registers
+constexpr int kBatch = 4;     // heads whose loads a thread has in flight
 
 struct RopeParams {
   const void* x[3];  // q, k, v
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __g
   for (int h = second; h < p.c.Hkv; h += BATCH * p.slices) batch(Kind<2>(), h, p.c.Hkv);
 }
 
-constexpr int kReadThreads = 256;
+constexpr int kReadThreads = 128;
 constexpr int kReadUnroll = 2;  // blocks of K and of V whose loads a thread has in flight
 
 struct ReadParams {
@@ -406,14 +409,15 @@ RF4_DEV void store_block(void* out, int64_t at, int q, const uint32_t (&h)[4], b
     uint32_t x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = OUT == 1 ? f16x2_to_bf16x2(h[i]) : h[i];
-    const uint2 lo = make_uint2(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410));
-    const uint2 hi = make_uint2(__byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
     const bool odd = q & 1;
-    const uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? lo.x : hi.x, 1), b = __shfl_xor_sync(0xffffffffu, odd ? lo.y : hi.y, 1);
+    const uint32_t mine = odd ? 0x7632 : 0x5410, other = odd ? 0x5410 : 0x7632;
+    const uint32_t k0 = __byte_perm(x[0], x[1], mine), k1 = __byte_perm(x[2], x[3], mine);
+    const uint32_t a = __shfl_xor_sync(0xffffffffu, __byte_perm(x[0], x[1], other), 1);
+    const uint32_t b = __shfl_xor_sync(0xffffffffu, __byte_perm(x[2], x[3], other), 1);
     if (!want) return;
     // even: 4q .. 4q + 7; odd: 16 + 4 (q - 1) .. + 7
     uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at + (odd ? 12 + 4 * q : 4 * q));
-    *o = odd ? make_uint4(a, b, hi.x, hi.y) : make_uint4(lo.x, lo.y, a, b);
+    *o = odd ? make_uint4(a, b, k0, k1) : make_uint4(k0, k1, a, b);
   }
 }
 
