@@ -29,7 +29,9 @@
  *     workspace (split-reduction partials and counters: about 0.18 MiB per
  *     SM, 27 MiB on a 152-SM GPU) is allocated once, on first use, 36 MiB more
  *     at the first rocmfp4_moe, 58 MiB more at the first
- *     rocmfp4_paged_attention, and released by rocmfp4_shutdown().
+ *     rocmfp4_paged_attention, and released by rocmfp4_shutdown().  The first
+ *     call on a device that takes the workspace must not stand in a stream
+ *     capture (it fails there); the additions may.
  *   - Calls on one device share that workspace: calls that overlap on the GPU
  *     (unordered streams, or graphs replayed concurrently) race and give wrong
  *     results.  Calls ordered on one stream are safe.
