@@ -428,7 +428,8 @@ class PagedCache:
     """A paged K/V cache of ROCmFP4 rows and the batch of rows that calls deal with (rocmfp4_paged_cache).
 
     K, V      uint8 tensors of num_pages x kv_heads x page_size rows of head / 32 blocks (page_size a multiple of 16);
-    table     int32 [B, pages]: token t of sequence b lies in page table[b, t // page_size], at t % page_size;
+    table     int32 [B, pages]: token t of sequence b lies in page table[b, t // page_size], at t % page_size (rows that do
+              not overlap, or one row that expand repeats: beams over one encoder's states, say);
     lens      int32 [B]: the tokens that each sequence holds, a call's new ones among them;
     cu        int32 [B + 1], from 0 on: rows cu[b] .. cu[b + 1] - 1 of a call are the last tokens of sequence b (or its
               queries, in a cross attention); rows from cu[B] on are padding, whose outputs stay as they are.
@@ -456,11 +457,14 @@ class PagedCache:
         if table.shape[1] > 1 and table.stride(1) != 1:
             raise ValueError("table must have contiguous rows")
         width = table.shape[1]
+        stride = table.stride(0) if B > 1 and width > 0 else width
+        if 0 < stride < width:
+            raise ValueError("table's rows must not overlap, unless all of them are one (a row that expand repeats)")
         self.K, self.V, self.table, self.lens, self.cu = K, V, table, lens, cu
         self.kv_heads, self.head, self.page_size, self.variant, self.device = kv_heads, head, page_size, variant, K.device
         self._index = K.device.index
         self._struct = _PagedCacheStruct(_ptr(K), _ptr(V), _ptr(table), lens.data_ptr(), cu.data_ptr(), B, width,
-                                         max(width, table.stride(0)) if B > 1 else width, K.numel() // page, page_size, kv_heads, head, variant)
+                                         stride, K.numel() // page, page_size, kv_heads, head, variant)
         self._at = ctypes.addressof(self._struct)
 
 

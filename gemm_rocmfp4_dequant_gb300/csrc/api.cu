@@ -495,7 +495,7 @@ rocmfp4_status paged_args(const rocmfp4_paged_cache* c, PagedArgs* out) {
   if (c->B < 0 || c->table_width < 0 || c->num_pages < 0) return fail(ROCMFP4_ERR_INVALID_ARG, "negative size");
   if (c->Hkv < 1 || c->D < 32 || c->page_size < 1) return fail(ROCMFP4_ERR_INVALID_ARG, "Hkv, D and page_size must be positive");
   if (c->D % 32 != 0) return fail(ROCMFP4_ERR_INVALID_ARG, "D must be a multiple of 32");
-  if (c->table_stride < c->table_width) return fail(ROCMFP4_ERR_INVALID_ARG, "table_stride below table_width");
+  if (c->table_stride != 0 && c->table_stride < c->table_width) return fail(ROCMFP4_ERR_INVALID_ARG, "table_stride below table_width");
   if (!c->cu || (c->B > 0 && !c->lens) || (c->table_width > 0 && !c->table) || (c->num_pages > 0 && (!c->K || !c->V)))
     return fail(ROCMFP4_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned_to(c->cu, 0) || !aligned_to(c->lens, 0) || !aligned_to(c->table, 0))

@@ -281,8 +281,9 @@ rocmfp4_status rocmfp4_logprobs(const void *logits, rocmfp4_out_dtype type, int6
  *            num_pages = B, page_size = Tmax, table[b] = {b};
  *   - lens   [B] int32: the tokens that sequence b holds, a call's new tokens
  *            among them;
- *   - table  [B] rows of table_width int32 page numbers, table_stride apart:
- *            token t of sequence b lies in page table[b][t / page_size], at
+ *   - table  [B] rows of table_width int32 page numbers, table_stride apart
+ *            (at least table_width, or 0: one row for all sequences): token t
+ *            of sequence b lies in page table[b][t / page_size], at
  *            t % page_size.  Sequences may share pages that are read;
  *   - cu     [B + 1] int32, cu[0] = 0, not decreasing: rows cu[b] ..
  *            cu[b + 1] - 1 of a call belong to sequence b.  Where a row is a
