@@ -955,9 +955,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
           if (have) next_own(vr, vj, ctl.v_full, ctl.v_empty);
           const bool more = next_own(kr, kj, ctl.k_full, ctl.k_empty);
           if (!have) {
-            // a chain waits for its own queries alone: the other half's barrier may be two phases ahead
+            // A chain waits for the queries that it reads, and for no others, whose barrier may be two phases ahead: the
+            // other half's, or those of a narrow row tile's only token tile.  Phases left out here are over before this
+            // chain's next look at the barrier: its turn comes only after the other chain has waited for them.
             const uint32_t half = wide & t;
-            wait.warp(&ctl.q_full[half], (half ? n_q1 : n_q0) & 1u);
+            if (more) wait.warp(&ctl.q_full[half], (half ? n_q1 : n_q0) & 1u);
             ++n_q0;
             n_q1 += wide;
           } else {
