@@ -48,8 +48,10 @@
 // 64 KB of decoded K and V, reads their raw rows, and the four products read Q, K
 // and V again, 2336 cycles at 128 bytes a cycle, and the 512 rows take about 4000 a
 // wide token tile.  In bf16 K needs a second conversion.
-// Every wait is bounded: a warp that gives up records kErrWaitTimeout and
-// goes on without waiting, so that all meet at the end.
+// Every wait is bounded, the chains' meetings among them (an mbarrier: warps of
+// a chain that gave up do not come): a warp that gives up records
+// kErrWaitTimeout and goes on without waiting, so that all meet at the end, each
+// issuer with its products and copies behind it.
 #include <cstddef>
 #include <cstring>
 
@@ -121,13 +123,14 @@ struct Control {  // at OFF_BAR
   uint64_t raw_empty[kMaxRaw];                         // 4: decode warps
   uint64_t item_full[kItems];                          // 1
   uint64_t item_empty[kItems];                         // 8 + 2: softmax and MMA warps
+  uint64_t meeting;                                    // 8: softmax warps
   Stretch work;
   int last;
   uint32_t tmem;
   Item items[kItems];
   Tile tiles[kTiles];
 };
-constexpr int kBars = 20 + 2 * kMaxRaw + 2 * kItems;
+constexpr int kBars = 21 + 2 * kMaxRaw + 2 * kItems;
 static_assert(offsetof(Control, work) == 8 * kBars && sizeof(Control) <= 2048, "control block");
 
 struct Shape {
@@ -237,7 +240,6 @@ template <int N>
 RF4_DEV void give_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-RF4_DEV void chains_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // A wait for a phase that the hardware may suspend the warp in (plain polls
 // measured the same).  Gives up after about 2^32 cycles.
@@ -261,6 +263,16 @@ struct Waits {
   RF4_DEV void warp(const uint64_t* bar, uint32_t parity) {
     if (__all_sync(0xffffffffu, mbar_try_wait(smem_addr(bar), parity))) return;
     if (ok) ok = __all_sync(0xffffffffu, wait_suspended(smem_addr(bar), parity));
+  }
+};
+
+// Both chains' softmax warps meet, and see what each other wrote before.
+struct Meeting {
+  uint32_t n = 0;
+  RF4_DEV void sync(uint64_t* bar, Waits& wait) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(bar));
+    wait.warp(bar, n++ & 1u);
   }
 };
 
@@ -605,7 +617,7 @@ struct Loader {
   uint8_t* raw;
   Ring ring;
   int tile = 0;
-  uint32_t issued = 0;
+  uint32_t issued = 0, stopped = 0;
   RF4_DEV Loader(int stages, uint8_t* raw) : stages(stages), raw(raw) {}
 
   RF4_DEV void item(const Params& p, Control& ctl, Waits& wait, const Item& it) {
@@ -660,13 +672,15 @@ struct Loader {
       ctl.tiles[tile % kTiles] = Tile{0, 0, 0, 1};
       mbar_arrive(smem_addr(&ctl.raw_full[ring.stage]));
     }
+    stopped = 1;
   }
 
-  // Where a wait gave up: copies in flight land before the block ends.
-  RF4_DEV void drain(Control& ctl, const Waits& wait) const {
-    if (wait.ok) return;
-    for (uint32_t i = issued > (uint32_t)stages ? issued - stages : 0; i < issued; ++i)
-      (void)mbar_wait_bounded(smem_addr(&ctl.raw_full[i % stages]), i / stages & 1u);
+  // Copies in flight land before the block ends, which those who were to read them may have given up before.  The stage
+  // that stop() took was empty, and its barrier is a phase further.  This may begin before any reader's wait: twice as long.
+  RF4_DEV void drain(Control& ctl) const {
+    for (uint32_t i = issued + stopped > (uint32_t)stages ? issued + stopped - stages : 0; i < issued; ++i)
+      if (!mbar_wait_bounded(smem_addr(&ctl.raw_full[i % stages]), i / stages & 1u))
+        (void)mbar_wait_bounded(smem_addr(&ctl.raw_full[i % stages]), i / stages & 1u);
   }
 };
 
@@ -721,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
 
   if (threadIdx.x < kBars) {
     const int i = threadIdx.x;
-    const uint32_t arrivals = i < 4 ? 4 : i < 8 ? 2 : i < 16 ? 1 : i < 20 ? 4 : i < 20 + kMaxRaw ? 1 : i < 20 + 2 * kMaxRaw ? 4 : i < 20 + 2 * kMaxRaw + kItems ? 1 : 8 + 2;
+    const uint32_t arrivals = i < 4 ? 4 : i < 8 ? 2 : i < 16 ? 1 : i < 20 ? 4 : i < 20 + kMaxRaw ? 1 : i < 20 + 2 * kMaxRaw ? 4 : i < 20 + 2 * kMaxRaw + kItems ? 1 : i < 20 + 2 * kMaxRaw + 2 * kItems ? 8 + 2 : 8;
     mbar_init(smem_addr(reinterpret_cast<uint64_t*>(&ctl) + i), arrivals);
     fence_mbar_init();
   }
@@ -753,6 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
     const uint32_t s_at = tmem + lanes + 128u * t, o_at = tmem + lanes + 256u + (uint32_t)D * t;
     uint32_t n_s = 0, n_o = 0;  // uses of s_full and o_full
     Items items;
+    Meeting chains;
     // Chain t's half of a row tile's queries; a narrow tile's one half is chain 0's to bring.
     auto bring_q = [&](const Item& of) __attribute__((always_inline)) {
       if (t == 1 && !of.wide) return;
@@ -842,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         tc_fence_before();
       }
       __threadfence();
-      chains_sync();
+      chains.sync(&ctl.meeting, wait);
       bool merge = true;
       if (!whole) {
         if (threadIdx.x == 0) {
@@ -850,14 +865,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
           ctl.last = n == (uint32_t)(it.last - it.first);
           if (ctl.last) store_relaxed_gpu(&p.cnt[it.first], 0u);
         }
-        chains_sync();
+        chains.sync(&ctl.meeting, wait);
         merge = ctl.last;
         if (merge) __threadfence();
       }
       if (merge) {
         merge_parts<D, ACT>(p, it, ml);
       }
-      chains_sync();  // the records and ctl.last may be written again
+      chains.sync(&ctl.meeting, wait);  // the records and ctl.last may be written again
       if (nx && !wide) bring_q(*nx);
     }
   } else if (warp < 12) {
@@ -989,11 +1004,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         }
         next_own(vr, vj, ctl.v_full, ctl.v_empty);  // the other chain's last tile, perhaps
       }
-      if (!wait.ok && lane == 0) {  // products in flight end before the tensor memory goes
+      // products in flight end before the tensor memory goes, whoever has given up waiting for them
+      bool over = true;
+      if (elect_one()) {
         mma_commit(smem_addr(&ctl.drained[t]));
-        (void)mbar_wait_bounded(smem_addr(&ctl.drained[t]), 0);
+        over = mbar_wait_bounded(smem_addr(&ctl.drained[t]), 0);
       }
-      __syncwarp();
+      if (!__all_sync(0xffffffffu, over)) wait.ok = false;
     } else if (warp == 14) {
       // ---- row tiles, raw rows ----
       Walk<Shape> walk(p, ctl.work);
@@ -1014,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         if (more) load.item(p, ctl, wait, it);
         else load.stop(ctl, wait);
       }
-      load.drain(ctl, wait);
+      load.drain(ctl);
     }
   }
   if (!wait.ok && lane == 0) atomicOr(p.c.err, kErrWaitTimeout);

@@ -15,7 +15,10 @@ LIMIT = 1e6  # a bounded wait gives up after that long; everything else takes ab
 def source_rules():
     with open(os.path.join(ROOT, "gemm_rocmfp4_dequant_gb300", "csrc", "paged_attention.cu")) as f:
         s = " ".join(f.read().split())
-    return {"queries_by_need": "if (more) wait.warp(&ctl.q_full" in s}
+    return {"queries_by_need": "if (more) wait.warp(&ctl.q_full" in s,
+            "bounded_meetings": "bar.sync" not in s and "chains.sync(&ctl.meeting, wait)" in s,
+            "products_drained": "bool over = true; if (elect_one()) { mma_commit(smem_addr(&ctl.drained[t]));" in s,
+            "copies_drained": "load.drain(ctl);" in s}
 
 
 class Bar:
@@ -151,6 +154,7 @@ def run(seed, stages, items, rules, slow=None, pause=None, late_copy=None):
     full, empty = [bars(2, 4), bars(2, 4)], [bars(2, 2), bars(2, 2)]  # of K, of V
     s_full, o_full, turn, drained = (bars(2, 1) for _ in range(4))
     p_full, q_full = bars(2, 4), bars(2, 4)
+    meeting_bar = Bar(sim, 8)
     raw_full, raw_empty = bars(stages, 1), bars(stages, 4)
     item_full, item_empty = bars(4, 1), bars(4, 10)
     slot, tiles, raw = [(None, 0)] * 4, [(None, True)] * 16, [None] * stages
@@ -218,9 +222,10 @@ def run(seed, stages, items, rules, slow=None, pause=None, late_copy=None):
                     raw_full[st].arrive()
                     stopped = 1
             n += 1
-        if not w.ok:
-            for i in range(max(issued - stages, 0), issued):
-                yield "drain", raw_full[i % stages], i // stages & 1
+        if rules["copies_drained"] or not w.ok:
+            for i in range(max(issued + stopped - stages, 0), issued):
+                for _ in range(2):  # the second time nothing to wait for, mostly
+                    yield "drain", raw_full[i % stages], i // stages & 1
 
     def decode(w, part):
         n = used = 0
@@ -321,12 +326,12 @@ def run(seed, stages, items, rules, slow=None, pause=None, late_copy=None):
                 n_turn += 1
                 turn[0].arrive()
             yield from own(1)
-        if not w.ok:
+        if rules["products_drained"] or not w.ok:
             product(t, 0, drained[t].arrive)
             yield "drain", drained[t], 0
 
     def softmax(w, t, part):
-        n = n_s = n_o = 0
+        n = n_s = n_o = met = 0
 
         def bring(it, number):
             if t == 1 and not it[0]:
@@ -343,7 +348,13 @@ def run(seed, stages, items, rules, slow=None, pause=None, late_copy=None):
             return slot[i % 4] if w.ok and slot[i % 4][0] is not None else None
 
         def meet():
-            yield "meet", meeting, 8
+            nonlocal met
+            if not rules["bounded_meetings"]:
+                yield "meet", meeting, 8
+                return
+            meeting_bar.arrive()
+            yield "wait", meeting_bar, met & 1
+            met += 1
         at = yield from get(0)
         if at:
             yield from bring(at[0], 1)

@@ -39,3 +39,27 @@ def test_row_tiles_of_one_token_tile():
 def test_the_model_sees_a_wait_that_nothing_orders():
     """With a wait for queries that the chain does not use, their barrier goes on by two phases unseen."""
     assert short_row_tiles(dict(pp.source_rules(), queries_by_need=False))
+
+
+def late_ends(rules, seeds):
+    """A warp that stops, or a copy that lands, later than any wait lasts: the draws after which some warp never ended, or ended
+    with a copy or a product of the block still on its way."""
+    bad = []
+    for seed in seeds:
+        stages, items, _ = draw(seed)
+        r = random.Random(seed)
+        late = {"late_copy": r.randint(1, 40)} if r.random() < .3 else {"pause": (r.choice(pp.NAMES), r.randint(1, 60))}
+        _, flying = pp.run(seed, stages, items, rules, **late)
+        if flying != 0:
+            bad.append((seed, late, flying))
+    return bad
+
+
+@pytest.mark.parametrize("block", range(6))
+def test_all_warps_end_after_waits_that_gave_up(block):
+    assert late_ends(pp.source_rules(), range(1000 * block, 1000 * block + 60)) == []
+
+
+@pytest.mark.parametrize("rule", ["bounded_meetings", "products_drained", "copies_drained"])
+def test_the_model_sees_warps_that_never_meet_and_what_is_left_on_its_way(rule):
+    assert late_ends(dict(pp.source_rules(), **{rule: False}), range(600))
