@@ -48,10 +48,10 @@
 // 64 KB of decoded K and V, reads their raw rows, and the four products read Q, K
 // and V again, 2336 cycles at 128 bytes a cycle, and the 512 rows take about 4000 a
 // wide token tile.  In bf16 K needs a second conversion.
-// Every wait is bounded, the chains' meetings among them (an mbarrier: warps of
-// a chain that gave up do not come): a warp that gives up records
-// kErrWaitTimeout and goes on without waiting, so that all meet at the end, each
-// issuer with its products and copies behind it.
+// Every wait is bounded: a warp that gives up goes on without waiting, so that
+// all meet at the end.  Where the chains meet, a warp that has no more row tiles,
+// or gave up, stands in until all are as far.  At the end kErrWaitTimeout is
+// recorded, and products and copies that nobody waited for are waited for.
 #include <cstddef>
 #include <cstring>
 
@@ -123,14 +123,14 @@ struct Control {  // at OFF_BAR
   uint64_t raw_empty[kMaxRaw];                         // 4: decode warps
   uint64_t item_full[kItems];                          // 1
   uint64_t item_empty[kItems];                         // 8 + 2: softmax and MMA warps
-  uint64_t meeting;                                    // 8: softmax warps
   Stretch work;
   int last;
   uint32_t tmem;
+  uint32_t first, copies;  // uses of raw stages: the first that the loader has not seen emptied, and how many there were
   Item items[kItems];
   Tile tiles[kTiles];
 };
-constexpr int kBars = 21 + 2 * kMaxRaw + 2 * kItems;
+constexpr int kBars = 20 + 2 * kMaxRaw + 2 * kItems;
 static_assert(offsetof(Control, work) == 8 * kBars && sizeof(Control) <= 2048, "control block");
 
 struct Shape {
@@ -241,6 +241,13 @@ RF4_DEV void give_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Both chains' softmax warps meet; true if all of them were leaving.
+RF4_DEV bool chains_meet(bool leaving) {
+  uint32_t all;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.and.pred p, 1, 256, q;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(all) : "r"((uint32_t)leaving) : "memory");
+  return all != 0;
+}
+
 // A wait for a phase that the hardware may suspend the warp in (plain polls
 // measured the same).  Gives up after about 2^32 cycles.
 RF4_DEV bool wait_suspended(uint32_t bar, uint32_t parity) {
@@ -263,16 +270,6 @@ struct Waits {
   RF4_DEV void warp(const uint64_t* bar, uint32_t parity) {
     if (__all_sync(0xffffffffu, mbar_try_wait(smem_addr(bar), parity))) return;
     if (ok) ok = __all_sync(0xffffffffu, wait_suspended(smem_addr(bar), parity));
-  }
-};
-
-// Both chains' softmax warps meet, and see what each other wrote before.
-struct Meeting {
-  uint32_t n = 0;
-  RF4_DEV void sync(uint64_t* bar, Waits& wait) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(bar));
-    wait.warp(bar, n++ & 1u);
   }
 };
 
@@ -664,7 +661,7 @@ struct Loader {
     }
   }
 
-  // No more tiles.
+  // No more tiles.  (The stage that this takes is empty, and its barrier goes on by a phase.)
   RF4_DEV void stop(Control& ctl, Waits& wait) {
     wait.warp(&ctl.raw_empty[ring.stage], ring.phase ^ 1u);
     if (!wait.ok) return;
@@ -675,12 +672,11 @@ struct Loader {
     stopped = 1;
   }
 
-  // Copies in flight land before the block ends, which those who were to read them may have given up before.  The stage
-  // that stop() took was empty, and its barrier is a phase further.  This may begin before any reader's wait: twice as long.
-  RF4_DEV void drain(Control& ctl) const {
-    for (uint32_t i = issued + stopped > (uint32_t)stages ? issued + stopped - stages : 0; i < issued; ++i)
-      if (!mbar_wait_bounded(smem_addr(&ctl.raw_full[i % stages]), i / stages & 1u))
-        (void)mbar_wait_bounded(smem_addr(&ctl.raw_full[i % stages]), i / stages & 1u);
+  // What a block that gave up waits for at its end.
+  RF4_DEV void leave(Control& ctl) const {
+    if ((threadIdx.x & 31) != 0) return;
+    ctl.copies = issued;
+    ctl.first = issued + stopped > (uint32_t)stages ? issued + stopped - stages : 0;
   }
 };
 
@@ -735,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
 
   if (threadIdx.x < kBars) {
     const int i = threadIdx.x;
-    const uint32_t arrivals = i < 4 ? 4 : i < 8 ? 2 : i < 16 ? 1 : i < 20 ? 4 : i < 20 + kMaxRaw ? 1 : i < 20 + 2 * kMaxRaw ? 4 : i < 20 + 2 * kMaxRaw + kItems ? 1 : i < 20 + 2 * kMaxRaw + 2 * kItems ? 8 + 2 : 8;
+    const uint32_t arrivals = i < 4 ? 4 : i < 8 ? 2 : i < 16 ? 1 : i < 20 ? 4 : i < 20 + kMaxRaw ? 1 : i < 20 + 2 * kMaxRaw ? 4 : i < 20 + 2 * kMaxRaw + kItems ? 1 : 8 + 2;
     mbar_init(smem_addr(reinterpret_cast<uint64_t*>(&ctl) + i), arrivals);
     fence_mbar_init();
   }
@@ -767,7 +763,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
     const uint32_t s_at = tmem + lanes + 128u * t, o_at = tmem + lanes + 256u + (uint32_t)D * t;
     uint32_t n_s = 0, n_o = 0;  // uses of s_full and o_full
     Items items;
-    Meeting chains;
     // Chain t's half of a row tile's queries; a narrow tile's one half is chain 0's to bring.
     auto bring_q = [&](const Item& of) __attribute__((always_inline)) {
       if (t == 1 && !of.wide) return;
@@ -857,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         tc_fence_before();
       }
       __threadfence();
-      chains.sync(&ctl.meeting, wait);
+      chains_meet(false);
       bool merge = true;
       if (!whole) {
         if (threadIdx.x == 0) {
@@ -865,15 +860,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
           ctl.last = n == (uint32_t)(it.last - it.first);
           if (ctl.last) store_relaxed_gpu(&p.cnt[it.first], 0u);
         }
-        chains.sync(&ctl.meeting, wait);
+        chains_meet(false);
         merge = ctl.last;
         if (merge) __threadfence();
       }
       if (merge) {
         merge_parts<D, ACT>(p, it, ml);
       }
-      chains.sync(&ctl.meeting, wait);  // the records and ctl.last may be written again
+      chains_meet(false);  // the records and ctl.last may be written again
       if (nx && !wide) bring_q(*nx);
+    }
+    while (!chains_meet(true)) {
     }
   } else if (warp < 12) {
     // ---- decode ----
@@ -1004,13 +1001,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         }
         next_own(vr, vj, ctl.v_full, ctl.v_empty);  // the other chain's last tile, perhaps
       }
-      // products in flight end before the tensor memory goes, whoever has given up waiting for them
-      bool over = true;
-      if (elect_one()) {
-        mma_commit(smem_addr(&ctl.drained[t]));
-        over = mbar_wait_bounded(smem_addr(&ctl.drained[t]), 0);
-      }
-      if (!__all_sync(0xffffffffu, over)) wait.ok = false;
     } else if (warp == 14) {
       // ---- row tiles, raw rows ----
       Walk<Shape> walk(p, ctl.work);
@@ -1031,12 +1021,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         if (more) load.item(p, ctl, wait, it);
         else load.stop(ctl, wait);
       }
-      load.drain(ctl);
+      load.leave(ctl);
     }
   }
-  if (!wait.ok && lane == 0) atomicOr(p.c.err, kErrWaitTimeout);
   tc_fence_before();
-  __syncthreads();
+  if (__syncthreads_or(!wait.ok)) {
+    // Some warp gave up.  Copies land and products end before the block does, by waits of their own.
+    if (threadIdx.x == 0) atomicOr(p.c.err, kErrWaitTimeout);
+    if (warp == 12 || warp == 13) {
+      const uint32_t bar = smem_addr(&ctl.drained[warp - 12]);
+      if (elect_one()) {
+        mma_commit(bar);
+        (void)mbar_wait_bounded(bar, 0);
+      }
+    } else if (warp == 14) {
+      for (uint32_t i = ctl.first; i < ctl.copies; ++i) (void)mbar_wait_bounded(smem_addr(&ctl.raw_full[i % raw_stages]), i / raw_stages & 1u);
+    }
+    __syncthreads();
+  }
   tc_fence_after();
   if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }

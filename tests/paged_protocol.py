@@ -16,9 +16,8 @@ def source_rules():
     with open(os.path.join(ROOT, "gemm_rocmfp4_dequant_gb300", "csrc", "paged_attention.cu")) as f:
         s = " ".join(f.read().split())
     return {"queries_by_need": "if (more) wait.warp(&ctl.q_full" in s,
-            "bounded_meetings": "bar.sync" not in s and "chains.sync(&ctl.meeting, wait)" in s,
-            "products_drained": "bool over = true; if (elect_one()) { mma_commit(smem_addr(&ctl.drained[t]));" in s,
-            "copies_drained": "load.drain(ctl);" in s}
+            "stand_in": "bar.sync" not in s and "while (!chains_meet(true)) { }" in s,
+            "end_together": "if (__syncthreads_or(!wait.ok)) {" in s}
 
 
 class Bar:
@@ -127,14 +126,14 @@ class Sim:
             self.wait(w, op[1], op[2], True)
         elif op[0] == "sleep":
             self.after(op[1] * self.r.choice((.1, .5, 1, 1, 2, 20)) * self.r.random(), lambda: self.step(w))
-        else:  # a barrier of the block's, without a limit
+        else:  # a barrier of the block's, without a limit: whether all said yes
             meeting = op[1]
-            meeting.append(w)
+            meeting.append((w, op[3]))
             if len(meeting) == op[2]:
-                there = list(meeting)
+                there, every = [x for x, _ in meeting], all(yes for _, yes in meeting)
                 meeting.clear()
                 for x in there:
-                    self.after(0.01, lambda x=x: self.step(x, True))
+                    self.after(0.01, lambda x=x: self.step(x, every))
 
     def run(self):
         while self.events:
@@ -154,13 +153,12 @@ def run(seed, stages, items, rules, slow=None, pause=None, late_copy=None):
     full, empty = [bars(2, 4), bars(2, 4)], [bars(2, 2), bars(2, 2)]  # of K, of V
     s_full, o_full, turn, drained = (bars(2, 1) for _ in range(4))
     p_full, q_full = bars(2, 4), bars(2, 4)
-    meeting_bar = Bar(sim, 8)
     raw_full, raw_empty = bars(stages, 1), bars(stages, 4)
     item_full, item_empty = bars(4, 1), bars(4, 10)
     slot, tiles, raw = [(None, 0)] * 4, [(None, True)] * 16, [None] * stages
     kv = [[[None] * 4 for _ in range(2)] for _ in range(2)]
     S, P, Q, q_by = [None] * 2, [[None] * 4, [None] * 4], [None] * 2, [[None] * 4, [None] * 4]
-    meeting, pipe, copies = [], [0.0, 0.0], [0]
+    meeting, ending, pipe, copies = [], [], [0.0, 0.0], [0]
     warps = []
 
     def warp(name):
@@ -174,6 +172,17 @@ def run(seed, stages, items, rules, slow=None, pause=None, late_copy=None):
     def product(t, dur, f):  # a chain's run in order
         pipe[t] = max(pipe[t], sim.now) + dur * r.choice((.2, 1, 1, 4)) * r.random()
         sim.flight(pipe[t] - sim.now, f)
+
+    def leave(w, left=(), start=lambda: None):
+        """The end of the block: what may be on its way is waited for where some warp gave up (by the former rule, only by those
+        who had)."""
+        late = not w.ok
+        if rules["end_together"]:
+            late = not (yield "meet", ending, len(NAMES), w.ok)
+        if late:
+            start()
+            for bar, parity in left:
+                yield "drain", bar, parity
 
     def loader(w):
         n = tile = issued = stopped = 0
@@ -222,12 +231,14 @@ def run(seed, stages, items, rules, slow=None, pause=None, late_copy=None):
                     raw_full[st].arrive()
                     stopped = 1
             n += 1
-        if rules["copies_drained"] or not w.ok:
-            for i in range(max(issued + stopped - stages, 0), issued):
-                for _ in range(2):  # the second time nothing to wait for, mostly
-                    yield "drain", raw_full[i % stages], i // stages & 1
+        left = [(raw_full[i % stages], i // stages & 1) for i in range(max(issued + stopped - stages, 0), issued)]
+        yield from leave(w, left)
 
     def decode(w, part):
+        yield from decode_all(w, part)
+        yield from leave(w)
+
+    def decode_all(w, part):
         n = used = 0
         while True:
             for which in range(2):
@@ -326,12 +337,10 @@ def run(seed, stages, items, rules, slow=None, pause=None, late_copy=None):
                 n_turn += 1
                 turn[0].arrive()
             yield from own(1)
-        if rules["products_drained"] or not w.ok:
-            product(t, 0, drained[t].arrive)
-            yield "drain", drained[t], 0
+        yield from leave(w, [(drained[t], 0)], lambda: product(t, 0, drained[t].arrive))
 
     def softmax(w, t, part):
-        n = n_s = n_o = met = 0
+        n = n_s = n_o = 0
 
         def bring(it, number):
             if t == 1 and not it[0]:
@@ -348,13 +357,7 @@ def run(seed, stages, items, rules, slow=None, pause=None, late_copy=None):
             return slot[i % 4] if w.ok and slot[i % 4][0] is not None else None
 
         def meet():
-            nonlocal met
-            if not rules["bounded_meetings"]:
-                yield "meet", meeting, 8
-                return
-            meeting_bar.arrive()
-            yield "wait", meeting_bar, met & 1
-            met += 1
+            yield "meet", meeting, 8, False
         at = yield from get(0)
         if at:
             yield from bring(at[0], 1)
@@ -389,6 +392,9 @@ def run(seed, stages, items, rules, slow=None, pause=None, late_copy=None):
             item_empty[n % 4].arrive()
             n += 1
             at = nx
+        while rules["stand_in"] and not (yield "meet", meeting, 8, True):
+            pass
+        yield from leave(w)
     w = warp("loader")
     sim.spawn(w, loader(w))
     for t in range(2):

@@ -60,6 +60,6 @@ def test_all_warps_end_after_waits_that_gave_up(block):
     assert late_ends(pp.source_rules(), range(1000 * block, 1000 * block + 60)) == []
 
 
-@pytest.mark.parametrize("rule", ["bounded_meetings", "products_drained", "copies_drained"])
+@pytest.mark.parametrize("rule", ["stand_in", "end_together"])
 def test_the_model_sees_warps_that_never_meet_and_what_is_left_on_its_way(rule):
     assert late_ends(dict(pp.source_rules(), **{rule: False}), range(600))
