@@ -78,19 +78,25 @@ RF4_DEV int sequence_of(const int32_t* cu, int B, int64_t row, uint32_t mask, in
   return lo;
 }
 
-// freq / 2 pi mod 1 in units of 2^-64: freq = m 2^-sh with a 24-bit m, so it is m times the first 64 bits of 1 / 2 pi, shifted
-// right.  In integers, as this GPU has few fp64 units (the product and floor in fp64 took a third of a long append's time).
-// At least 2 radians a token: in fp64, which keeps 2^-53 of them.
+// freq / 2 pi mod 1 in units of 2^-64: freq = m 2^-sh with a 24-bit m, so it is m times the bits of 1 / 2 pi, shifted, of which
+// the turns above 1 fall away.  In integers, as this GPU has few fp64 units (the product and floor in fp64 took a third of a
+// long append's time).  Below 2 radians a token the first 64 bits do; above, 128 of the first 256 (the digits come from
+// arctangents of 1/5 and 1/239 in long integers).  Less than 2^-62 off, then, whatever the frequency.
 RF4_DEV uint64_t turn_fraction(float freq) {
+  constexpr uint64_t k0 = 0x28BE60DB9391054Aull, k1 = 0x7F09D5F47D4D3770ull, k2 = 0x36D8A5664F10E410ull, k3 = 0x7F9458EAF7AEF158ull;
   const uint32_t u = __float_as_uint(freq), E = u >> 23 & 255u;
-  uint64_t r = 0;
+  const uint64_t m = E ? (u & 0x7FFFFFu) | 0x800000u : 0u;
+  uint64_t r;
   if (E > 127u) {
-    const double f = (double)fabsf(freq) * 0.15915494309189533577;
-    r = (uint64_t)((f - floor(f)) * 18446744073709551616.0);
+    // from bit `skip` on: before it stand whole turns for any m
+    const uint32_t skip = E > 150u ? E - 150u : 0u, sh = E < 150u ? 150u - E : 0u, part = skip & 63u;
+    const uint64_t a = skip < 64u ? k0 : k1, b = skip < 64u ? k1 : k2, c = skip < 64u ? k2 : k3;
+    const uint64_t w0 = part ? a << part | b >> (64u - part) : a, w1 = part ? b << part | c >> (64u - part) : b;
+    const uint64_t lo = m * w0, mid = lo + __umul64hi(m, w1), hi = __umul64hi(m, w0) + (mid < lo);
+    r = sh ? hi << (64u - sh) | mid >> sh : mid;
   } else {
-    const uint64_t m = E ? (u & 0x7FFFFFu) | 0x800000u : 0u, k = 0x28BE60DB9391054Aull;
     const uint32_t sh = 150u - E;  // at least 23
-    const uint64_t lo = m * k, hi = __umul64hi(m, k);
+    const uint64_t lo = m * k0, hi = __umul64hi(m, k0);
     r = sh < 64u ? hi << (64u - sh) | lo >> sh : sh < 128u ? hi >> (sh - 64u) : 0u;
   }
   return u >> 31 ? 0ull - r : r;
@@ -254,7 +260,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __g
     const int d = d0 + i;
     if (PAIRS == kWhole || d < rot) {
       turned |= 1u << i;
-      if (PAIRS != kInterleaved || i % 2 == 0) turns[i] = turn_fraction(p.freq[PAIRS == kInterleaved ? d / 2 : PAIRS == kWhole || d < half ? d : d - half]);
+      if (PAIRS != kInterleaved || i % 2 == 0) {
+        const float f = p.freq[PAIRS == kInterleaved ? d / 2 : PAIRS == kWhole || d < half ? d : d - half];
+        turns[i] = turn_fraction(f);
+        if (!(fabsf(f) <= 3.402823466e38f)) turned |= 16u << i;  // no angle: NaN
+      }
     }
   }
 
@@ -284,6 +294,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __g
       continue;
     }
     turn(turns[i] * (uint64_t)pos, cs[i], sn[i]);
+    if (turned >> (4 + i) & 1u) cs[i] = sn[i] = __uint_as_float(0x7FC00000u);
     cs[i] *= p.amplitude;
     sn[i] *= PAIRS != kHalves || d0 + i < half ? -p.amplitude : p.amplitude;
   }

@@ -325,11 +325,12 @@ typedef struct rocmfp4_paged_cache {
  * the format definition.
  *   - x          [M] rows of H heads of D values of x_type, rows ldx apart;
  *   - positions  [M] int32, of either sign;
- *   - freq       [rot / 2] fp32.  rot even, 0 .. D (0: only the rounding);
+ *   - freq       [rot / 2] fp32, of any size and sign (not finite: its pairs
+ *                are NaN).  rot even, 0 .. D (0: only the rounding);
  *   - y          [M][H][D] of y_type, contiguous, 8-byte aligned.
  *   - D a multiple of 32, at most 256.
- *   - The angle is exact to about 2^-32 of a turn at any position; the turn is
- *     fp32, and each output is rounded once.
+ *   - The angle is exact to about 2^-31 of a turn at any position and frequency;
+ *     the turn is fp32, and each output is rounded once.
  *   - One programmatic dependent launch on `stream`. */
 rocmfp4_status rocmfp4_rotary(const void *x, rocmfp4_out_dtype x_type, int64_t ldx,
                               const int32_t *positions, const float *freq, int64_t rot,
