@@ -549,7 +549,7 @@ def rotary_frequencies(rot: int, base: float = 10000.0, *, method: str = "none",
 def rotary(x, freq, positions, *, interleaved: bool = False, amplitude: float = 1.0, dtype=None, out=None, stream=None):
     """y [M, H, D] of the heads x [M, H, D] (float32, bfloat16 or float16, rows of contiguous heads) at positions [M]
     (int32): the first 2 * len(freq) values of each head turned, pairs (i, i + rot / 2), or (2i, 2i + 1) if interleaved, by
-    positions * freq[i], times amplitude.  float16 or bfloat16, into ``out`` or a new tensor of ``dtype`` (float16)."""
+    positions * freq[i], times amplitude.  float16 or bfloat16, into ``out`` (apart from x) or a new tensor of ``dtype`` (float16)."""
     torch = _torch()
     codes = _DTYPES or _dtypes()
     M, H, ld = _heads(x, "x", x.shape[-1])
@@ -572,7 +572,7 @@ def rope_append(cache: PagedCache, q, k, v, freq=None, *, positions=None, interl
     q [M, H, D] (or None), k and v [M, kv_heads, D] float32, bfloat16 or float16, alike, with rows of contiguous heads (parts
     of a QKV product's rows, say).  The first 2 * len(freq) values of q's and k's heads are turned as by rotary(), at
     positions (int32 [M]; None: each token's place in its sequence); freq None turns nothing.  k and v are packed from
-    their float32 values by the quantiser's rule.  cache.lens counts the new tokens already."""
+    their float32 values by the quantiser's rule.  cache.lens counts the new tokens already.  q_out lies apart from q, k and v."""
     torch = _torch()
     codes = _DTYPES or _dtypes()
     D, index = cache.head, cache._index

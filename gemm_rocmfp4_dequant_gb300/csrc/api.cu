@@ -523,6 +523,13 @@ rocmfp4_status paged_args(const rocmfp4_paged_cache* c, PagedArgs* out) {
   return ROCMFP4_OK;
 }
 
+// Whether rows of `width` bytes, `stride` apart, touch the `bytes` from `out` on; rows with gaps count whole.
+bool rows_touch(const void* x, int64_t rows, int64_t stride, int64_t width, const void* out, int64_t bytes) {
+  if (x == nullptr || rows == 0 || bytes == 0) return false;
+  const unsigned __int128 a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(out);
+  return a < b + bytes && b < a + (unsigned __int128)(rows - 1) * stride + width;
+}
+
 // Shared by rocmfp4_rotary and rocmfp4_rope_append (`cache` not NULL).
 rocmfp4_status rope(RopeArgs a, const rocmfp4_paged_cache* cache, cudaStream_t s) {
   rocmfp4_status st;
@@ -555,6 +562,11 @@ rocmfp4_status rope(RopeArgs a, const rocmfp4_paged_cache* cache, cudaStream_t s
   if (a.H > 65536 || a.M * (a.D / 32) >= (int64_t(1) << 31)) return fail(ROCMFP4_ERR_UNSUPPORTED, "rotary positions: sizes too large");
   if ((reinterpret_cast<uintptr_t>(a.q_out) & 7u) != 0)
     return fail(ROCMFP4_ERR_UNSUPPORTED, "rotary positions: the output must be 8-byte aligned");
+  // Partners of a pair may be read by another block after a value's output: in place the results would depend on the order.
+  const int64_t size = a.type == ROCMFP4_OUT_F32 ? 4 : 2;
+  for (int i = 0; i < 3; ++i)
+    if (rows_touch(a.x[i], a.M, a.ld[i] * size, widths[i] * size, a.q_out, a.M * widths[0] * 2))
+      return fail(ROCMFP4_ERR_INVALID_ARG, "the output must not overlap the inputs");
   DeviceState* d = nullptr;
   if ((st = device_state(&d)) != ROCMFP4_OK) return st;
   a.cache.err = d->err;

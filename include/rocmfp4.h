@@ -327,7 +327,8 @@ typedef struct rocmfp4_paged_cache {
  *   - positions  [M] int32, of either sign;
  *   - freq       [rot / 2] fp32, of any size and sign (not finite: its pairs
  *                are NaN).  rot even, 0 .. D (0: only the rounding);
- *   - y          [M][H][D] of y_type, contiguous, 8-byte aligned.
+ *   - y          [M][H][D] of y_type, contiguous, 8-byte aligned, apart from x
+ *                (ROCMFP4_ERR_INVALID_ARG).
  *   - D a multiple of 32, at most 256.
  *   - The angle is exact to about 2^-31 of a turn at any position and frequency;
  *     the turn is fp32, and each output is rounded once.
@@ -345,7 +346,8 @@ rocmfp4_status rocmfp4_rotary(const void *x, rocmfp4_out_dtype x_type, int64_t l
  *                tensors of their own.  H may be 0 (no q, no q_out);
  *   - positions  [M] int32, or NULL: a token's place in its sequence;
  *   - freq, rot, interleaved, amplitude as for rocmfp4_rotary; v is not turned;
- *   - q_out      [M][H][D] of q_type, contiguous, 8-byte aligned.
+ *   - q_out      [M][H][D] of q_type, contiguous, 8-byte aligned, apart from q,
+ *                k and v (ROCMFP4_ERR_INVALID_ARG).
  *   - A row whose place is before its sequence's first token (cu gives more
  *     rows than lens tokens) goes to no page; its q is turned all the same.
  *   - The rows of one call must lie in distinct slots: of two rows for one
