@@ -7,7 +7,7 @@
 // row r is row r / G of the chunk, head r % G.  They are cut into tiles of up to
 // 256; a tile walks over the tokens it sees, 128 at a time:
 //   S = Q K^T    tcgen05.mma, 128 rows x 128 tokens, Q and K in shared memory
-//   P = 2^(S scale log2 e - m + 7), m a running maximum, into tensor memory
+//   P = 2^((S - m) scale log2 e + 7), m a running maximum, into tensor memory
 //   O += P V     tcgen05.mma, P from tensor memory, V from shared memory
 // K and V are decoded from their blocks into shared memory, exact in fp16 (K in
 // q's type), once for all rows of the tile.
@@ -72,6 +72,7 @@ constexpr int kSlots = 3;     // parts a CTA may hold: of its first, its last, a
 constexpr uint32_t kSuspendNs = 1000000;
 constexpr float kGrow = 8.f;  // log2 of how far a maximum may lead its reference
 constexpr float kLift = 7.f;  // log2 of P's factor
+constexpr float kLarge = 4096.f;  // references (times scale log2 e) from which on scores are subtracted before they are scaled
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Params : Batch {
@@ -413,11 +414,11 @@ RF4_DEV float top_of(const float (&x)[32], uint32_t keep) {
 
 // 32 columns of S to P, packed; their sum is added to `sum`.
 template <bool MASK>
-RF4_DEV void weights(const float (&x)[32], uint32_t (&h)[16], uint64_t scale2, uint64_t shift2, uint64_t (&sum)[2], uint32_t keep) {
+RF4_DEV void weights(const float (&x)[32], uint32_t (&h)[16], uint64_t scale2, uint64_t lift2, uint64_t (&sum)[2], uint32_t keep) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     float y0, y1;
-    un2(fma2(f2(masked<MASK>(x[2 * i], 2 * i, keep), masked<MASK>(x[2 * i + 1], 2 * i + 1, keep)), scale2, shift2), y0, y1);
+    un2(fma2(f2(masked<MASK>(x[2 * i], 2 * i, keep), masked<MASK>(x[2 * i + 1], 2 * i + 1, keep)), scale2, lift2), y0, y1);
     y0 = ex2(y0);
     y1 = ex2(y1);
     sum[i & 1] = add2(sum[i & 1], f2(y0, y1));
@@ -425,13 +426,31 @@ RF4_DEV void weights(const float (&x)[32], uint32_t (&h)[16], uint64_t scale2, u
   }
 }
 
+// S of a tile's row in tensor memory less its reference where that is kLarge or more.  Below, (S - m) scale
+// is S scale - m scale, fused, with the second product rounded: off by 2^-24 of it, 2^-12 at most, the same for a whole
+// row; where scores are in the millions it would be powers of two, and P outside of fp16.  (The difference first for all:
+// a prompt of 4096 255 us, not 246.)
+__device__ __noinline__ void subtract(uint32_t s, float ref) {
+#pragma unroll 1
+  for (int c = 0; c < kTok; c += 32) {
+    float x[32];
+    tmem_ld32(s + c, x);
+    tmem_wait_ld(x);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] -= ref;
+    tmem_st32(s + c, x);
+  }
+  tmem_wait_st();
+}
+
 // S of this lane's row in tensor memory at `s` -> P at the same columns, O
 // (at `o`, D columns) scaled where the reference moves.  Tokens a .. e - 1 of
 // the tile are seen, but for `bad` groups of 16.  S is read twice, in loops that
 // are kept short: this serves a row tile's first and last token tiles, and code
 // that runs seldom had better not push the rest out of the instruction cache.
+// Returns whether the warp has a large reference.
 template <int D>
-RF4_DEV void softmax_tile(uint32_t s, uint32_t o, Row& st, float scale_log2, bool first, bool used, int a, int e, uint32_t bad) {
+RF4_DEV bool softmax_tile(uint32_t s, uint32_t o, Row& st, float scale_log2, bool first, bool used, int a, int e, uint32_t bad) {
   float x[32], top = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < kTok; c += 32) {
@@ -440,13 +459,12 @@ RF4_DEV void softmax_tile(uint32_t s, uint32_t o, Row& st, float scale_log2, boo
     tmem_wait_ld(x);
     top = fmaxf(top, top_of<true>(x, keep));
   }
-  top *= scale_log2;
   if (first) {
     st.m = top;
   } else {
-    const bool grow = used && top > st.m + kGrow;
+    const bool grow = used && (top - st.m) * scale_log2 > kGrow;
     if (__any_sync(0xffffffffu, grow)) {
-      const float alpha = grow ? ex2(st.m - top) : 1.f;
+      const float alpha = grow ? ex2((st.m - top) * scale_log2) : 1.f;
       if (grow) st.m = top;
       st.l *= alpha;
 #pragma unroll 1
@@ -459,8 +477,14 @@ RF4_DEV void softmax_tile(uint32_t s, uint32_t o, Row& st, float scale_log2, boo
       }
     }
   }
-  const float shift = kLift - (st.m == -INFINITY ? 0.f : st.m);
-  const uint64_t scale2 = f2(scale_log2, scale_log2), shift2 = f2(shift, shift);
+  float ref = st.m == -INFINITY ? 0.f : st.m;
+  const bool mine = used && fabsf(ref) * scale_log2 >= kLarge, large = __any_sync(0xffffffffu, mine);
+  if (large) {
+    subtract(s, mine ? ref : 0.f);  // a row's results do not depend on its neighbours'
+    if (mine) ref = 0.f;
+  }
+  const float lift = fmaf(-ref, scale_log2, kLift);
+  const uint64_t scale2 = f2(scale_log2, scale_log2), lift2 = f2(lift, lift);
   uint64_t sum[2] = {0, 0};
 #pragma unroll 1
   for (int c = 0; c < kTok; c += 32) {
@@ -468,23 +492,25 @@ RF4_DEV void softmax_tile(uint32_t s, uint32_t o, Row& st, float scale_log2, boo
     tmem_ld32(s + c, x);
     const uint32_t keep = kept(c, a, e, bad);
     tmem_wait_ld(x);
-    weights<true>(x, h, scale2, shift2, sum, keep);
+    weights<true>(x, h, scale2, lift2, sum, keep);
     tmem_st16(s + c / 2, h);
   }
   float s0, s1;
   un2(add2(sum[0], sum[1]), s0, s1);
   st.l += s0 + s1;
   tmem_wait_st();
+  return large;
 }
 
-// The same for a tile that is seen whole and is not the row's first: P by the
+// The same for a tile that is seen whole and is not the row's first, of a warp without large
+// references: P by the
 // reference as it stands, in one pass, with the maximum beside it; P waits in
 // registers until that shows whether the reference holds, and where it does
 // not (a maximum that has grown by more than 2^8, seldom) the tile is done again.
 template <int D>
 RF4_DEV bool softmax_next(uint32_t s, Row& st, float scale_log2, bool used) {
-  const float shift = kLift - (st.m == -INFINITY ? 0.f : st.m);
-  const uint64_t scale2 = f2(scale_log2, scale_log2), shift2 = f2(shift, shift);
+  const float ref = st.m == -INFINITY ? 0.f : st.m, lift = fmaf(-ref, scale_log2, kLift);
+  const uint64_t scale2 = f2(scale_log2, scale_log2), lift2 = f2(lift, lift);
   uint64_t sum[2] = {0, 0};
   uint32_t h[4][16];
   float x[32], y[32];
@@ -492,19 +518,19 @@ RF4_DEV bool softmax_next(uint32_t s, Row& st, float scale_log2, bool used) {
   tmem_wait_ld(x);
   tmem_ld32(s + 32, y);
   float top = top_of<false>(x, 0);
-  weights<false>(x, h[0], scale2, shift2, sum, 0);
+  weights<false>(x, h[0], scale2, lift2, sum, 0);
   tmem_wait_ld(y);
   tmem_ld32(s + 64, x);
   top = fmaxf(top, top_of<false>(y, 0));
-  weights<false>(y, h[1], scale2, shift2, sum, 0);
+  weights<false>(y, h[1], scale2, lift2, sum, 0);
   tmem_wait_ld(x);
   tmem_ld32(s + 96, y);
   top = fmaxf(top, top_of<false>(x, 0));
-  weights<false>(x, h[2], scale2, shift2, sum, 0);
+  weights<false>(x, h[2], scale2, lift2, sum, 0);
   tmem_wait_ld(y);
   top = fmaxf(top, top_of<false>(y, 0));
-  weights<false>(y, h[3], scale2, shift2, sum, 0);
-  if (__any_sync(0xffffffffu, used && top * scale_log2 > st.m + kGrow)) {
+  weights<false>(y, h[3], scale2, lift2, sum, 0);
+  if (__any_sync(0xffffffffu, used && (top - st.m) * scale_log2 > kGrow)) {
     return false;
   }
 #pragma unroll
@@ -566,7 +592,7 @@ RF4_DEV void merge_parts(const Params& p, const Item& it, const float2* ml) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         // a sum of zero: nothing seen, O may never have been written
-        const float e = v[u].y == 0.f ? 0.f : ex2(v[u].x - M[u]);
+        const float e = v[u].y == 0.f ? 0.f : ex2((v[u].x - M[u]) * p.scale_log2);
         L[u] += e * v[u].y;
         O[u].x += v[u].y == 0.f ? 0.f : e * x[u].x;
         O[u].y += v[u].y == 0.f ? 0.f : e * x[u].y;
@@ -782,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
       int lo = 0, hi = 0;
       if (used) seen(p, it.s, row / p.G, lo, hi);
       Row st;
-      bool first = true;
+      bool first = true, large = false;
       for (int j = wide ? 0 : t; j < tiles; j += wide ? 1 : 2) {
         const int t0 = (c0 + j) * kTok;
         const int a = max(lo - t0, 0), e = min(max(hi - t0, 0), kTok);
@@ -791,8 +817,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         const uint32_t bad = ctl.tiles[(tile0 + j) % kTiles].bad;
         const bool part = __any_sync(0xffffffffu, used && (a > 0 || e < kTok)) || bad;
         // (P of rows that nobody reads may be anything)
-        if (!idle && (part || first || !softmax_next<D>(s_at, st, p.scale_log2, used)))
-          softmax_tile<D>(s_at, o_at, st, p.scale_log2, first, used, a, e, bad);
+        if (!idle && (part || first || large || !softmax_next<D>(s_at, st, p.scale_log2, used)))
+          large = softmax_tile<D>(s_at, o_at, st, p.scale_log2, first, used, a, e, bad);
         first = false;
         tc_fence_before();
         __syncwarp();

@@ -6,7 +6,8 @@
 //   scores: A = 16 tokens x 16 of D of K, decoded in registers (exact), B = q;
 //   P V:    A = 16 of D x 16 tokens of V^T (decoded rows, transposed by
 //           movmatrix), B = P^T, rounded to fp16 after a factor of 2^15.
-// Scores, maxima, sums and the weighted sum are fp32.  P's half step of 2^-11 is
+// Scores, maxima, sums and the weighted sum are fp32; a score is subtracted from its maximum before
+// the scaling, so that large ones differ as they do.  P's half step of 2^-11 is
 // the output type's own (fp16) or an eighth of it (bf16).
 //
 // A CTA's four warps take a row tile's 32-token chunks in turn, each with a ring
@@ -101,7 +102,7 @@ RF4_DEV void add_parts(const Params& p, const Item& it, const float2* ml, float*
     if (M == -INFINITY) M = 0.f;
     for (int n = lane; n < parts; n += 32) {
       const float2 v = __ldcg(&ml[record(n) + row]);
-      const float e = v.y == 0.f ? 0.f : ex2_approx(v.x - M);
+      const float e = v.y == 0.f ? 0.f : ex2_approx((v.x - M) * p.scale_log2);
       weight[row * parts + n] = e;
       L += e * v.y;
     }
@@ -290,7 +291,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_few_kernel(const _
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[mt][e] *= p.scale_log2;
           if (part) {
             const int t = t0 + 16 * mt + r + (e >= 2 ? 8 : 0);
             if (t < clo[e & 1] || t >= chi[e & 1] || !(have >> mt & 1u)) x[mt][e] = -INFINITY;
@@ -304,14 +304,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_few_kernel(const _
         cmax[j] = fmaxf(cmax[j], __shfl_xor_sync(0xffffffffu, cmax[j], 8));
         cmax[j] = fmaxf(cmax[j], __shfl_xor_sync(0xffffffffu, cmax[j], 16));
         const float m = fmaxf(mrun[j], cmax[j]), ref = m == -INFINITY ? 0.f : m;
-        alpha[j] = ex2_approx(mrun[j] - ref);
+        alpha[j] = ex2_approx((mrun[j] - ref) * p.scale_log2);
         mrun[j] = m;
         float sum = 0.f;
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int e = j; e < 4; e += 2) {
-            pv[mt][e] = ex2_approx(x[mt][e] - ref);
+            pv[mt][e] = ex2_approx((x[mt][e] - ref) * p.scale_log2);
             sum += pv[mt][e];
           }
         lrun[j] = lrun[j] * alpha[j] + sum;
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_few_kernel(const _
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float* s = area + w * F::STATE;
-        const float e = ex2_approx(s[rr] - ref);
+        const float e = ex2_approx((s[rr] - ref) * p.scale_log2);
         L += e * s[kCols + rr];
         x += e * s[2 * kCols + rr * D + d];
         y += e * s[2 * kCols + rr * D + d + 1];
