@@ -1042,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         if (lane == 0) {
           ctl.items[n % kItems] = it;
           mbar_arrive(smem_addr(&ctl.item_full[n % kItems]));
-          if (more && it.s.len > it.s.lim) atomicOr(p.c.err, kErrBadPage);
+          if (more && it.s.over) atomicOr(p.c.err, kErrBadPage);
         }
         if (more) load.item(p, ctl, wait, it);
         else load.stop(ctl, wait);

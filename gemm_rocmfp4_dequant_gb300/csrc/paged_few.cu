@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_few_kernel(const _
     int lo, hi, lo1, hi0;
     seen(p, it.s, it.r0 / p.G, lo, hi0);
     seen(p, it.s, (it.r0 + it.rows - 1) / p.G, lo1, hi);
-    if (threadIdx.x == 0 && it.s.len > it.s.lim) atomicOr(p.c.err, kErrBadPage);
+    if (threadIdx.x == 0 && it.s.over) atomicOr(p.c.err, kErrBadPage);
     const int first = max(4 * it.c0, lo / kChunk), end = min(4 * (it.c0 + it.tiles), (hi + kChunk - 1) / kChunk);
     const int32_t* pages = p.c.table + (int64_t)it.b * p.c.ldt;
     const int64_t head = (int64_t)it.hk * ps * F::RB;

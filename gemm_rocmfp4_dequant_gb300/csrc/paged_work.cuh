@@ -22,8 +22,9 @@ struct Batch {
 
 struct Seq {
   int row0, n;  // rows of the call
-  int len;      // tokens
+  int at;       // token that the first of them is, counted from the sequence's last row, which may lie behind the call's
   int lim;      // tokens that the table has room for
+  bool over;    // whether the sequence has more
 };
 
 // A row tile's share of this CTA.
@@ -50,9 +51,11 @@ RF4_DEV Seq sequence(const Batch& p, int b) {
   const int r0 = min(max(p.c.cu[b], 0), p.M), r1 = min(max(p.c.cu[b + 1], 0), p.M);
   s.row0 = r0;
   s.n = max(r1 - r0, 0);
-  s.len = max(p.c.lens[b], 0);
+  const int len = max(p.c.lens[b], 0);
+  s.at = len - max(max(p.c.cu[b + 1], 0) - r0, 0);
   const long long room = (long long)p.c.width * p.c.page_size;
-  s.lim = (int)(s.len < room ? s.len : room);
+  s.lim = (int)(len < room ? len : room);
+  s.over = len > s.lim;
   return s;
 }
 
@@ -61,7 +64,7 @@ RF4_DEV void seen(const Batch& p, const Seq& s, int i, int& lo, int& hi) {
   lo = 0;
   hi = s.lim;
   if (p.causal) {
-    const long long end = (long long)s.len - s.n + i + 1;
+    const long long end = (long long)s.at + i + 1;
     hi = (int)(end < 0 ? 0 : end < s.lim ? end : s.lim);
     if (p.window > 0 && end > p.window) lo = (int)(end - p.window < hi ? end - p.window : hi);
   }

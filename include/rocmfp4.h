@@ -289,7 +289,8 @@ rocmfp4_status rocmfp4_logprobs(const void *logits, rocmfp4_out_dtype type, int6
  *            cu[b + 1] - 1 of a call belong to sequence b.  Where a row is a
  *            token of its sequence, the rows are the last ones: row i of n is
  *            token lens[b] - n + i.  Rows at or behind cu[B] are padding: they
- *            are not read, and their outputs are left as they are.
+ *            are not read, and their outputs are left as they are.  A call of
+ *            fewer rows than cu[B] deals with the first of them;
  *   - The struct is host memory, read during the call; table, lens and cu
  *     are device memory, read by the kernels (a captured graph follows
  *     their contents).
