@@ -627,7 +627,8 @@ def cache_read(cache: PagedCache, rows=None, *, dtype=None, k_out=None, v_out=No
 def paged_attention(q, cache: PagedCache, scale: float, *, causal: bool = True, window: int = 0, out=None, stream=None):
     """out [M, H, D] of q's type: attention of the batch's rows q [M, H, D] (float16 or bfloat16, rows of contiguous heads)
     over the pages of their sequences.  causal: row i of the n of sequence b sees the tokens up to lens[b] - n + i, with a
-    window only the last ``window`` of them; else every row sees all lens[b] tokens.  A row that sees none gives zeros."""
+    window only the last ``window`` of them; else every row sees all lens[b] tokens.  A row that sees none gives zeros.  Single tokens
+    and long chunks in one batch are right, but faster as a call each (the kernel is chosen by the batch's average)."""
     M, H, ldq = _heads(q, "q", cache.head)
     index = cache._index
     if q.device.index != index:

@@ -624,7 +624,8 @@ rocmfp4_status paged_attention(const rocmfp4_paged_cache* cache, PagedAttnArgs a
   // At most 16 (row, head) pairs a sequence and KV head, on the average: the kernel of few rows, tiles of 8; else tiles of 128
   // and 256.  Measured, few against many: 16 rows: 41 / 62 us (32768 tokens), 68 / 69 (16 sequences of 4096), 71 / 86 (64 of 1000),
   // 19 / 27 (9 of 3001, D = 64); 20 to 24 rows: 52 / 62, 90 / 70, 100 / 89, 23 / 28.  The lengths of the chunks are on the device:
-  // either kernel is right for any.
+  // either kernel is right for any.  A batch of unequal chunks is served by the one that its average names: 64 single tokens over
+  // 4096 with 512 rows over 16384 take 479 us, in two calls 111 + 167.
   const bool few = a.M * (H / cache->Hkv) <= 16 * (int64_t)cache->B;
   cudaError_t e = few ? launch_paged_few(cache->variant, act, a, d->sms, s) : launch_paged_attention(cache->variant, act, a, d->sms, s);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");

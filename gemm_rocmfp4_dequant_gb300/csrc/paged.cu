@@ -23,12 +23,13 @@
 // halves of whole blocks (rot = D, a multiple of 64) they own the partners' block
 // too.  Few rows: one head a walk, for latency; many rows: one wave of walks.
 // Measured, 4096 tokens of 40 + 8 + 8 heads of 128 in fp32, in a graph with their
-// reading back: 53 us, about 42 of them here (163 MB in and out, 3.9 TB/s).  82 with a
+// reading back: 52 us, 41 of them here (163 MB in and out, 4.0 TB/s).  82 with a
 // block a thread, angles in fp64 and five walks; 64 with angles in integers and four
 // heads' loads in flight; 56 with pairs of blocks; 55 with one wave of walks, in CTAs
-// of 256 threads, four an SM, which leave some SMs three.  Six CTAs an SM: 60.  512 x
-// 40 x 128 alone: 5.5 us.  Bound by issue and latency together: 24 warps an SM, 41 %
-// of the issue slots.
+// of 256 threads, four an SM, which leave some SMs three; 53 with fp64 for frequencies
+// of 2 and more.  Six CTAs an SM: 60.  512 x 40 x 128 alone: 4.5 us, 8192 rows 40 us (6.2
+// TB/s).  Bound by issue and latency together: 28 warps an SM, 23 on the average, 43 % of
+// the issue slots.
 //
 // cache_read_kernel.  The rows' blocks back as dense values, exact in every
 // output type; four threads a block, one or four tokens a warp.  Measured,

@@ -42,9 +42,9 @@
 // warps, which leave the softmax 144 registers, 322; decode warps that fetch
 // their own rows 376.)
 //
-// Measured (40 query heads over 8 of D = 128, in a graph): a prompt of 4096 245 us
+// Measured (40 query heads over 8 of D = 128, in a graph): a prompt of 4096 246 us
 // in bf16 (700 TFLOP/s of the products a causal mask asks for), 229 in fp16; 512 rows
-// over 33280 tokens 290 us (1190 TFLOP/s, fp16).  Bound by shared memory: a wide token tile stores
+// over 33280 tokens 283 us (1225 TFLOP/s, fp16).  Bound by shared memory: a wide token tile stores
 // 64 KB of decoded K and V, reads their raw rows, and the four products read Q, K
 // and V again, 2336 cycles at 128 bytes a cycle, and the 512 rows take about 4000 a
 // wide token tile.  In bf16 K needs a second conversion.

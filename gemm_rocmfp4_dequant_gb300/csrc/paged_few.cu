@@ -18,8 +18,8 @@
 // tile adds the parts, its warps a quarter of them each.
 //
 // Measured (40 query heads over 8 of D = 128, in a graph): one token over 32768
-// 24.6 us (38 MB, 1.5 TB/s), 16 over 4096 40.4 us (71 MB, 1.8 TB/s), 64 over 2000
-// 64.3 us (147 MB, 2.3 TB/s), one over 100 7.2 us.  What bounds it is the decode and its
+// 24.7 us (38 MB, 1.5 TB/s), 16 over 4096 40.4 us (71 MB, 1.8 TB/s), 64 over 2000
+// 64.6 us (147 MB, 2.3 TB/s), one over 100 7.1 us.  What bounds it is the decode and its
 // latencies (about 1400 warp instructions a chunk, half of the issue slots used);
 // of the 40.4 us, copies and the joining of parts alone take 20.  Tried
 // and not better: three CTAs an SM (40.9 / 66.9 us), V transposed by byte permutes instead of movmatrix

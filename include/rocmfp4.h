@@ -384,10 +384,13 @@ rocmfp4_status rocmfp4_cache_read(const rocmfp4_paged_cache *cache, void *k_out,
  *   - q    [M] rows of H heads of D values of type act, rows ldq apart, 16-byte
  *          aligned; out [M][H][D] of type act, contiguous, 16-byte aligned.
  *   - H a multiple of Hkv; D 64 or 128; scale from 1e-30 to 1e30.
- *   - Scores, maxima, sums and the weighted sum are fp32; p is rounded to fp16
+ *   - Scores, maxima, sums and the weighted sum are fp32 (a score q . K[t] beyond
+ *     fp32 makes its row NaN); p is rounded to fp16
  *     for the product with V, and the output once.  Results are bitwise
  *     repeatable for the same inputs on the same device.
- *   - Rows at or behind lens[b] of a page need not hold valid blocks. */
+ *   - Rows at or behind lens[b] of a page need not hold valid blocks.
+ *   - One of two kernels runs, by the batch's average M * H / (B * Hkv): single
+ *     tokens and long chunks together are faster as a call each. */
 rocmfp4_status rocmfp4_paged_attention(const void *q, int64_t ldq, const rocmfp4_paged_cache *cache,
                                        void *out, int64_t M, int64_t H, float scale, int causal,
                                        int64_t window, rocmfp4_act act, rocmfp4_stream_t stream);
